@@ -26,12 +26,23 @@ Q_SR, Q_2D = 2, 4
 # enum fp4_out / fp4_act (fp4_gemm_ex)
 OUT_F32, OUT_BF16, OUT_MXFP4, OUT_MXFP4_OCP, OUT_NVFP4 = 0, 1, 2, 3, 4
 ACT_NONE, ACT_RELU = 0, 1
+# enum fp4_kv_fmt (cache rows)
+KV_BF16, KV_MXFP8, KV_MXFP4 = 0, 1, 2
 
 FUNCTIONS = ("fp4_scale_bytes", "fp4_workspace_size", "fp4_quantize", "fp4_quantize_noalloc", "fp4_quantize_sr",
              "fp4_quantize_ex",
              "fp4_hadamard16", "fp4_dequantize", "fp4_gemm", "fp4_gemm_ex",
              "fp4_gemm_grouped", "fp4_gemm_nvfp4_act", "fp4_gemm_nvfp4_act_supported", "fp4_gemm_w4a8",
-             "fp4_status_string", "fp4_set_debug")
+             "fp4_status_string", "fp4_set_debug", "fp4_kv_append", "fp4_attn_decode_workspace", "fp4_attn_decode",
+             "fp4_kv_evict_workspace", "fp4_kv_evict", "fp4_logprobs_workspace", "fp4_logprobs",
+             "fp4_logprobs_backward")
+
+
+class KVCacheStruct(ctypes.Structure):
+    """struct fp4_kv_cache of include/fp4.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
 
 
 class Fp4Error(RuntimeError):
@@ -60,6 +71,7 @@ def lib():
             pass
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, U32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+        F32C, CACHE = ctypes.c_float, ctypes.POINTER(KVCacheStruct)
         sig = {
             "fp4_scale_bytes": (I64, [I32, I64, I64]),
             "fp4_workspace_size": (SZ, [I32, I32, I64, I64, I64, I32]),
@@ -77,6 +89,16 @@ def lib():
             "fp4_gemm_w4a8": (I32, [P, P, P, P, P, I32, P, I64, I64, I64, I32, P]),
             "fp4_status_string": (ctypes.c_char_p, [I32]),
             "fp4_set_debug": (I32, [I32]),
+            "fp4_kv_append": (I32, [CACHE, P, P, I32, I64, I64, P, I64, I64, P, P, I64, P]),
+            "fp4_attn_decode_workspace": (SZ, [CACHE, I64, I64, I64, I32]),
+            "fp4_attn_decode": (I32, [CACHE, P, I32, I64, P, I64, P, I64, I64, I64, I64, F32C, P, I32, P, P, P, I64,
+                                      P, SZ, P]),
+            "fp4_kv_evict_workspace": (SZ, [CACHE, I64, I64, I64]),
+            "fp4_kv_evict": (I32, [CACHE, P, I64, P, P, I64, CACHE, P, I64, P, P, I64, P, I64, I64, I64, I64, P, SZ,
+                                   P]),
+            "fp4_logprobs_workspace": (SZ, [I64, I64, I32]),
+            "fp4_logprobs": (I32, [P, I32, I64, I64, I64, F32C, P, I32, P, P, P, I32, P, P, P, SZ, P]),
+            "fp4_logprobs_backward": (I32, [P, I32, I64, I64, I64, F32C, P, I32, P, P, P, P, P, I64, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -159,6 +181,49 @@ def fp4_gemm_nvfp4_act_supported(M, N, K, x_dtype):
 
 def fp4_gemm_w4a8(A, sA, B, sB, bias, act, C, M, N, K, out_dtype, stream):
     return lib().fp4_gemm_w4a8(A, sA, B, sB, bias, act, C, M, N, K, out_dtype, stream)
+
+
+def fp4_kv_append(cache, k, v, in_dtype, k_stride, v_stride, page_table, table_width, seqs, seq, pos, rows, stream):
+    return lib().fp4_kv_append(cache, k, v, in_dtype, k_stride, v_stride, page_table, table_width, seqs, seq, pos,
+                               rows, stream)
+
+
+def fp4_attn_decode_workspace(cache, B, q_heads, max_len, weights):
+    return lib().fp4_attn_decode_workspace(cache, B, q_heads, max_len, weights)
+
+
+def fp4_attn_decode(cache, q, q_dtype, q_stride, page_table, table_width, lens, B, q_heads, max_len, window, scale,
+                    out, out_dtype, lse, weights_in, weights_out, weights_stride, workspace, workspace_bytes, stream):
+    return lib().fp4_attn_decode(cache, q, q_dtype, q_stride, page_table, table_width, lens, B, q_heads, max_len,
+                                 window, scale, out, out_dtype, lse, weights_in, weights_out, weights_stride,
+                                 workspace, workspace_bytes, stream)
+
+
+def fp4_kv_evict_workspace(cache, B, max_len, budget):
+    return lib().fp4_kv_evict_workspace(cache, B, max_len, budget)
+
+
+def fp4_kv_evict(src, src_table, src_width, lens, weights, weights_stride, dst, dst_table, dst_width, out_lens,
+                 out_weights, out_stride, kept, B, max_len, budget, recent, workspace, workspace_bytes, stream):
+    return lib().fp4_kv_evict(src, src_table, src_width, lens, weights, weights_stride, dst, dst_table, dst_width,
+                              out_lens, out_weights, out_stride, kept, B, max_len, budget, recent, workspace,
+                              workspace_bytes, stream)
+
+
+def fp4_logprobs_workspace(N, V, top_k):
+    return lib().fp4_logprobs_workspace(N, V, top_k)
+
+
+def fp4_logprobs(x, dtype, stride_, N, V, scale, tokens, M, logp, entropy, lse, top_k, top_logp, top_index, workspace,
+                 workspace_bytes, stream):
+    return lib().fp4_logprobs(x, dtype, stride_, N, V, scale, tokens, M, logp, entropy, lse, top_k, top_logp,
+                              top_index, workspace, workspace_bytes, stream)
+
+
+def fp4_logprobs_backward(x, dtype, stride_, N, V, scale, tokens, M, lse, entropy, g_logp, g_entropy, dx, dx_stride,
+                          stream):
+    return lib().fp4_logprobs_backward(x, dtype, stride_, N, V, scale, tokens, M, lse, entropy, g_logp, g_entropy, dx,
+                                       dx_stride, stream)
 
 
 # ---- torch helpers: allocation + pointer/stream marshalling only -------------
@@ -492,4 +557,321 @@ def gemm_nvfp4_act(x, w, tensor_scale=None, ts_out=None, out_dtype=None, out=Non
     rc = fp4_gemm_nvfp4_act(_ptr(x), _dtype_code(x), _ptr(ts), flags, _ptr(w.codes), _ptr(w.scales),
                             _ptr(w.tensor_scale), _ptr(out), M, N, K, _dtype_code(out), _stream(stream))
     _check(rc, "fp4_gemm_nvfp4_act")
+    return out
+
+
+# ---- decode-step operators: cache, attention, eviction, log probabilities ------
+def _need_rows(t, name, dtypes, ndim, device=None, shape=None):
+    """Check a tensor whose dimensions after the first are dense and whose
+    first may have any stride (columns of a wider matrix).  Returns that
+    stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor, got %s" % (name, type(t).__name__))
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    if t.dim() != ndim:
+        raise ValueError("%s must have %d dimensions, got shape %s" % (name, ndim, tuple(t.shape)))
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    width, strides = 1, t.stride()
+    for i in range(ndim - 1, 0, -1):
+        if t.shape[i] != 1 and strides[i] != width:
+            raise ValueError("%s must be dense but for its first dimension, got strides %s" % (name, strides))
+        width *= t.shape[i]
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor, got device %s" % (name, t.device))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the call's operands on %s" % (name, t.device, device))
+    if t.shape[0] <= 1:
+        return width
+    if strides[0] < width:
+        raise ValueError("%s has overlapping rows (strides %s)" % (name, strides))
+    return strides[0]
+
+
+class _Alloc:
+    """Allocates a call's outputs and workspace for the stream it runs on: from
+    that stream's memory, so that what the current stream still does with
+    memory freed there cannot meet the call's writes, and marked as used on
+    the current stream too, where the caller goes on with them."""
+
+    def __init__(self, stream, device):
+        torch = _torch()
+        self.device = device
+        self.stream = stream if stream is not None and stream != torch.cuda.current_stream() else None
+
+    def __call__(self, make, *args, **kw):
+        if self.stream is None:
+            return make(*args, device=self.device, **kw)
+        torch = _torch()
+        with torch.cuda.stream(self.stream):
+            t = make(*args, device=self.device, **kw)
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream())
+        return t
+
+
+class KVCache:
+    """A pool of key-value cache pages (struct fp4_kv_cache of include/fp4.h).
+
+    k, v: the pool tensors, pages x kv_heads x page_size x row, where a row is
+    head_dim bfloat16 values (format KV_BF16), head_dim uint8 E4M3 codes
+    (KV_MXFP8) or head_dim / 2 uint8 bytes of E2M1 codes (KV_MXFP4); the MX
+    formats also take k_scales, v_scales, uint8, pages x kv_heads x page_size x
+    head_dim / 32.  The tensors are checked once, here; the object holds them.
+    KVCache.empty allocates a pool."""
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        torch = _torch()
+        _need(k, "k", (torch.bfloat16, torch.uint8), ndim=4)
+        dev = k.device
+        _need_out(v, "v", k.shape, (k.dtype,), dev)
+        pages, heads, page_size, row = k.shape
+        if k.dtype == torch.bfloat16:
+            if k_scales is not None or v_scales is not None:
+                raise ValueError("a bfloat16 cache has no scales")
+            fmt, dim = KV_BF16, row
+        else:
+            for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+                _need(t, name, (torch.uint8,), None, dev, ndim=4)
+            blocks = k_scales.shape[3]
+            if blocks * 32 == row:
+                fmt, dim = KV_MXFP8, row
+            elif blocks * 16 == row:
+                fmt, dim = KV_MXFP4, 2 * row
+            else:
+                raise ValueError("rows of %d bytes and %d scales are neither MXFP8 nor MXFP4" % (row, blocks))
+            for t, name in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+                _need_out(t, name, (pages, heads, page_size, blocks), (torch.uint8,), dev)
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.fmt, self.pages, self.kv_heads, self.page_size, self.head_dim = fmt, pages, heads, page_size, dim
+        self.device = dev
+        self.struct = KVCacheStruct(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), pages, page_size, heads, dim,
+                                    fmt)
+
+    @classmethod
+    def empty(cls, pages, page_size, kv_heads, head_dim, fmt=KV_BF16, device="cuda"):
+        """A pool of uninitialised pages."""
+        torch = _torch()
+        if fmt not in (KV_BF16, KV_MXFP8, KV_MXFP4):
+            raise ValueError("unknown cache format %r" % (fmt,))
+        lead = (pages, kv_heads, page_size)
+        if fmt == KV_BF16:
+            return cls(*(torch.empty(lead + (head_dim,), dtype=torch.bfloat16, device=device) for _ in range(2)))
+        row = head_dim if fmt == KV_MXFP8 else head_dim // 2
+        return cls(*(torch.empty(lead + (w,), dtype=torch.uint8, device=device)
+                     for w in (row, row, head_dim // 32, head_dim // 32)))
+
+
+def _need_cache(cache, name="cache"):
+    if not isinstance(cache, KVCache):
+        raise TypeError("%s must be a KVCache, got %s" % (name, type(cache).__name__))
+    return cache.device
+
+
+def kv_append(cache, k, v, table, seq, pos, stream=None):
+    """Write new keys and values (n x kv_heads x head_dim float32/bfloat16, any
+    row stride) into the cache: row i becomes token pos[i] of sequence seq[i]
+    of the page table (int32, sequences x pages); seq -1 skips a row.  See
+    fp4_kv_append in include/fp4.h."""
+    torch = _torch()
+    dev = _need_cache(cache)
+    ks = _need_rows(k, "k", (torch.float32, torch.bfloat16), 3, dev)
+    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
+    if tuple(k.shape) != shape:
+        raise ValueError("k must have shape %s, got %s" % (shape, tuple(k.shape)))
+    vs = _need_rows(v, "v", (k.dtype,), 3, dev, shape)
+    _need(table, "table", (torch.int32,), None, dev, ndim=2)
+    _need(seq, "seq", (torch.int32,), shape[0], dev, ndim=1)
+    _need(pos, "pos", (torch.int32,), shape[0], dev, ndim=1)
+    rc = fp4_kv_append(cache.struct, _ptr(k), _ptr(v), _dtype_code(k), ks, vs, _ptr(table), table.shape[1],
+                       table.shape[0], _ptr(seq), _ptr(pos), shape[0], _stream(stream))
+    _check(rc, "fp4_kv_append")
+    return cache
+
+
+def attention_workspace(cache, batch, q_heads, max_len, weights=False, device=None):
+    """A zero-filled workspace tensor for decode_attention (or None)."""
+    torch = _torch()
+    dev = _need_cache(cache)
+    n = fp4_attn_decode_workspace(cache.struct, batch, q_heads, max_len, 1 if weights else 0)
+    return torch.zeros(n, dtype=torch.uint8, device=dev if device is None else device) if n else None
+
+
+def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, out=None, out_dtype=None, lse=None,
+                     weights=None, weights_out=None, ws=None, stream=None):
+    """Attention of one new token per sequence over the paged cache; see
+    fp4_attn_decode in include/fp4.h.
+
+    q: batch x q_heads x head_dim float32/bfloat16 (any row stride); table:
+    int32 batch x pages; lens: int32 batch.  max_len bounds lens (default: what
+    the table holds).  scale: default 1 / sqrt(head_dim).  lse: optional
+    float32 batch x q_heads output.  weights_out: optional float32 batch x
+    kv_heads x (>= max_len) output of weights (or 0) plus every token's
+    attention weight; it may be weights itself.  Returns out (dtype of q, or
+    out_dtype)."""
+    torch = _torch()
+    dev = _need_cache(cache)
+    floats = (torch.float32, torch.bfloat16)
+    qs = _need_rows(q, "q", floats, 3, dev)
+    B, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError("q has head_dim %d, the cache %d" % (dim, cache.head_dim))
+    _need(table, "table", (torch.int32,), None, dev, ndim=2)
+    _need(lens, "lens", (torch.int32,), B, dev, ndim=1)
+    if table.shape[0] != B:
+        raise ValueError("table has %d rows, q %d" % (table.shape[0], B))
+    if max_len is None:
+        max_len = table.shape[1] * cache.page_size
+    alloc = _Alloc(stream, dev)
+    if out is None:
+        out = alloc(torch.empty, (B, heads, dim), dtype=q.dtype if out_dtype is None else out_dtype)
+    else:
+        _need_out(out, "out", (B, heads, dim), floats, dev)
+    if lse is not None:
+        _need_out(lse, "lse", (B, heads), (torch.float32,), dev)
+    stride = 0
+    if weights_out is not None:
+        _need(weights_out, "weights_out", (torch.float32,), None, dev, ndim=3)
+        stride = weights_out.shape[2]
+        _need_out(weights_out, "weights_out", (B, cache.kv_heads, stride), (torch.float32,), dev)
+        if weights is not None:
+            _need_out(weights, "weights", (B, cache.kv_heads, stride), (torch.float32,), dev)
+    elif weights is not None:
+        raise ValueError("weights needs weights_out")
+    if ws is None:
+        ws = alloc(attention_workspace, cache, B, heads, max_len, weights_out is not None)
+    else:
+        _need(ws, "ws", (torch.uint8,), None, dev)
+    rc = fp4_attn_decode(cache.struct, _ptr(q), _dtype_code(q), qs, _ptr(table), table.shape[1], _ptr(lens), B, heads,
+                         max_len, window, dim ** -0.5 if scale is None else scale, _ptr(out), _dtype_code(out),
+                         _ptr(lse), _ptr(weights), _ptr(weights_out), stride, _ptr(ws),
+                         0 if ws is None else ws.numel(), _stream(stream))
+    _check(rc, "fp4_attn_decode")
+    return out
+
+
+def evict_workspace(cache, batch, max_len, budget, device=None):
+    """A zero-filled workspace tensor for kv_evict (or None)."""
+    torch = _torch()
+    dev = _need_cache(cache)
+    n = fp4_kv_evict_workspace(cache.struct, batch, max_len, budget)
+    return torch.zeros(n, dtype=torch.uint8, device=dev if device is None else device) if n else None
+
+
+def kv_evict(cache, table, lens, weights, budget, recent, out_table, out_cache=None, ws=None, stream=None):
+    """Keep `budget` tokens of every longer (sequence, kv head): the last
+    `recent` and the largest accumulated attention weights; see fp4_kv_evict
+    in include/fp4.h.
+
+    weights: float32 batch x kv_heads x (>= what the table holds).  The kept
+    tokens move, in order, to out_table's pages (of out_cache; default the
+    same pool), which must not be pages that table reads.  Returns
+    (lens int32 batch, weights float32 batch x kv_heads x what out_table
+    holds, kept int32 batch x kv_heads x budget: old token numbers, then -1)."""
+    torch = _torch()
+    dev = _need_cache(cache)
+    out_cache = cache if out_cache is None else out_cache
+    _need_cache(out_cache, "out_cache")
+    if out_cache.device != dev:
+        raise ValueError("out_cache is on %s, the call's operands on %s" % (out_cache.device, dev))
+    _need(table, "table", (torch.int32,), None, dev, ndim=2)
+    B = table.shape[0]
+    _need(lens, "lens", (torch.int32,), B, dev, ndim=1)
+    _need(out_table, "out_table", (torch.int32,), None, dev, ndim=2)
+    if out_table.shape[0] != B:
+        raise ValueError("out_table has %d rows, table %d" % (out_table.shape[0], B))
+    if budget < 0:
+        raise ValueError("budget is negative")
+    cap = table.shape[1] * cache.page_size
+    _need(weights, "weights", (torch.float32,), None, dev, ndim=3)
+    if tuple(weights.shape[:2]) != (B, cache.kv_heads) or weights.shape[2] < cap:
+        raise ValueError("weights must have shape (%d, %d, >= %d), got %s"
+                         % (B, cache.kv_heads, cap, tuple(weights.shape)))
+    room = max(out_table.shape[1] * cache.page_size, budget)
+    alloc = _Alloc(stream, dev)
+    out_lens = alloc(torch.empty, B, dtype=torch.int32)
+    out_weights = alloc(torch.empty, (B, cache.kv_heads, room), dtype=torch.float32)
+    kept = alloc(torch.empty, (B, cache.kv_heads, budget), dtype=torch.int32)
+    if ws is None:
+        ws = alloc(evict_workspace, cache, B, cap, budget)
+    else:
+        _need(ws, "ws", (torch.uint8,), None, dev)
+    rc = fp4_kv_evict(cache.struct, _ptr(table), table.shape[1], _ptr(lens), _ptr(weights), weights.shape[2],
+                      out_cache.struct, _ptr(out_table), out_table.shape[1], _ptr(out_lens), _ptr(out_weights), room,
+                      _ptr(kept), B, cap, budget, recent, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(rc, "fp4_kv_evict")
+    return out_lens, out_weights, kept
+
+
+class LogProbs:
+    """logprobs' results: logp (N x M), entropy, lse (N), top_logp, top_index (N x top_k, or None)."""
+
+    def __init__(self, logp, entropy, lse, top_logp, top_index):
+        self.logp, self.entropy, self.lse = logp, entropy, lse
+        self.top_logp, self.top_index = top_logp, top_index
+
+
+def logprobs_workspace(n, vocab, top_k=0, device="cuda"):
+    """A zero-filled workspace tensor for logprobs (or None)."""
+    b = fp4_logprobs_workspace(n, vocab, top_k)
+    return _torch().zeros(b, dtype=_torch().uint8, device=device) if b else None
+
+
+def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
+    """Log probabilities of the given tokens (int32 N x M; outside [0, V):
+    padding, 0) under softmax(scale * x), x: N x V float32/bfloat16 logits
+    (any row stride), with the entropy, the log-sum-exp and the top_k <= 32
+    largest alternatives; see fp4_logprobs in include/fp4.h."""
+    torch = _torch()
+    xs = _need_rows(x, "x", (torch.float32, torch.bfloat16), 2)
+    N, V = x.shape
+    dev = x.device
+    _need(tokens, "tokens", (torch.int32,), None, dev, ndim=2)
+    if tokens.shape[0] != N:
+        raise ValueError("tokens has %d rows, x %d" % (tokens.shape[0], N))
+    M = tokens.shape[1]
+    alloc = _Alloc(stream, dev)
+    logp = alloc(torch.empty, (N, M), dtype=torch.float32)
+    stats = alloc(torch.empty, (2, N), dtype=torch.float32)
+    top = alloc(torch.empty, (N, top_k), dtype=torch.float32) if top_k > 0 else None
+    index = alloc(torch.empty, (N, top_k), dtype=torch.int32) if top_k > 0 else None
+    if ws is None:
+        ws = alloc(logprobs_workspace, N, V, top_k)
+    else:
+        _need(ws, "ws", (torch.uint8,), None, dev)
+    entropy, lse = stats[0], stats[1]
+    rc = fp4_logprobs(_ptr(x), _dtype_code(x), xs, N, V, scale, _ptr(tokens), M, _ptr(logp), _ptr(entropy), _ptr(lse),
+                      top_k, _ptr(top), _ptr(index), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
+    _check(rc, "fp4_logprobs")
+    return LogProbs(logp, entropy, lse, top, index)
+
+
+def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scale=1.0, out=None, stream=None):
+    """Gradient of logprobs with respect to x from the gradients of logp
+    (N x M) and, if given, of the entropy (N; then entropy too); lse and
+    entropy as logprobs returned them; see fp4_logprobs_backward in
+    include/fp4.h.  Returns dx of x's dtype."""
+    torch = _torch()
+    xs = _need_rows(x, "x", (torch.float32, torch.bfloat16), 2)
+    N, V = x.shape
+    dev = x.device
+    _need(tokens, "tokens", (torch.int32,), None, dev, ndim=2)
+    if tokens.shape[0] != N:
+        raise ValueError("tokens has %d rows, x %d" % (tokens.shape[0], N))
+    M = tokens.shape[1]
+    _need_out(g_logp, "g_logp", (N, M), (torch.float32,), dev)
+    _need(lse, "lse", (torch.float32,), N, dev, ndim=1)
+    if g_entropy is not None:
+        if entropy is None:
+            raise ValueError("g_entropy needs entropy")
+        _need(g_entropy, "g_entropy", (torch.float32,), N, dev, ndim=1)
+        _need(entropy, "entropy", (torch.float32,), N, dev, ndim=1)
+    if out is None:
+        out = _Alloc(stream, dev)(torch.empty, (N, V), dtype=x.dtype)
+    os_ = _need_rows(out, "out", (x.dtype,), 2, dev, (N, V))
+    rc = fp4_logprobs_backward(_ptr(x), _dtype_code(x), xs, N, V, scale, _ptr(tokens), M, _ptr(lse), _ptr(entropy),
+                               _ptr(g_logp), _ptr(g_entropy), _ptr(out), os_, _stream(stream))
+    _check(rc, "fp4_logprobs_backward")
     return out

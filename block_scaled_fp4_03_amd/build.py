@@ -18,7 +18,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 ARCH = "gfx950"
 
 SOURCES = ["abi.cpp", "quantize.hip", "gemm.hip", "gemm_w4a8.hip", "gemv_nv.hip", "gemv_nv_blocksum.hip",
-           "gemv_nv_dot.hip"]
+           "gemv_nv_dot.hip", "kv_cache.hip", "attn_decode.hip", "logprobs.hip"]
 
 # -ffp-contract=off: no silent a*b+c fusion (the quantiser must round exactly
 # like the IEEE definition).  The packed-FP32 feature is switched off for the

@@ -7,6 +7,7 @@
 #include "fp4_launch.h"
 
 #include <atomic>
+#include <cfloat>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -166,6 +167,48 @@ uint64_t elem_bytes(int dt) { return dt == FP4_F32 ? 4u : 2u; }
 // Code bytes of a rows x K quantised matrix.
 uint64_t code_bytes(int fmt, int64_t rows, int64_t K) {
   return (uint64_t)rows * (uint64_t)K / (is_mx8(fmt) ? 1u : 2u);
+}
+
+// ---- the decode-step operators' arguments ----
+
+// Rows of a cache pool in bytes, and whether its scale bytes exist.
+bool kv_mx(int fmt) { return fmt != FP4_KV_BF16; }
+uint64_t kv_row_bytes(const fp4_kv_cache& c) {
+  const uint64_t d = (uint64_t)c.head_dim;
+  return c.fmt == FP4_KV_BF16 ? 2u * d : c.fmt == FP4_KV_MXFP8 ? d : d / 2u;
+}
+uint64_t kv_rows(const fp4_kv_cache& c) { return (uint64_t)c.pages * (uint64_t)c.kv_heads * (uint64_t)c.page_size; }
+
+// The parts of a cache that do not need its buffers: format and sizes.
+int kv_check_shape(const fp4_kv_cache* c) {
+  if (!c) return FP4_ERR_NULL;
+  if (c->fmt != FP4_KV_BF16 && c->fmt != FP4_KV_MXFP8 && c->fmt != FP4_KV_MXFP4) return FP4_ERR_FMT;
+  if (c->page_size < 16 || c->page_size > 4096 || (c->page_size & (c->page_size - 1)) != 0) return FP4_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 192 && c->head_dim != 256) return FP4_ERR_SHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 65535 || c->pages < 0 || c->pages > kMaxDim) return FP4_ERR_SHAPE;
+  return FP4_OK;
+}
+int kv_check_buffers(const fp4_kv_cache& c) {
+  if (c.pages == 0) return FP4_OK;
+  if (!c.k || !c.v || (kv_mx(c.fmt) && (!c.k_scales || !c.v_scales))) return FP4_ERR_NULL;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16)) return FP4_ERR_ALIGN;
+  if (kv_mx(c.fmt) && (!aligned(c.k_scales, 8) || !aligned(c.v_scales, 8))) return FP4_ERR_ALIGN;
+  return FP4_OK;
+}
+int kv_debug(const fp4_kv_cache& c) {
+  const uint64_t scales = kv_mx(c.fmt) ? kv_rows(c) * (uint64_t)(c.head_dim / 32) : 0u;
+  return debug_buffers({{c.k, kv_rows(c) * kv_row_bytes(c)},
+                        {c.v, kv_rows(c) * kv_row_bytes(c)},
+                        {scales ? c.k_scales : nullptr, scales},
+                        {scales ? c.v_scales : nullptr, scales}});
+}
+fp4::KvPool kv_pool(const fp4_kv_cache& c) {
+  return fp4::KvPool{c.k,       c.v, c.k_scales, c.v_scales, c.pages, c.page_size, c.kv_heads, c.head_dim,
+                     c.fmt};
+}
+// Elements of the last of `rows` rows `stride` apart, each `width` wide.
+uint64_t strided(int64_t rows, int64_t stride, int64_t width) {
+  return rows == 0 ? 0u : (uint64_t)(rows - 1) * (uint64_t)stride + (uint64_t)width;
 }
 
 }  // namespace
@@ -550,6 +593,229 @@ int fp4_gemm_w4a8(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const u
   }
   return finish(launched(fp4::launch_gemm_w4a8(A, sA, B, sB, bias, act, C, M, N, K, out_dtype, as_stream(stream))),
                 as_stream(stream));
+}
+
+int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, int in_dtype, int64_t k_stride,
+                  int64_t v_stride, const int32_t* page_table, int64_t table_width, int64_t seqs, const int32_t* seq,
+                  const int32_t* pos, int64_t rows, void* stream) {
+  int rc = kv_check_shape(cache);
+  if (rc != FP4_OK) return rc;
+  if (!dtype_ok(in_dtype)) return FP4_ERR_DTYPE;
+  const int64_t width = (int64_t)cache->kv_heads * cache->head_dim;
+  if (rows < 0 || rows > kMaxDim || seqs < 0 || seqs > kMaxDim || table_width < 0 || table_width > kMaxDim)
+    return FP4_ERR_SHAPE;
+  if (k_stride < width || v_stride < width || k_stride > kMaxDim || v_stride > kMaxDim) return FP4_ERR_SHAPE;
+  // One thread per 8 values of a row.
+  if (rows * (width / 8) + 255 > kMaxWorkItems) return FP4_ERR_SHAPE;
+  if (rows == 0 || seqs == 0 || table_width == 0 || cache->pages == 0) return FP4_OK;
+  if ((rc = kv_check_buffers(*cache)) != FP4_OK) return rc;
+  if (!k || !v || !page_table || !seq || !pos) return FP4_ERR_NULL;
+  const int64_t per16 = in_dtype == FP4_F32 ? 4 : 8;
+  if (!aligned(k, 16) || !aligned(v, 16) || k_stride % per16 != 0 || v_stride % per16 != 0) return FP4_ERR_ALIGN;
+  if (!aligned(page_table, 4) || !aligned(seq, 4) || !aligned(pos, 4)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    rc = kv_debug(*cache);
+    if (rc == FP4_OK)
+      rc = debug_buffers({{k, strided(rows, k_stride, width) * elem_bytes(in_dtype)},
+                          {v, strided(rows, v_stride, width) * elem_bytes(in_dtype)},
+                          {page_table, (uint64_t)seqs * (uint64_t)table_width * 4u},
+                          {seq, (uint64_t)rows * 4u},
+                          {pos, (uint64_t)rows * 4u}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_kv_append(kv_pool(*cache), k, v, in_dtype, k_stride, v_stride, page_table,
+                                               table_width, seqs, seq, pos, rows, s)),
+                s);
+}
+
+// Shapes of an attention call that the workspace's size and the call share.
+static int attn_check_shape(const fp4_kv_cache* cache, int64_t B, int64_t q_heads, int64_t max_len) {
+  const int rc = kv_check_shape(cache);
+  if (rc != FP4_OK) return rc;
+  // Grid: sequences in z, kv heads x tiles of 16 query heads in y.
+  if (B < 0 || B > 65535 || q_heads < 0 || q_heads % cache->kv_heads != 0 || q_heads > 65535) return FP4_ERR_SHAPE;
+  if (max_len < 0 || max_len > kMaxDim) return FP4_ERR_SHAPE;
+  return FP4_OK;
+}
+
+size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q_heads, int64_t max_len,
+                                 int weights) {
+  if (attn_check_shape(cache, B, q_heads, max_len) != FP4_OK) return 0;
+  return fp4::attn_decode_workspace(B, q_heads, cache->kv_heads, cache->head_dim, max_len, weights != 0);
+}
+
+int fp4_attn_decode(const fp4_kv_cache* cache, const void* q, int q_dtype, int64_t q_stride,
+                    const int32_t* page_table, int64_t table_width, const int32_t* lens, int64_t B, int64_t q_heads,
+                    int64_t max_len, int64_t window, float scale, void* out, int out_dtype, float* lse,
+                    const float* weights_in, float* weights_out, int64_t weights_stride, void* workspace,
+                    size_t workspace_bytes, void* stream) {
+  int rc = attn_check_shape(cache, B, q_heads, max_len);
+  if (rc != FP4_OK) return rc;
+  if (!dtype_ok(q_dtype) || !dtype_ok(out_dtype)) return FP4_ERR_DTYPE;
+  if (table_width < 0 || table_width > kMaxDim || max_len > table_width * cache->page_size) return FP4_ERR_SHAPE;
+  if (window < 0 || q_stride < q_heads * cache->head_dim || q_stride > kMaxDim) return FP4_ERR_SHAPE;
+  if (weights_out && (weights_stride < max_len || weights_stride > kMaxDim)) return FP4_ERR_SHAPE;
+  if (B == 0 || q_heads == 0) return FP4_OK;
+  if ((rc = kv_check_buffers(*cache)) != FP4_OK) return rc;
+  if (!q || !out || !lens || (max_len > 0 && !page_table)) return FP4_ERR_NULL;
+  if (weights_in && !weights_out) return FP4_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || q_stride % (q_dtype == FP4_F32 ? 4 : 8) != 0) return FP4_ERR_ALIGN;
+  if (!aligned(page_table, 4) || !aligned(lens, 4) || !aligned(lse, 4) || !aligned(weights_in, 4) ||
+      !aligned(weights_out, 4))
+    return FP4_ERR_ALIGN;
+  const size_t need = fp4::attn_decode_workspace(B, q_heads, cache->kv_heads, cache->head_dim, max_len,
+                                                 weights_out != nullptr);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t wbytes = (uint64_t)B * (uint64_t)cache->kv_heads * (uint64_t)weights_stride * 4u;
+    const uint64_t values = (uint64_t)B * (uint64_t)q_heads * (uint64_t)cache->head_dim;
+    rc = kv_debug(*cache);
+    if (rc == FP4_OK)
+      rc = debug_buffers({{q, strided(B, q_stride, q_heads * cache->head_dim) * elem_bytes(q_dtype)},
+                          {page_table, (uint64_t)B * (uint64_t)table_width * 4u},
+                          {lens, (uint64_t)B * 4u},
+                          {out, values * elem_bytes(out_dtype)},
+                          {lse, (uint64_t)B * (uint64_t)q_heads * 4u},
+                          {weights_in, wbytes},
+                          {weights_out, wbytes},
+                          {need ? workspace : nullptr, need}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_attn_decode(kv_pool(*cache), q, q_dtype, q_stride, page_table, table_width, lens,
+                                                 B, q_heads, max_len, window, scale, out, out_dtype, lse, weights_in,
+                                                 weights_out, weights_stride, workspace, s)),
+                s);
+}
+
+size_t fp4_kv_evict_workspace(const fp4_kv_cache* cache, int64_t B, int64_t max_len, int64_t budget) {
+  if (kv_check_shape(cache) != FP4_OK || B < 0 || B > 65535 || max_len < 0 || max_len > kMaxDim || budget < 0 ||
+      budget > kMaxDim)
+    return 0;
+  return fp4::kv_evict_workspace(B, cache->kv_heads, max_len, budget);
+}
+
+int fp4_kv_evict(const fp4_kv_cache* src, const int32_t* src_table, int64_t src_width, const int32_t* lens,
+                 const float* weights, int64_t weights_stride, const fp4_kv_cache* dst, const int32_t* dst_table,
+                 int64_t dst_width, int32_t* out_lens, float* out_weights, int64_t out_stride, int32_t* kept,
+                 int64_t B, int64_t max_len, int64_t budget, int64_t recent, void* workspace,
+                 size_t workspace_bytes, void* stream) {
+  int rc = kv_check_shape(src);
+  if (rc == FP4_OK) rc = kv_check_shape(dst);
+  if (rc != FP4_OK) return rc;
+  if (src->fmt != dst->fmt) return FP4_ERR_FMT;
+  if (src->kv_heads != dst->kv_heads || src->head_dim != dst->head_dim || src->page_size != dst->page_size)
+    return FP4_ERR_SHAPE;
+  if (B < 0 || B > 65535 || max_len < 0 || max_len > kMaxDim || budget < 0 || budget > kMaxDim || recent < 0)
+    return FP4_ERR_SHAPE;
+  if (src_width < 0 || src_width > kMaxDim || dst_width < 0 || dst_width > kMaxDim) return FP4_ERR_SHAPE;
+  const int64_t most = budget < max_len ? budget : max_len;
+  if (max_len > src_width * src->page_size || most > dst_width * dst->page_size) return FP4_ERR_SHAPE;
+  if (weights_stride < max_len || out_stride < budget || weights_stride > kMaxDim || out_stride > kMaxDim)
+    return FP4_ERR_SHAPE;
+  if (B == 0) return FP4_OK;
+  if ((rc = kv_check_buffers(*src)) != FP4_OK || (rc = kv_check_buffers(*dst)) != FP4_OK) return rc;
+  if (!lens || !out_lens || (max_len > 0 && (!src_table || !weights))) return FP4_ERR_NULL;
+  if ((most > 0 && !dst_table) || (out_stride > 0 && !out_weights) || (budget > 0 && !kept)) return FP4_ERR_NULL;
+  if (!aligned(src_table, 4) || !aligned(dst_table, 4) || !aligned(lens, 4) || !aligned(weights, 4) ||
+      !aligned(out_lens, 4) || !aligned(out_weights, 4) || !aligned(kept, 4))
+    return FP4_ERR_ALIGN;
+  const size_t need = fp4::kv_evict_workspace(B, src->kv_heads, max_len, budget);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t heads = (uint64_t)B * (uint64_t)src->kv_heads;
+    rc = kv_debug(*src);
+    if (rc == FP4_OK) rc = kv_debug(*dst);
+    if (rc == FP4_OK)
+      rc = debug_buffers({{src_table, (uint64_t)B * (uint64_t)src_width * 4u},
+                          {lens, (uint64_t)B * 4u},
+                          {weights, heads * (uint64_t)weights_stride * 4u},
+                          {dst_table, (uint64_t)B * (uint64_t)dst_width * 4u},
+                          {out_lens, (uint64_t)B * 4u},
+                          {out_weights, heads * (uint64_t)out_stride * 4u},
+                          {kept, heads * (uint64_t)budget * 4u},
+                          {need ? workspace : nullptr, need}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_kv_evict(kv_pool(*src), src_table, src_width, lens, weights, weights_stride,
+                                              kv_pool(*dst), dst_table, dst_width, out_lens, out_weights, out_stride,
+                                              kept, B, max_len, budget, recent, workspace, s)),
+                s);
+}
+
+// Sizes that fp4_logprobs, its workspace and its gradient share.
+static bool logprobs_shape_ok(int64_t N, int64_t V) {
+  return N >= 0 && N <= kMaxDim && V >= 1 && V <= kMaxDim;
+}
+constexpr int32_t kMaxTopK = 32, kMaxTokens = 1024;
+
+size_t fp4_logprobs_workspace(int64_t N, int64_t V, int32_t top_k) {
+  if (!logprobs_shape_ok(N, V) || top_k < 0 || top_k > kMaxTopK) return 0;
+  return fp4::logprobs_workspace(N, V, top_k);
+}
+
+int fp4_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale, const int32_t* tokens,
+                 int32_t M, float* logp, float* entropy, float* lse, int32_t top_k, float* top_logp,
+                 int32_t* top_index, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!logprobs_shape_ok(N, V) || stride < V || stride > kMaxDim || M < 0 || M > kMaxTokens || top_k < 0 ||
+      top_k > kMaxTopK || !(scale > 0.0f) || scale > FLT_MAX)
+    return FP4_ERR_SHAPE;
+  if (N == 0) return FP4_OK;
+  if (!x || (M > 0 && (!tokens || !logp)) || (top_k > 0 && (!top_logp || !top_index))) return FP4_ERR_NULL;
+  if (!aligned(x, elem_bytes(dtype)) || !aligned(tokens, 4) || !aligned(logp, 4) || !aligned(entropy, 4) ||
+      !aligned(lse, 4) || !aligned(top_logp, 4) || !aligned(top_index, 4))
+    return FP4_ERR_ALIGN;
+  const size_t need = fp4::logprobs_workspace(N, V, top_k);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const int rc = debug_buffers({{x, strided(N, stride, V) * elem_bytes(dtype)},
+                                  {tokens, (uint64_t)N * (uint64_t)M * 4u},
+                                  {logp, (uint64_t)N * (uint64_t)M * 4u},
+                                  {entropy, (uint64_t)N * 4u},
+                                  {lse, (uint64_t)N * 4u},
+                                  {top_logp, (uint64_t)N * (uint64_t)top_k * 4u},
+                                  {top_index, (uint64_t)N * (uint64_t)top_k * 4u},
+                                  {need ? workspace : nullptr, need}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_logprobs(x, dtype, stride, N, V, scale, tokens, M, logp, entropy, lse, top_k,
+                                              top_logp, top_index, workspace, s)),
+                s);
+}
+
+int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
+                          const int32_t* tokens, int32_t M, const float* lse, const float* entropy,
+                          const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!logprobs_shape_ok(N, V) || stride < V || stride > kMaxDim || dx_stride < V || dx_stride > kMaxDim || M < 0 ||
+      M > kMaxTokens || !(scale > 0.0f) || scale > FLT_MAX)
+    return FP4_ERR_SHAPE;
+  if (N == 0) return FP4_OK;
+  if (!x || !dx || !lse || (M > 0 && (!tokens || !g_logp)) || (g_entropy && !entropy)) return FP4_ERR_NULL;
+  if (!aligned(x, elem_bytes(dtype)) || !aligned(dx, elem_bytes(dtype)) || !aligned(tokens, 4) || !aligned(lse, 4) ||
+      !aligned(entropy, 4) || !aligned(g_logp, 4) || !aligned(g_entropy, 4))
+    return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const int rc = debug_buffers({{x, strided(N, stride, V) * elem_bytes(dtype)},
+                                  {tokens, (uint64_t)N * (uint64_t)M * 4u},
+                                  {lse, (uint64_t)N * 4u},
+                                  {g_entropy ? entropy : nullptr, (uint64_t)N * 4u},
+                                  {g_logp, (uint64_t)N * (uint64_t)M * 4u},
+                                  {g_entropy, (uint64_t)N * 4u},
+                                  {dx, strided(N, dx_stride, V) * elem_bytes(dtype)}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_logprobs_backward(x, dtype, stride, N, V, scale, tokens, M, lse, entropy, g_logp,
+                                                       g_entropy, dx, dx_stride, s)),
+                s);
 }
 
 const char* fp4_status_string(int status) {

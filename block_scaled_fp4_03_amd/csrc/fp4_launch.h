@@ -111,4 +111,49 @@ hipError_t launch_gemv_nv_fused(const void* X, int x_dtype, float* x_tensor_scal
                                 const uint8_t* B, const uint8_t* sB, const float* tsB, void* C, int64_t M,
                                 int64_t N, int64_t K, int out_dtype, hipStream_t stream);
 
+// ---- decode-step operators ----
+
+// A cache pool as the kernels take it (fp4_kv_cache of the C ABI).
+struct KvPool {
+  void* k;
+  void* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  int64_t pages;
+  int32_t page_size;  // a power of two
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t fmt;
+};
+
+// Cache append and eviction (kv_cache.hip).
+hipError_t launch_kv_append(const KvPool& c, const void* k, const void* v, int in_dtype, int64_t k_stride,
+                            int64_t v_stride, const int32_t* table, int64_t width, int64_t seqs, const int32_t* seq,
+                            const int32_t* pos, int64_t rows, hipStream_t stream);
+size_t kv_evict_workspace(int64_t B, int64_t kv_heads, int64_t max_len, int64_t budget);
+hipError_t launch_kv_evict(const KvPool& src, const int32_t* src_table, int64_t src_width, const int32_t* lens,
+                           const float* weights, int64_t weights_stride, const KvPool& dst, const int32_t* dst_table,
+                           int64_t dst_width, int32_t* out_lens, float* out_weights, int64_t out_stride,
+                           int32_t* kept, int64_t B, int64_t max_len, int64_t budget, int64_t recent,
+                           void* workspace, hipStream_t stream);
+
+// Single-token attention over the cache (attn_decode.hip).
+size_t attn_decode_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_len,
+                             bool weights);
+hipError_t launch_attn_decode(const KvPool& c, const void* q, int q_dtype, int64_t q_stride, const int32_t* table,
+                              int64_t width, const int32_t* lens, int64_t B, int64_t q_heads, int64_t max_len,
+                              int64_t window, float scale, void* out, int out_dtype, float* lse,
+                              const float* weights_in, float* weights_out, int64_t weights_stride, void* workspace,
+                              hipStream_t stream);
+
+// Log probabilities and their gradient (logprobs.hip).
+size_t logprobs_workspace(int64_t N, int64_t V, int32_t top_k);
+hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
+                           const int32_t* tokens, int32_t M, float* logp, float* entropy, float* lse, int32_t top_k,
+                           float* top_logp, int32_t* top_index, void* workspace, hipStream_t stream);
+hipError_t launch_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
+                                    const int32_t* tokens, int32_t M, const float* lse, const float* entropy,
+                                    const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride,
+                                    hipStream_t stream);
+
 }  // namespace fp4

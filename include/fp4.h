@@ -419,6 +419,149 @@ int fp4_gemm_ex(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uin
 int fp4_gemm_w4a8(const uint8_t* A, const uint8_t* sA, const uint8_t* B, const uint8_t* sB, const float* bias,
                   int act, void* C, int64_t M, int64_t N, int64_t K, int out_dtype, void* stream);
 
+/* ---- decode-step operators: paged key-value cache, attention, eviction, log
+ * probabilities (the rest of a decode step beside the linear layers above;
+ * "Rubin FP4 GEMM deep dive" §1.2, §6.2: decoding is bound by the bytes it
+ * streams, so the cache takes the block-scaled formats too). ---- */
+
+/* Row formats of a cache.  A row is one token's D key (or value) values of one
+ * head: FP4_KV_BF16 2*D bytes; FP4_KV_MXFP8 D E4M3 bytes and FP4_KV_MXFP4 D/2
+ * bytes of E2M1 codes (element order as above), each with D/32 E8M0 scale
+ * bytes, the scale of every 32 values as fp4_quantize chooses it for FP4_MXFP8
+ * / FP4_MXFP4. */
+enum fp4_kv_fmt { FP4_KV_BF16 = 0, FP4_KV_MXFP8 = 1, FP4_KV_MXFP4 = 2 };
+
+/* A pool of cache pages (a host struct; the pointers are device pointers the
+ * caller owns).  Row of page p, head h, slot s: row number
+ * (p * kv_heads + h) * page_size + s, rows dense in that order in k and v, and
+ * likewise the D/32 scale bytes of each row in k_scales and v_scales (MX
+ * formats; else ignored).  page_size: a power of two from 16 to 4096.
+ * head_dim: 64, 128, 192 or 256.  k, v 16-byte, scales 8-byte aligned.
+ *   A page table (device int32, sequences x table_width, dense) maps token t
+ * of sequence b to slot t % page_size of page table[b][t / page_size].
+ * Sequences may share pages.  The calls below check every entry they use: a
+ * page outside [0, pages) is never touched (its tokens count as masked). */
+typedef struct fp4_kv_cache {
+    void* k;
+    void* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    int64_t pages;
+    int32_t page_size;
+    int32_t kv_heads;
+    int32_t head_dim;
+    int32_t fmt; /* enum fp4_kv_fmt */
+} fp4_kv_cache;
+
+/* Write new keys and values into the cache, converted to its format (BF16:
+ * round to nearest even; MX formats: bit for bit what fp4_quantize gives).
+ *   k, v: `rows` rows of kv_heads x head_dim values of in_dtype, row i at
+ *   element i * k_stride (v_stride), the heads dense within a row; 16-byte
+ *   aligned, strides a multiple of 16 bytes and >= kv_heads * head_dim.
+ *   Row i becomes token pos[i] of sequence seq[i] (device int32).  A row with
+ *   seq outside [0, seqs), pos outside the table or a page outside the pool is
+ *   skipped (seq = -1 pads a batch).  Two rows for one token race.
+ * rows == 0 is a no-op. */
+int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, int in_dtype, int64_t k_stride,
+                  int64_t v_stride, const int32_t* page_table, int64_t table_width, int64_t seqs,
+                  const int32_t* seq, const int32_t* pos, int64_t rows, void* stream);
+
+/* Workspace bytes of fp4_attn_decode (0: none needed).  As for the operations
+ * above it must be zero-filled once; calls leave its control words zero.
+ * weights: whether weights_out will be given.  0 for invalid arguments. */
+size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q_heads, int64_t max_len, int weights);
+
+/* Attention of one new token per sequence over the paged cache.  For query
+ * head h of sequence b (reading kv head h / (q_heads / kv_heads)) over the
+ * tokens t of [max(0, len - window), len), len = min(lens[b], max_len):
+ *   s_t = scale * sum_d q[b,h,d] K[t,d];  p = softmax(s);
+ *   out[b,h,:] = sum_t p_t V[t,:];  lse[b,h] = log sum_t exp s_t.
+ *   A row with no tokens (length 0, or all pages masked) gives out = 0 and
+ *   lse = -inf.  Slots outside the range never influence the result, whatever
+ *   bits they hold.
+ *   q: B x q_heads x head_dim of q_dtype, sequence b at element b * q_stride
+ *   (heads dense; 16-byte aligned, stride a multiple of 16 bytes).  out: B x
+ *   q_heads x head_dim of out_dtype, dense, 16-byte aligned.  lse: B x q_heads
+ *   FP32 or NULL.  q_heads a multiple of kv_heads.
+ *   lens: B device int32 (negative reads as 0).  max_len <= table_width *
+ *   page_size bounds the lengths (and sizes the workspace).  window: 0 for
+ *   none.
+ *   weights_out (optional): FP32 B x kv_heads x weights_stride, receives for
+ *   every t < len  weights_in[b,kv,t] + sum over the kv head's query heads of
+ *   p_t  (weights_in NULL: 0; it may equal weights_out); entries t >= len are
+ *   left alone.  weights_stride >= max_len.
+ *   Scores, softmax and sums in FP32.  With BF16 q and out the probabilities
+ *   enter the product with V as two BF16 terms (relative error 2^-17); with
+ *   either in FP32, q and the probabilities enter as three (FP32's 24 bits).
+ *   Sums are in a fixed order: results do not depend on timing.
+ * B == 0 or q_heads == 0 is a no-op; max_len == 0 writes the empty result. */
+int fp4_attn_decode(const fp4_kv_cache* cache, const void* q, int q_dtype, int64_t q_stride,
+                    const int32_t* page_table, int64_t table_width, const int32_t* lens, int64_t B, int64_t q_heads,
+                    int64_t max_len, int64_t window, float scale, void* out, int out_dtype, float* lse,
+                    const float* weights_in, float* weights_out, int64_t weights_stride, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fp4_kv_evict (zero-filled once; 0: none needed, also
+ * for invalid arguments).  max_len: the longest sequence's length. */
+size_t fp4_kv_evict_workspace(const fp4_kv_cache* cache, int64_t B, int64_t max_len, int64_t budget);
+
+/* Evict by accumulated attention weight: every (sequence, kv head) with more
+ * than `budget` tokens keeps budget of them -- the last min(recent, budget),
+ * and of the others those with the largest weights[b,kv,t] (ties to the lowest
+ * token; +0 equals -0; a NaN counts as largest) -- and one with at most budget
+ * keeps all.  The kept tokens, in their order, become tokens 0, 1, ... of
+ * dst_table's pages in dst (which may be the same pool; the destination pages
+ * must not be pages the call reads, so pages shared with other sequences stay
+ * whole and the old ones can be freed afterwards).
+ *   weights: FP32 B x kv_heads x weights_stride; weights_stride >= max_len,
+ *   the bound of lens (longer ones read as max_len).
+ *   out_lens[b] = min(lens[b], budget).  out_weights: FP32 B x kv_heads x
+ *   out_stride, the kept tokens' weights, then zeros; out_stride >= budget.
+ *   kept: int32 B x kv_heads x budget, the kept tokens' old numbers, then -1.
+ *   dst has src's fmt, heads, head_dim and page_size; dst_width * page_size >=
+ *   min(budget, max_len).  A kept token whose page (old or new) is outside the
+ *   pool is not copied.
+ * B == 0 is a no-op. */
+int fp4_kv_evict(const fp4_kv_cache* src, const int32_t* src_table, int64_t src_width, const int32_t* lens,
+                 const float* weights, int64_t weights_stride, const fp4_kv_cache* dst, const int32_t* dst_table,
+                 int64_t dst_width, int32_t* out_lens, float* out_weights, int64_t out_stride, int32_t* kept,
+                 int64_t B, int64_t max_len, int64_t budget, int64_t recent, void* workspace,
+                 size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of fp4_logprobs (zero-filled once; 0: none needed, also for
+ * invalid arguments). */
+size_t fp4_logprobs_workspace(int64_t N, int64_t V, int32_t top_k);
+
+/* Log probabilities of given tokens under softmax(y), y = scale * x, with the
+ * entropy and the largest alternatives, in one pass over the logits:
+ *   lse[n] = log sum_i exp y[n,i];  logp[n,j] = y[n, tokens[n,j]] - lse[n];
+ *   entropy[n] = lse[n] - sum_i p_i y_i  (p_i = 0 contributes 0);
+ *   top_index[n,:] / top_logp[n,:]: the top_k largest x (ties to the lowest
+ *   index, NaN above all, +0 equal to -0) and their log probabilities, in
+ *   that order; past V entries: index -1, log probability -inf.
+ *   A token outside [0, V) is padding: its logp is 0.  A row whose logits are
+ *   all -inf has lse -inf, log probabilities -inf and entropy 0; a NaN or
+ *   +inf logit gives NaN.
+ *   x: N rows of V values of dtype, row n at element n * stride (stride >= V),
+ *   aligned to its element size only.  tokens: int32 N x M, dense (M <= 1024).  entropy
+ *   and lse may be NULL; top_k 0..32; scale finite, > 0.  All sums in FP32.
+ * N == 0 is a no-op; V >= 1. */
+int fp4_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale, const int32_t* tokens,
+                 int32_t M, float* logp, float* entropy, float* lse, int32_t top_k, float* top_logp,
+                 int32_t* top_index, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of fp4_logprobs with respect to x, given lse (and entropy) as it
+ * returned them, the gradients g_logp (N x M FP32) and g_entropy (N FP32, or
+ * NULL for none; then entropy is not read):
+ *   dx_i = scale * (sum_{j: tokens_j = i} g_j
+ *                   - p_i * (sum_j g_j + g_entropy * (log p_i + entropy))),
+ *   padding tokens' g_j left out, p_i = 0 giving 0 for the second term (so a
+ *   row of -inf logits gives 0 there).  dx: N rows of V values of dtype, row
+ *   n at element n * dx_stride; rounded once.  dx must not overlap x. */
+int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
+                          const int32_t* tokens, int32_t M, const float* lse, const float* entropy,
+                          const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride, void* stream);
+
 /* Static string naming a status code. */
 const char* fp4_status_string(int status);
 

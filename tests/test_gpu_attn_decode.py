@@ -1,0 +1,295 @@
+"""fp4_attn_decode on the GPU against attention in FP64.
+
+Tolerance, per output element (u = 2^-24).  A score is a sum of D exact
+products in FP32: |ds| <= (D + 4) 2u scale sum_d |q_d K_td| (each addition
+rounds or truncates: 2u), plus 4u |s| for the scaling and the subtraction of
+the maximum.  exp2 is good to 4u, so a probability's relative error is at
+most r = 2 max|ds| + (T + 16) 2u, where T 2u bounds the sums over T tokens of
+numerator and denominator.  With BF16 in and out the probabilities enter the
+product as two BF16 terms (2^-17 more) and the result is rounded to BF16
+(2^-8 |out|, one unit).  So |d out| <= sum_t p_t |V_td| (r + 2^-17) + 2^-8
+|out|; in FP32 the 2^-17 is 2^-23 and the last term 2u |out|."""
+import numpy as np
+import pytest
+
+import decode_reference as ref
+import synth
+from gpu_helpers import say, to_dev, to_host
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+def _bf16(x):
+    return (synth.to_bf16_bits(np.asarray(x, np.float32)).astype(np.uint32) << 16).view(np.float32)
+
+
+def make(seed, fmt, pages, heads, page, dim):
+    """A pool's host arrays: k, v codes (uint16 bits for BF16) and scales."""
+    rng = np.random.default_rng(seed)
+    out = []
+    for _ in range(2):
+        if fmt == "bf16":
+            out.append((synth.to_bf16_bits(rng.standard_normal((pages, heads, page, dim)).astype(np.float32)), None))
+        else:
+            row = dim if fmt == "mxfp8" else dim // 2
+            codes = rng.integers(0, 256, (pages, heads, page, row)).astype(np.uint8)
+            if fmt == "mxfp8":
+                codes = np.where((codes & 0x78) == 0x78, codes & 0x87, codes).astype(np.uint8)   # to 240, no NaN
+            low = 119 if fmt == "mxfp8" else 124
+            out.append((codes, rng.integers(low, low + 4, (pages, heads, page, dim // 32)).astype(np.uint8)))
+    return out
+
+
+def cache_of(pools):
+    import block_scaled_fp4_03_amd as fp4
+    (k, ks), (v, vs) = pools
+    return fp4.KVCache(to_dev(k), to_dev(v), None if ks is None else to_dev(ks), None if vs is None else to_dev(vs))
+
+
+def check(pools, fmt, table, lens, q, out, page, scale, window=0, f32=False, lse=None, w_in=None, w_out=None,
+          what=""):
+    """out, lse, w_out (host arrays) against FP64."""
+    (k, ks), (v, vs) = pools
+    B, Hq, D = q.shape
+    Hkv = k.shape[1]
+    G = Hq // Hkv
+    for b in range(B):
+        n = min(max(int(lens[b]), 0), table.shape[1] * page)
+        first = max(0, n - window) if window else 0
+        toks = [t for t in range(first, n) if 0 <= table[b, t // page] < k.shape[0]]
+        pg, sl = table[b, np.array(toks, int) // page], np.array(toks, int) % page
+        for h in range(Hkv):
+            K = ref.row_values(k[pg, h, sl], None if ks is None else ks[pg, h, sl], fmt)
+            V = ref.row_values(v[pg, h, sl], None if vs is None else vs[pg, h, sl], fmt)
+            qs = q[b, h * G:(h + 1) * G].astype(np.float64)
+            o, l, p, s = ref.attend(qs, K, V, scale)
+            got = out[b, h * G:(h + 1) * G].astype(np.float64)
+            if not toks:
+                assert not got.any(), "%s: b %d h %d empty row not zero" % (what, b, h)
+                if lse is not None:
+                    assert np.all(lse[b, h * G:(h + 1) * G] == -np.inf)
+                if w_out is not None and n:
+                    np.testing.assert_array_equal(w_out[b, h, :n], w_in[b, h, :n] if w_in is not None else 0)
+                continue
+            ds = (D + 4) * 2 * U * scale * (np.abs(qs) @ np.abs(K).T) + 4 * U * np.abs(s)
+            r = 2 * ds.max(axis=1, keepdims=True) + (len(toks) + 16) * 2 * U
+            tol = (p @ np.abs(V)) * (r + (2.0 ** -23 if f32 else 2.0 ** -17)) + (2 * U if f32 else 2.0 ** -8) * np.abs(o)
+            bad = ~(np.abs(got - o) <= tol + 1e-37)
+            assert not bad.any(), "%s: b %d h %d: %d wrong, worst %g over %g" % (
+                what, b, h, bad.sum(), np.abs(got - o).max(), tol.max())
+            if lse is not None:
+                lt = ds.max(axis=1) + (len(toks) + 16) * 2 * U + 4 * U * np.abs(l)
+                assert np.all(np.abs(lse[b, h * G:(h + 1) * G] - l) <= lt), what + " lse"
+            if w_out is not None:
+                want = np.zeros(n) if w_in is None else w_in[b, h, :n].astype(np.float64)
+                wt = (G + 4) * 2 * U * np.abs(want)
+                want[toks] += p.sum(axis=0)
+                wt[toks] += (p * r).sum(axis=0) + (G + 4) * 2 * U * p.sum(axis=0)
+                assert np.all(np.abs(w_out[b, h, :n] - want) <= wt + 1e-37), what + " weights"
+
+
+def run_case(seed, fmt, lens, Hkv, G, D, page, f32=False, out_f32=None, window=0, weights=False, scale=None,
+             spread=1.0, hide=()):
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    out_f32 = f32 if out_f32 is None else out_f32
+    B = len(lens)
+    width = max(1, -(-max(max(lens), 1) // page))
+    rng = np.random.default_rng(seed)
+    pages = B * width + 2
+    pools = make(seed, fmt, pages, Hkv, page, D)
+    table = rng.permutation(pages)[:B * width].reshape(B, width).astype(np.int32)
+    for b, w, p in hide:
+        table[b, w] = p
+    q = (rng.standard_normal((B, Hkv * G, D)) * spread).astype(np.float32)
+    if not f32:
+        q = _bf16(q)
+    scale = D ** -0.5 if scale is None else scale
+    what = "attn %s lens %s Hkv %d G %d D %d page %d f32 %d window %d" % (fmt, lens[:6], Hkv, G, D, page, f32, window)
+    say(what)
+    cache = cache_of(pools)
+    dt = torch.float32 if f32 else torch.bfloat16
+    qd = torch.from_numpy(q).cuda().to(dt)
+    w_in = w_out = None
+    if weights:
+        w_in = rng.random((B, Hkv, width * page)).astype(np.float32)
+        w_out = torch.full((B, Hkv, width * page), -7.0, device="cuda")
+    lse = torch.empty((B, Hkv * G), device="cuda")
+    out = fp4.decode_attention(qd, cache, to_dev(table), to_dev(np.array(lens, np.int32)), window=window, scale=scale,
+                               out_dtype=torch.float32 if out_f32 else torch.bfloat16, lse=lse,
+                               weights=to_dev(w_in) if weights else None, weights_out=w_out)
+    torch.cuda.synchronize()
+    w_host = to_host(w_out) if weights else None
+    if weights:
+        for b, n in enumerate(lens):
+            assert np.all(w_host[b, :, max(0, n):] == -7.0), "weights past the length written"
+    check(pools, fmt, table, lens, q, out.float().cpu().numpy(), page, np.float64(np.float32(scale)), window,
+          out_f32, to_host(lse), w_in, w_host, what)
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "mxfp8", "mxfp4"))
+@pytest.mark.parametrize("lens,Hkv,G,D,page", [
+    ([1], 1, 1, 64, 16), ([0], 2, 2, 64, 16), ([2, 0, 31, 32, 33], 2, 4, 128, 16), ([100, 7], 8, 4, 128, 64),
+    ([129], 8, 8, 64, 32), ([300, 1, 513], 1, 16, 128, 64), ([257], 2, 5, 192, 32), ([65, 200], 1, 3, 256, 128),
+    ([40], 1, 17, 64, 16), ([77, 130], 2, 40, 128, 16), ([4099], 2, 7, 128, 64), ([2500, 17, 0, 1025], 1, 8, 64, 32),
+    ([20000], 1, 4, 64, 256),
+])
+def test_attention_bf16(fmt, lens, Hkv, G, D, page):
+    run_case(sum(lens) + G, fmt, lens, Hkv, G, D, page)
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "mxfp8", "mxfp4"))
+@pytest.mark.parametrize("lens,Hkv,G,D,page", [([1, 0, 50], 2, 3, 64, 16), ([700, 90], 1, 8, 128, 32),
+                                               ([333], 2, 18, 192, 16), ([1200], 1, 2, 256, 64)])
+def test_attention_f32(fmt, lens, Hkv, G, D, page):
+    run_case(sum(lens) + 31 * G, fmt, lens, Hkv, G, D, page, f32=True)
+
+
+def test_attention_mixed_dtypes():
+    run_case(51, "bf16", [200, 33], 2, 4, 128, 16, f32=False, out_f32=True)
+    run_case(52, "mxfp8", [200, 33], 2, 4, 128, 16, f32=True, out_f32=False)
+
+
+@pytest.mark.parametrize("window", [1, 15, 32, 100, 2000, 10 ** 6])
+def test_attention_window(window):
+    run_case(60 + window, "bf16", [0, 1, 99, 1500, 2100], 2, 4, 64, 32, window=window, weights=True)
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "mxfp8", "mxfp4"))
+@pytest.mark.parametrize("lens,Hkv,G,D,page", [([1], 1, 1, 64, 16), ([0, 5, 64, 1300], 2, 4, 128, 16),
+                                               ([3000, 20], 1, 20, 64, 64), ([5000], 2, 2, 256, 128)])
+def test_attention_weights(fmt, lens, Hkv, G, D, page):
+    run_case(sum(lens) + 7 * G, fmt, lens, Hkv, G, D, page, weights=True)
+
+
+def test_attention_large_scores():
+    """Scores of hundreds: the maximum moves, sums rescale, nothing overflows."""
+    run_case(71, "bf16", [900, 40], 2, 4, 128, 16, spread=60.0, weights=True)
+    run_case(72, "mxfp4", [900, 40], 1, 8, 64, 16, spread=200.0)
+    run_case(73, "bf16", [700], 1, 4, 64, 16, scale=0.0)
+
+
+def test_attention_hidden_pages():
+    """Pages outside the pool are masked; a row of nothing else is empty."""
+    run_case(81, "bf16", [100, 40], 2, 4, 64, 16, hide=[(0, 0, -1), (0, 3, 10 ** 6), (1, 0, -5), (1, 1, -1),
+                                                       (1, 2, 2 ** 31 - 1)], weights=True)
+
+
+@pytest.mark.parametrize("fmt", ("bf16", "mxfp8", "mxfp4"))
+def test_attention_ignores_what_lies_past_the_length(fmt):
+    """Slots past the length hold NaN and infinity (MX: every code and scale
+    bit set); the result has the same bits as with zeros there."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    lens, Hkv, G, D, page = [37, 1, 0, 64, 95], 2, 4, 128, 32
+    width = 3
+    pools = make(90, fmt, len(lens) * width, Hkv, page, D)
+    table = np.arange(len(lens) * width, dtype=np.int32).reshape(len(lens), width)
+    outs = []
+    for fill in (0, 1):
+        ps = [(c.copy(), None if s is None else s.copy()) for c, s in pools]
+        for b, n in enumerate(lens):
+            for t in range(n, width * page):
+                for i, (c, s) in enumerate(ps):
+                    c[table[b, t // page], :, t % page] = 0 if fill == 0 else (0x7FC0, 0x7F80)[i] if fmt == "bf16" \
+                        else 0xFF
+                    if s is not None:
+                        s[table[b, t // page], :, t % page] = 0 if fill == 0 else 0xFF
+        q = torch.from_numpy(_bf16(np.random.default_rng(1).standard_normal((len(lens), Hkv * G, D)))).cuda()
+        say("attention with filler %d, %s" % (fill, fmt))
+        w = torch.zeros((len(lens), Hkv, width * page), device="cuda")
+        out = fp4.decode_attention(q.to(torch.bfloat16), cache_of(ps), to_dev(table),
+                                   to_dev(np.array(lens, np.int32)), weights_out=w)
+        outs.append((out.float().cpu().numpy(), to_host(w)))
+    np.testing.assert_array_equal(outs[0][0], outs[1][0])
+    np.testing.assert_array_equal(outs[0][1], outs[1][1])
+    assert np.isfinite(outs[1][0]).all()
+
+
+def test_attention_nan_in_a_valid_key_shows():
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    pools = make(91, "bf16", 2, 1, 16, 64)
+    pools[0][0][0, 0, 3, 5] = 0x7FC0
+    q = torch.ones((1, 2, 64), dtype=torch.bfloat16, device="cuda")
+    say("attention with a NaN key")
+    out = fp4.decode_attention(q, cache_of(pools), to_dev(np.array([[0, 1]], np.int32)),
+                               to_dev(np.array([20], np.int32)))
+    assert torch.isnan(out).all()
+
+
+def test_attention_strides_and_max_len():
+    """q as columns of a wider matrix; lens beyond max_len read as max_len; negative ones as 0."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    pools = make(92, "bf16", 12, 2, 16, 64)
+    cache, table = cache_of(pools), to_dev(np.arange(12, dtype=np.int32).reshape(2, 6))
+    wide = torch.randn((2, 3, 8, 64), device="cuda").to(torch.bfloat16)
+    lens = to_dev(np.array([90, -3], np.int32))
+    say("attention on strided q")
+    out = fp4.decode_attention(wide[:, 1], cache, table, lens, max_len=50)
+    same = fp4.decode_attention(wide[:, 1].contiguous(), cache, table, to_dev(np.array([50, 0], np.int32)))
+    assert torch.equal(out, same) and not out[1].any()
+
+
+def test_attention_repeats_bit_for_bit_and_reuses_its_workspace():
+    """One workspace over calls of other shapes, many splits: the same bits each time."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    pools = make(93, "mxfp8", 700, 1, 16, 128)
+    cache = cache_of(pools)
+    rng = np.random.default_rng(2)
+    t1 = to_dev(rng.permutation(600)[:600].reshape(1, 600).astype(np.int32))
+    t2 = to_dev(rng.permutation(700)[:40].reshape(4, 10).astype(np.int32))
+    q1 = torch.randn((1, 8, 128), device="cuda").to(torch.bfloat16)
+    q2 = torch.randn((4, 8, 128), device="cuda").to(torch.bfloat16)
+    l1, l2 = to_dev(np.array([9500], np.int32)), to_dev(np.array([160, 3, 0, 80], np.int32))
+    sizes = [fp4.attention_workspace(cache, 1, 8, 9600), fp4.attention_workspace(cache, 4, 8, 160)]
+    ws = max((s for s in sizes if s is not None), key=lambda s: s.numel(), default=None)
+    say("attention, one workspace over several calls")
+    first = (fp4.decode_attention(q1, cache, t1, l1, ws=ws), fp4.decode_attention(q2, cache, t2, l2, ws=ws))
+    for _ in range(20):
+        assert torch.equal(first[0], fp4.decode_attention(q1, cache, t1, l1, ws=ws))
+        assert torch.equal(first[1], fp4.decode_attention(q2, cache, t2, l2, ws=ws))
+
+
+def test_attention_on_another_stream():
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    pools = make(94, "bf16", 40, 2, 16, 64)
+    cache, table = cache_of(pools), to_dev(np.arange(40, dtype=np.int32).reshape(1, 40))
+    q, lens = torch.randn((1, 8, 64), device="cuda").to(torch.bfloat16), to_dev(np.array([600], np.int32))
+    want = fp4.decode_attention(q, cache, table, lens)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    say("attention on a side stream")
+    got = [fp4.decode_attention(q, cache, table, lens, stream=s) for _ in range(5)]
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(g, want) for g in got)
+
+
+def test_attention_cache_beyond_32_bits():
+    """A pool over 4 GiB: rows whose byte offset passes 32 bits are the right ones."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    page, D, pages = 4096, 256, 2300                       # 2300 x 4096 x 512 bytes = 4.8 GB
+    say("attention over a pool of 4.8 GB")
+    k = torch.zeros((pages, 1, page, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros((pages, 1, page, D), dtype=torch.bfloat16, device="cuda")
+    cache = fp4.KVCache(k, v)
+    table = to_dev(np.array([[2299, 3], [1030, 2298]], np.int32))
+    rows = torch.randn((2, 5000, D), device="cuda").to(torch.bfloat16)
+    seq = to_dev(np.repeat([0, 1], 5000).astype(np.int32))
+    pos = to_dev(np.tile(np.arange(5000), 2).astype(np.int32))
+    flat = rows.view(10000, 1, D)
+    fp4.kv_append(cache, flat, -flat, table, seq, pos)
+    q = torch.randn((2, 2, D), device="cuda").to(torch.bfloat16)
+    out = fp4.decode_attention(q, cache, table, to_dev(np.array([5000, 4990], np.int32)))
+    for b, n in ((0, 5000), (1, 4990)):
+        K = rows[b, :n].double().cpu().numpy()
+        o, _, p, s = ref.attend(q[b].double().cpu().numpy(), K, -K, D ** -0.5)
+        ds = (D + 4) * 2 * U * D ** -0.5 * (np.abs(q[b].double().cpu().numpy()) @ np.abs(K).T) + 4 * U * np.abs(s)
+        r = 2 * ds.max(axis=1, keepdims=True) + (n + 16) * 2 * U
+        tol = (p @ np.abs(K)) * (r + 2.0 ** -17) + 2.0 ** -8 * np.abs(o)
+        assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
