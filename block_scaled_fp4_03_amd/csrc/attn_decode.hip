@@ -1,5 +1,30 @@
 // attn_decode.hip -- attention of one new token per sequence over the paged
-// key-value cache.
+// key-value cache, split over the cache's length and joined.
+//
+// For the G query heads of a kv head, s = scale q.K^T, p = softmax(s), o = p V.
+// Each K and V row is read once and serves all G heads, so the work is bound
+// by the cache's bytes (G FLOP a byte in BF16, 4 G in MXFP4, far below the
+// matrix core's rate) as long as decoding, softmax and moving stay cheap:
+//
+//   - A wave takes 32 tokens at a time.  S^T = K Q^T on the 16x16x32 BF16
+//     matrix instruction puts a head in each lane column and tokens in the
+//     lanes' registers: a lane (c = lane & 15, g = lane >> 4) gets head c,
+//     tokens 4g..4g+3 of each 16-token half.  Those eight probabilities are,
+//     as they lie, the B operand of O^T += V^T P^T when the contraction
+//     index 8g + j stands for token 4g + j (j < 4) or 16 + 4g + j - 4: no
+//     move across lanes between the two products.
+//   - V^T's A operand wants eight tokens of one element d per lane.  Lane
+//     (c, g) loads, of its eight tokens, elements c D/16 .. of the row (all
+//     16 lanes together: whole rows), and pairs of tokens are interleaved by
+//     v_perm: one VALU operation per two elements, no LDS.  Output row c of
+//     product e then stands for d = c D/16 + e.
+//   - K's elements may be contracted in any order too: lane (c, g) holds
+//     elements g D/4 .. (g+1) D/4 of token c, contiguous in memory.
+//   - MXFP8 / MXFP4 rows are converted to BF16 by the scaling converters
+//     (exact: at most 4 significant bits).
+//   - Softmax statistics are FP32 and running.  The reference maximum of a
+//     head moves only when a score passes it by 2^kLazy, so most tiles need
+//     no reduction across lanes and no rescaling.
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
@@ -7,111 +32,641 @@
 namespace fp4 {
 namespace {
 
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kTile = 32;             // tokens of a wave's step
+constexpr int kWaves = 4;             // waves of a workgroup, taking every fourth tile
+constexpr int kMinTiles = 8;          // tiles below which a sequence is not split further
+constexpr int kMaxSplits = 64;
+constexpr int kHeadTile = 16;         // query heads of a workgroup
+// Scores may pass the reference maximum by this much (in powers of two)
+// before it moves: probabilities up to 2^8, no loss in FP32 or BF16.
+constexpr float kLazy = 8.0f;
 
-// Element d of cache row `row`.
-__device__ __forceinline__ float kv_value(const KvPool& c, const void* pool, const uint8_t* scales, uint64_t row,
-                                          uint32_t d) {
-  const uint32_t D = (uint32_t)c.head_dim;
-  if (c.fmt == kKvBf16) return u2f((uint32_t) static_cast<const uint16_t*>(pool)[row * D + d] << 16);
-  const float s = u2f((uint32_t)scales[row * (D / 32u) + d / 32u] << 23);
-  if (c.fmt == kKvMx8) {
-    const uint32_t b = static_cast<const uint8_t*>(pool)[row * D + d];
-    return (b & 0x80u ? -e4m3_value(b & 0x7Fu) : e4m3_value(b)) * s;
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+struct AttnArgs {
+  KvPool c;
+  const void* q;
+  int64_t q_stride;
+  const int32_t* table;
+  int64_t width;
+  const int32_t* lens;
+  int32_t q_heads;
+  int32_t group;       // query heads of a kv head
+  int32_t head_tiles;  // ceil(group / 16)
+  int64_t max_len;
+  int64_t window;
+  float scale_log2;    // scale * log2 e
+  void* out;
+  float* lse;
+  int32_t q_f32, out_f32;
+  uint32_t* done;      // B x kv_heads x head_tiles arrival counters
+  float* part;         // B x q_heads x splits x D partial sums
+  float* stats;        // B x q_heads x splits x (maximum, sum)
+  float* final_stats;  // B x q_heads x (maximum, 1 / sum), for the weights
+  float* scores;       // B x q_heads x score_stride, or null
+  int64_t score_stride;
+  const float* w_in;
+  float* w_out;
+  int64_t w_stride;
+};
+
+// ---- loads ----
+// BYTES bytes from p (aligned to their largest power of two, at most 16) as dwords.
+template <int BYTES>
+__device__ __forceinline__ void load_bytes(const uint8_t* __restrict__ p, uint32_t (&w)[(BYTES + 3) / 4]) {
+  constexpr int kAlign = BYTES & -BYTES;
+  if constexpr (kAlign >= 16) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      const u32x4 v = reinterpret_cast<const u32x4*>(p)[i];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
+    }
+  } else if constexpr (kAlign == 8) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 8; ++i) {
+      const u32x2 v = reinterpret_cast<const u32x2*>(p)[i];
+      w[2 * i] = v[0];
+      w[2 * i + 1] = v[1];
+    }
+  } else if constexpr (kAlign == 4) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 4; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  } else {
+    static_assert(kAlign == 2, "rows are whole multiples of 32 bytes");
+#pragma unroll
+    for (int i = 0; i < (BYTES + 3) / 4; ++i) {
+      w[i] = reinterpret_cast<const uint16_t*>(p)[2 * i];
+      if (4 * i + 2 < BYTES) w[i] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[2 * i + 1] << 16;
+    }
   }
-  const uint32_t b = (static_cast<const uint8_t*>(pool)[(row * D + d) / 2u] >> (4u * (d & 1u))) & 15u;
-  return (b & 8u ? -e2m1_grid(b & 7u) : e2m1_grid(b)) * s;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-  for (int i = 32; i > 0; i >>= 1) v += __shfl_xor(v, i);
-  return v;
+__device__ __forceinline__ float e8m0(uint32_t byte) { return u2f(byte << 23); }
+
+// Elements 2i, 2i + 1 of a lane's piece of a row (its dwords w) times s, as a BF16 pair.
+template <int FMT, int N>
+__device__ __forceinline__ uint32_t pair_of(const uint32_t (&w)[N], int i, float s) {
+  if constexpr (FMT == kKvBf16) {
+    return w[i];
+  } else if constexpr (FMT == kKvMx8) {
+    return (i & 1) ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], s, true))
+                   : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i >> 1], s, false));
+  } else {
+    switch (i & 3) {
+      case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i >> 2], s, 0));
+      case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i >> 2], s, 1));
+      case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i >> 2], s, 2));
+      default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i >> 2], s, 3));
+    }
+  }
 }
 
-// One workgroup per sequence and kv head; its four waves take every fourth
-// token, one query head of the group after the other.
-__global__ __launch_bounds__(256) void attn_simple_kernel(KvPool c, const void* q, int q_dtype, int64_t q_stride,
-                                                          const int32_t* table, int64_t width, const int32_t* lens,
-                                                          int64_t q_heads, int64_t max_len, int64_t window,
-                                                          float scale, void* out, int out_dtype, float* lse,
-                                                          const float* w_in, float* w_out, int64_t w_stride) {
-  __shared__ float part[4][256 + 2];
-  const uint32_t h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const uint32_t D = (uint32_t)c.head_dim, group = (uint32_t)(q_heads / c.kv_heads);
-  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)c.page_size);
-  const int64_t len = lens[b] < 0 ? 0 : (lens[b] < max_len ? lens[b] : max_len);
-  const int64_t first = window > 0 && window < len ? len - window : 0;
-  for (uint32_t g = 0; g < group; ++g) {
-    const uint32_t qh = h * group + g;
-    float qv[4], acc[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.0f;
-    for (uint32_t i = 0; i < D / 64u; ++i) {
-      const size_t at = (size_t)b * q_stride + qh * D + i * 64u + lane;
-      qv[i] = q_dtype == kDtF32 ? static_cast<const float*>(q)[at]
-                                : u2f((uint32_t) static_cast<const uint16_t*>(q)[at] << 16);
+__device__ __forceinline__ v8bf frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_bit_cast(v8bf, u32x4{a, b, c, d});
+}
+
+__device__ __forceinline__ v4f mfma(v8bf a, v8bf b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// v as TERMS BF16 terms (each the remainder's nearest BF16): TERMS = 3 is
+// exact for normal FP32, 2 leaves at most 2^-17 relative.
+template <int TERMS, int N>
+__device__ __forceinline__ void split_terms(const float (&v)[N], uint32_t (&t)[TERMS][N / 2]) {
+  float r[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = v[i];
+#pragma unroll
+  for (int k = 0; k < TERMS; ++k) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      t[k][i] = bf16_pair(r[2 * i], r[2 * i + 1]);
+      if (k + 1 < TERMS) {
+        r[2 * i] -= u2f(t[k][i] << 16);
+        r[2 * i + 1] -= u2f(t[k][i] & 0xFFFF0000u);
+      }
     }
-    for (int pass = 0; pass < (w_out ? 2 : 1); ++pass) {
-      for (int64_t t = pass == 0 ? first + wave : wave; t < len; t += 4) {
-        const int32_t page = table[(size_t)b * width + (t >> shift)];
-        const bool ok = t >= first && page >= 0 && page < c.pages;
-        float s = 0.0f;
-        const uint64_t row =
-            ok ? (((uint64_t)(uint32_t)page * c.kv_heads + h) << shift) + (t & (c.page_size - 1)) : 0u;
-        if (ok) {
-          for (uint32_t i = 0; i < D / 64u; ++i)
-            s = __builtin_fmaf(qv[i], kv_value(c, c.k, c.ks, row, i * 64u + lane), s);
-          s = wave_sum(s) * scale;
-        }
-        if (pass == 1) {
-          const size_t at = ((size_t)b * c.kv_heads + h) * w_stride + t;
-          const float p = ok ? expf(s - m) / l : 0.0f;
-          if (lane == 0) w_out[at] = (g == 0 ? (w_in ? w_in[at] : 0.0f) : w_out[at]) + p;
-        } else if (ok) {
-          const float m1 = fmaxf(m, s), f = m1 == -INFINITY ? 1.0f : expf(m - m1), p = expf(s - m1);
-          l = l * f + p;
-          for (uint32_t i = 0; i < D / 64u; ++i)
-            acc[i] = acc[i] * f + p * kv_value(c, c.v, c.vs, row, i * 64u + lane);
-          m = m1;
-        }
+  }
+}
+
+// Two floats through the device's coherence point (other XCDs' workgroups
+// read them; a plain store could stay in this XCD's L2).
+__device__ __forceinline__ void store2_agent(float* p, float a, float b) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p), (uint64_t)f2u(a) | ((uint64_t)f2u(b) << 32), __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ v2f load2_agent(const float* p) {
+  const uint64_t u = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  return v2f{u2f((uint32_t)u), u2f((uint32_t)(u >> 32))};
+}
+
+__device__ __forceinline__ void store_out2(const AttnArgs& a, size_t i, float x, float y) {
+  if (a.out_f32)
+    *reinterpret_cast<v2f*>(static_cast<float*>(a.out) + i) = v2f{x, y};
+  else
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + i) = bf16_pair(x, y);
+}
+
+// The tokens of a sequence that the call attends to, in tiles of 32 aligned
+// to the pages (a page is at least 16 tokens), and their split.
+struct Range {
+  uint32_t first, len;     // tokens [first, len)
+  uint32_t tile0, tiles;   // tiles of the sequence from tile0 on
+  uint32_t per, splits;    // tiles of a split; splits that have any
+};
+__device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b, uint32_t max_splits) {
+  Range r;
+  const int64_t l = a.lens[b];
+  r.len = (uint32_t)(l < 0 ? 0 : l < a.max_len ? l : a.max_len);
+  r.first = a.window > 0 && a.window < (int64_t)r.len ? r.len - (uint32_t)a.window : 0u;
+  r.tile0 = r.first / kTile;
+  r.tiles = a.c.pages > 0 ? (r.len + kTile - 1) / kTile - r.tile0 : 0u;  // an empty pool has nothing to read
+  r.per = (r.tiles + max_splits - 1) / max_splits;
+  if (r.per < (uint32_t)kMinTiles) r.per = kMinTiles;
+  r.splits = (r.tiles + r.per - 1) / r.per;
+  return r;
+}
+
+template <int FMT, int D, bool EX>
+__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
+  constexpr int kRow = (int)kv_row_bytes(FMT, D);
+  constexpr int kSteps = D / 32;               // matrix instructions along D for 16 tokens
+  constexpr int EV = D / 16;                   // elements of V per lane and token
+  constexpr int kKB = kRow / 4, kVB = kRow / 16;
+  constexpr int kKW = kKB / 4, kVW = (kVB + 3) / 4;
+  constexpr bool MX = FMT != kKvBf16;
+  constexpr int kBlocks = D / 32;
+  constexpr int kQTerms = EX ? 3 : 1, kPTerms = EX ? 3 : 2;
+  constexpr int kPad = D + 4;
+
+  __shared__ float red[2][kHeadTile][kPad];
+  __shared__ float wave_m[kWaves][kHeadTile], wave_l[kWaves][kHeadTile];
+  __shared__ uint32_t last_arrival;
+
+  const uint32_t split = blockIdx.x, max_splits = gridDim.x, b = blockIdx.z;
+  const uint32_t h = blockIdx.y / (uint32_t)a.head_tiles, ht = blockIdx.y % (uint32_t)a.head_tiles;
+  const Range r = range_of(a, b, max_splits);
+  if (split >= r.splits && split > 0u) return;
+
+  const uint32_t lane = threadIdx.x & 63u, c = lane & 15u, g = lane >> 4;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
+  const uint32_t head0 = h * (uint32_t)a.group + ht * kHeadTile;  // first query head
+  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)a.c.page_size), in_page = (uint32_t)a.c.page_size - 1u;
+
+  // Q: head c's elements g D/4 + 8 s .. + 7 in step s; zero for heads past the group.
+  v8bf q[kQTerms][kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const size_t at =
+        (size_t)b * (size_t)a.q_stride + (size_t)(head0 + (c < heads ? c : 0u)) * D + g * (D / 4) + 8 * s;
+    if constexpr (EX) {
+      float v[8];
+      if (a.q_f32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = static_cast<const float*>(a.q)[at + i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = u2f((uint32_t) static_cast<const uint16_t*>(a.q)[at + i] << 16);
       }
-      if (pass == 1) break;
-      for (uint32_t i = 0; i < D / 64u; ++i) part[wave][2 + i * 64u + lane] = acc[i];
-      if (lane == 0) {
-        part[wave][0] = m;
-        part[wave][1] = l;
-      }
-      __syncthreads();
-      m = fmaxf(fmaxf(part[0][0], part[1][0]), fmaxf(part[2][0], part[3][0]));
-      l = 0.0f;
-      for (int i = 0; i < 4; ++i)
-        if (part[i][1] != 0.0f) l += part[i][1] * expf(part[i][0] - m);
-      for (uint32_t d = threadIdx.x; d < D; d += 256u) {
-        float o = 0.0f;
-        for (int i = 0; i < 4; ++i)
-          if (part[i][1] != 0.0f) o += part[i][2 + d] * (expf(part[i][0] - m) / l);
-        const size_t at = ((size_t)b * q_heads + qh) * D + d;
-        if (out_dtype == kDtF32)
-          static_cast<float*>(out)[at] = o;
-        else
-          static_cast<uint16_t*>(out)[at] = (uint16_t)bf16_pair(o, 0.0f);
-      }
-      if (threadIdx.x == 0 && lse) lse[(size_t)b * q_heads + qh] = l == 0.0f ? -INFINITY : m + logf(l);
-      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c < heads ? v[i] : 0.0f;
+      uint32_t t[3][4];
+      split_terms<3>(v, t);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) q[k][s] = frag(t[k][0], t[k][1], t[k][2], t[k][3]);
+    } else {
+      u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at);
+      if (c >= heads) v = u32x4{0u, 0u, 0u, 0u};
+      q[0][s] = __builtin_bit_cast(v8bf, v);
     }
-    __syncthreads();
+  }
+
+  v4f o[EV];
+#pragma unroll
+  for (int e = 0; e < EV; ++e) o[e] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  float m = -INFINITY, l = 0.0f;  // of head c; l of this lane's tokens alone
+
+  const uint32_t t_end = min((split + 1u) * r.per, r.tiles);
+  const uint32_t pages_used = (r.len + in_page) >> shift;
+  const int32_t* table = a.table + (size_t)b * (size_t)a.width;
+
+  // Row number of a half tile's first token, or ~0 where its page is not in the pool.
+  const auto half_row = [&](uint32_t tile, uint32_t j) -> uint64_t {
+    const uint32_t t = (r.tile0 + tile) * kTile + 16u * j, p = t >> shift;
+    const int32_t page = tile < t_end && p < pages_used ? table[p] : -1;
+    if (page < 0 || page >= a.c.pages) return ~0ull;
+    return (((uint64_t)(uint32_t)page * (uint32_t)a.c.kv_heads + h) << shift) + (t & in_page);
+  };
+
+  uint32_t kw[2][kKW], vw[8][kVW];
+  uint32_t kb[2][2], vb[8][2];  // MX: the scale bytes (two where a lane's elements touch two blocks)
+  const uint32_t k_off = c * kRow + g * kKB, v_off = 4u * g * kRow + c * kVB;
+  constexpr int kKScales = D <= 128 ? 1 : 2, kVScales = 32 % EV == 0 ? 1 : 2;
+  const uint32_t k_blk = g * (D / 4) / 32u, v_blk = c * EV / 32u;
+
+  const auto load_k = [&](const uint64_t (&row)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint64_t at = row[j] == ~0ull ? 0u : row[j];
+      load_bytes<kKB>(static_cast<const uint8_t*>(a.c.k) + at * kRow + k_off, kw[j]);
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < kKScales; ++i) kb[j][i] = (a.c.ks + at * kBlocks)[c * kBlocks + k_blk + i];
+      }
+    }
+  };
+  const auto load_v = [&](const uint64_t (&row)[2]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t at = row[j >> 2] == ~0ull ? 0u : row[j >> 2];
+      load_bytes<kVB>(static_cast<const uint8_t*>(a.c.v) + at * kRow + v_off + (j & 3) * kRow, vw[j]);
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < kVScales; ++i)
+          vb[j][i] = (a.c.vs + at * kBlocks)[(4u * g + (j & 3)) * kBlocks + min(v_blk + i, (uint32_t)kBlocks - 1u)];
+      }
+    }
+  };
+
+  uint32_t tile = split * r.per + wave;
+  uint64_t row[2] = {~0ull, ~0ull}, next[2] = {~0ull, ~0ull};
+  if (tile < t_end) {
+    row[0] = half_row(tile, 0);
+    row[1] = half_row(tile, 1);
+    next[0] = half_row(tile + kWaves, 0);
+    next[1] = half_row(tile + kWaves, 1);
+    load_k(row);
+    load_v(row);
+  }
+  for (; tile < t_end; tile += kWaves) {
+    const bool more = tile + kWaves < t_end;
+    // S^T: rows tokens, columns heads.
+    v4f st[2] = {v4f{0.0f, 0.0f, 0.0f, 0.0f}, v4f{0.0f, 0.0f, 0.0f, 0.0f}};
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float ks[2] = {1.0f, 1.0f};
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < kKScales; ++i) ks[i] = e8m0(kb[j][i]);
+      }
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        // The block of elements g D/4 + 8 s .., counted from the lane's first.
+        float sc = ks[0];
+        if constexpr (D == 256) sc = ks[s >> 2];
+        if constexpr (D == 192) sc = (g & 1u) ? ks[(s + 2) >> 2] : ks[s >> 2];
+        const v8bf kf = frag(pair_of<FMT>(kw[j], 4 * s, sc), pair_of<FMT>(kw[j], 4 * s + 1, sc),
+                             pair_of<FMT>(kw[j], 4 * s + 2, sc), pair_of<FMT>(kw[j], 4 * s + 3, sc));
+#pragma unroll
+        for (int k = 0; k < kQTerms; ++k) st[j] = mfma(kf, q[k][s], st[j]);
+      }
+    }
+    const bool in0 = row[0] != ~0ull, in1 = row[1] != ~0ull;
+    if (more) load_k(next);
+
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = st[i >> 2][i & 3] * a.scale_log2;
+    const uint32_t t0 = (r.tile0 + tile) * kTile;
+    const bool full = t0 >= r.first && t0 + kTile <= r.len && in0 && in1;
+    if (!full) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t t = t0 + 16u * (i >> 2) + 4u * g + (i & 3);
+        const bool ok = t >= r.first && t < r.len && ((i >> 2) ? in1 : in0);
+        x[i] = ok ? x[i] : -INFINITY;
+      }
+    }
+    if (a.scores && c < heads) {
+      float* at = a.scores + ((size_t)b * (uint32_t)a.q_heads + head0 + c) * (size_t)a.score_stride + t0 + 4u * g;
+      *reinterpret_cast<v4f*>(at) = v4f{x[0], x[1], x[2], x[3]};
+      *reinterpret_cast<v4f*>(at + 16) = v4f{x[4], x[5], x[6], x[7]};
+    }
+    float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    if (__any(top > m + kLazy)) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const float to = fmaxf(m, top);
+      const float f = m == -INFINITY ? 0.0f : exp2_fast(m - to);
+      l *= f;
+#pragma unroll
+      for (int e = 0; e < EV; ++e) o[e] *= f;
+      m = to;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m;  // nothing but masked tokens so far: all p are 0
+    float p[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = exp2_fast(x[i] - ref);
+      l += p[i];
+    }
+    uint32_t pt[kPTerms][4];
+    split_terms<kPTerms>(p, pt);
+
+    // V: tokens paired two by two per element.
+    uint32_t vp[8][EV / 2];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float vs[2] = {1.0f, 1.0f};
+      if constexpr (MX) {
+#pragma unroll
+        for (int i = 0; i < kVScales; ++i) vs[i] = e8m0(vb[j][i]);
+      }
+#pragma unroll
+      for (int i = 0; i < EV / 2; ++i) {
+        float sc = vs[0];
+        if constexpr (kVScales == 2) sc = c * EV + 2 * i >= 32u * (v_blk + 1u) ? vs[1] : vs[0];
+        vp[j][i] = pair_of<FMT>(vw[j], i, sc);
+      }
+    }
+    if (!full) {
+      // Whatever lies in a masked slot (NaN too) must not meet p = 0.
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t t = t0 + 16u * (j >> 2) + 4u * g + (j & 3);
+        const bool ok = t >= r.first && t < r.len && ((j >> 2) ? in1 : in0);
+#pragma unroll
+        for (int i = 0; i < EV / 2; ++i) vp[j][i] = ok ? vp[j][i] : 0u;
+      }
+    }
+    if constexpr (MX) {  // the raw registers are free once converted
+      if (more) load_v(next);
+    }
+#pragma unroll
+    for (int e = 0; e < EV; ++e) {
+      constexpr uint32_t kLo = 0x05040100u, kHi = 0x07060302u;
+      const uint32_t sel = (e & 1) ? kHi : kLo;
+      const int i = e >> 1;
+      const v8bf vf = frag(__builtin_amdgcn_perm(vp[1][i], vp[0][i], sel), __builtin_amdgcn_perm(vp[3][i], vp[2][i], sel),
+                           __builtin_amdgcn_perm(vp[5][i], vp[4][i], sel), __builtin_amdgcn_perm(vp[7][i], vp[6][i], sel));
+#pragma unroll
+      for (int k = 0; k < kPTerms; ++k) o[e] = mfma(vf, frag(pt[k][0], pt[k][1], pt[k][2], pt[k][3]), o[e]);
+    }
+    if constexpr (!MX) {
+      if (more) load_v(next);
+    }
+    row[0] = next[0];
+    row[1] = next[1];
+    if (more) {
+      next[0] = half_row(tile + 2 * kWaves, 0);
+      next[1] = half_row(tile + 2 * kWaves, 1);
+    }
+  }
+
+  // ---- the four waves' results: a common maximum, then sums in fixed order ----
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (lane < 16u) {
+    wave_m[wave][c] = m;
+    wave_l[wave][c] = l;
+  }
+  __syncthreads();
+  float M = wave_m[0][c];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) M = fmaxf(M, wave_m[w][c]);
+  const float f = m == -INFINITY ? 0.0f : exp2_fast(m - M);
+  // Lane (c, g) holds head c, d = (4g + i) EV + e of o[e][i].
+  if (wave < 2u && c < heads) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < EV; ++e) red[wave][c][(4 * g + i) * EV + e] = o[e][i] * f;
+  }
+  __syncthreads();
+  if (wave >= 2u && c < heads) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < EV; ++e) red[wave - 2u][c][(4 * g + i) * EV + e] += o[e][i] * f;
+  }
+  __syncthreads();
+
+  // Sum of head hd over the waves, with the workgroup's maximum.
+  const auto head_sum = [&](uint32_t hd, float& mx) {
+    mx = wave_m[0][hd];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, wave_m[w][hd]);
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+      s += wave_m[w][hd] == -INFINITY ? 0.0f : wave_l[w][hd] * exp2_fast(wave_m[w][hd] - mx);
+    return s;
+  };
+  const auto finish_head = [&](uint32_t hd, float mx, float s) {  // one thread per head
+    const size_t at = (size_t)b * (uint32_t)a.q_heads + head0 + hd;
+    if (a.lse) a.lse[at] = s == 0.0f ? -INFINITY : (mx + __builtin_log2f(s)) * kLn2;
+    if (a.final_stats) *reinterpret_cast<v2f*>(a.final_stats + 2 * at) = v2f{mx, s == 0.0f ? 0.0f : 1.0f / s};
+  };
+
+  if (r.splits <= 1u) {
+    for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
+      const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
+      float mx;
+      const float s = head_sum(hd, mx), inv = s == 0.0f ? 0.0f : 1.0f / s;
+      store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + d, (red[0][hd][d] + red[1][hd][d]) * inv,
+                 (red[0][hd][d + 1] + red[1][hd][d + 1]) * inv);
+    }
+    if (threadIdx.x < heads) {
+      float mx;
+      const float s = head_sum(threadIdx.x, mx);
+      finish_head(threadIdx.x, mx, s);
+    }
+    return;
+  }
+
+  // ---- the splits' results: written through, then the last to arrive joins ----
+  const size_t part0 = ((size_t)b * (uint32_t)a.q_heads + head0) * max_splits;
+  for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
+    const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
+    store2_agent(a.part + (part0 + (size_t)hd * max_splits + split) * D + d, red[0][hd][d] + red[1][hd][d],
+                 red[0][hd][d + 1] + red[1][hd][d + 1]);
+  }
+  if (threadIdx.x < heads) {
+    float mx;
+    const float s = head_sum(threadIdx.x, mx);
+    store2_agent(a.stats + 2 * (part0 + (size_t)threadIdx.x * max_splits + split), mx, s);
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
+  __syncthreads();
+  uint32_t* done = a.done + ((size_t)b * gridDim.y + blockIdx.y);
+  if (threadIdx.x == 0u) {
+    const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last_arrival = before == r.splits - 1u;
+    if (last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last_arrival) return;
+
+  // Factors 2^(m_s - M) of every head and split (the red array is free now).
+  float* factor = &red[0][0][0];  // heads x kMaxSplits, fits: 16 x 64 <= 2 x 16 x 68
+  static_assert(kHeadTile * kMaxSplits <= 2 * kHeadTile * kPad, "factors fit in the array they reuse");
+  for (uint32_t hd = wave; hd < heads; hd += kWaves) {
+    v2f ms = v2f{-INFINITY, 0.0f};
+    if (lane < r.splits) ms = load2_agent(a.stats + 2 * (part0 + (size_t)hd * max_splits + lane));
+    float mx = ms[0];
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
+    const float fs = ms[0] == -INFINITY ? 0.0f : exp2_fast(ms[0] - mx);
+    float s = ms[1] * fs;
+#pragma unroll
+    for (int i = 32; i > 0; i >>= 1) s += __shfl_xor(s, i);
+    factor[hd * kMaxSplits + lane] = s == 0.0f ? 0.0f : fs / s;
+    if (lane == 0u) finish_head(hd, mx, s);
+  }
+  __syncthreads();
+  for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
+    const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
+    const float* from = a.part + (part0 + (size_t)hd * max_splits) * D + d;
+    float x = 0.0f, y = 0.0f;
+    for (uint32_t s0 = 0u; s0 < r.splits; s0 += 8u) {
+      v2f v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = load2_agent(from + (size_t)min(s0 + k, r.splits - 1u) * D);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float w = s0 + k < r.splits ? factor[hd * kMaxSplits + s0 + k] : 0.0f;
+        x = s0 + k < r.splits ? __builtin_fmaf(w, v[k][0], x) : x;
+        y = s0 + k < r.splits ? __builtin_fmaf(w, v[k][1], y) : y;
+      }
+    }
+    store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + d, x, y);
+  }
+}
+
+// weights_out = weights_in + sum over the kv head's query heads of p, from the
+// stored scores: p = 2^(x - M) / L.  Four tokens a thread.
+__global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
+  const uint32_t h = blockIdx.y, b = blockIdx.z, t = (blockIdx.x * 256u + threadIdx.x) * 4u;
+  const Range r = range_of(a, b, 1u);
+  if (t >= r.len) return;
+  const size_t at = ((size_t)b * gridDim.y + h) * (size_t)a.w_stride + t;
+  const uint32_t n = min(r.len - t, 4u);
+  float w[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (r.tiles > 0u && t >= r.tile0 * kTile) {  // earlier tiles were not scored: all before the window
+    const size_t head0 = (size_t)b * (uint32_t)a.q_heads + (size_t)h * (uint32_t)a.group;
+    for (uint32_t k = 0u; k < (uint32_t)a.group; ++k) {
+      const v4f x = *reinterpret_cast<const v4f*>(a.scores + (head0 + k) * (size_t)a.score_stride + t);
+      const v2f ms = *reinterpret_cast<const v2f*>(a.final_stats + 2 * (head0 + k));
+      const float ref = ms[0] == -INFINITY ? 0.0f : ms[0];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] += exp2_fast(x[i] - ref) * ms[1];
+    }
+  }
+#pragma unroll
+  for (uint32_t i = 0; i < 4u; ++i)
+    if (i < n) a.w_out[at + i] = (a.w_in ? a.w_in[at + i] : 0.0f) + w[i];
+}
+
+// Workgroups that fill the chip's 256 CUs a few times over even where the
+// lengths are ragged.
+uint32_t splits_of(int64_t B, int64_t units, int64_t max_len) {
+  int64_t s = (2048 + B * units - 1) / (B * units);
+  if (s < 8) s = 8;
+  if (s > kMaxSplits) s = kMaxSplits;
+  const int64_t most = (max_len + kMinTiles * kTile - 1) / (kMinTiles * kTile) + 1;  // + 1: a window may start inside a tile
+  if (s > most) s = most;
+  return (uint32_t)(s < 1 ? 1 : s);
+}
+
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
+// The workspace: arrival counters, then statistics, partial sums, scores.
+struct Layout {
+  uint32_t splits;
+  int64_t head_tiles, score_stride;
+  size_t done, stats, final_stats, part, scores, total;
+};
+Layout layout_of(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len, bool weights) {
+  Layout w{};
+  w.head_tiles = (q_heads / kv_heads + kHeadTile - 1) / kHeadTile;
+  w.score_stride = (max_len + kTile - 1) / kTile * kTile;
+  w.splits = B == 0 || q_heads == 0 ? 1u : splits_of(B, kv_heads * w.head_tiles, max_len);
+  const bool join = w.splits > 1;
+  w.done = 0;
+  w.stats = w.done + (join ? round16((size_t)(B * kv_heads * w.head_tiles) * 4) : 0);
+  w.final_stats = w.stats + (join ? round16((size_t)(B * q_heads) * w.splits * 8) : 0);
+  w.part = w.final_stats + (weights ? round16((size_t)(B * q_heads) * 8) : 0);
+  w.scores = w.part + (join ? round16((size_t)(B * q_heads) * w.splits * (size_t)D * 4) : 0);
+  w.total = w.scores + (weights ? (size_t)(B * q_heads) * (size_t)w.score_stride * 4 : 0);
+  return w;
+}
+
+template <int FMT, int D>
+void launch_d(const AttnArgs& a, dim3 grid, bool exact, hipStream_t stream) {
+  if (exact)
+    attn_decode_kernel<FMT, D, true><<<grid, 256, 0, stream>>>(a);
+  else
+    attn_decode_kernel<FMT, D, false><<<grid, 256, 0, stream>>>(a);
+}
+
+template <int FMT>
+void launch_fmt(const AttnArgs& a, dim3 grid, bool exact, hipStream_t stream) {
+  switch (a.c.head_dim) {
+    case 64: return launch_d<FMT, 64>(a, grid, exact, stream);
+    case 128: return launch_d<FMT, 128>(a, grid, exact, stream);
+    case 192: return launch_d<FMT, 192>(a, grid, exact, stream);
+    default: return launch_d<FMT, 256>(a, grid, exact, stream);
   }
 }
 
 }  // namespace
 
-size_t attn_decode_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, bool) { return 0; }
+size_t attn_decode_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_len,
+                             bool weights) {
+  if (B == 0 || q_heads == 0) return 0;
+  return layout_of(B, q_heads, kv_heads, head_dim, max_len, weights).total;
+}
 
 hipError_t launch_attn_decode(const KvPool& c, const void* q, int q_dtype, int64_t q_stride, const int32_t* table,
                               int64_t width, const int32_t* lens, int64_t B, int64_t q_heads, int64_t max_len,
                               int64_t window, float scale, void* out, int out_dtype, float* lse,
-                              const float* weights_in, float* weights_out, int64_t weights_stride, void*,
+                              const float* weights_in, float* weights_out, int64_t weights_stride, void* workspace,
                               hipStream_t stream) {
-  attn_simple_kernel<<<dim3((uint32_t)c.kv_heads, (uint32_t)B), 256, 0, stream>>>(
-      c, q, q_dtype, q_stride, table, width, lens, q_heads, max_len, window, scale, out, out_dtype, lse, weights_in,
-      weights_out, weights_stride);
+  const Layout w = layout_of(B, q_heads, c.kv_heads, c.head_dim, max_len, weights_out != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttnArgs a{};
+  a.c = c;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.table = table;
+  a.width = width;
+  a.lens = lens;
+  a.q_heads = (int32_t)q_heads;
+  a.group = (int32_t)(q_heads / c.kv_heads);
+  a.head_tiles = (int32_t)w.head_tiles;
+  a.max_len = max_len;
+  a.window = window;
+  a.scale_log2 = scale * kLog2e;
+  a.out = out;
+  a.lse = lse;
+  a.q_f32 = q_dtype == kDtF32;
+  a.out_f32 = out_dtype == kDtF32;
+  a.done = reinterpret_cast<uint32_t*>(ws + w.done);
+  a.stats = reinterpret_cast<float*>(ws + w.stats);
+  a.part = reinterpret_cast<float*>(ws + w.part);
+  if (weights_out) {
+    a.final_stats = reinterpret_cast<float*>(ws + w.final_stats);
+    a.scores = reinterpret_cast<float*>(ws + w.scores);
+    a.score_stride = w.score_stride;
+    a.w_in = weights_in;
+    a.w_out = weights_out;
+    a.w_stride = weights_stride;
+  }
+  const bool exact = q_dtype == kDtF32 || out_dtype == kDtF32;
+  const dim3 grid(w.splits, (uint32_t)(c.kv_heads * w.head_tiles), (uint32_t)B);
+  switch (c.fmt) {
+    case kKvBf16: launch_fmt<kKvBf16>(a, grid, exact, stream); break;
+    case kKvMx8: launch_fmt<kKvMx8>(a, grid, exact, stream); break;
+    default: launch_fmt<kKvMx4>(a, grid, exact, stream); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !weights_out || max_len == 0) return e;
+  attn_weights_kernel<<<dim3((uint32_t)((max_len + 1023) / 1024), (uint32_t)c.kv_heads, (uint32_t)B), 256, 0,
+                        stream>>>(a);
   return hipGetLastError();
 }
 

@@ -293,3 +293,18 @@ def test_attention_cache_beyond_32_bits():
         r = 2 * ds.max(axis=1, keepdims=True) + (n + 16) * 2 * U
         tol = (p @ np.abs(K)) * (r + 2.0 ** -17) + 2.0 ** -8 * np.abs(o)
         assert np.all(np.abs(out[b].double().cpu().numpy() - o) <= tol)
+
+
+def test_attention_of_an_empty_pool():
+    """A pool without pages: every token is masked; the weights are passed on."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    cache = fp4.KVCache.empty(0, 16, 2, 64)
+    q = torch.ones((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    w = torch.rand((1, 2, 320), device="cuda")
+    w_out = torch.zeros_like(w)
+    say("attention of an empty pool")
+    out = fp4.decode_attention(q, cache, to_dev(np.zeros((1, 20), np.int32)), to_dev(np.array([300], np.int32)),
+                               weights=w, weights_out=w_out)
+    assert not out.any()
+    assert torch.equal(w_out[..., :300], w[..., :300]) and not w_out[..., 300:].any()
