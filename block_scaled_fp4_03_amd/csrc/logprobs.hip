@@ -1,12 +1,46 @@
 // logprobs.hip -- log probabilities of given tokens, entropy and the largest
-// alternatives, and their gradient.
+// alternatives, in one pass over the logits; and their gradient.
+//
+// Forward.  With a running reference r (a logit), t_i = scale (x_i - r):
+//   S = sum e^t_i,  W = sum t_i e^t_i;  lse = scale r + log S,
+//   entropy = log S - W / S.
+// Moving r to r' multiplies S by f = e^(scale (r - r')) and turns W into
+// f (W + scale (r - r') S).  Each thread keeps its own (r, S, W) and moves r
+// only when a logit passes it by 2^kLazy, so the common step is five VALU
+// operations and one exponential an element, below the memory's time.  All in
+// base 2 (t times log2 e), FP32.
+//
+// The top k in the same pass: the first 16 KB give a threshold with at least
+// k elements at or above it (the k-th largest of 64 groups' maxima), and from
+// then on only elements above it are looked at: k V / 8192 of them in the
+// mean, collected in LDS and ranked at the end.  Elements equal to the
+// threshold are needed only if fewer than k lie above it, and then the first
+// ones in order; they lie in the first 16 KB.  A row that overflows the
+// buffer (a rising row) is collected again above the k-th largest of the
+// groups' maxima over everything; one that overflows again, or holds a NaN,
+// is searched k times.
+//
+// Few rows are split over workgroups; the last to arrive joins them.
 #include "fp4_device.h"
 #include "fp4_launch.h"
+#include "kv_device.h"
 
 namespace fp4 {
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr uint32_t kThreads = 256, kWaves = 4;
+constexpr uint32_t kUnroll = 4;                      // 16-byte blocks of a thread's step
+constexpr uint32_t kStepBlocks = kThreads * kUnroll;  // 16 KB
+constexpr uint32_t kGroups = 64;                     // groups of four threads
+constexpr uint32_t kCand = 1024;                     // candidates a workgroup can hold
+constexpr uint32_t kMaxSplits = 64, kMaxTop = 32;
+constexpr float kLazy = 8.0f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int DT>
+constexpr uint32_t kElem = DT == kDtF32 ? 4u : 8u;  // elements of a 16-byte block
 
 template <int DT>
 __device__ __forceinline__ float logit(const void* x, size_t i) {
@@ -14,154 +48,552 @@ __device__ __forceinline__ float logit(const void* x, size_t i) {
   return u2f((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
 }
 
-// 64-bit key ordering (value, lower index first): NaN above all, +0 equal to -0.
+// A row as aligned 16-byte blocks: block j holds elements j E - head .. (the
+// first and the last block may be partly outside the row).
+template <int DT>
+struct Row {
+  const uint8_t* p;  // the row's first element
+  uint32_t V, head, blocks;
+  __device__ __forceinline__ Row(const void* x, size_t at, uint32_t V_) : V(V_) {
+    constexpr uint32_t size = DT == kDtF32 ? 4u : 2u;
+    p = static_cast<const uint8_t*>(x) + at * size;
+    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / size;
+    blocks = (V + head + kElem<DT> - 1u) / kElem<DT>;
+  }
+  // Elements of block j; `outside` for those not in the row.
+  __device__ __forceinline__ void load(uint32_t j, float (&v)[kElem<DT>]) const {
+    constexpr uint32_t E = kElem<DT>;
+    const int64_t i0 = (int64_t)j * E - head;
+    if (i0 >= 0 && i0 + E <= V) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p + i0 * (DT == kDtF32 ? 4 : 2));
+      if constexpr (DT == kDtF32) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = u2f(w[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[2 * k] = u2f(w[k] << 16);
+          v[2 * k + 1] = u2f(w[k] & 0xFFFF0000u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (uint32_t k = 0; k < E; ++k) {
+        const int64_t i = i0 + k;
+        v[k] = i >= 0 && i < V ? logit<DT>(p, (size_t)i) : -INFINITY;
+      }
+    }
+  }
+  __device__ __forceinline__ float at(uint32_t i) const { return logit<DT>(p, i); }
+};
+
+// 64-bit key in the order (value, lower index first): NaN above all, +0 equal
+// to -0.  0 is below every key.
 __device__ __forceinline__ uint64_t top_key(float v, uint32_t i) {
   uint32_t u = f2u(v + 0.0f);
   u = v != v ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
   return ((uint64_t)u << 32) | (uint32_t)~i;
 }
 
-// m, s, w: the running maximum of y and the sums of e^(y - m) and
-// (y - m) e^(y - m); a second set joins the first.
 struct Stats {
-  float m, s, w;
+  float r, s, w;  // reference (a logit), S, W (base 2)
 };
-__device__ __forceinline__ Stats join(Stats a, Stats b) {
-  const float m = fmaxf(a.m, b.m);
-  const float da = a.m == m ? 0.0f : a.m - m, db = b.m == m ? 0.0f : b.m - m;
-  const float fa = exp2f(da * kLog2e), fb = exp2f(db * kLog2e);
-  Stats r;
-  r.m = m;
-  r.s = a.s * fa + b.s * fb;
+// c2 = scale log2 e.
+__device__ __forceinline__ Stats join(Stats a, Stats b, float c2) {
+  const float r = fmaxf(a.r, b.r);
+  const float da = a.r == r ? 0.0f : (a.r - r) * c2, db = b.r == r ? 0.0f : (b.r - r) * c2;
+  const float fa = exp2_fast(da), fb = exp2_fast(db);
   // A side that vanishes adds nothing, however far below it lies (da may overflow).
-  r.w = (fa == 0.0f ? 0.0f : (a.w + da * a.s) * fa) + (fb == 0.0f ? 0.0f : (b.w + db * b.s) * fb);
-  return r;
+  return Stats{r, a.s * fa + b.s * fb,
+               (fa == 0.0f ? 0.0f : (a.w + da * a.s) * fa) + (fb == 0.0f ? 0.0f : (b.w + db * b.s) * fb)};
+}
+__device__ __forceinline__ Stats shuffle_xor(Stats a, int d) {
+  return Stats{__shfl_xor(a.r, d), __shfl_xor(a.s, d), __shfl_xor(a.w, d)};
 }
 
-template <int DT>
-__global__ __launch_bounds__(256) void logprobs_simple_kernel(const void* __restrict__ x, int64_t stride, uint32_t V,
-                                                              float scale, const int32_t* __restrict__ tokens,
-                                                              int32_t M, float* __restrict__ logp,
-                                                              float* __restrict__ entropy, float* __restrict__ lse,
-                                                              int32_t top_k, float* __restrict__ top_logp,
-                                                              int32_t* __restrict__ top_index) {
-  __shared__ Stats part[256];
-  __shared__ uint64_t best[256];
-  const size_t n = blockIdx.x, row = n * (size_t)stride;
-  const uint32_t tid = threadIdx.x;
-  Stats a = {-INFINITY, 0.0f, 0.0f};
-  for (uint32_t i = tid; i < V; i += 256u) {
-    const float y = logit<DT>(x, row + i) * scale;
-    a = join(a, Stats{y, y == -INFINITY ? 0.0f : 1.0f, 0.0f});
-    if (y != y) a.s = y;
-  }
-  part[tid] = a;
+struct Args {
+  const void* x;
+  int64_t stride;
+  uint32_t V;
+  float scale;
+  const int32_t* tokens;
+  int32_t M;
+  float* logp;
+  float* entropy;
+  float* lse;
+  int32_t top_k;
+  float* top_logp;
+  int32_t* top_index;
+  uint32_t* done;   // arrival counters, one a row
+  float* stats;     // rows x splits x 4
+  uint64_t* keys;   // rows x splits x top_k
+};
+
+struct Shared {
+  uint64_t cand[kCand];
+  uint64_t best[kMaxTop];
+  float group[kGroups];
+  float tau[2];
+  uint32_t count, flag;
+  Stats part[kWaves];
+  uint64_t wave_key[kWaves];
+};
+
+// The k-th largest of the 64 groups' maxima (each thread gives its own; a
+// lane ranks one group against all).  Every thread of the workgroup calls it.
+__device__ __forceinline__ float threshold(Shared& sh, float mine, uint32_t k) {
+  mine = fmaxf(mine, lane_xor1(mine));
+  mine = fmaxf(mine, lane_xor2(mine));
+  if ((threadIdx.x & 3u) == 0u) sh.group[threadIdx.x >> 2] = mine;
   __syncthreads();
-  for (uint32_t d = 128u; d > 0u; d >>= 1) {
-    if (tid < d) part[tid] = join(part[tid], part[tid + d]);
-    __syncthreads();
-  }
-  a = part[0];
-  if (a.m == INFINITY) a.s = NAN;  // inf - inf
-  const float ls = a.s == 0.0f ? -INFINITY : a.m + logf(a.s);
-  if (tid == 0u) {
-    if (entropy) entropy[n] = a.s == 0.0f ? 0.0f : logf(a.s) - a.w / a.s;
-    if (lse) lse[n] = ls;
-  }
-  for (int32_t j = (int32_t)tid; j < M; j += 256) {
-    const int32_t t = tokens[n * (size_t)M + j];
-    float r = 0.0f;
-    if (t >= 0 && (uint32_t)t < V) {
-      const float y = logit<DT>(x, row + (uint32_t)t) * scale;
-      r = y == -INFINITY && ls == ls ? -INFINITY : y - ls;
+  const uint32_t lane = threadIdx.x & 63u;
+  if (threadIdx.x < 64u) {
+    const float v = sh.group[lane];
+    uint32_t rank = 0u;
+#pragma unroll 16
+    for (uint32_t i = 0u; i < kGroups; ++i) {
+      const float u = sh.group[i];
+      rank += (u > v || (u == v && i < lane)) ? 1u : 0u;
     }
-    logp[n * (size_t)M + j] = r;
+    if (rank == k - 1u) sh.tau[0] = v;
   }
+  __syncthreads();
+  return sh.tau[0];
+}
+
+__device__ __forceinline__ void push(Shared& sh, float v, uint32_t i) {
+  const uint32_t at = atomicAdd(&sh.count, 1u);
+  if (at < kCand) sh.cand[at] = top_key(v, i);
+}
+
+// The largest k of cand[0 .. n) into best, in order (fewer: the rest 0), by
+// counting for each how many are above it.
+__device__ __forceinline__ void rank_candidates(Shared& sh, uint32_t n, uint32_t k) {
+  if (threadIdx.x < k && threadIdx.x >= n) sh.best[threadIdx.x] = 0ull;
+  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+    const uint64_t key = sh.cand[i];
+    uint32_t rank = 0u;
+    for (uint32_t j = 0u; j < n; ++j) rank += sh.cand[j] > key ? 1u : 0u;
+    if (rank < k) sh.best[rank] = key;
+  }
+  __syncthreads();
+}
+
+// k searches of blocks [b0, b1) for the largest key below the last.
+template <int DT>
+__device__ __noinline__ void search(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, uint32_t k) {
+  constexpr uint32_t E = kElem<DT>;
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   uint64_t below = ~0ull;
-  for (int32_t k = 0; k < top_k; ++k) {
+  for (uint32_t n = 0u; n < k; ++n) {
     uint64_t most = 0ull;
-    for (uint32_t i = tid; i < V; i += 256u) {
-      const uint64_t key = top_key(logit<DT>(x, row + i), i);
-      if (key < below && key > most) most = key;
-    }
-    __syncthreads();
-    best[tid] = most;
-    __syncthreads();
-    for (uint32_t d = 128u; d > 0u; d >>= 1) {
-      if (tid < d && best[tid + d] > best[tid]) best[tid] = best[tid + d];
-      __syncthreads();
-    }
-    below = best[0];
-    if (tid == 0u) {
-      const uint32_t i = ~(uint32_t)below;
-      float r = -INFINITY;
-      if (k < (int32_t)V) {
-        const float y = logit<DT>(x, row + i) * scale;
-        r = y == -INFINITY && ls == ls ? -INFINITY : y - ls;
+    for (uint32_t j = b0 + threadIdx.x; j < b1; j += kThreads) {
+      for (uint32_t e = 0u; e < E; ++e) {
+        const int64_t i = (int64_t)j * E + e - row.head;
+        if (i < 0 || i >= row.V) continue;
+        const uint64_t key = top_key(row.at((uint32_t)i), (uint32_t)i);
+        if (key < below && key > most) most = key;
       }
-      top_index[n * (size_t)top_k + k] = k < (int32_t)V ? (int32_t)i : -1;
-      top_logp[n * (size_t)top_k + k] = r;
     }
+    for (int d = 32; d > 0; d >>= 1) {
+      const uint64_t o = __shfl_xor((unsigned long long)most, d);
+      most = o > most ? o : most;
+    }
+    if (lane == 0u) sh.wave_key[wave] = most;
+    __syncthreads();
+    for (uint32_t w = 0u; w < kWaves; ++w) most = sh.wave_key[w] > most ? sh.wave_key[w] : most;
+    __syncthreads();
+    below = most;
+    if (threadIdx.x == 0u) sh.best[n] = most;
+  }
+  __syncthreads();
+}
+
+// best[have .. k): the first elements of blocks [b0, b1) equal to tau.
+template <int DT>
+__device__ __noinline__ void fill_ties(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, float tau,
+                                       uint32_t have, uint32_t k) {
+  if (threadIdx.x < 64u) {
+    const int64_t first = (int64_t)b0 * kElem<DT> - row.head, end = (int64_t)b1 * kElem<DT> - row.head;
+    const int64_t lo = first < 0 ? 0 : first, hi = end < row.V ? end : row.V;
+    for (int64_t i0 = lo; i0 < hi && have < k; i0 += 64) {
+      const int64_t i = i0 + threadIdx.x;
+      const float v = i < hi ? row.at((uint32_t)i) : 0.0f;
+      const bool eq = i < hi && v == tau;
+      const uint64_t all = __ballot(eq);
+      const uint32_t at = have + (uint32_t)__popcll(all & ((1ull << threadIdx.x) - 1ull));
+      if (eq && at < k) sh.best[at] = top_key(v, (uint32_t)i);
+      have += (uint32_t)__popcll(all);
+    }
+  }
+  __syncthreads();
+}
+
+// lse and entropy of joined statistics.  Nothing but -inf: -inf and 0; a NaN
+// or +inf logit: NaN.
+__device__ __forceinline__ void finish(Stats a, float scale, float& lse, float& entropy) {
+  if (a.r == INFINITY) a.s = NAN;  // inf - inf
+  const float ls = logf(a.s);
+  lse = a.s == 0.0f ? -INFINITY : __builtin_fmaf(a.r, scale, ls);
+  entropy = a.s == 0.0f ? 0.0f : ls - kLn2 * a.w / a.s;
+}
+
+template <int DT>
+__device__ __forceinline__ float log_prob(const Row<DT>& row, uint32_t i, float scale, float lse) {
+  const float y = row.at(i) * scale;
+  return y == -INFINITY && lse == lse ? -INFINITY : y - lse;
+}
+
+// One row's outputs: statistics a in every thread, the top keys in sh.best.
+template <int DT>
+__device__ __forceinline__ void write_row(const Args& a, Shared& sh, const Row<DT>& row, size_t n, Stats st) {
+  float lse, entropy;
+  finish(st, a.scale, lse, entropy);
+  if (threadIdx.x == 0u) {
+    if (a.lse) a.lse[n] = lse;
+    if (a.entropy) a.entropy[n] = entropy;
+  }
+  for (int32_t j = (int32_t)threadIdx.x; j < a.M; j += (int32_t)kThreads) {
+    const int32_t t = a.tokens[n * (size_t)a.M + j];
+    a.logp[n * (size_t)a.M + j] =
+        t >= 0 && (uint32_t)t < a.V ? log_prob<DT>(row, (uint32_t)t, a.scale, lse) : 0.0f;
+  }
+  if ((int32_t)threadIdx.x < a.top_k) {
+    const bool some = threadIdx.x < a.V;
+    const uint32_t i = ~(uint32_t)sh.best[threadIdx.x];
+    const size_t at = n * (size_t)a.top_k + threadIdx.x;
+    a.top_index[at] = some ? (int32_t)i : -1;
+    a.top_logp[at] = some ? log_prob<DT>(row, i, a.scale, lse) : -INFINITY;
   }
 }
 
 template <int DT>
-__device__ __forceinline__ void store_value(void* p, size_t i, float v) {
-  if (DT == kDtF32)
-    static_cast<float*>(p)[i] = v;
-  else
-    static_cast<__bf16*>(p)[i] = (__bf16)v;
+__global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
+  constexpr uint32_t E = kElem<DT>;
+  __shared__ Shared sh;
+  const uint32_t split = blockIdx.x, splits = gridDim.x, tid = threadIdx.x;
+  const size_t n = blockIdx.y;
+  const Row<DT> row(a.x, n * (size_t)a.stride, a.V);
+  const uint32_t per = (row.blocks + splits - 1u) / splits;
+  const uint32_t b0 = min(split * per, row.blocks), b1 = min(b0 + per, row.blocks);
+  const uint32_t k = (uint32_t)a.top_k;
+  const float c2 = a.scale * kLog2e;
+
+  if (tid == 0u) sh.count = 0u;
+  Stats st = {-INFINITY, 0.0f, 0.0f};
+  float mine = -INFINITY, tau = INFINITY;  // this thread's largest; nothing passes until the threshold is known
+  for (uint32_t s0 = b0; s0 < b1; s0 += kStepBlocks) {
+    float v[kUnroll][E];
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u) {
+      const uint32_t j = s0 + u * kThreads + tid;
+      if (j < b1) {
+        row.load(j, v[u]);
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) v[u][e] = -INFINITY;
+      }
+    }
+    float hi[kUnroll];
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u) {
+      float lo = v[u][0];
+      hi[u] = v[u][0];
+#pragma unroll
+      for (uint32_t e = 1; e < E; ++e) {
+        hi[u] = fmaxf(hi[u], v[u][e]);
+        lo = fminf(lo, v[u][e]);
+      }
+      if (__any((hi[u] - st.r) * c2 > kLazy || st.r == -INFINITY)) {
+        const float r = fmaxf(st.r, hi[u]), d = st.r == r ? 0.0f : (st.r - r) * c2, f = exp2_fast(d);
+        st.w = f == 0.0f ? 0.0f : (st.w + d * st.s) * f;
+        st.s *= f;
+        st.r = r;
+      }
+      const float ref = st.r == -INFINITY ? 0.0f : st.r;
+      if (__any(!(lo - ref > -1e30f))) {
+        // Masked logits (-inf, the type's lowest): e^t = 0, and t e^t is 0 too.
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) {
+          const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
+          st.s += p;
+          st.w = __builtin_fmaf(fmaxf(t, -1000.0f), p, st.w);
+        }
+      } else {
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e) {
+          const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
+          st.s += p;
+          st.w = __builtin_fmaf(t, p, st.w);
+        }
+      }
+      mine = fmaxf(mine, hi[u]);
+    }
+    if (k > 0u) {
+      if (s0 == b0) tau = threshold(sh, mine, k);
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u) {
+        if (hi[u] > tau) {
+          const uint32_t i0 = (s0 + u * kThreads + tid) * E - row.head;
+#pragma unroll
+          for (uint32_t e = 0; e < E; ++e)
+            if (v[u][e] > tau) push(sh, v[u][e], i0 + e);
+        }
+      }
+    }
+  }
+
+  // The workgroup's statistics, in a fixed order.
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) st = join(st, shuffle_xor(st, d), c2);
+  if ((tid & 63u) == 0u) sh.part[tid >> 6] = st;
+  __syncthreads();
+  st = join(join(sh.part[0], sh.part[1], c2), join(sh.part[2], sh.part[3], c2), c2);
+
+  if (k > 0u) {
+    uint32_t n_cand = sh.count;
+    const bool special = !(st.s == st.s) || st.r == INFINITY;
+    if (!special && n_cand > kCand) {
+      // Too many: again, above the k-th largest of the groups' maxima over all.
+      __syncthreads();
+      tau = threshold(sh, mine, k);
+      if (tid == 0u) sh.count = 0u;
+      __syncthreads();
+      for (uint32_t j = b0 + tid; j < b1; j += kThreads) {
+        float v[E];
+        row.load(j, v);
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e)
+          if (v[e] > tau) push(sh, v[e], j * E - row.head + e);
+      }
+      __syncthreads();
+      n_cand = sh.count;
+    }
+    if (special || n_cand > kCand) {
+      search<DT>(sh, row, b0, b1, k);
+    } else {
+      rank_candidates(sh, n_cand, k);
+      if (n_cand < k) fill_ties<DT>(sh, row, b0, b1, tau, n_cand, k);
+    }
+  }
+  if (splits == 1u) {
+    write_row<DT>(a, sh, row, n, st);
+    return;
+  }
+
+  // ---- the splits' results, written through; the last to arrive joins them ----
+  const size_t part = n * splits;
+  if (tid < k)
+    __hip_atomic_store(a.keys + (part + split) * k + tid, sh.best[tid], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (tid < 3u)
+    __hip_atomic_store(a.stats + (part + split) * 4u + tid, tid == 0u ? st.r : tid == 1u ? st.s : st.w,
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
+  __syncthreads();
+  if (tid == 0u) {
+    const uint32_t before = __hip_atomic_fetch_add(a.done + n, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sh.flag = before == splits - 1u;
+    if (sh.flag) __hip_atomic_store(a.done + n, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!sh.flag) return;
+  Stats all = {-INFINITY, 0.0f, 0.0f};
+  if ((tid & 63u) < splits) {
+    const float* from = a.stats + (part + (tid & 63u)) * 4u;
+    all.r = __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    all.s = __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    all.w = __hip_atomic_load(from + 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) all = join(all, shuffle_xor(all, d), c2);
+  if (k > 0u) {
+    // splits x k <= kCand keys (the host's choice of splits); those of splits
+    // with fewer than k elements are 0, below all.
+    for (uint32_t i = tid; i < splits * k; i += kThreads)
+      sh.cand[i] = __hip_atomic_load(a.keys + part * k + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    // Equal keys are only the zeros of short splits, and V >= 1 others rank first.
+    rank_candidates(sh, splits * k, k);
+  }
+  write_row<DT>(a, sh, row, n, all);
 }
 
+// ---------------------------------------------------------------------------
+// Gradient: dx_i = scale (hot_i - p_i (G + ge (log p_i + H))), one pass, 16
+// bytes a step.  The tokens' own terms are rare: a bitmap marks the blocks
+// that hold one, and only those look through the row's tokens.
+// ---------------------------------------------------------------------------
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 template <int DT>
-__global__ __launch_bounds__(256) void logprobs_backward_simple_kernel(
+__global__ __launch_bounds__(256) void logprobs_backward_kernel(
     const void* __restrict__ x, int64_t stride, uint32_t V, float scale, const int32_t* __restrict__ tokens, int32_t M,
     const float* __restrict__ lse, const float* __restrict__ entropy, const float* __restrict__ g_logp,
     const float* __restrict__ g_entropy, void* __restrict__ dx, int64_t dx_stride) {
-  const size_t n = blockIdx.x;
-  float g = 0.0f;
-  for (int32_t j = 0; j < M; ++j) {
-    const int32_t t = tokens[n * (size_t)M + j];
-    if (t >= 0 && (uint32_t)t < V) g += g_logp[n * (size_t)M + j];
+  constexpr uint32_t E = kElem<DT>;
+  __shared__ uint32_t marked[kStepBlocks / 32u];
+  __shared__ float sums[kWaves];
+  const size_t n = blockIdx.y;
+  const uint32_t tid = threadIdx.x;
+  const Row<DT> row(x, n * (size_t)stride, V);
+  const uint32_t b0 = blockIdx.x * kStepBlocks;
+  if (b0 >= row.blocks) return;
+  float v[kUnroll][E];
+#pragma unroll
+  for (uint32_t u = 0; u < kUnroll; ++u) {
+    const uint32_t j = b0 + u * kThreads + tid;
+    if (j < row.blocks) row.load(j, v[u]);
   }
-  const float ge = g_entropy ? g_entropy[n] : 0.0f, h = g_entropy ? entropy[n] : 0.0f, ls = lse[n];
-  for (uint32_t i = threadIdx.x; i < V; i += 256u) {
-    const float y = logit<DT>(x, n * (size_t)stride + i) * scale;
-    const float lp = y == -INFINITY && ls == ls ? -INFINITY : y - ls, p = expf(lp);
-    float d = p == 0.0f ? 0.0f : -p * (g + ge * (lp + h));
-    for (int32_t j = 0; j < M; ++j)
-      if (tokens[n * (size_t)M + j] == (int32_t)i) d += g_logp[n * (size_t)M + j];
-    store_value<DT>(dx, n * (size_t)dx_stride + i, d * scale);
+  if (tid < kStepBlocks / 32u) marked[tid] = 0u;
+  __syncthreads();
+  const int32_t* tok = tokens + n * (size_t)M;
+  const float* gl = g_logp + n * (size_t)M;
+  float g = 0.0f;
+  for (int32_t j = (int32_t)tid; j < M; j += (int32_t)kThreads) {
+    const int32_t t = tok[j];
+    if (t < 0 || (uint32_t)t >= V) continue;
+    g += gl[j];
+    const uint32_t blk = ((uint32_t)t + row.head) / E - b0;
+    if (blk < kStepBlocks) atomicOr(&marked[blk >> 5], 1u << (blk & 31u));
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) g += __shfl_xor(g, d);
+  if ((tid & 63u) == 0u) sums[tid >> 6] = g;
+  __syncthreads();
+  g = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+
+  const float ge = g_entropy ? g_entropy[n] : 0.0f, h = g_entropy ? entropy[n] : 0.0f;
+  // A row of -inf logits: every p is 0 (its lse of -inf would give NaN).
+  const float ls = lse[n] == -INFINITY ? INFINITY : lse[n];
+  const float A = -(g + ge * h), B = -ge;
+  uint8_t* out = static_cast<uint8_t*>(dx) + n * (size_t)dx_stride * (DT == kDtF32 ? 4u : 2u);
+#pragma unroll
+  for (uint32_t u = 0; u < kUnroll; ++u) {
+    const uint32_t blk = u * kThreads + tid, j = b0 + blk;
+    if (j >= row.blocks) continue;
+    const int64_t i0 = (int64_t)j * E - row.head;
+    float d[E];
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) {
+      const float lp = __builtin_fmaf(v[u][e], scale, -ls), p = exp2_fast(lp * kLog2e);
+      // p = 0 from lp = -inf must not meet an infinite factor.
+      d[e] = p * __builtin_fmaf(B, fmaxf(lp, -1000.0f), A);
+    }
+    if (marked[blk >> 5] & (1u << (blk & 31u))) {
+      for (int32_t q = 0; q < M; ++q) {
+        const int64_t e = (int64_t)tok[q] - i0;
+        if (tok[q] < 0 || (uint32_t)tok[q] >= V || e < 0 || e >= E) continue;
+#pragma unroll
+        for (uint32_t f = 0; f < E; ++f) d[f] += f == (uint32_t)e ? gl[q] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (uint32_t e = 0; e < E; ++e) d[e] *= scale;
+    if (i0 >= 0 && i0 + E <= V) {
+      u32x4_any w;
+      if constexpr (DT == kDtF32) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = f2u(d[k]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = bf16_pair(d[2 * k], d[2 * k + 1]);
+      }
+      // (The output's rows may be aligned otherwise than the input's.)
+      *reinterpret_cast<u32x4_any*>(out + i0 * (DT == kDtF32 ? 4 : 2)) = w;
+    } else {
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) {
+        if (i0 + e < 0 || i0 + e >= V) continue;
+        if constexpr (DT == kDtF32)
+          reinterpret_cast<float*>(out)[i0 + e] = d[e];
+        else
+          reinterpret_cast<__bf16*>(out)[i0 + e] = (__bf16)d[e];
+      }
+    }
   }
 }
 
+// Workgroups of a row: one where the rows alone fill the chip, else pieces of
+// at least a step (16 KB), as many as give about 512 workgroups, with all
+// their top keys within one workgroup's candidates.
+uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
+  int64_t s = (512 + N - 1) / N;
+  const int64_t most = (V + 4 * kStepBlocks - 1) / (4 * kStepBlocks);  // FP32 steps; a BF16 piece is half as long
+  if (s > most) s = most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  if (top_k > 0 && s > (int64_t)kCand / top_k) s = kCand / top_k;
+  return (uint32_t)(s < 1 ? 1 : s);
+}
+
+size_t round16(size_t n) { return (n + 15) / 16 * 16; }
+
 }  // namespace
 
-size_t logprobs_workspace(int64_t, int64_t, int32_t) { return 0; }
+size_t logprobs_workspace(int64_t N, int64_t V, int32_t top_k) {
+  if (N == 0) return 0;
+  const size_t s = splits_of(N, V, top_k);
+  return s == 1 ? 0 : round16((size_t)N * 4) + (size_t)N * s * (16 + 8 * (size_t)top_k);
+}
 
 hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
                            const int32_t* tokens, int32_t M, float* logp, float* entropy, float* lse, int32_t top_k,
-                           float* top_logp, int32_t* top_index, void*, hipStream_t stream) {
-  if (dtype == kDtF32)
-    logprobs_simple_kernel<kDtF32><<<(uint32_t)N, 256, 0, stream>>>(x, stride, (uint32_t)V, scale, tokens, M, logp,
-                                                                    entropy, lse, top_k, top_logp, top_index);
-  else
-    logprobs_simple_kernel<kDtBF16><<<(uint32_t)N, 256, 0, stream>>>(x, stride, (uint32_t)V, scale, tokens, M, logp,
-                                                                     entropy, lse, top_k, top_logp, top_index);
-  return hipGetLastError();
+                           float* top_logp, int32_t* top_index, void* workspace, hipStream_t stream) {
+  const uint32_t s = splits_of(N, V, top_k);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Args a{x, stride, (uint32_t)V, scale, tokens, M, logp, entropy, lse, top_k, top_logp, top_index, nullptr, nullptr,
+         nullptr};
+  if (s > 1) {
+    a.done = reinterpret_cast<uint32_t*>(ws);
+    a.stats = reinterpret_cast<float*>(ws + round16((size_t)N * 4));
+    a.keys = reinterpret_cast<uint64_t*>(ws + round16((size_t)N * 4) + (size_t)N * s * 16);
+  }
+  // Rows in the grid's y, at most 65535 a launch.
+  for (int64_t n0 = 0; n0 < N; n0 += 65535) {
+    const int64_t rows = N - n0 < 65535 ? N - n0 : 65535;
+    Args b = a;
+    b.x = static_cast<const uint8_t*>(x) + (size_t)n0 * (size_t)stride * (dtype == kDtF32 ? 4 : 2);
+    b.tokens = tokens + n0 * M;
+    b.logp = logp + n0 * M;
+    b.entropy = entropy ? entropy + n0 : nullptr;
+    b.lse = lse ? lse + n0 : nullptr;
+    b.top_logp = top_logp + n0 * top_k;
+    b.top_index = top_index + n0 * top_k;
+    const dim3 grid(s, (uint32_t)rows);
+    if (dtype == kDtF32)
+      logprobs_kernel<kDtF32><<<grid, kThreads, 0, stream>>>(b);
+    else
+      logprobs_kernel<kDtBF16><<<grid, kThreads, 0, stream>>>(b);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
                                     const int32_t* tokens, int32_t M, const float* lse, const float* entropy,
                                     const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride,
                                     hipStream_t stream) {
-  if (dtype == kDtF32)
-    logprobs_backward_simple_kernel<kDtF32><<<(uint32_t)N, 256, 0, stream>>>(
-        x, stride, (uint32_t)V, scale, tokens, M, lse, entropy, g_logp, g_entropy, dx, dx_stride);
-  else
-    logprobs_backward_simple_kernel<kDtBF16><<<(uint32_t)N, 256, 0, stream>>>(
-        x, stride, (uint32_t)V, scale, tokens, M, lse, entropy, g_logp, g_entropy, dx, dx_stride);
-  return hipGetLastError();
+  const size_t size = dtype == kDtF32 ? 4 : 2;
+  const int64_t step = kStepBlocks * (16 / (int64_t)size);
+  // One more step than the row's length where its start is not aligned.
+  const uint32_t steps = (uint32_t)((V + (int64_t)(16 / size) - 1 + step - 1) / step);
+  for (int64_t n0 = 0; n0 < N; n0 += 65535) {
+    const int64_t rows = N - n0 < 65535 ? N - n0 : 65535;
+    const void* xr = static_cast<const uint8_t*>(x) + (size_t)n0 * (size_t)stride * size;
+    void* dr = static_cast<uint8_t*>(dx) + (size_t)n0 * (size_t)dx_stride * size;
+    const dim3 grid(steps, (uint32_t)rows);
+    const float* ent = entropy ? entropy + n0 : nullptr;
+    const float* ge = g_entropy ? g_entropy + n0 : nullptr;
+    if (dtype == kDtF32)
+      logprobs_backward_kernel<kDtF32><<<grid, kThreads, 0, stream>>>(
+          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride);
+    else
+      logprobs_backward_kernel<kDtBF16><<<grid, kThreads, 0, stream>>>(
+          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp4
