@@ -561,7 +561,21 @@ def gemm_nvfp4_act(x, w, tensor_scale=None, ts_out=None, out_dtype=None, out=Non
 
 
 # ---- decode-step operators: cache, attention, eviction, log probabilities ------
-def _need_rows(t, name, dtypes, ndim, device=None, shape=None):
+# These calls take microseconds on the GPU, so their wrappers are kept short:
+# one test for a well-formed tensor, with _need naming the fault of any other.
+def _is(t, dtype, ndim, device):
+    torch = _torch()
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.device == device
+            and t.is_contiguous())
+
+
+def _want(t, name, dtype, ndim, device, numel=None):
+    """_need for one dtype and dimension count, quickly."""
+    if not _is(t, dtype, ndim, device) or (numel is not None and t.numel() < numel):
+        _need(t, name, (dtype,), numel, device, ndim)
+
+
+def _want_rows(t, name, dtypes, ndim, device=None, shape=None):
     """Check a tensor whose dimensions after the first are dense and whose
     first may have any stride (columns of a wider matrix).  Returns that
     stride."""
@@ -570,46 +584,46 @@ def _need_rows(t, name, dtypes, ndim, device=None, shape=None):
         raise TypeError("%s must be a torch.Tensor, got %s" % (name, type(t).__name__))
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
-    if t.dim() != ndim:
-        raise ValueError("%s must have %d dimensions, got shape %s" % (name, ndim, tuple(t.shape)))
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    width, strides = 1, t.stride()
+    sizes, strides = t.shape, t.stride()
+    if len(sizes) != ndim:
+        raise ValueError("%s must have %d dimensions, got shape %s" % (name, ndim, tuple(sizes)))
+    if shape is not None and sizes != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(sizes)))
+    width = 1
     for i in range(ndim - 1, 0, -1):
-        if t.shape[i] != 1 and strides[i] != width:
+        if strides[i] != width and sizes[i] != 1:
             raise ValueError("%s must be dense but for its first dimension, got strides %s" % (name, strides))
-        width *= t.shape[i]
+        width *= sizes[i]
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor, got device %s" % (name, t.device))
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, the call's operands on %s" % (name, t.device, device))
-    if t.shape[0] <= 1:
+    if sizes[0] <= 1:
         return width
     if strides[0] < width:
         raise ValueError("%s has overlapping rows (strides %s)" % (name, strides))
     return strides[0]
 
 
-class _Alloc:
-    """Allocates a call's outputs and workspace for the stream it runs on: from
-    that stream's memory, so that what the current stream still does with
-    memory freed there cannot meet the call's writes, and marked as used on
-    the current stream too, where the caller goes on with them."""
+def _run_on(stream, device):
+    """The raw handle of the stream a call runs on: the given one, or the
+    device's current one."""
+    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
 
-    def __init__(self, stream, device):
-        torch = _torch()
-        self.device = device
-        self.stream = stream if stream is not None and stream != torch.cuda.current_stream() else None
 
-    def __call__(self, make, *args, **kw):
-        if self.stream is None:
-            return make(*args, device=self.device, **kw)
-        torch = _torch()
-        with torch.cuda.stream(self.stream):
-            t = make(*args, device=self.device, **kw)
-        if t is not None:
-            t.record_stream(torch.cuda.current_stream())
-        return t
+def _alloc(stream, make, *args, **kw):
+    """make(*args, **kw), a call's output or workspace, for the stream it runs
+    on: from that stream's memory, so that what the current stream still does
+    with memory freed there cannot meet the call's writes, and marked as used
+    on the current stream too, where the caller goes on with it."""
+    if stream is None:
+        return make(*args, **kw)
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if t is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
 
 
 class KVCache:
@@ -677,26 +691,30 @@ def kv_append(cache, k, v, table, seq, pos, stream=None):
     fp4_kv_append in include/fp4.h."""
     torch = _torch()
     dev = _need_cache(cache)
-    ks = _need_rows(k, "k", (torch.float32, torch.bfloat16), 3, dev)
-    shape = (k.shape[0], cache.kv_heads, cache.head_dim)
-    if tuple(k.shape) != shape:
-        raise ValueError("k must have shape %s, got %s" % (shape, tuple(k.shape)))
-    vs = _need_rows(v, "v", (k.dtype,), 3, dev, shape)
-    _need(table, "table", (torch.int32,), None, dev, ndim=2)
-    _need(seq, "seq", (torch.int32,), shape[0], dev, ndim=1)
-    _need(pos, "pos", (torch.int32,), shape[0], dev, ndim=1)
-    rc = fp4_kv_append(cache.struct, _ptr(k), _ptr(v), _dtype_code(k), ks, vs, _ptr(table), table.shape[1],
-                       table.shape[0], _ptr(seq), _ptr(pos), shape[0], _stream(stream))
-    _check(rc, "fp4_kv_append")
+    ks = _want_rows(k, "k", (torch.float32, torch.bfloat16), 3, dev)
+    shape = k.shape
+    n = shape[0]
+    if shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
+        raise ValueError("k must have shape %s, got %s" % ((n, cache.kv_heads, cache.head_dim), tuple(shape)))
+    vs = _want_rows(v, "v", (k.dtype,), 3, dev, shape)
+    i32 = torch.int32
+    _want(table, "table", i32, 2, dev)
+    _want(seq, "seq", i32, 1, dev, n)
+    _want(pos, "pos", i32, 1, dev, n)
+    seqs, width = table.shape
+    rc = lib().fp4_kv_append(cache.struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs, table.data_ptr(), width,
+                             seqs, seq.data_ptr(), pos.data_ptr(), n, _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_kv_append")
     return cache
 
 
-def attention_workspace(cache, batch, q_heads, max_len, weights=False, device=None):
+def attention_workspace(cache, batch, q_heads, max_len, weights=False):
     """A zero-filled workspace tensor for decode_attention (or None)."""
     torch = _torch()
     dev = _need_cache(cache)
     n = fp4_attn_decode_workspace(cache.struct, batch, q_heads, max_len, 1 if weights else 0)
-    return torch.zeros(n, dtype=torch.uint8, device=dev if device is None else device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
 
 
 def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, out=None, out_dtype=None, lse=None,
@@ -709,31 +727,32 @@ def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, 
     the table holds).  scale: default 1 / sqrt(head_dim).  lse: optional
     float32 batch x q_heads output.  weights_out: optional float32 batch x
     kv_heads x (>= max_len) output of weights (or 0) plus every token's
-    attention weight; it may be weights itself.  Returns out (dtype of q, or
-    out_dtype)."""
+    attention weight; it may be weights itself.  ws: attention_workspace's
+    tensor, kept by the caller from call to call (one is allocated here if
+    None).  Returns out (dtype of q, or out_dtype)."""
     torch = _torch()
     dev = _need_cache(cache)
-    floats = (torch.float32, torch.bfloat16)
-    qs = _need_rows(q, "q", floats, 3, dev)
-    B, heads, dim = q.shape
+    qs = _want_rows(q, "q", (torch.float32, torch.bfloat16), 3, dev)
+    shape = q.shape
+    B, heads, dim = shape
     if dim != cache.head_dim:
         raise ValueError("q has head_dim %d, the cache %d" % (dim, cache.head_dim))
-    _need(table, "table", (torch.int32,), None, dev, ndim=2)
-    _need(lens, "lens", (torch.int32,), B, dev, ndim=1)
-    if table.shape[0] != B:
-        raise ValueError("table has %d rows, q %d" % (table.shape[0], B))
+    _want(table, "table", torch.int32, 2, dev)
+    _want(lens, "lens", torch.int32, 1, dev, B)
+    rows, width = table.shape
+    if rows != B:
+        raise ValueError("table has %d rows, q %d" % (rows, B))
     if max_len is None:
-        max_len = table.shape[1] * cache.page_size
-    alloc = _Alloc(stream, dev)
+        max_len = width * cache.page_size
     if out is None:
-        out = alloc(torch.empty, (B, heads, dim), dtype=q.dtype if out_dtype is None else out_dtype)
+        out = _alloc(stream, torch.empty, shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
     else:
-        _need_out(out, "out", (B, heads, dim), floats, dev)
+        _need_out(out, "out", shape, (torch.float32, torch.bfloat16), dev)
     if lse is not None:
         _need_out(lse, "lse", (B, heads), (torch.float32,), dev)
     stride = 0
     if weights_out is not None:
-        _need(weights_out, "weights_out", (torch.float32,), None, dev, ndim=3)
+        _want(weights_out, "weights_out", torch.float32, 3, dev)
         stride = weights_out.shape[2]
         _need_out(weights_out, "weights_out", (B, cache.kv_heads, stride), (torch.float32,), dev)
         if weights is not None:
@@ -741,23 +760,24 @@ def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, 
     elif weights is not None:
         raise ValueError("weights needs weights_out")
     if ws is None:
-        ws = alloc(attention_workspace, cache, B, heads, max_len, weights_out is not None)
+        ws = _alloc(stream, attention_workspace, cache, B, heads, max_len, weights_out is not None)
     else:
-        _need(ws, "ws", (torch.uint8,), None, dev)
-    rc = fp4_attn_decode(cache.struct, _ptr(q), _dtype_code(q), qs, _ptr(table), table.shape[1], _ptr(lens), B, heads,
-                         max_len, window, dim ** -0.5 if scale is None else scale, _ptr(out), _dtype_code(out),
-                         _ptr(lse), _ptr(weights), _ptr(weights_out), stride, _ptr(ws),
-                         0 if ws is None else ws.numel(), _stream(stream))
-    _check(rc, "fp4_attn_decode")
+        _want(ws, "ws", torch.uint8, 1, dev)
+    rc = lib().fp4_attn_decode(cache.struct, q.data_ptr(), _dtype_code(q), qs, table.data_ptr(), width,
+                               lens.data_ptr(), B, heads, max_len, window, dim ** -0.5 if scale is None else scale,
+                               out.data_ptr(), _dtype_code(out), _ptr(lse), _ptr(weights), _ptr(weights_out), stride,
+                               _ptr(ws), 0 if ws is None else ws.numel(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_attn_decode")
     return out
 
 
-def evict_workspace(cache, batch, max_len, budget, device=None):
+def evict_workspace(cache, batch, max_len, budget):
     """A zero-filled workspace tensor for kv_evict (or None)."""
     torch = _torch()
     dev = _need_cache(cache)
     n = fp4_kv_evict_workspace(cache.struct, batch, max_len, budget)
-    return torch.zeros(n, dtype=torch.uint8, device=dev if device is None else device) if n else None
+    return torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
 
 
 def kv_evict(cache, table, lens, weights, budget, recent, out_table, out_cache=None, ws=None, stream=None):
@@ -767,41 +787,43 @@ def kv_evict(cache, table, lens, weights, budget, recent, out_table, out_cache=N
 
     weights: float32 batch x kv_heads x (>= what the table holds).  The kept
     tokens move, in order, to out_table's pages (of out_cache; default the
-    same pool), which must not be pages that table reads.  Returns
-    (lens int32 batch, weights float32 batch x kv_heads x what out_table
-    holds, kept int32 batch x kv_heads x budget: old token numbers, then -1)."""
+    same pool), which must not be pages that table reads.  ws:
+    evict_workspace's tensor (one is allocated here if None).  Returns (lens
+    int32 batch, weights float32 batch x kv_heads x what out_table holds, kept
+    int32 batch x kv_heads x budget: old token numbers, then -1)."""
     torch = _torch()
     dev = _need_cache(cache)
-    out_cache = cache if out_cache is None else out_cache
-    _need_cache(out_cache, "out_cache")
-    if out_cache.device != dev:
+    if out_cache is None:
+        out_cache = cache
+    elif _need_cache(out_cache, "out_cache") != dev:
         raise ValueError("out_cache is on %s, the call's operands on %s" % (out_cache.device, dev))
-    _need(table, "table", (torch.int32,), None, dev, ndim=2)
-    B = table.shape[0]
-    _need(lens, "lens", (torch.int32,), B, dev, ndim=1)
-    _need(out_table, "out_table", (torch.int32,), None, dev, ndim=2)
+    _want(table, "table", torch.int32, 2, dev)
+    B, width = table.shape
+    _want(lens, "lens", torch.int32, 1, dev, B)
+    _want(out_table, "out_table", torch.int32, 2, dev)
     if out_table.shape[0] != B:
         raise ValueError("out_table has %d rows, table %d" % (out_table.shape[0], B))
     if budget < 0:
         raise ValueError("budget is negative")
-    cap = table.shape[1] * cache.page_size
-    _need(weights, "weights", (torch.float32,), None, dev, ndim=3)
-    if tuple(weights.shape[:2]) != (B, cache.kv_heads) or weights.shape[2] < cap:
-        raise ValueError("weights must have shape (%d, %d, >= %d), got %s"
-                         % (B, cache.kv_heads, cap, tuple(weights.shape)))
-    room = max(out_table.shape[1] * cache.page_size, budget)
-    alloc = _Alloc(stream, dev)
-    out_lens = alloc(torch.empty, B, dtype=torch.int32)
-    out_weights = alloc(torch.empty, (B, cache.kv_heads, room), dtype=torch.float32)
-    kept = alloc(torch.empty, (B, cache.kv_heads, budget), dtype=torch.int32)
+    cap, heads = width * cache.page_size, cache.kv_heads
+    _want(weights, "weights", torch.float32, 3, dev)
+    if weights.shape[0] != B or weights.shape[1] != heads or weights.shape[2] < cap:
+        raise ValueError("weights must have shape (%d, %d, >= %d), got %s" % (B, heads, cap, tuple(weights.shape)))
+    out_width = out_table.shape[1]
+    room = max(out_width * cache.page_size, budget)
+    out_lens = _alloc(stream, torch.empty, B, dtype=torch.int32, device=dev)
+    out_weights = _alloc(stream, torch.empty, (B, heads, room), dtype=torch.float32, device=dev)
+    kept = _alloc(stream, torch.empty, (B, heads, budget), dtype=torch.int32, device=dev)
     if ws is None:
-        ws = alloc(evict_workspace, cache, B, cap, budget)
+        ws = _alloc(stream, evict_workspace, cache, B, cap, budget)
     else:
-        _need(ws, "ws", (torch.uint8,), None, dev)
-    rc = fp4_kv_evict(cache.struct, _ptr(table), table.shape[1], _ptr(lens), _ptr(weights), weights.shape[2],
-                      out_cache.struct, _ptr(out_table), out_table.shape[1], _ptr(out_lens), _ptr(out_weights), room,
-                      _ptr(kept), B, cap, budget, recent, _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
-    _check(rc, "fp4_kv_evict")
+        _want(ws, "ws", torch.uint8, 1, dev)
+    rc = lib().fp4_kv_evict(cache.struct, table.data_ptr(), width, lens.data_ptr(), weights.data_ptr(),
+                            weights.shape[2], out_cache.struct, out_table.data_ptr(), out_width, out_lens.data_ptr(),
+                            out_weights.data_ptr(), room, kept.data_ptr(), B, cap, budget, recent, _ptr(ws),
+                            0 if ws is None else ws.numel(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_kv_evict")
     return out_lens, out_weights, kept
 
 
@@ -815,36 +837,42 @@ class LogProbs:
 
 def logprobs_workspace(n, vocab, top_k=0, device="cuda"):
     """A zero-filled workspace tensor for logprobs (or None)."""
+    torch = _torch()
     b = fp4_logprobs_workspace(n, vocab, top_k)
-    return _torch().zeros(b, dtype=_torch().uint8, device=device) if b else None
+    return torch.zeros(b, dtype=torch.uint8, device=device) if b else None
 
 
 def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
     """Log probabilities of the given tokens (int32 N x M; outside [0, V):
     padding, 0) under softmax(scale * x), x: N x V float32/bfloat16 logits
     (any row stride), with the entropy, the log-sum-exp and the top_k <= 32
-    largest alternatives; see fp4_logprobs in include/fp4.h."""
+    largest alternatives; see fp4_logprobs in include/fp4.h.  ws:
+    logprobs_workspace's tensor (one is allocated here if None)."""
     torch = _torch()
-    xs = _need_rows(x, "x", (torch.float32, torch.bfloat16), 2)
-    N, V = x.shape
+    xs = _want_rows(x, "x", (torch.float32, torch.bfloat16), 2)
     dev = x.device
-    _need(tokens, "tokens", (torch.int32,), None, dev, ndim=2)
-    if tokens.shape[0] != N:
-        raise ValueError("tokens has %d rows, x %d" % (tokens.shape[0], N))
-    M = tokens.shape[1]
-    alloc = _Alloc(stream, dev)
-    logp = alloc(torch.empty, (N, M), dtype=torch.float32)
-    stats = alloc(torch.empty, (2, N), dtype=torch.float32)
-    top = alloc(torch.empty, (N, top_k), dtype=torch.float32) if top_k > 0 else None
-    index = alloc(torch.empty, (N, top_k), dtype=torch.int32) if top_k > 0 else None
+    N, V = x.shape
+    _want(tokens, "tokens", torch.int32, 2, dev)
+    rows, M = tokens.shape
+    if rows != N:
+        raise ValueError("tokens has %d rows, x %d" % (rows, N))
+    f32 = torch.float32
+    logp = _alloc(stream, torch.empty, (N, M), dtype=f32, device=dev)
+    entropy = _alloc(stream, torch.empty, N, dtype=f32, device=dev)
+    lse = _alloc(stream, torch.empty, N, dtype=f32, device=dev)
+    top = index = None
+    if top_k > 0:
+        top = _alloc(stream, torch.empty, (N, top_k), dtype=f32, device=dev)
+        index = _alloc(stream, torch.empty, (N, top_k), dtype=torch.int32, device=dev)
     if ws is None:
-        ws = alloc(logprobs_workspace, N, V, top_k)
+        ws = _alloc(stream, logprobs_workspace, N, V, top_k, dev)
     else:
-        _need(ws, "ws", (torch.uint8,), None, dev)
-    entropy, lse = stats[0], stats[1]
-    rc = fp4_logprobs(_ptr(x), _dtype_code(x), xs, N, V, scale, _ptr(tokens), M, _ptr(logp), _ptr(entropy), _ptr(lse),
-                      top_k, _ptr(top), _ptr(index), _ptr(ws), 0 if ws is None else ws.numel(), _stream(stream))
-    _check(rc, "fp4_logprobs")
+        _want(ws, "ws", torch.uint8, 1, dev)
+    rc = lib().fp4_logprobs(x.data_ptr(), _dtype_code(x), xs, N, V, scale, tokens.data_ptr(), M, logp.data_ptr(),
+                            entropy.data_ptr(), lse.data_ptr(), top_k, _ptr(top), _ptr(index), _ptr(ws),
+                            0 if ws is None else ws.numel(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_logprobs")
     return LogProbs(logp, entropy, lse, top, index)
 
 
@@ -854,24 +882,31 @@ def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scal
     entropy as logprobs returned them; see fp4_logprobs_backward in
     include/fp4.h.  Returns dx of x's dtype."""
     torch = _torch()
-    xs = _need_rows(x, "x", (torch.float32, torch.bfloat16), 2)
-    N, V = x.shape
+    xs = _want_rows(x, "x", (torch.float32, torch.bfloat16), 2)
     dev = x.device
-    _need(tokens, "tokens", (torch.int32,), None, dev, ndim=2)
-    if tokens.shape[0] != N:
-        raise ValueError("tokens has %d rows, x %d" % (tokens.shape[0], N))
-    M = tokens.shape[1]
-    _need_out(g_logp, "g_logp", (N, M), (torch.float32,), dev)
-    _need(lse, "lse", (torch.float32,), N, dev, ndim=1)
+    N, V = x.shape
+    _want(tokens, "tokens", torch.int32, 2, dev)
+    rows, M = tokens.shape
+    if rows != N:
+        raise ValueError("tokens has %d rows, x %d" % (rows, N))
+    f32 = torch.float32
+    _want(g_logp, "g_logp", f32, 2, dev)
+    if g_logp.shape != tokens.shape:
+        raise ValueError("g_logp must have shape %s, got %s" % (tuple(tokens.shape), tuple(g_logp.shape)))
+    _want(lse, "lse", f32, 1, dev, N)
     if g_entropy is not None:
         if entropy is None:
             raise ValueError("g_entropy needs entropy")
-        _need(g_entropy, "g_entropy", (torch.float32,), N, dev, ndim=1)
-        _need(entropy, "entropy", (torch.float32,), N, dev, ndim=1)
+        _want(g_entropy, "g_entropy", f32, 1, dev, N)
+        _want(entropy, "entropy", f32, 1, dev, N)
     if out is None:
-        out = _Alloc(stream, dev)(torch.empty, (N, V), dtype=x.dtype)
-    os_ = _need_rows(out, "out", (x.dtype,), 2, dev, (N, V))
-    rc = fp4_logprobs_backward(_ptr(x), _dtype_code(x), xs, N, V, scale, _ptr(tokens), M, _ptr(lse), _ptr(entropy),
-                               _ptr(g_logp), _ptr(g_entropy), _ptr(out), os_, _stream(stream))
-    _check(rc, "fp4_logprobs_backward")
+        out = _alloc(stream, torch.empty, (N, V), dtype=x.dtype, device=dev)
+        os_ = V
+    else:
+        os_ = _want_rows(out, "out", (x.dtype,), 2, dev, x.shape)
+    rc = lib().fp4_logprobs_backward(x.data_ptr(), _dtype_code(x), xs, N, V, scale, tokens.data_ptr(), M,
+                                     lse.data_ptr(), _ptr(entropy), g_logp.data_ptr(), _ptr(g_entropy),
+                                     out.data_ptr(), os_, _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_logprobs_backward")
     return out

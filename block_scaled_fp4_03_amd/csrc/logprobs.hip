@@ -60,28 +60,38 @@ struct Row {
     head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / size;
     blocks = (V + head + kElem<DT> - 1u) / kElem<DT>;
   }
-  // Elements of block j; `outside` for those not in the row.
-  __device__ __forceinline__ void load(uint32_t j, float (&v)[kElem<DT>]) const {
-    constexpr uint32_t E = kElem<DT>;
-    const int64_t i0 = (int64_t)j * E - head;
-    if (i0 >= 0 && i0 + E <= V) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p + i0 * (DT == kDtF32 ? 4 : 2));
-      if constexpr (DT == kDtF32) {
+  // Whether blocks [j, j + n) lie wholly inside the row.
+  __device__ __forceinline__ bool inside(uint32_t j, uint32_t n) const {
+    return (j > 0u || head == 0u) && (uint64_t)(j + n) * kElem<DT> <= (uint64_t)V + head;
+  }
+  // Block j, which does, as it lies in memory; and as values.
+  __device__ __forceinline__ u32x4 raw(uint32_t j) const {
+    return *reinterpret_cast<const u32x4*>(p + ((int64_t)j * kElem<DT> - head) * (DT == kDtF32 ? 4 : 2));
+  }
+  static __device__ __forceinline__ void values(u32x4 w, float (&v)[kElem<DT>]) {
+    if constexpr (DT == kDtF32) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = u2f(w[k]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          v[2 * k] = u2f(w[k] << 16);
-          v[2 * k + 1] = u2f(w[k] & 0xFFFF0000u);
-        }
-      }
+      for (int k = 0; k < 4; ++k) v[k] = u2f(w[k]);
     } else {
 #pragma unroll
-      for (uint32_t k = 0; k < E; ++k) {
-        const int64_t i = i0 + k;
-        v[k] = i >= 0 && i < V ? logit<DT>(p, (size_t)i) : -INFINITY;
+      for (int k = 0; k < 4; ++k) {
+        v[2 * k] = u2f(w[k] << 16);
+        v[2 * k + 1] = u2f(w[k] & 0xFFFF0000u);
       }
+    }
+  }
+  // Elements of any block j; -inf for those outside the row.
+  __device__ __forceinline__ void load(uint32_t j, float (&v)[kElem<DT>]) const {
+    constexpr uint32_t E = kElem<DT>;
+    if (inside(j, 1u)) {
+      values(raw(j), v);
+      return;
+    }
+    const int64_t i0 = (int64_t)j * E - head;
+#pragma unroll
+    for (uint32_t k = 0; k < E; ++k) {
+      const int64_t i = i0 + k;
+      v[k] = i >= 0 && i < V ? logit<DT>(p, (size_t)i) : -INFINITY;
     }
   }
   __device__ __forceinline__ float at(uint32_t i) const { return logit<DT>(p, i); }
@@ -107,8 +117,11 @@ __device__ __forceinline__ Stats join(Stats a, Stats b, float c2) {
   return Stats{r, a.s * fa + b.s * fb,
                (fa == 0.0f ? 0.0f : (a.w + da * a.s) * fa) + (fb == 0.0f ? 0.0f : (b.w + db * b.s) * fb)};
 }
-__device__ __forceinline__ Stats shuffle_xor(Stats a, int d) {
-  return Stats{__shfl_xor(a.r, d), __shfl_xor(a.s, d), __shfl_xor(a.w, d)};
+// The wavefront's statistics joined, in every lane.
+__device__ __forceinline__ Stats wave_join(Stats a, float c2) {
+  const float r = wave_fmax(a.r);
+  const float d = a.r == r ? 0.0f : (a.r - r) * c2, f = exp2_fast(d);
+  return Stats{r, wave_fsum(a.s * f), wave_fsum(f == 0.0f ? 0.0f : (a.w + d * a.s) * f)};
 }
 
 struct Args {
@@ -130,11 +143,14 @@ struct Args {
 };
 
 struct Shared {
-  uint64_t cand[kCand];
+  uint64_t cand[kCand];  // candidates, in no order
+  uint64_t few[kCand];   // those that can still be among the k largest
   uint64_t best[kMaxTop];
+  uint64_t group_key[kGroups];
   float group[kGroups];
-  float tau[2];
-  uint32_t count, flag;
+  float tau;
+  uint64_t tau_key;
+  uint32_t count, few_count, flag;
   Stats part[kWaves];
   uint64_t wave_key[kWaves];
 };
@@ -155,10 +171,10 @@ __device__ __forceinline__ float threshold(Shared& sh, float mine, uint32_t k) {
       const float u = sh.group[i];
       rank += (u > v || (u == v && i < lane)) ? 1u : 0u;
     }
-    if (rank == k - 1u) sh.tau[0] = v;
+    if (rank == k - 1u) sh.tau = v;
   }
   __syncthreads();
-  return sh.tau[0];
+  return sh.tau;
 }
 
 __device__ __forceinline__ void push(Shared& sh, float v, uint32_t i) {
@@ -166,22 +182,78 @@ __device__ __forceinline__ void push(Shared& sh, float v, uint32_t i) {
   if (at < kCand) sh.cand[at] = top_key(v, i);
 }
 
-// The largest k of cand[0 .. n) into best, in order (fewer: the rest 0), by
-// counting for each how many are above it.
-__device__ __forceinline__ void rank_candidates(Shared& sh, uint32_t n, uint32_t k) {
-  if (threadIdx.x < k && threadIdx.x >= n) sh.best[threadIdx.x] = 0ull;
+// The larger of a lane's key and its neighbour's (lane ^ 1, lane ^ 2), by DPP.
+template <int CTRL>
+__device__ __forceinline__ uint64_t max_key_dpp(uint64_t a) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)a, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(a >> 32), CTRL, 0xF, 0xF, false);
+  const uint64_t b = ((uint64_t)hi << 32) | lo;
+  return a > b ? a : b;
+}
+
+// The value a key stands for (-0 as +0).
+__device__ __forceinline__ float key_value(uint64_t key) {
+  const uint32_t u = (uint32_t)(key >> 32);
+  return u == 0xFFFFFFFFu ? NAN : u2f((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
+}
+
+// Ranks keys[0 .. n) into best by counting for each how many are above it.
+__device__ __forceinline__ void rank_keys(Shared& sh, const uint64_t* keys, uint32_t n, uint32_t k) {
   for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t key = sh.cand[i];
+    const uint64_t v = keys[i];
     uint32_t rank = 0u;
-    for (uint32_t j = 0u; j < n; ++j) rank += sh.cand[j] > key ? 1u : 0u;
-    if (rank < k) sh.best[rank] = key;
+#pragma unroll 8
+    for (uint32_t j = 0u; j < n; ++j) rank += keys[j] > v ? 1u : 0u;
+    if (rank < k) sh.best[rank] = v;
   }
   __syncthreads();
 }
 
+// The largest k of cand[0 .. n) into best, in order (fewer: the rest 0).
+// Many: the k-th largest of 64 groups' maxima bounds the k-th largest from
+// below first, which leaves little more than k to rank.
+__device__ __forceinline__ void rank_candidates(Shared& sh, uint32_t n, uint32_t k) {
+  const uint32_t tid = threadIdx.x;
+  if (n <= 64u) {
+    if (tid < k) sh.best[tid] = 0ull;
+    __syncthreads();
+    rank_keys(sh, sh.cand, n, k);
+    return;
+  }
+  uint64_t key[kCand / kThreads], mine = 0ull;
+#pragma unroll
+  for (uint32_t i = 0; i < kCand / kThreads; ++i) {
+    key[i] = i * kThreads + tid < n ? sh.cand[i * kThreads + tid] : 0ull;
+    mine = key[i] > mine ? key[i] : mine;
+  }
+  mine = max_key_dpp<0xB1>(mine);
+  mine = max_key_dpp<0x4E>(mine);
+  if ((tid & 3u) == 0u) sh.group_key[tid >> 2] = mine;
+  if (tid == 0u) sh.few_count = 0u;
+  if (tid < k) sh.best[tid] = 0ull;
+  __syncthreads();
+  if (tid < 64u) {
+    const uint64_t v = sh.group_key[tid];
+    uint32_t rank = 0u;
+#pragma unroll 16
+    for (uint32_t i = 0u; i < kGroups; ++i) {
+      const uint64_t u = sh.group_key[i];
+      rank += (u > v || (u == v && i < tid)) ? 1u : 0u;
+    }
+    if (rank == k - 1u) sh.tau_key = v;
+  }
+  __syncthreads();
+  const uint64_t tau = sh.tau_key;
+#pragma unroll
+  for (uint32_t i = 0; i < kCand / kThreads; ++i)
+    if (key[i] != 0ull && key[i] >= tau) sh.few[atomicAdd(&sh.few_count, 1u)] = key[i];
+  __syncthreads();
+  rank_keys(sh, sh.few, sh.few_count, k);
+}
+
 // k searches of blocks [b0, b1) for the largest key below the last.
 template <int DT>
-__device__ __noinline__ void search(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, uint32_t k) {
+__device__ __forceinline__ void search(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, uint32_t k) {
   constexpr uint32_t E = kElem<DT>;
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   uint64_t below = ~0ull;
@@ -211,7 +283,7 @@ __device__ __noinline__ void search(Shared& sh, const Row<DT>& row, uint32_t b0,
 
 // best[have .. k): the first elements of blocks [b0, b1) equal to tau.
 template <int DT>
-__device__ __noinline__ void fill_ties(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, float tau,
+__device__ __forceinline__ void fill_ties(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, float tau,
                                        uint32_t have, uint32_t k) {
   if (threadIdx.x < 64u) {
     const int64_t first = (int64_t)b0 * kElem<DT> - row.head, end = (int64_t)b1 * kElem<DT> - row.head;
@@ -238,15 +310,24 @@ __device__ __forceinline__ void finish(Stats a, float scale, float& lse, float& 
   entropy = a.s == 0.0f ? 0.0f : ls - kLn2 * a.w / a.s;
 }
 
-template <int DT>
-__device__ __forceinline__ float log_prob(const Row<DT>& row, uint32_t i, float scale, float lse) {
-  const float y = row.at(i) * scale;
+__device__ __forceinline__ float log_prob(float x, float scale, float lse) {
+  const float y = x * scale;
   return y == -INFINITY && lse == lse ? -INFINITY : y - lse;
 }
 
-// One row's outputs: statistics a in every thread, the top keys in sh.best.
+// The logit of the row's token j, and whether it is one (else padding).
 template <int DT>
-__device__ __forceinline__ void write_row(const Args& a, Shared& sh, const Row<DT>& row, size_t n, Stats st) {
+__device__ __forceinline__ float token_logit(const Args& a, const Row<DT>& row, size_t n, int32_t j, bool& is) {
+  const int32_t t = j < a.M ? a.tokens[n * (size_t)a.M + j] : -1;
+  is = t >= 0 && (uint32_t)t < a.V;
+  return is ? row.at((uint32_t)t) : 0.0f;
+}
+
+// One row's outputs: statistics in every thread, the top keys in sh.best, the
+// thread's first token's logit in x0 (asked for before the statistics were).
+template <int DT>
+__device__ __forceinline__ void write_row(const Args& a, Shared& sh, const Row<DT>& row, size_t n, Stats st, float x0,
+                                          bool is0) {
   float lse, entropy;
   finish(st, a.scale, lse, entropy);
   if (threadIdx.x == 0u) {
@@ -254,16 +335,15 @@ __device__ __forceinline__ void write_row(const Args& a, Shared& sh, const Row<D
     if (a.entropy) a.entropy[n] = entropy;
   }
   for (int32_t j = (int32_t)threadIdx.x; j < a.M; j += (int32_t)kThreads) {
-    const int32_t t = a.tokens[n * (size_t)a.M + j];
-    a.logp[n * (size_t)a.M + j] =
-        t >= 0 && (uint32_t)t < a.V ? log_prob<DT>(row, (uint32_t)t, a.scale, lse) : 0.0f;
+    if (j >= (int32_t)kThreads) x0 = token_logit<DT>(a, row, n, j, is0);
+    a.logp[n * (size_t)a.M + j] = is0 ? log_prob(x0, a.scale, lse) : 0.0f;
   }
   if ((int32_t)threadIdx.x < a.top_k) {
     const bool some = threadIdx.x < a.V;
-    const uint32_t i = ~(uint32_t)sh.best[threadIdx.x];
+    const uint64_t key = sh.best[threadIdx.x];
     const size_t at = n * (size_t)a.top_k + threadIdx.x;
-    a.top_index[at] = some ? (int32_t)i : -1;
-    a.top_logp[at] = some ? log_prob<DT>(row, i, a.scale, lse) : -INFINITY;
+    a.top_index[at] = some ? (int32_t)~(uint32_t)key : -1;
+    a.top_logp[at] = some ? log_prob(key_value(key), a.scale, lse) : -INFINITY;
   }
 }
 
@@ -282,52 +362,66 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   if (tid == 0u) sh.count = 0u;
   Stats st = {-INFINITY, 0.0f, 0.0f};
   float mine = -INFINITY, tau = INFINITY;  // this thread's largest; nothing passes until the threshold is known
+  u32x4 next[kUnroll];
+  const auto whole = [&](uint32_t s0) { return s0 + kStepBlocks <= b1 && row.inside(s0, kStepBlocks); };
+  const auto fetch = [&](uint32_t s0) {
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u) next[u] = row.raw(s0 + u * kThreads + tid);
+  };
+  if (b0 < b1 && whole(b0)) fetch(b0);
   for (uint32_t s0 = b0; s0 < b1; s0 += kStepBlocks) {
     float v[kUnroll][E];
+    if (whole(s0)) {
 #pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) {
-      const uint32_t j = s0 + u * kThreads + tid;
-      if (j < b1) {
-        row.load(j, v[u]);
-      } else {
+      for (uint32_t u = 0; u < kUnroll; ++u) Row<DT>::values(next[u], v[u]);
+    } else {
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u) {
+        const uint32_t j = s0 + u * kThreads + tid;
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) v[u][e] = -INFINITY;
+        if (j < b1) row.load(j, v[u]);
       }
     }
-    float hi[kUnroll];
+    if (s0 + kStepBlocks < b1 && whole(s0 + kStepBlocks)) fetch(s0 + kStepBlocks);
+    float hi[kUnroll], top = -INFINITY, low = INFINITY;
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u) {
-      float lo = v[u][0];
       hi[u] = v[u][0];
 #pragma unroll
-      for (uint32_t e = 1; e < E; ++e) {
-        hi[u] = fmaxf(hi[u], v[u][e]);
-        lo = fminf(lo, v[u][e]);
+      for (uint32_t e = 0; e < E; ++e) {
+        if (e > 0u) hi[u] = fmaxf(hi[u], v[u][e]);
+        low = fminf(low, v[u][e]);
       }
-      if (__any((hi[u] - st.r) * c2 > kLazy || st.r == -INFINITY)) {
-        const float r = fmaxf(st.r, hi[u]), d = st.r == r ? 0.0f : (st.r - r) * c2, f = exp2_fast(d);
-        st.w = f == 0.0f ? 0.0f : (st.w + d * st.s) * f;
-        st.s *= f;
-        st.r = r;
-      }
-      const float ref = st.r == -INFINITY ? 0.0f : st.r;
-      if (__any(!(lo - ref > -1e30f))) {
-        // Masked logits (-inf, the type's lowest): e^t = 0, and t e^t is 0 too.
+      top = fmaxf(top, hi[u]);
+    }
+    mine = fmaxf(mine, top);
+    if (__any((top - st.r) * c2 > kLazy || st.r == -INFINITY)) {
+      const float r = fmaxf(st.r, top), d = st.r == r ? 0.0f : (st.r - r) * c2, f = exp2_fast(d);
+      st.w = f == 0.0f ? 0.0f : (st.w + d * st.s) * f;
+      st.s *= f;
+      st.r = r;
+    }
+    const float ref = st.r == -INFINITY ? 0.0f : st.r;
+    if (__any(!(low - ref > -1e30f))) {
+      // Masked logits (-inf, the type's lowest): e^t = 0, and t e^t is 0 too.
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) {
           const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
           st.s += p;
           st.w = __builtin_fmaf(fmaxf(t, -1000.0f), p, st.w);
         }
-      } else {
+    } else {
+#pragma unroll
+      for (uint32_t u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) {
           const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
           st.s += p;
           st.w = __builtin_fmaf(t, p, st.w);
         }
-      }
-      mine = fmaxf(mine, hi[u]);
     }
     if (k > 0u) {
       if (s0 == b0) tau = threshold(sh, mine, k);
@@ -344,8 +438,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   }
 
   // The workgroup's statistics, in a fixed order.
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) st = join(st, shuffle_xor(st, d), c2);
+  st = wave_join(st, c2);
   if ((tid & 63u) == 0u) sh.part[tid >> 6] = st;
   __syncthreads();
   st = join(join(sh.part[0], sh.part[1], c2), join(sh.part[2], sh.part[3], c2), c2);
@@ -376,8 +469,11 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       if (n_cand < k) fill_ties<DT>(sh, row, b0, b1, tau, n_cand, k);
     }
   }
+  float x0 = 0.0f;
+  bool is0 = false;
   if (splits == 1u) {
-    write_row<DT>(a, sh, row, n, st);
+    x0 = token_logit<DT>(a, row, n, (int32_t)tid, is0);
+    write_row<DT>(a, sh, row, n, st, x0, is0);
     return;
   }
 
@@ -397,6 +493,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   }
   __syncthreads();
   if (!sh.flag) return;
+  x0 = token_logit<DT>(a, row, n, (int32_t)tid, is0);
   Stats all = {-INFINITY, 0.0f, 0.0f};
   if ((tid & 63u) < splits) {
     const float* from = a.stats + (part + (tid & 63u)) * 4u;
@@ -404,8 +501,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     all.s = __hip_atomic_load(from + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     all.w = __hip_atomic_load(from + 2, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) all = join(all, shuffle_xor(all, d), c2);
+  all = wave_join(all, c2);
   if (k > 0u) {
     // splits x k <= kCand keys (the host's choice of splits); those of splits
     // with fewer than k elements are 0, below all.
@@ -415,7 +511,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     // Equal keys are only the zeros of short splits, and V >= 1 others rank first.
     rank_candidates(sh, splits * k, k);
   }
-  write_row<DT>(a, sh, row, n, all);
+  write_row<DT>(a, sh, row, n, all, x0, is0);
 }
 
 // ---------------------------------------------------------------------------
@@ -439,10 +535,16 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
   const uint32_t b0 = blockIdx.x * kStepBlocks;
   if (b0 >= row.blocks) return;
   float v[kUnroll][E];
+  if (row.inside(b0, kStepBlocks)) {
+    u32x4 w[kUnroll];
 #pragma unroll
-  for (uint32_t u = 0; u < kUnroll; ++u) {
-    const uint32_t j = b0 + u * kThreads + tid;
-    if (j < row.blocks) row.load(j, v[u]);
+    for (uint32_t u = 0; u < kUnroll; ++u) w[u] = row.raw(b0 + u * kThreads + tid);
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u) Row<DT>::values(w[u], v[u]);
+  } else {
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u)
+      if (b0 + u * kThreads + tid < row.blocks) row.load(b0 + u * kThreads + tid, v[u]);
   }
   if (tid < kStepBlocks / 32u) marked[tid] = 0u;
   __syncthreads();
@@ -456,8 +558,7 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
     const uint32_t blk = ((uint32_t)t + row.head) / E - b0;
     if (blk < kStepBlocks) atomicOr(&marked[blk >> 5], 1u << (blk & 31u));
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) g += __shfl_xor(g, d);
+  g = wave_fsum(g);
   if ((tid & 63u) == 0u) sums[tid >> 6] = g;
   __syncthreads();
   g = (sums[0] + sums[1]) + (sums[2] + sums[3]);
@@ -514,11 +615,11 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
 }
 
 // Workgroups of a row: one where the rows alone fill the chip, else pieces of
-// at least a step (16 KB), as many as give about 512 workgroups, with all
-// their top keys within one workgroup's candidates.
+// at least 2048 logits (8 a thread), as many as give about 512 workgroups,
+// with all their top keys within one workgroup's candidates.
 uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
   int64_t s = (512 + N - 1) / N;
-  const int64_t most = (V + 4 * kStepBlocks - 1) / (4 * kStepBlocks);  // FP32 steps; a BF16 piece is half as long
+  const int64_t most = (V + 2047) / 2048;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;
   if (top_k > 0 && s > (int64_t)kCand / top_k) s = kCand / top_k;
