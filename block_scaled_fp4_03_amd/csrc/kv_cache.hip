@@ -113,11 +113,18 @@ hipError_t append_fmt(const KvPool& c, const void* k, const void* v, int in_dtyp
 //
 // Which: with R = min(recent, budget) tokens kept for being last, the others'
 // weights become 32-bit keys in the weights' order, and a radix selection
-// (four 8-bit digits, high to low, LDS histograms) finds the key T of the
-// (budget - R)-th largest and how many equal to T still belong.  One more
-// pass in token order writes the kept tokens' numbers and weights.
+// finds the key T of the (budget - R)-th largest and how many equal to T still
+// belong.  Its first digit is the top 11 bits of the keys' actual range
+// (smallest to largest), so that the LDS histogram's counts spread however
+// narrow the weights lie, and two more digits at most look at one bin's keys
+// alone.  32768 keys (32 a thread) stay in registers from digit to digit;
+// longer sequences are read again.  Then the kept tokens are counted per 64
+// (ballots), the counts scanned once, and numbers and weights written in
+// order.
 // ---------------------------------------------------------------------------
-constexpr int kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+constexpr uint32_t kSelThreads = 1024, kSelWaves = kSelThreads / 64, kPer = 32, kChunk = kSelThreads * kPer;
+constexpr uint32_t kDigit = 11, kBins = 1u << kDigit;
+static_assert(kBins == 2 * kSelThreads, "two bins a thread");
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFFu;
@@ -125,13 +132,37 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+// Sum of v over the threads before this one; `all`: over all of them.
+__device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* wave_sum, uint32_t& all) {
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  uint32_t s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(s, d);
+    if (lane >= (uint32_t)d) s += o;
+  }
+  __syncthreads();  // wave_sum may still be read from the last scan
+  if (lane == 63u) wave_sum[wave] = s;
+  __syncthreads();
+  uint32_t before = 0u;
+  all = 0u;
+#pragma unroll
+  for (uint32_t i = 0; i < kSelWaves; ++i) {
+    const uint32_t x = wave_sum[i];
+    before += i < wave ? x : 0u;
+    all += x;
+  }
+  return before + s - v;
+}
+
 __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
     const int32_t* __restrict__ lens, const float* __restrict__ weights, int64_t weights_stride,
     int32_t* __restrict__ out_lens, float* __restrict__ out_weights, int64_t out_stride, int32_t* __restrict__ kept,
     uint32_t heads, int64_t max_len, int64_t budget, int64_t recent) {
-  __shared__ uint32_t hist[256];
-  __shared__ uint32_t pick[2];
-  __shared__ uint32_t count[2][kSelWaves];
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t wave_sum[kSelWaves];
+  __shared__ uint32_t pick[3];
+  __shared__ uint32_t count[kPer * kSelWaves];
   const uint32_t h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
   const size_t bh = (size_t)b * heads + h;
   const float* w = weights + bh * (size_t)weights_stride;
@@ -140,74 +171,155 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
   const int64_t len64 = lens[b] < 0 ? 0 : (lens[b] < max_len ? lens[b] : max_len);
   const uint32_t n = (uint32_t)len64, keep = (uint32_t)(len64 < budget ? len64 : budget);
   if (h == 0u && tid == 0u) out_lens[b] = (int32_t)keep;
+  for (uint32_t t = keep + tid; t < (uint32_t)budget; t += kSelThreads) kp[t] = -1;
+  for (uint32_t t = keep + tid; t < (uint32_t)out_stride; t += kSelThreads) ow[t] = 0.0f;
   if (n <= keep) {
     for (uint32_t t = tid; t < n; t += kSelThreads) {
       kp[t] = (int32_t)t;
       ow[t] = w[t];
     }
-  } else {
-    const uint32_t last = (uint32_t)(recent < (int64_t)keep ? recent : (int64_t)keep);
-    const uint32_t cand = n - last;
-    uint32_t rem = keep - last, prefix = 0u, mask = 0u;
-    if (rem == 0u) prefix = 0xFFFFFFFFu;  // nothing beyond the last tokens
-    for (int shift = 24; shift >= 0 && rem > 0u; shift -= 8) {
-      if (tid < 256u) hist[tid] = 0u;
+    return;
+  }
+  const uint32_t last = (uint32_t)(recent < (int64_t)keep ? recent : (int64_t)keep);
+  const uint32_t cand = n - last;  // >= 1: n > keep >= last
+  uint32_t rem = keep - last;      // of the candidates
+  const uint32_t chunks = (n + kChunk - 1u) / kChunk;
+
+  uint32_t key[kPer];
+  // Key i of chunk c: token c kChunk + i kSelThreads + tid (past the candidates: the last one's).
+  const auto load = [&](uint32_t c) {
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+      const uint32_t t0 = c * kChunk + i * kSelThreads;
+      if (t0 < cand) key[i] = weight_key(w[min(t0 + tid, cand - 1u)]);
+    }
+  };
+  load(0u);
+
+  uint32_t T = 0xFFFFFFFFu, equal = 0u;  // rem == 0: no key is above T, and none equal is taken
+  if (rem > 0u) {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+    for (uint32_t c = 0; c < chunks; ++c) {
+      if (chunks > 1u) load(c);
+#pragma unroll
+      for (uint32_t i = 0; i < kPer; ++i)
+        if (c * kChunk + i * kSelThreads < cand) {
+          lo = min(lo, key[i]);
+          hi = max(hi, key[i]);
+        }
+    }
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      lo = min(lo, (uint32_t)__shfl_xor(lo, d));
+      hi = max(hi, (uint32_t)__shfl_xor(hi, d));
+    }
+    if (lane == 0u) {
+      hist[wave] = lo;
+      hist[kSelWaves + wave] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kSelWaves; ++i) {
+      lo = min(lo, hist[i]);
+      hi = max(hi, hist[kSelWaves + i]);
+    }
+    __syncthreads();
+    T = lo;
+    equal = cand;
+    uint32_t bits = hi == lo ? 0u : 32u - (uint32_t)__builtin_clz(hi - lo);  // keys of interest: T .. T + 2^bits - 1
+    while (bits > 0u) {
+      const uint32_t shift = bits > kDigit ? bits - kDigit : 0u, bins = 1u << (bits - shift);
+      hist[tid] = 0u;
+      hist[kSelThreads + tid] = 0u;
       __syncthreads();
-      for (uint32_t t = tid; t < cand; t += kSelThreads) {
-        const uint32_t key = weight_key(w[t]);
-        if (((key ^ prefix) & mask) == 0u) atomicAdd(&hist[(key >> shift) & 255u], 1u);
-      }
-      __syncthreads();
-      if (tid < 256u) {
-        uint32_t above = 0u;
-        for (uint32_t d = tid + 1u; d < 256u; ++d) above += hist[d];
-        if (above < rem && rem <= above + hist[tid]) {
-          pick[0] = tid;
-          pick[1] = rem - above;
+      for (uint32_t c = 0; c < chunks; ++c) {
+        if (chunks > 1u) load(c);
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; ++i) {
+          const uint32_t t = c * kChunk + i * kSelThreads + tid;
+          const uint32_t bin = (key[i] - T) >> shift;
+          if (t < cand && key[i] >= T && bin < bins) atomicAdd(&hist[bin], 1u);
         }
       }
       __syncthreads();
-      prefix |= pick[0] << shift;
-      mask |= 255u << shift;
+      // Two bins a thread, the highest first: where the count from the top passes rem.
+      const uint32_t d1 = kBins - 1u - 2u * tid, d0 = d1 - 1u, n1 = hist[d1], n0 = hist[d0];
+      uint32_t all;
+      const uint32_t above = scan_before(n1 + n0, wave_sum, all);
+      if (above < rem && rem <= above + n1 + n0) {
+        const bool first = rem <= above + n1;
+        pick[0] = first ? d1 : d0;
+        pick[1] = first ? rem - above : rem - above - n1;
+        pick[2] = first ? n1 : n0;
+      }
+      __syncthreads();
+      T += pick[0] << shift;
       rem = pick[1];
+      equal = pick[2];
+      bits = shift;
+    }
+  }
+
+  // Tokens in order: key > T, or one of the first `rem` equal to T, or last.
+  const bool all_equal = rem == equal;  // no tie to break (and rem == 0 takes none)
+  uint32_t base = 0u, eq_base = 0u;
+  for (uint32_t c = 0; c < chunks; ++c) {
+    if (chunks > 1u) load(c);
+    uint32_t flags = 0u;  // bit i: token i stays
+    uint32_t eq = 0u;     // bit i: equal to T
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+      const uint32_t t = c * kChunk + i * kSelThreads + tid;
+      if (t < n && (t >= cand || key[i] > T)) flags |= 1u << i;
+      if (t < cand && key[i] == T) eq |= 1u << i;
+    }
+    const uint64_t below = (1ull << lane) - 1ull;
+    uint32_t all;
+    if (all_equal) {
+      if (rem > 0u) flags |= eq;
+    } else {
+#pragma unroll
+      for (uint32_t i = 0; i < kPer; ++i) {
+        const uint64_t m = __ballot((eq >> i) & 1u);
+        if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
+      }
+      __syncthreads();
+      const uint32_t mine = tid < kPer * kSelWaves ? count[tid] : 0u;
+      const uint32_t at = scan_before(mine, wave_sum, all);
+      if (tid < kPer * kSelWaves) count[tid] = eq_base + at;
+      __syncthreads();
+#pragma unroll
+      for (uint32_t i = 0; i < kPer; ++i) {
+        const uint64_t m = __ballot((eq >> i) & 1u);
+        if (((eq >> i) & 1u) && count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below) < rem) flags |= 1u << i;
+      }
+      eq_base += all;
       __syncthreads();
     }
-    // Tokens in order: key > T, or one of the first `rem` equal to T, or last.
-    uint32_t base = 0u, eq_base = 0u;
-    for (uint32_t t0 = 0u; t0 < n; t0 += kSelThreads) {
-      const uint32_t t = t0 + tid;
-      const uint32_t key = t < cand ? weight_key(w[t]) : 0u;
-      const bool eq = t < cand && key == prefix;
-      const uint64_t eqs = __ballot(eq), below = (1ull << lane) - 1ull;
-      if (lane == 0u) count[0][wave] = (uint32_t)__popcll(eqs);
-      __syncthreads();
-      uint32_t eq_before = eq_base, eq_all = 0u;
-      for (uint32_t i = 0u; i < kSelWaves; ++i) {
-        if (i < wave) eq_before += count[0][i];
-        eq_all += count[0][i];
-      }
-      const bool stays =
-          t < n && (t >= cand || key > prefix || (eq && eq_before + (uint32_t)__popcll(eqs & below) < rem));
-      const uint64_t st = __ballot(stays);
-      if (lane == 0u) count[1][wave] = (uint32_t)__popcll(st);
-      __syncthreads();
-      uint32_t at = base, all = 0u;
-      for (uint32_t i = 0u; i < kSelWaves; ++i) {
-        if (i < wave) at += count[1][i];
-        all += count[1][i];
-      }
-      at += (uint32_t)__popcll(st & below);
-      if (stays && at < keep) {
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+      const uint64_t m = __ballot((flags >> i) & 1u);
+      if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
+    }
+    __syncthreads();
+    const uint32_t mine = tid < kPer * kSelWaves ? count[tid] : 0u;
+    const uint32_t at0 = scan_before(mine, wave_sum, all);
+    if (tid < kPer * kSelWaves) count[tid] = base + at0;
+    __syncthreads();
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i) {
+      if (c * kChunk + i * kSelThreads >= n) break;
+      const uint64_t m = __ballot((flags >> i) & 1u);
+      const uint32_t at = count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below);
+      if (((flags >> i) & 1u) && at < keep) {
+        const uint32_t t = c * kChunk + i * kSelThreads + tid;
         kp[at] = (int32_t)t;
         ow[at] = w[t];
       }
-      base += all;
-      eq_base += eq_all;
-      __syncthreads();
     }
+    base += all;
+    __syncthreads();
   }
-  for (uint32_t t = keep + tid; t < (uint32_t)budget; t += kSelThreads) kp[t] = -1;
-  for (uint32_t t = keep + tid; t < (uint32_t)out_stride; t += kSelThreads) ow[t] = 0.0f;
 }
 
 // Rows of the kept tokens to their new places: 16 bytes a thread, the K row
@@ -233,10 +345,10 @@ __global__ __launch_bounds__(256) void evict_copy_kernel(KvPool src, const int32
   *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(dst.k) + to * row_bytes + piece * 16u) = k;
   *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(dst.v) + to * row_bytes + piece * 16u) = v;
   if (src.fmt != kKvBf16) {
-    const uint32_t blocks = (uint32_t)src.head_dim / 32u;
-    for (uint32_t i = piece; i < blocks; i += pieces) {
-      dst.ks[to * blocks + i] = src.ks[from * blocks + i];
-      dst.vs[to * blocks + i] = src.vs[from * blocks + i];
+    const uint32_t pairs = (uint32_t)src.head_dim / 64u;  // scale bytes two by two
+    for (uint32_t i = piece; i < pairs; i += pieces) {
+      reinterpret_cast<uint16_t*>(dst.ks)[to * pairs + i] = reinterpret_cast<const uint16_t*>(src.ks)[from * pairs + i];
+      reinterpret_cast<uint16_t*>(dst.vs)[to * pairs + i] = reinterpret_cast<const uint16_t*>(src.vs)[from * pairs + i];
     }
   }
 }

@@ -221,3 +221,13 @@ def test_evict_zero_budget_and_masked_pages():
     np.testing.assert_array_equal(to_host(kept)[0, 0], list(range(12)) + list(range(24, 32)))
     before[2, :, :12] = before[0, :, :12]
     np.testing.assert_array_equal(_bits(cache.k), before)
+
+
+@pytest.mark.parametrize("n,budget,recent,levels", [(40000, 5000, 100, 0), (70001, 33000, 7, 50), (33000, 32999, 0, 3),
+                                                    (32768, 1, 0, 0), (32769, 32768, 32768, 0), (100000, 70000, 0, 1)])
+def test_evict_long_sequences(n, budget, recent, levels):
+    """Sequences past what a workgroup holds in registers; weights of few distinct levels tie across its pieces."""
+    rng = np.random.default_rng(n)
+    cap = -(-n // 64) * 64
+    w = rng.random((1, 1, cap)) if levels == 0 else rng.integers(0, levels, (1, 1, cap))
+    _evict_case("mxfp4", [n], 1, 64, 64, budget, recent, w.astype(np.float32), 51)
