@@ -116,20 +116,27 @@ hipError_t append_fmt(const KvPool& c, const void* k, const void* v, int in_dtyp
 // finds the key T of the (budget - R)-th largest and how many equal to T still
 // belong.  Its first digit is the top 11 bits of the keys' actual range
 // (smallest to largest), so that the LDS histogram's counts spread however
-// narrow the weights lie, and two more digits at most look at one bin's keys
-// alone.  32768 keys (32 a thread) stay in registers from digit to digit;
+// narrow the weights lie.  The bin then in question mostly holds few keys,
+// which are ranked directly; else more digits narrow it (three in all at
+// most).  32768 keys (32 a thread) stay in registers from digit to digit;
 // longer sequences are read again.  Then the kept tokens are counted per 64
 // (ballots), the counts scanned once, and numbers and weights written in
 // order.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kSelThreads = 1024, kSelWaves = kSelThreads / 64, kPer = 32, kChunk = kSelThreads * kPer;
 constexpr uint32_t kDigit = 11, kBins = 1u << kDigit;
+constexpr uint32_t kFew = 256;  // keys ranked directly
 static_assert(kBins == 2 * kSelThreads, "two bins a thread");
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFFu;
   const uint32_t u = f2u(w + 0.0f);  // -0 -> +0
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+// The weight of a key (-0 as +0).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+  return k == 0xFFFFFFFFu ? NAN : u2f((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
 // Sum of v over the threads before this one; `all`: over all of them.
@@ -155,13 +162,14 @@ __device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* wave_sum, 
   return before + s - v;
 }
 
-__global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
+// (One workgroup of 16 waves fills a CU: four waves a SIMD may use 128 registers each.)
+__global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(4, 4))) void evict_select_kernel(
     const int32_t* __restrict__ lens, const float* __restrict__ weights, int64_t weights_stride,
     int32_t* __restrict__ out_lens, float* __restrict__ out_weights, int64_t out_stride, int32_t* __restrict__ kept,
     uint32_t heads, int64_t max_len, int64_t budget, int64_t recent) {
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t wave_sum[kSelWaves];
-  __shared__ uint32_t pick[3];
+  __shared__ uint32_t pick[3], few;
   __shared__ uint32_t count[kPer * kSelWaves];
   const uint32_t h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
   const size_t bh = (size_t)b * heads + h;
@@ -186,13 +194,20 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
   const uint32_t chunks = (n + kChunk - 1u) / kChunk;
 
   uint32_t key[kPer];
-  // Key i of chunk c: token c kChunk + i kSelThreads + tid (past the candidates: the last one's).
+  // Key i of chunk c: token c kChunk + i kSelThreads + tid (past the end: the last one's).
   const auto load = [&](uint32_t c) {
+    // Eight loads at a time without a branch between them, so that they are
+    // all on their way together.
+    float x[kPer] = {};
 #pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i) {
-      const uint32_t t0 = c * kChunk + i * kSelThreads;
-      if (t0 < cand) key[i] = weight_key(w[min(t0 + tid, cand - 1u)]);
-    }
+    for (uint32_t i0 = 0; i0 < kPer; i0 += 8u)
+      if (c * kChunk + i0 * kSelThreads < n) {
+#pragma unroll
+        for (uint32_t i = i0; i < i0 + 8u; ++i) x[i] = w[min(c * kChunk + i * kSelThreads + tid, n - 1u)];
+      }
+#pragma unroll
+    for (uint32_t i = 0; i < kPer; ++i)
+      if (c * kChunk + i * kSelThreads < n) key[i] = weight_key(x[i]);
   };
   load(0u);
 
@@ -204,8 +219,9 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
 #pragma unroll
       for (uint32_t i = 0; i < kPer; ++i)
         if (c * kChunk + i * kSelThreads < cand) {
-          lo = min(lo, key[i]);
-          hi = max(hi, key[i]);
+          const bool is = c * kChunk + i * kSelThreads + tid < cand;
+          lo = min(lo, is ? key[i] : 0xFFFFFFFFu);
+          hi = max(hi, is ? key[i] : 0u);
         }
     }
 #pragma unroll
@@ -231,11 +247,13 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
       const uint32_t shift = bits > kDigit ? bits - kDigit : 0u, bins = 1u << (bits - shift);
       hist[tid] = 0u;
       hist[kSelThreads + tid] = 0u;
+      if (tid == 0u) few = 0u;
       __syncthreads();
       for (uint32_t c = 0; c < chunks; ++c) {
         if (chunks > 1u) load(c);
 #pragma unroll
         for (uint32_t i = 0; i < kPer; ++i) {
+          if (c * kChunk + i * kSelThreads >= cand) continue;  // (uniform: short sequences skip what they lack)
           const uint32_t t = c * kChunk + i * kSelThreads + tid;
           const uint32_t bin = (key[i] - T) >> shift;
           if (t < cand && key[i] >= T && bin < bins) atomicAdd(&hist[bin], 1u);
@@ -257,6 +275,38 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
       rem = pick[1];
       equal = pick[2];
       bits = shift;
+      if (bits == 0u || equal > kFew) continue;
+      // Few keys left: collected, and each counts those above it.
+      for (uint32_t c = 0; c < chunks; ++c) {
+        if (chunks > 1u) load(c);
+#pragma unroll
+        for (uint32_t i = 0; i < kPer; ++i) {
+          if (c * kChunk + i * kSelThreads >= cand) continue;
+          const uint32_t t = c * kChunk + i * kSelThreads + tid;
+          if (t < cand && key[i] >= T && (key[i] - T) >> bits == 0u) hist[atomicAdd(&few, 1u)] = key[i];
+        }
+      }
+      __syncthreads();
+      if (tid < equal) {
+        const uint32_t mine = hist[tid];
+        uint32_t above_it = 0u, same = 0u;
+#pragma unroll 8
+        for (uint32_t i = 0; i < equal; ++i) {
+          const uint32_t o = hist[i];
+          above_it += o > mine ? 1u : 0u;
+          same += o == mine ? 1u : 0u;
+        }
+        if (above_it < rem && rem <= above_it + same) {  // every key equal to the one wanted writes the same
+          pick[0] = mine;
+          pick[1] = rem - above_it;
+          pick[2] = same;
+        }
+      }
+      __syncthreads();
+      T = pick[0];
+      rem = pick[1];
+      equal = pick[2];
+      bits = 0u;
     }
   }
 
@@ -265,10 +315,12 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
   uint32_t base = 0u, eq_base = 0u;
   for (uint32_t c = 0; c < chunks; ++c) {
     if (chunks > 1u) load(c);
+    const uint32_t counts = min((n - c * kChunk + kSelThreads - 1u) / kSelThreads, kPer) * kSelWaves;
     uint32_t flags = 0u;  // bit i: token i stays
     uint32_t eq = 0u;     // bit i: equal to T
 #pragma unroll
     for (uint32_t i = 0; i < kPer; ++i) {
+      if (c * kChunk + i * kSelThreads >= n) continue;
       const uint32_t t = c * kChunk + i * kSelThreads + tid;
       if (t < n && (t >= cand || key[i] > T)) flags |= 1u << i;
       if (t < cand && key[i] == T) eq |= 1u << i;
@@ -280,16 +332,18 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
     } else {
 #pragma unroll
       for (uint32_t i = 0; i < kPer; ++i) {
+        if (c * kChunk + i * kSelThreads >= n) continue;
         const uint64_t m = __ballot((eq >> i) & 1u);
         if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
       }
       __syncthreads();
-      const uint32_t mine = tid < kPer * kSelWaves ? count[tid] : 0u;
+      const uint32_t mine = tid < counts ? count[tid] : 0u;
       const uint32_t at = scan_before(mine, wave_sum, all);
-      if (tid < kPer * kSelWaves) count[tid] = eq_base + at;
+      if (tid < counts) count[tid] = eq_base + at;
       __syncthreads();
 #pragma unroll
       for (uint32_t i = 0; i < kPer; ++i) {
+        if (c * kChunk + i * kSelThreads >= n) continue;
         const uint64_t m = __ballot((eq >> i) & 1u);
         if (((eq >> i) & 1u) && count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below) < rem) flags |= 1u << i;
       }
@@ -298,23 +352,24 @@ __global__ __launch_bounds__(kSelThreads) void evict_select_kernel(
     }
 #pragma unroll
     for (uint32_t i = 0; i < kPer; ++i) {
+      if (c * kChunk + i * kSelThreads >= n) continue;
       const uint64_t m = __ballot((flags >> i) & 1u);
       if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
     }
     __syncthreads();
-    const uint32_t mine = tid < kPer * kSelWaves ? count[tid] : 0u;
+    const uint32_t mine = tid < counts ? count[tid] : 0u;
     const uint32_t at0 = scan_before(mine, wave_sum, all);
-    if (tid < kPer * kSelWaves) count[tid] = base + at0;
+    if (tid < counts) count[tid] = base + at0;
     __syncthreads();
 #pragma unroll
     for (uint32_t i = 0; i < kPer; ++i) {
-      if (c * kChunk + i * kSelThreads >= n) break;
+      if (c * kChunk + i * kSelThreads >= n) continue;
       const uint64_t m = __ballot((flags >> i) & 1u);
       const uint32_t at = count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below);
       if (((flags >> i) & 1u) && at < keep) {
         const uint32_t t = c * kChunk + i * kSelThreads + tid;
         kp[at] = (int32_t)t;
-        ow[at] = w[t];
+        ow[at] = key_weight(key[i]);
       }
     }
     base += all;

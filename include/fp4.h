@@ -516,7 +516,7 @@ size_t fp4_kv_evict_workspace(const fp4_kv_cache* cache, int64_t B, int64_t max_
  *   weights: FP32 B x kv_heads x weights_stride; weights_stride >= max_len,
  *   the bound of lens (longer ones read as max_len).
  *   out_lens[b] = min(lens[b], budget).  out_weights: FP32 B x kv_heads x
- *   out_stride, the kept tokens' weights, then zeros; out_stride >= budget.
+ *   out_stride, the kept tokens' weights (-0 as +0), then zeros; out_stride >= budget.
  *   kept: int32 B x kv_heads x budget, the kept tokens' old numbers, then -1.
  *   dst has src's fmt, heads, head_dim and page_size; dst_width * page_size >=
  *   min(budget, max_len).  A kept token whose page (old or new) is outside the
