@@ -108,8 +108,14 @@ hipError_t append_fmt(const KvPool& c, const void* k, const void* v, int in_dtyp
 }
 
 // ---------------------------------------------------------------------------
-// Eviction, in two launches: which tokens stay (one workgroup per sequence
-// and head), then their rows' copies (spread over the chip).
+// Eviction: which tokens stay, then their rows' copies.  One launch for
+// sequences of up to 32768 tokens: the selection is short next to the copies,
+// but one workgroup per (sequence, head) would leave most of the chip idle,
+// so `parts` workgroups each make the whole selection (from L2) and write and
+// copy their share of the kept tokens.  Longer sequences, whose selection
+// reads the weights several times, take a launch for it and one for the
+// copies.  Two launches for all measured 14.7 + 4.7 us for 16 heads of 1100
+// tokens (and the host's second launch), one 9.9 us.
 //
 // Which: with R = min(recent, budget) tokens kept for being last, the others'
 // weights become 32-bit keys in the weights' order, and a radix selection
@@ -118,15 +124,20 @@ hipError_t append_fmt(const KvPool& c, const void* k, const void* v, int in_dtyp
 // (smallest to largest), so that the LDS histogram's counts spread however
 // narrow the weights lie.  The bin then in question mostly holds few keys,
 // which are ranked directly; else more digits narrow it (three in all at
-// most).  32768 keys (32 a thread) stay in registers from digit to digit;
-// longer sequences are read again.  Then the kept tokens are counted per 64
-// (ballots), the counts scanned once, and numbers and weights written in
-// order.
+// most).  32768 keys stay in LDS from pass to pass; longer sequences are read
+// again.  For the output every thread takes a run of tokens, so one scan over
+// the threads gives all places.  (Keys in registers were slower: every pass
+// is then code unrolled 32 times, run once, and fetching it took longer than
+// running it: 14.8 us against 7.7 us for 1100 tokens.)
 // ---------------------------------------------------------------------------
-constexpr uint32_t kSelThreads = 1024, kSelWaves = kSelThreads / 64, kPer = 32, kChunk = kSelThreads * kPer;
+constexpr uint32_t kSelThreads = 1024, kSelWaves = kSelThreads / 64;
+constexpr uint32_t kChunk = 32768;  // keys held at a time
 constexpr uint32_t kDigit = 11, kBins = 1u << kDigit;
 constexpr uint32_t kFew = 256;  // keys ranked directly
 static_assert(kBins == 2 * kSelThreads, "two bins a thread");
+static_assert(kChunk / kSelThreads == 32, "a thread's run fits a 32-bit mask");
+
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));  // weights' rows have any stride
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
   if (w != w) return 0xFFFFFFFFu;
@@ -139,7 +150,20 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
   return k == 0xFFFFFFFFu ? NAN : u2f((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
+// Smallest and largest over the wavefront, in every lane.
+template <bool MAX>
+__device__ __forceinline__ uint32_t wave_extreme(uint32_t v) {
+  const auto pick = [](uint32_t x, uint32_t y) { return MAX ? max(x, y) : min(x, y); };
+  v = pick(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x121, 0xF, 0xF, false));
+  v = pick(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x122, 0xF, 0xF, false));
+  v = pick(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x124, 0xF, 0xF, false));
+  v = pick(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, false));
+  return pick(pick((uint32_t)__builtin_amdgcn_readlane((int)v, 0), (uint32_t)__builtin_amdgcn_readlane((int)v, 16)),
+              pick((uint32_t)__builtin_amdgcn_readlane((int)v, 32), (uint32_t)__builtin_amdgcn_readlane((int)v, 48)));
+}
+
 // Sum of v over the threads before this one; `all`: over all of them.
+// wave_sum is not in use by an earlier scan (a barrier lies between).
 __device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* wave_sum, uint32_t& all) {
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
   uint32_t s = v;
@@ -148,7 +172,6 @@ __device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* wave_sum, 
     const uint32_t o = __shfl_up(s, d);
     if (lane >= (uint32_t)d) s += o;
   }
-  __syncthreads();  // wave_sum may still be read from the last scan
   if (lane == 63u) wave_sum[wave] = s;
   __syncthreads();
   uint32_t before = 0u;
@@ -162,108 +185,200 @@ __device__ __forceinline__ uint32_t scan_before(uint32_t v, uint32_t* wave_sum, 
   return before + s - v;
 }
 
-// (One workgroup of 16 waves fills a CU: four waves a SIMD may use 128 registers each.)
-__global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(4, 4))) void evict_select_kernel(
-    const int32_t* __restrict__ lens, const float* __restrict__ weights, int64_t weights_stride,
-    int32_t* __restrict__ out_lens, float* __restrict__ out_weights, int64_t out_stride, int32_t* __restrict__ kept,
-    uint32_t heads, int64_t max_len, int64_t budget, int64_t recent) {
-  __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t wave_sum[kSelWaves];
-  __shared__ uint32_t pick[3], few;
-  __shared__ uint32_t count[kPer * kSelWaves];
-  const uint32_t h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-  const size_t bh = (size_t)b * heads + h;
-  const float* w = weights + bh * (size_t)weights_stride;
-  float* ow = out_weights + bh * (size_t)out_stride;
-  int32_t* kp = kept + bh * (size_t)budget;
-  const int64_t len64 = lens[b] < 0 ? 0 : (lens[b] < max_len ? lens[b] : max_len);
-  const uint32_t n = (uint32_t)len64, keep = (uint32_t)(len64 < budget ? len64 : budget);
-  if (h == 0u && tid == 0u) out_lens[b] = (int32_t)keep;
-  for (uint32_t t = keep + tid; t < (uint32_t)budget; t += kSelThreads) kp[t] = -1;
-  for (uint32_t t = keep + tid; t < (uint32_t)out_stride; t += kSelThreads) ow[t] = 0.0f;
-  if (n <= keep) {
-    for (uint32_t t = tid; t < n; t += kSelThreads) {
-      kp[t] = (int32_t)t;
-      ow[t] = w[t];
+struct EvictArgs {
+  KvPool src;
+  const int32_t* src_table;
+  int64_t src_width;
+  const int32_t* lens;
+  const float* weights;
+  int64_t weights_stride;
+  KvPool dst;
+  const int32_t* dst_table;
+  int64_t dst_width;
+  int32_t* out_lens;
+  float* out_weights;
+  int64_t out_stride;
+  int32_t* kept;
+  int64_t max_len, budget, recent;
+  uint32_t row_bytes;
+};
+
+// Copies the rows of kept tokens [from, to) of sequence b, head h to their
+// places: 16 bytes a thread, K and V of kRows tokens at a time in flight.
+template <uint32_t THREADS>
+__device__ __forceinline__ void copy_rows(const EvictArgs& a, uint32_t b, uint32_t h, uint32_t from, uint32_t to) {
+  constexpr uint32_t kRows = 4;
+  const uint32_t pieces = a.row_bytes / 16u, step = THREADS / pieces;  // threads of a row; rows of a step
+  const uint32_t r = threadIdx.x / pieces, piece = threadIdx.x % pieces;
+  if (r >= step) return;
+  const int32_t* kept = a.kept + ((size_t)b * a.src.kv_heads + h) * (size_t)a.budget;
+  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)a.src.page_size), in_page = (uint32_t)a.src.page_size - 1u;
+  const uint32_t pairs = (uint32_t)a.src.head_dim / 64u;  // scale bytes two by two
+  for (uint32_t at0 = from + r; at0 < to; at0 += kRows * step) {
+    uint64_t s[kRows], d[kRows];
+    bool ok[kRows];
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k) {
+      const uint32_t at = min(at0 + k * step, to - 1u);
+      const int32_t t = kept[at];
+      const int32_t sp = a.src_table[(size_t)b * a.src_width + ((uint32_t)max(t, 0) >> shift)];
+      const int32_t dp = a.dst_table[(size_t)b * a.dst_width + (at >> shift)];
+      ok[k] = at0 + k * step < to && t >= 0 && sp >= 0 && sp < a.src.pages && dp >= 0 && dp < a.dst.pages;
+      s[k] = ok[k] ? (((uint64_t)(uint32_t)sp * a.src.kv_heads + h) << shift) + ((uint32_t)t & in_page) : 0u;
+      d[k] = ok[k] ? (((uint64_t)(uint32_t)dp * a.dst.kv_heads + h) << shift) + (at & in_page) : 0u;
     }
+    u32x4 x[kRows], y[kRows];
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k) {
+      // (Row 0 stands in for one that is not copied; a pool without pages has none to copy.)
+      if (a.src.pages > 0) {
+        x[k] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.k) + s[k] * a.row_bytes + piece * 16u);
+        y[k] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.v) + s[k] * a.row_bytes + piece * 16u);
+      }
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kRows; ++k) {
+      if (!ok[k]) continue;
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.k) + d[k] * a.row_bytes + piece * 16u) = x[k];
+      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.v) + d[k] * a.row_bytes + piece * 16u) = y[k];
+      if (a.src.fmt != kKvBf16) {
+        for (uint32_t i = piece; i < pairs; i += pieces) {
+          reinterpret_cast<uint16_t*>(a.dst.ks)[d[k] * pairs + i] =
+              reinterpret_cast<const uint16_t*>(a.src.ks)[s[k] * pairs + i];
+          reinterpret_cast<uint16_t*>(a.dst.vs)[d[k] * pairs + i] =
+              reinterpret_cast<const uint16_t*>(a.src.vs)[s[k] * pairs + i];
+        }
+      }
+    }
+  }
+}
+
+// Workgroup (part, head, sequence); `copy`: also the rows of its share.
+__global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(4, 4))) void evict_kernel(EvictArgs a,
+                                                                                                      bool copy) {
+  extern __shared__ __attribute__((aligned(16))) uint32_t keys[];  // min(max_len, kChunk) of them, to a multiple of 4
+  __shared__ uint32_t hist[kBins];
+  __shared__ uint32_t wave_sum[2][kSelWaves];
+  __shared__ uint32_t pick[3], few;
+  const uint32_t part = blockIdx.x, parts = gridDim.x, h = blockIdx.y, b = blockIdx.z;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  const size_t bh = (size_t)b * a.src.kv_heads + h;
+  const float* __restrict__ w = a.weights + bh * (size_t)a.weights_stride;
+  float* ow = a.out_weights + bh * (size_t)a.out_stride;
+  int32_t* kp = a.kept + bh * (size_t)a.budget;
+  const int64_t l = a.lens[b], len64 = l < 0 ? 0 : (l < a.max_len ? l : a.max_len);
+  const uint32_t n = (uint32_t)len64, keep = (uint32_t)(len64 < a.budget ? len64 : a.budget);
+  // This workgroup's share of the kept tokens.
+  const uint32_t share = (keep + parts - 1u) / parts, from = min(part * share, keep), to = min(from + share, keep);
+  if (part == 0u) {
+    if (h == 0u && tid == 0u) a.out_lens[b] = (int32_t)keep;
+    for (uint32_t t = keep + tid; t < (uint32_t)a.budget; t += kSelThreads) kp[t] = -1;
+    for (uint32_t t = keep + tid; t < (uint32_t)a.out_stride; t += kSelThreads) ow[t] = 0.0f;
+  }
+  if (from >= to) return;
+  if (n <= keep) {
+    for (uint32_t t = from + tid; t < to; t += kSelThreads) {
+      kp[t] = (int32_t)t;
+      ow[t] = key_weight(weight_key(w[t]));
+    }
+    __syncthreads();
+    if (copy) copy_rows<kSelThreads>(a, b, h, from, to);
     return;
   }
-  const uint32_t last = (uint32_t)(recent < (int64_t)keep ? recent : (int64_t)keep);
+  const uint32_t last = (uint32_t)(a.recent < (int64_t)keep ? a.recent : (int64_t)keep);
   const uint32_t cand = n - last;  // >= 1: n > keep >= last
   uint32_t rem = keep - last;      // of the candidates
   const uint32_t chunks = (n + kChunk - 1u) / kChunk;
 
-  uint32_t key[kPer];
-  // Key i of chunk c: token c kChunk + i kSelThreads + tid (past the end: the last one's).
-  const auto load = [&](uint32_t c) {
-    // Eight loads at a time without a branch between them, so that they are
-    // all on their way together.
-    float x[kPer] = {};
+  // The keys of tokens c kChunk .., and their smallest and largest among the candidates.
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+  const auto load = [&](uint32_t c) __attribute__((always_inline)) {
+    const uint32_t t0 = c * kChunk, here = min(n - t0, kChunk), here4 = here / 4u;
+    // 16 bytes a load and eight loads a thread: a whole chunk is on its way at once.
+    for (uint32_t i0 = tid; i0 < here4; i0 += 8u * kSelThreads) {
+      f32x4_any x[8];
 #pragma unroll
-    for (uint32_t i0 = 0; i0 < kPer; i0 += 8u)
-      if (c * kChunk + i0 * kSelThreads < n) {
+      for (uint32_t k = 0; k < 8u; ++k)
+        x[k] = *reinterpret_cast<const f32x4_any*>(w + t0 + 4u * min(i0 + k * kSelThreads, here4 - 1u));
 #pragma unroll
-        for (uint32_t i = i0; i < i0 + 8u; ++i) x[i] = w[min(c * kChunk + i * kSelThreads + tid, n - 1u)];
+      for (uint32_t k = 0; k < 8u; ++k) {
+        const uint32_t i = i0 + k * kSelThreads;
+        if (i < here4) {
+          u32x4 q;
+#pragma unroll
+          for (uint32_t j = 0; j < 4u; ++j) {
+            q[j] = weight_key(x[k][j]);
+            const bool is = t0 + 4u * i + j < cand;
+            lo = min(lo, is ? q[j] : 0xFFFFFFFFu);
+            hi = max(hi, is ? q[j] : 0u);
+          }
+          reinterpret_cast<u32x4*>(keys)[i] = q;
+        }
       }
-#pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i)
-      if (c * kChunk + i * kSelThreads < n) key[i] = weight_key(x[i]);
+    }
+    if (tid < (here & 3u)) {
+      const uint32_t i = 4u * here4 + tid, key = weight_key(w[t0 + i]);
+      keys[i] = key;
+      lo = min(lo, t0 + i < cand ? key : 0xFFFFFFFFu);
+      hi = max(hi, t0 + i < cand ? key : 0u);
+    }
   };
-  load(0u);
+  // f of every candidate's key in chunk c.
+  const auto each = [&](uint32_t c, auto f) __attribute__((always_inline)) {
+    const uint32_t here = c * kChunk < cand ? min(cand - c * kChunk, kChunk) : 0u;
+#pragma unroll 2
+    for (uint32_t i = 4u * tid; i < here; i += 4u * kSelThreads) {
+      const u32x4 q = *reinterpret_cast<const u32x4*>(keys + i);  // (the array is a multiple of four long)
+#pragma unroll
+      for (uint32_t j = 0; j < 4u; ++j)
+        if (i + j < here) f(q[j]);
+    }
+  };
+  for (uint32_t c = 0; c < chunks; ++c) {
+    if (c > 0u) __syncthreads();
+    load(c);
+  }
+  uint32_t held = chunks - 1u;
+  // Chunk c in LDS, for every thread.
+  const auto hold = [&](uint32_t c) __attribute__((always_inline)) {
+    if (held == c) return;
+    __syncthreads();
+    load(c);
+    held = c;
+    __syncthreads();
+  };
+  hist[tid] = 0u;
+  hist[kSelThreads + tid] = 0u;
+  if (tid == 0u) few = 0u;
+  lo = wave_extreme<false>(lo);
+  hi = wave_extreme<true>(hi);
+  if (lane == 0u) {
+    wave_sum[0][wave] = lo;
+    wave_sum[1][wave] = hi;
+  }
+  __syncthreads();
 
   uint32_t T = 0xFFFFFFFFu, equal = 0u;  // rem == 0: no key is above T, and none equal is taken
   if (rem > 0u) {
-    uint32_t lo = 0xFFFFFFFFu, hi = 0u;
-    for (uint32_t c = 0; c < chunks; ++c) {
-      if (chunks > 1u) load(c);
-#pragma unroll
-      for (uint32_t i = 0; i < kPer; ++i)
-        if (c * kChunk + i * kSelThreads < cand) {
-          const bool is = c * kChunk + i * kSelThreads + tid < cand;
-          lo = min(lo, is ? key[i] : 0xFFFFFFFFu);
-          hi = max(hi, is ? key[i] : 0u);
-        }
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) {
-      lo = min(lo, (uint32_t)__shfl_xor(lo, d));
-      hi = max(hi, (uint32_t)__shfl_xor(hi, d));
-    }
-    if (lane == 0u) {
-      hist[wave] = lo;
-      hist[kSelWaves + wave] = hi;
-    }
-    __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kSelWaves; ++i) {
-      lo = min(lo, hist[i]);
-      hi = max(hi, hist[kSelWaves + i]);
-    }
-    __syncthreads();
+    lo = wave_extreme<false>(wave_sum[0][lane & (kSelWaves - 1u)]);
+    hi = wave_extreme<true>(wave_sum[1][lane & (kSelWaves - 1u)]);
     T = lo;
     equal = cand;
     uint32_t bits = hi == lo ? 0u : 32u - (uint32_t)__builtin_clz(hi - lo);  // keys of interest: T .. T + 2^bits - 1
     while (bits > 0u) {
       const uint32_t shift = bits > kDigit ? bits - kDigit : 0u, bins = 1u << (bits - shift);
-      hist[tid] = 0u;
-      hist[kSelThreads + tid] = 0u;
-      if (tid == 0u) few = 0u;
-      __syncthreads();
       for (uint32_t c = 0; c < chunks; ++c) {
-        if (chunks > 1u) load(c);
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; ++i) {
-          if (c * kChunk + i * kSelThreads >= cand) continue;  // (uniform: short sequences skip what they lack)
-          const uint32_t t = c * kChunk + i * kSelThreads + tid;
-          const uint32_t bin = (key[i] - T) >> shift;
-          if (t < cand && key[i] >= T && bin < bins) atomicAdd(&hist[bin], 1u);
-        }
+        hold(c);
+        each(c, [&](uint32_t key) __attribute__((always_inline)) {
+          const uint32_t bin = (key - T) >> shift;
+          if (key >= T && bin < bins) atomicAdd(&hist[bin], 1u);
+        });
       }
       __syncthreads();
       // Two bins a thread, the highest first: where the count from the top passes rem.
       const uint32_t d1 = kBins - 1u - 2u * tid, d0 = d1 - 1u, n1 = hist[d1], n0 = hist[d0];
       uint32_t all;
-      const uint32_t above = scan_before(n1 + n0, wave_sum, all);
+      const uint32_t above = scan_before(n1 + n0, wave_sum[0], all);
       if (above < rem && rem <= above + n1 + n0) {
         const bool first = rem <= above + n1;
         pick[0] = first ? d1 : d0;
@@ -275,16 +390,19 @@ __global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(4, 
       rem = pick[1];
       equal = pick[2];
       bits = shift;
-      if (bits == 0u || equal > kFew) continue;
+      if (bits == 0u) break;
+      if (equal > kFew) {
+        hist[tid] = 0u;
+        hist[kSelThreads + tid] = 0u;
+        __syncthreads();
+        continue;
+      }
       // Few keys left: collected, and each counts those above it.
       for (uint32_t c = 0; c < chunks; ++c) {
-        if (chunks > 1u) load(c);
-#pragma unroll
-        for (uint32_t i = 0; i < kPer; ++i) {
-          if (c * kChunk + i * kSelThreads >= cand) continue;
-          const uint32_t t = c * kChunk + i * kSelThreads + tid;
-          if (t < cand && key[i] >= T && (key[i] - T) >> bits == 0u) hist[atomicAdd(&few, 1u)] = key[i];
-        }
+        hold(c);
+        each(c, [&](uint32_t key) __attribute__((always_inline)) {
+          if (key >= T && (key - T) >> bits == 0u) hist[atomicAdd(&few, 1u)] = key;
+        });
       }
       __syncthreads();
       if (tid < equal) {
@@ -310,102 +428,56 @@ __global__ __launch_bounds__(kSelThreads) __attribute__((amdgpu_waves_per_eu(4, 
     }
   }
 
+  __syncthreads();  // wave_sum is free
+
   // Tokens in order: key > T, or one of the first `rem` equal to T, or last.
-  const bool all_equal = rem == equal;  // no tie to break (and rem == 0 takes none)
+  // A thread's run has an odd length, or 32 read from another place by each
+  // lane, so that the threads' reads of one step fall into different banks.
   uint32_t base = 0u, eq_base = 0u;
   for (uint32_t c = 0; c < chunks; ++c) {
-    if (chunks > 1u) load(c);
-    const uint32_t counts = min((n - c * kChunk + kSelThreads - 1u) / kSelThreads, kPer) * kSelWaves;
-    uint32_t flags = 0u;  // bit i: token i stays
-    uint32_t eq = 0u;     // bit i: equal to T
-#pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i) {
-      if (c * kChunk + i * kSelThreads >= n) continue;
-      const uint32_t t = c * kChunk + i * kSelThreads + tid;
-      if (t < n && (t >= cand || key[i] > T)) flags |= 1u << i;
-      if (t < cand && key[i] == T) eq |= 1u << i;
+    hold(c);
+    const uint32_t t0 = c * kChunk, here = min(n - t0, kChunk), per = (here + kSelThreads - 1u) / kSelThreads;
+    const uint32_t run = per == 32u ? 32u : per | 1u, turn = per == 32u ? lane : 0u;
+    const uint32_t i0 = min(tid * run, here), i1 = min(i0 + run, here);
+    uint32_t stay = 0u, eq = 0u;  // bit i - i0
+#pragma unroll 8
+    for (uint32_t s = 0; s < run; ++s) {
+      const uint32_t i = (s + turn) & 31u, key = keys[min(i0 + i, here - 1u)];
+      stay |= (key > T ? 1u : 0u) << i;
+      eq |= (key == T ? 1u : 0u) << i;
     }
-    const uint64_t below = (1ull << lane) - 1ull;
-    uint32_t all;
-    if (all_equal) {
-      if (rem > 0u) flags |= eq;
-    } else {
-#pragma unroll
-      for (uint32_t i = 0; i < kPer; ++i) {
-        if (c * kChunk + i * kSelThreads >= n) continue;
-        const uint64_t m = __ballot((eq >> i) & 1u);
-        if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
-      }
-      __syncthreads();
-      const uint32_t mine = tid < counts ? count[tid] : 0u;
-      const uint32_t at = scan_before(mine, wave_sum, all);
-      if (tid < counts) count[tid] = eq_base + at;
-      __syncthreads();
-#pragma unroll
-      for (uint32_t i = 0; i < kPer; ++i) {
-        if (c * kChunk + i * kSelThreads >= n) continue;
-        const uint64_t m = __ballot((eq >> i) & 1u);
-        if (((eq >> i) & 1u) && count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below) < rem) flags |= 1u << i;
-      }
-      eq_base += all;
-      __syncthreads();
+    // Only what is in the run; the last tokens, no candidates, all stay.
+    const auto first = [](uint32_t k) { return k >= 32u ? 0xFFFFFFFFu : (1u << k) - 1u; };
+    const uint32_t in = first(i1 - i0), cands = first(t0 + i0 < cand ? cand - (t0 + i0) : 0u);
+    stay = in & (stay | ~cands);
+    eq &= in & cands;
+    uint32_t all, eq_all;
+    uint32_t at = base + scan_before((uint32_t)__popc(stay), wave_sum[0], all);
+    const uint32_t eq_at = eq_base + scan_before((uint32_t)__popc(eq), wave_sum[1], eq_all);
+    // Of the equal ones before this run, the first rem stayed; of its own, as many as are left.
+    at += min(eq_at, rem) - min(eq_base, rem);
+    for (uint32_t left = rem - min(eq_at, rem); left > 0u && eq != 0u; --left) {
+      stay |= eq & -eq;
+      eq &= eq - 1u;
     }
-#pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i) {
-      if (c * kChunk + i * kSelThreads >= n) continue;
-      const uint64_t m = __ballot((flags >> i) & 1u);
-      if (lane == 0u) count[i * kSelWaves + wave] = (uint32_t)__popcll(m);
+    for (; stay != 0u && at < to; stay &= stay - 1u, ++at) {
+      const uint32_t i = i0 + (uint32_t)__builtin_ctz(stay);
+      if (at < from) continue;
+      kp[at] = (int32_t)(t0 + i);
+      ow[at] = key_weight(keys[i]);
     }
-    __syncthreads();
-    const uint32_t mine = tid < counts ? count[tid] : 0u;
-    const uint32_t at0 = scan_before(mine, wave_sum, all);
-    if (tid < counts) count[tid] = base + at0;
-    __syncthreads();
-#pragma unroll
-    for (uint32_t i = 0; i < kPer; ++i) {
-      if (c * kChunk + i * kSelThreads >= n) continue;
-      const uint64_t m = __ballot((flags >> i) & 1u);
-      const uint32_t at = count[i * kSelWaves + wave] + (uint32_t)__popcll(m & below);
-      if (((flags >> i) & 1u) && at < keep) {
-        const uint32_t t = c * kChunk + i * kSelThreads + tid;
-        kp[at] = (int32_t)t;
-        ow[at] = key_weight(key[i]);
-      }
-    }
-    base += all;
-    __syncthreads();
+    base += all + min(eq_base + eq_all, rem) - min(eq_base, rem);
+    eq_base += eq_all;
+    __syncthreads();  // wave_sum is free again; the share's tokens are written
   }
+  if (copy) copy_rows<kSelThreads>(a, b, h, from, to);
 }
 
-// Rows of the kept tokens to their new places: 16 bytes a thread, the K row
-// and the V row of one token; the scale bytes by the row's first threads.
-__global__ __launch_bounds__(256) void evict_copy_kernel(KvPool src, const int32_t* __restrict__ src_table,
-                                                         int64_t src_width, KvPool dst,
-                                                         const int32_t* __restrict__ dst_table, int64_t dst_width,
-                                                         const int32_t* __restrict__ kept, int64_t budget,
-                                                         uint32_t pieces, uint32_t row_bytes) {
-  const uint32_t h = blockIdx.y, b = blockIdx.z;
-  const uint32_t at = blockIdx.x * (256u / pieces) + threadIdx.x / pieces, piece = threadIdx.x % pieces;
-  if (at >= (uint32_t)budget || threadIdx.x >= 256u / pieces * pieces) return;
-  const int32_t t = kept[((size_t)b * src.kv_heads + h) * (size_t)budget + at];
-  if (t < 0) return;
-  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)src.page_size), in_page = (uint32_t)src.page_size - 1u;
-  const int32_t sp = src_table[(size_t)b * src_width + ((uint32_t)t >> shift)];
-  const int32_t dp = dst_table[(size_t)b * dst_width + (at >> shift)];
-  if (sp < 0 || sp >= src.pages || dp < 0 || dp >= dst.pages) return;
-  const uint64_t from = (((uint64_t)(uint32_t)sp * src.kv_heads + h) << shift) + ((uint32_t)t & in_page);
-  const uint64_t to = (((uint64_t)(uint32_t)dp * dst.kv_heads + h) << shift) + (at & in_page);
-  const u32x4 k = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(src.k) + from * row_bytes + piece * 16u);
-  const u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(src.v) + from * row_bytes + piece * 16u);
-  *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(dst.k) + to * row_bytes + piece * 16u) = k;
-  *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(dst.v) + to * row_bytes + piece * 16u) = v;
-  if (src.fmt != kKvBf16) {
-    const uint32_t pairs = (uint32_t)src.head_dim / 64u;  // scale bytes two by two
-    for (uint32_t i = piece; i < pairs; i += pieces) {
-      reinterpret_cast<uint16_t*>(dst.ks)[to * pairs + i] = reinterpret_cast<const uint16_t*>(src.ks)[from * pairs + i];
-      reinterpret_cast<uint16_t*>(dst.vs)[to * pairs + i] = reinterpret_cast<const uint16_t*>(src.vs)[from * pairs + i];
-    }
-  }
+constexpr uint32_t kCopyThreads = 256, kCopyRows = 64;  // of a workgroup of the copies' own launch
+__global__ __launch_bounds__(kCopyThreads) void evict_copy_kernel(EvictArgs a) {
+  const int64_t l = a.lens[blockIdx.z], len = l < 0 ? 0 : (l < a.max_len ? l : a.max_len);
+  const uint32_t keep = (uint32_t)(len < a.budget ? len : a.budget), from = blockIdx.x * kCopyRows;
+  if (from < keep) copy_rows<kCopyThreads>(a, blockIdx.z, blockIdx.y, from, min(from + kCopyRows, keep));
 }
 
 }  // namespace
@@ -430,15 +502,21 @@ hipError_t launch_kv_evict(const KvPool& src, const int32_t* src_table, int64_t 
                            int64_t dst_width, int32_t* out_lens, float* out_weights, int64_t out_stride,
                            int32_t* kept, int64_t B, int64_t max_len, int64_t budget, int64_t recent, void*,
                            hipStream_t stream) {
-  evict_select_kernel<<<dim3((uint32_t)src.kv_heads, (uint32_t)B), kSelThreads, 0, stream>>>(
-      lens, weights, weights_stride, out_lens, out_weights, out_stride, kept, (uint32_t)src.kv_heads, max_len, budget,
-      recent);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || budget == 0 || max_len == 0) return e;
-  const uint32_t row_bytes = kv_row_bytes(src.fmt, (uint32_t)src.head_dim), pieces = row_bytes / 16u;
-  const uint32_t rows = 256u / pieces;
-  evict_copy_kernel<<<dim3((uint32_t)((budget + rows - 1) / rows), (uint32_t)src.kv_heads, (uint32_t)B), 256, 0,
-                      stream>>>(src, src_table, src_width, dst, dst_table, dst_width, kept, budget, pieces, row_bytes);
+  const EvictArgs a{src, src_table, src_width, lens, weights, weights_stride, dst, dst_table, dst_width, out_lens,
+                    out_weights, out_stride, kept, max_len, budget, recent,
+                    kv_row_bytes(src.fmt, (uint32_t)src.head_dim)};
+  const uint32_t lds = (uint32_t)(max_len < (int64_t)kChunk ? (max_len + 3) / 4 * 4 : (int64_t)kChunk) * 4u;
+  const int64_t heads = B * src.kv_heads, most = budget < max_len ? budget : max_len;
+  const bool one = max_len <= (int64_t)kChunk;
+  // One launch: parts that bring the workgroups to about one a CU, of at least 16 tokens each.
+  int64_t parts = one ? 256 / heads : 1;
+  if (parts > (most + 15) / 16) parts = (most + 15) / 16;
+  if (parts < 1) parts = 1;
+  evict_kernel<<<dim3((uint32_t)parts, (uint32_t)src.kv_heads, (uint32_t)B), kSelThreads, lds, stream>>>(a, one);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || one || most == 0) return e;
+  evict_copy_kernel<<<dim3((uint32_t)((most + kCopyRows - 1) / kCopyRows), (uint32_t)src.kv_heads, (uint32_t)B),
+                      kCopyThreads, 0, stream>>>(a);
   return hipGetLastError();
 }
 

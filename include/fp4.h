@@ -518,6 +518,7 @@ size_t fp4_kv_evict_workspace(const fp4_kv_cache* cache, int64_t B, int64_t max_
  *   out_lens[b] = min(lens[b], budget).  out_weights: FP32 B x kv_heads x
  *   out_stride, the kept tokens' weights (-0 as +0), then zeros; out_stride >= budget.
  *   kept: int32 B x kv_heads x budget, the kept tokens' old numbers, then -1.
+ *   No output may overlap an input (other than the pools, as said).
  *   dst has src's fmt, heads, head_dim and page_size; dst_width * page_size >=
  *   min(budget, max_len).  A kept token whose page (old or new) is outside the
  *   pool is not copied.
