@@ -22,6 +22,14 @@
 //     elements g D/4 .. (g+1) D/4 of token c, contiguous in memory.
 //   - MXFP8 / MXFP4 rows are converted to BF16 by the scaling converters
 //     (exact: at most 4 significant bits).
+//   - The tiles of all (sequence, kv head) units laid end to end are cut into
+//     equal shares, one for each of two workgroups a CU, whatever the lengths:
+//     a workgroup walks its share, which may end one unit, hold several and
+//     begin another.  The units that are cut are joined from the workgroups'
+//     partial results by the last of them to arrive.  (A fixed number of
+//     splits per sequence leaves the chip waiting for the longest: 4 x 131071
+//     MXFP8 tokens took 239 us in 2048 workgroups of which 1280 fit, 202 us in
+//     512 that all fit and are equal.)
 //   - Softmax statistics are FP32 and running.  The reference maximum of a
 //     head moves only when a score passes it by 2^kLazy, so most tiles need
 //     no reduction across lanes and no rescaling.
@@ -35,8 +43,8 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kTile = 32;             // tokens of a wave's step
 constexpr int kWaves = 4;             // waves of a workgroup, taking every fourth tile
-constexpr int kMinTiles = 8;          // tiles below which a sequence is not split further
-constexpr int kMaxSplits = 64;
+constexpr uint32_t kGrain = 8;        // shares and units are whole multiples of this many tiles
+constexpr uint32_t kGroups = 512;     // workgroups: two a CU
 constexpr int kHeadTile = 16;         // query heads of a workgroup
 // Scores may pass the reference maximum by this much (in powers of two)
 // before it moves: probabilities up to 2^8, no loss in FP32 or BF16.
@@ -60,9 +68,10 @@ struct AttnArgs {
   void* out;
   float* lse;
   int32_t q_f32, out_f32;
-  uint32_t* done;      // B x kv_heads x head_tiles arrival counters
-  float* part;         // B x q_heads x splits x D partial sums
-  float* stats;        // B x q_heads x splits x (maximum, sum)
+  int32_t batch;
+  uint32_t* done;      // arrival counters, one for each workgroup that begins a unit
+  float* part;         // partial sums: workgroups x 2 x 16 heads x D
+  float* stats;        // (maximum, sum): workgroups x 2 x 16 heads x 2
   float* final_stats;  // B x q_heads x (maximum, 1 / sum), for the weights
   float* scores;       // B x q_heads x score_stride, or null
   int64_t score_stride;
@@ -171,23 +180,68 @@ __device__ __forceinline__ void store_out2(const AttnArgs& a, size_t i, float x,
 }
 
 // The tokens of a sequence that the call attends to, in tiles of 32 aligned
-// to the pages (a page is at least 16 tokens), and their split.
+// to the pages (a page is at least 16 tokens).
 struct Range {
-  uint32_t first, len;     // tokens [first, len)
-  uint32_t tile0, tiles;   // tiles of the sequence from tile0 on
-  uint32_t per, splits;    // tiles of a split; splits that have any
+  uint32_t first, len;    // tokens [first, len)
+  uint32_t tile0, tiles;  // tiles of the sequence from tile0 on
+  // Tiles the work is counted in: whole grains, and one at least (an empty
+  // sequence's result has to be written too).
+  __device__ __forceinline__ uint32_t counted() const { return max((tiles + kGrain - 1u) / kGrain, 1u) * kGrain; }
 };
-__device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b, uint32_t max_splits) {
+__device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b) {
   Range r;
   const int64_t l = a.lens[b];
   r.len = (uint32_t)(l < 0 ? 0 : l < a.max_len ? l : a.max_len);
   r.first = a.window > 0 && a.window < (int64_t)r.len ? r.len - (uint32_t)a.window : 0u;
   r.tile0 = r.first / kTile;
   r.tiles = a.c.pages > 0 ? (r.len + kTile - 1) / kTile - r.tile0 : 0u;  // an empty pool has nothing to read
-  r.per = (r.tiles + max_splits - 1) / max_splits;
-  if (r.per < (uint32_t)kMinTiles) r.per = kMinTiles;
-  r.splits = (r.tiles + r.per - 1) / r.per;
   return r;
+}
+
+// A workgroup's share [pos, end) of the tiles laid end to end, sequence b
+// beginning at `base` (in tiles of one unit; a sequence has `units` of them).
+struct Share {
+  uint64_t pos, end, base;
+  uint32_t share, b;
+};
+__device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
+  const uint32_t lane = threadIdx.x & 63u, B = (uint32_t)a.batch;
+  const uint32_t each = (B + 63u) / 64u, b0 = lane * each;  // sequences of a lane
+  uint64_t mine = 0u;
+  for (uint32_t i = 0u; i < each; ++i)
+    if (b0 + i < B) mine += range_of(a, b0 + i).counted();
+  uint64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up((unsigned long long)upto, d);
+    if (lane >= (uint32_t)d) upto += o;
+  }
+  Share s;
+  const uint64_t total = __shfl((unsigned long long)upto, 63) * units;
+  s.share = (uint32_t)((total + kGrain * gridDim.x - 1u) / (kGrain * gridDim.x)) * kGrain;
+  s.pos = (uint64_t)blockIdx.x * s.share;
+  s.end = min(s.pos + s.share, total);
+  const uint64_t past = __ballot(upto * units > s.pos);
+  const int at = past == 0u ? 0 : (int)__builtin_ctzll(past);
+  s.base = __shfl((unsigned long long)(upto - mine), at);
+  s.b = (uint32_t)at * each;
+  while (s.pos < s.end) {
+    const uint32_t v = range_of(a, s.b).counted();
+    if ((s.base + v) * units > s.pos) break;
+    s.base += v;
+    ++s.b;
+  }
+  // The same in every lane; said so, for scalar registers.
+  const auto uniform = [](uint64_t x) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x) |
+           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(x >> 32)) << 32;
+  };
+  s.pos = uniform(s.pos);
+  s.end = uniform(s.end);
+  s.base = uniform(s.base);
+  s.share = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.share);
+  s.b = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.b);
+  return s;
 }
 
 template <int FMT, int D, bool EX>
@@ -206,16 +260,26 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   __shared__ float wave_m[kWaves][kHeadTile], wave_l[kWaves][kHeadTile];
   __shared__ uint32_t last_arrival;
 
-  const uint32_t split = blockIdx.x, max_splits = gridDim.x, b = blockIdx.z;
-  const uint32_t h = blockIdx.y / (uint32_t)a.head_tiles, ht = blockIdx.y % (uint32_t)a.head_tiles;
-  const Range r = range_of(a, b, max_splits);
-  if (split >= r.splits && split > 0u) return;
-
   const uint32_t lane = threadIdx.x & 63u, c = lane & 15u, g = lane >> 4;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)a.c.page_size), in_page = (uint32_t)a.c.page_size - 1u;
+  const uint32_t units = (uint32_t)a.c.kv_heads * (uint32_t)a.head_tiles;
+  Share w = share_of(a, units);
+
+  for (; w.pos < w.end;) {
+  // The share's next piece: tiles [t_begin, t_end) of unit `unit` of sequence b.
+  const uint32_t b = w.b;
+  const Range r = range_of(a, b);
+  const uint32_t counted = r.counted(), unit = (uint32_t)((w.pos - w.base * units) / counted);
+  const uint64_t unit0 = w.base * units + (uint64_t)unit * counted;
+  const uint32_t t_begin = (uint32_t)(w.pos - unit0);
+  const uint32_t t_upto = (uint32_t)min((uint64_t)counted, (uint64_t)t_begin + (w.end - w.pos));
+  const uint32_t t_end = min(t_upto, r.tiles);
+  // The workgroups that have a piece of the unit.
+  const uint32_t wg0 = (uint32_t)(unit0 / w.share), pieces = (uint32_t)((unit0 + counted - 1u) / w.share) - wg0 + 1u;
+  const uint32_t h = unit / (uint32_t)a.head_tiles, ht = unit % (uint32_t)a.head_tiles;
   const uint32_t heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
   const uint32_t head0 = h * (uint32_t)a.group + ht * kHeadTile;  // first query head
-  const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)a.c.page_size), in_page = (uint32_t)a.c.page_size - 1u;
 
   // Q: head c's elements g D/4 + 8 s .. + 7 in step s; zero for heads past the group.
   v8bf q[kQTerms][kSteps];
@@ -250,7 +314,6 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   for (int e = 0; e < EV; ++e) o[e] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
   float m = -INFINITY, l = 0.0f;  // of head c; l of this lane's tokens alone
 
-  const uint32_t t_end = min((split + 1u) * r.per, r.tiles);
   const uint32_t pages_used = (r.len + in_page) >> shift;
   const int32_t* table = a.table + (size_t)b * (size_t)a.width;
 
@@ -292,7 +355,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     }
   };
 
-  uint32_t tile = split * r.per + wave;
+  uint32_t tile = t_begin + wave;
   uint64_t row[2] = {~0ull, ~0ull}, next[2] = {~0ull, ~0ull};
   if (tile < t_end) {
     row[0] = half_row(tile, 0);
@@ -462,7 +525,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     if (a.final_stats) *reinterpret_cast<v2f*>(a.final_stats + 2 * at) = v2f{mx, s == 0.0f ? 0.0f : 1.0f / s};
   };
 
-  if (r.splits <= 1u) {
+  if (pieces == 1u) {
     for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
       const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
       float mx;
@@ -475,65 +538,99 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       const float s = head_sum(threadIdx.x, mx);
       finish_head(threadIdx.x, mx, s);
     }
-    return;
-  }
-
-  // ---- the splits' results: written through, then the last to arrive joins ----
-  const size_t part0 = ((size_t)b * (uint32_t)a.q_heads + head0) * max_splits;
-  for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
-    const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-    store2_agent(a.part + (part0 + (size_t)hd * max_splits + split) * D + d, red[0][hd][d] + red[1][hd][d],
-                 red[0][hd][d + 1] + red[1][hd][d + 1]);
-  }
-  if (threadIdx.x < heads) {
-    float mx;
-    const float s = head_sum(threadIdx.x, mx);
-    store2_agent(a.stats + 2 * (part0 + (size_t)threadIdx.x * max_splits + split), mx, s);
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
-  __syncthreads();
-  uint32_t* done = a.done + ((size_t)b * gridDim.y + blockIdx.y);
-  if (threadIdx.x == 0u) {
-    const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last_arrival = before == r.splits - 1u;
-    if (last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!last_arrival) return;
-
-  // Factors 2^(m_s - M) of every head and split (the red array is free now).
-  float* factor = &red[0][0][0];  // heads x kMaxSplits, fits: 16 x 64 <= 2 x 16 x 68
-  static_assert(kHeadTile * kMaxSplits <= 2 * kHeadTile * kPad, "factors fit in the array they reuse");
-  for (uint32_t hd = wave; hd < heads; hd += kWaves) {
-    v2f ms = v2f{-INFINITY, 0.0f};
-    if (lane < r.splits) ms = load2_agent(a.stats + 2 * (part0 + (size_t)hd * max_splits + lane));
-    float mx = ms[0];
+  } else {
+    // ---- the pieces' results: written through, then the last to arrive joins ----
+    // A workgroup has two places: for a unit it begins, and for one begun before.
+    const uint32_t mine = (2u * blockIdx.x + (t_begin == 0u ? 1u : 0u)) * kHeadTile;
+    for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
+      const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
+      store2_agent(a.part + (size_t)(mine + hd) * D + d, red[0][hd][d] + red[1][hd][d],
+                   red[0][hd][d + 1] + red[1][hd][d + 1]);
+    }
+    if (threadIdx.x < heads) {
+      float mx;
+      const float s = head_sum(threadIdx.x, mx);
+      store2_agent(a.stats + 2u * (mine + threadIdx.x), mx, s);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
+    __syncthreads();
+    if (threadIdx.x == 0u) {
+      uint32_t* done = a.done + wg0;  // of the units a workgroup begins only the last is cut
+      const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last_arrival = before == pieces - 1u;
+      if (last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (last_arrival) {
+      // Place of piece p, and its head hd.
+      const auto place = [&](uint32_t p, uint32_t hd) { return (2u * (wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile + hd; };
+      // Maximum and sum of every head over the pieces; then 64 pieces at a
+      // time, factors 2^(m_p - M) / L in the red array, free now.
+      for (uint32_t hd = wave; hd < heads; hd += kWaves) {
+        float mx = -INFINITY, s = 0.0f;
+        for (uint32_t p = lane; p < pieces; p += 64u) {
+          const v2f ms = load2_agent(a.stats + 2u * place(p, hd));
+          const float to = fmaxf(mx, ms[0]);
+          s = (mx == -INFINITY ? 0.0f : s * exp2_fast(mx - to)) + (ms[0] == -INFINITY ? 0.0f : ms[1] * exp2_fast(ms[0] - to));
+          mx = to;
+        }
+        const float all = wave_fmax(mx);
+        s = wave_fsum(mx == -INFINITY ? 0.0f : s * exp2_fast(mx - all));
+        if (lane == 0u) {
+          wave_m[0][hd] = all;
+          wave_l[0][hd] = s == 0.0f ? 0.0f : 1.0f / s;
+          finish_head(hd, all, s);
+        }
+      }
+      __syncthreads();
+      float* factor = &red[0][0][0];  // 16 x 64
+      static_assert(kHeadTile * 64 <= 2 * kHeadTile * kPad, "factors fit in the array they reuse");
+      constexpr uint32_t kItems = kHeadTile * (D / 2) / 256;  // pairs of elements of a thread, at most
+      float x[kItems], y[kItems];
 #pragma unroll
-    for (int i = 32; i > 0; i >>= 1) mx = fmaxf(mx, __shfl_xor(mx, i));
-    const float fs = ms[0] == -INFINITY ? 0.0f : exp2_fast(ms[0] - mx);
-    float s = ms[1] * fs;
+      for (uint32_t k = 0; k < kItems; ++k) x[k] = y[k] = 0.0f;
+      for (uint32_t p0 = 0u; p0 < pieces; p0 += 64u) {
+        const uint32_t here = min(pieces - p0, 64u);
+        for (uint32_t hd = wave; hd < heads; hd += kWaves) {
+          const float m_p = lane < here ? load2_agent(a.stats + 2u * place(p0 + lane, hd))[0] : -INFINITY;
+          factor[hd * 64u + lane] = m_p == -INFINITY ? 0.0f : exp2_fast(m_p - wave_m[0][hd]) * wave_l[0][hd];
+        }
+        __syncthreads();
 #pragma unroll
-    for (int i = 32; i > 0; i >>= 1) s += __shfl_xor(s, i);
-    factor[hd * kMaxSplits + lane] = s == 0.0f ? 0.0f : fs / s;
-    if (lane == 0u) finish_head(hd, mx, s);
-  }
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
-    const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-    const float* from = a.part + (part0 + (size_t)hd * max_splits) * D + d;
-    float x = 0.0f, y = 0.0f;
-    for (uint32_t s0 = 0u; s0 < r.splits; s0 += 8u) {
-      v2f v[8];
+        for (uint32_t k = 0; k < kItems; ++k) {
+          const uint32_t i = k * 256u + threadIdx.x;
+          if (i < heads * (D / 2)) {
+            const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
+            for (uint32_t q0 = 0u; q0 < here; q0 += 8u) {
+              v2f v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = load2_agent(from + (size_t)min(s0 + k, r.splits - 1u) * D);
+              for (uint32_t j = 0; j < 8u; ++j)
+                v[j] = load2_agent(a.part + (size_t)place(p0 + min(q0 + j, here - 1u), hd) * D + d);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float w = s0 + k < r.splits ? factor[hd * kMaxSplits + s0 + k] : 0.0f;
-        x = s0 + k < r.splits ? __builtin_fmaf(w, v[k][0], x) : x;
-        y = s0 + k < r.splits ? __builtin_fmaf(w, v[k][1], y) : y;
+              for (uint32_t j = 0; j < 8u; ++j) {
+                if (q0 + j >= here) continue;
+                x[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][0], x[k]);
+                y[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][1], y[k]);
+              }
+            }
+          }
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (uint32_t k = 0; k < kItems; ++k) {
+        const uint32_t i = k * 256u + threadIdx.x;
+        if (i < heads * (D / 2))
+          store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + i / (D / 2)) * D + 2u * (i % (D / 2)), x[k], y[k]);
       }
     }
-    store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + d, x, y);
+  }
+  w.pos += t_upto - t_begin;
+  if (t_upto == counted && unit + 1u == units) {
+    w.base += counted;
+    ++w.b;
+  }
+  __syncthreads();  // the shared arrays are free for the next piece
   }
 }
 
@@ -541,7 +638,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 // stored scores: p = 2^(x - M) / L.  Four tokens a thread.
 __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
   const uint32_t h = blockIdx.y, b = blockIdx.z, t = (blockIdx.x * 256u + threadIdx.x) * 4u;
-  const Range r = range_of(a, b, 1u);
+  const Range r = range_of(a, b);
   if (t >= r.len) return;
   const size_t at = ((size_t)b * gridDim.y + h) * (size_t)a.w_stride + t;
   const uint32_t n = min(r.len - t, 4u);
@@ -561,22 +658,11 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
     if (i < n) a.w_out[at + i] = (a.w_in ? a.w_in[at + i] : 0.0f) + w[i];
 }
 
-// Workgroups that fill the chip's 256 CUs a few times over even where the
-// lengths are ragged.
-uint32_t splits_of(int64_t B, int64_t units, int64_t max_len) {
-  int64_t s = (2048 + B * units - 1) / (B * units);
-  if (s < 8) s = 8;
-  if (s > kMaxSplits) s = kMaxSplits;
-  const int64_t most = (max_len + kMinTiles * kTile - 1) / (kMinTiles * kTile) + 1;  // + 1: a window may start inside a tile
-  if (s > most) s = most;
-  return (uint32_t)(s < 1 ? 1 : s);
-}
-
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
-// The workspace: arrival counters, then statistics, partial sums, scores.
+// The workspace: arrival counters (zero between calls), then statistics, partial sums, scores.
 struct Layout {
-  uint32_t splits;
+  uint32_t groups;
   int64_t head_tiles, score_stride;
   size_t done, stats, final_stats, part, scores, total;
 };
@@ -584,19 +670,24 @@ Layout layout_of(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_
   Layout w{};
   w.head_tiles = (q_heads / kv_heads + kHeadTile - 1) / kHeadTile;
   w.score_stride = (max_len + kTile - 1) / kTile * kTile;
-  w.splits = B == 0 || q_heads == 0 ? 1u : splits_of(B, kv_heads * w.head_tiles, max_len);
-  const bool join = w.splits > 1;
+  const int64_t units = B * kv_heads * w.head_tiles;
+  const int64_t grains = max_len == 0 ? 1 : (max_len + kTile * kGrain - 1) / (kTile * kGrain);
+  w.groups = units > kGroups || units * grains > kGroups ? kGroups : (uint32_t)(units * grains);
+  // Units of one grain each are never cut.
+  const bool join = grains > 1;
+  // The counters take the same place whatever the sizes, so that no other
+  // call's data ever lies where a call expects zeros.
   w.done = 0;
-  w.stats = w.done + (join ? round16((size_t)(B * kv_heads * w.head_tiles) * 4) : 0);
-  w.final_stats = w.stats + (join ? round16((size_t)(B * q_heads) * w.splits * 8) : 0);
+  w.stats = join || weights ? (size_t)kGroups * 4 : 0;
+  w.final_stats = w.stats + (join ? (size_t)w.groups * 2 * kHeadTile * 8 : 0);
   w.part = w.final_stats + (weights ? round16((size_t)(B * q_heads) * 8) : 0);
-  w.scores = w.part + (join ? round16((size_t)(B * q_heads) * w.splits * (size_t)D * 4) : 0);
+  w.scores = w.part + (join ? (size_t)w.groups * 2 * kHeadTile * (size_t)D * 4 : 0);
   w.total = w.scores + (weights ? (size_t)(B * q_heads) * (size_t)w.score_stride * 4 : 0);
   return w;
 }
 
 template <int FMT, int D>
-void launch_d(const AttnArgs& a, dim3 grid, bool exact, hipStream_t stream) {
+void launch_d(const AttnArgs& a, uint32_t grid, bool exact, hipStream_t stream) {
   if (exact)
     attn_decode_kernel<FMT, D, true><<<grid, 256, 0, stream>>>(a);
   else
@@ -604,7 +695,7 @@ void launch_d(const AttnArgs& a, dim3 grid, bool exact, hipStream_t stream) {
 }
 
 template <int FMT>
-void launch_fmt(const AttnArgs& a, dim3 grid, bool exact, hipStream_t stream) {
+void launch_fmt(const AttnArgs& a, uint32_t grid, bool exact, hipStream_t stream) {
   switch (a.c.head_dim) {
     case 64: return launch_d<FMT, 64>(a, grid, exact, stream);
     case 128: return launch_d<FMT, 128>(a, grid, exact, stream);
@@ -638,6 +729,7 @@ hipError_t launch_attn_decode(const KvPool& c, const void* q, int q_dtype, int64
   a.q_heads = (int32_t)q_heads;
   a.group = (int32_t)(q_heads / c.kv_heads);
   a.head_tiles = (int32_t)w.head_tiles;
+  a.batch = (int32_t)B;
   a.max_len = max_len;
   a.window = window;
   a.scale_log2 = scale * kLog2e;
@@ -657,11 +749,10 @@ hipError_t launch_attn_decode(const KvPool& c, const void* q, int q_dtype, int64
     a.w_stride = weights_stride;
   }
   const bool exact = q_dtype == kDtF32 || out_dtype == kDtF32;
-  const dim3 grid(w.splits, (uint32_t)(c.kv_heads * w.head_tiles), (uint32_t)B);
   switch (c.fmt) {
-    case kKvBf16: launch_fmt<kKvBf16>(a, grid, exact, stream); break;
-    case kKvMx8: launch_fmt<kKvMx8>(a, grid, exact, stream); break;
-    default: launch_fmt<kKvMx4>(a, grid, exact, stream); break;
+    case kKvBf16: launch_fmt<kKvBf16>(a, w.groups, exact, stream); break;
+    case kKvMx8: launch_fmt<kKvMx8>(a, w.groups, exact, stream); break;
+    default: launch_fmt<kKvMx4>(a, w.groups, exact, stream); break;
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !weights_out || max_len == 0) return e;

@@ -617,8 +617,13 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
 // Workgroups of a row: one where the rows alone fill the chip, else pieces of
 // at least 2048 logits (8 a thread), as many as give about 512 workgroups,
 // with all their top keys within one workgroup's candidates.
+constexpr int64_t kRowGroups = 512;
+// The counters take the same place whatever the sizes, so that no other
+// call's data ever lies where a call expects zeros.  (Rows are split only
+// where there are fewer than kRowGroups.)
+constexpr size_t kDoneBytes = (size_t)kRowGroups * 4;
 uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
-  int64_t s = (512 + N - 1) / N;
+  int64_t s = (kRowGroups + N - 1) / N;
   const int64_t most = (V + 2047) / 2048;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;
@@ -626,14 +631,12 @@ uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
   return (uint32_t)(s < 1 ? 1 : s);
 }
 
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
-
 }  // namespace
 
 size_t logprobs_workspace(int64_t N, int64_t V, int32_t top_k) {
   if (N == 0) return 0;
   const size_t s = splits_of(N, V, top_k);
-  return s == 1 ? 0 : round16((size_t)N * 4) + (size_t)N * s * (16 + 8 * (size_t)top_k);
+  return s == 1 ? 0 : kDoneBytes + (size_t)N * s * (16 + 8 * (size_t)top_k);
 }
 
 hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale,
@@ -645,8 +648,8 @@ hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, 
          nullptr};
   if (s > 1) {
     a.done = reinterpret_cast<uint32_t*>(ws);
-    a.stats = reinterpret_cast<float*>(ws + round16((size_t)N * 4));
-    a.keys = reinterpret_cast<uint64_t*>(ws + round16((size_t)N * 4) + (size_t)N * s * 16);
+    a.stats = reinterpret_cast<float*>(ws + kDoneBytes);
+    a.keys = reinterpret_cast<uint64_t*>(ws + kDoneBytes + (size_t)N * s * 16);
   }
   // Rows in the grid's y, at most 65535 a launch.
   for (int64_t n0 = 0; n0 < N; n0 += 65535) {

@@ -308,3 +308,38 @@ def test_attention_of_an_empty_pool():
                                weights=w, weights_out=w_out)
     assert not out.any()
     assert torch.equal(w_out[..., :300], w[..., :300]) and not w_out[..., 300:].any()
+
+
+def test_decode_calls_share_one_workspace():
+    """Attention of many and of few sequences, long and short, and log
+    probabilities in turn on one zero-filled workspace of the largest size:
+    each call's bits are those of a workspace of its own."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    pools = make(95, "bf16", 600, 2, 32, 64)
+    cache = cache_of(pools)
+    rng = np.random.default_rng(5)
+    calls = []
+    for B, width, G in ((1, 100, 4), (40, 12, 1), (3, 80, 16), (200, 3, 2), (7, 60, 20)):
+        table = to_dev(rng.integers(0, 600, (B, width)).astype(np.int32))
+        lens = to_dev(rng.integers(0, width * 32 + 1, B).astype(np.int32))
+        q = torch.randn((B, 2 * G, 64), device="cuda").to(torch.bfloat16)
+        w = torch.zeros((B, 2, width * 32), device="cuda") if G == 4 else None
+        size = fp4.attention_workspace(cache, B, 2 * G, width * 32, w is not None)
+        calls.append((size, lambda ws, q=q, t=table, n=lens, w=w: [
+            fp4.decode_attention(q, cache, t, n, weights_out=w, ws=ws)] + ([] if w is None else [w.clone()])))
+    for n, v in ((1, 60000), (300, 9000)):
+        x, tok = torch.randn((n, v), device="cuda"), torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+        size = fp4.logprobs_workspace(n, v, 20)
+
+        def call(ws, x=x, tok=tok):
+            r = fp4.logprobs(x, tok, top_k=20, ws=ws)
+            return [r.logp, r.entropy, r.top_logp, r.top_index]
+        calls.append((size, call))
+    say("decode calls on workspaces of their own")
+    want = [f(None if s is None else s) for s, f in calls]
+    ws = torch.zeros(max(s.numel() for s, _ in calls if s is not None), dtype=torch.uint8, device="cuda")
+    say("decode calls on one workspace")
+    for i in list(range(len(calls))) * 2 + list(range(len(calls)))[::-1] * 2:
+        for got, w in zip(calls[i][1](ws), want[i]):
+            assert torch.equal(got, w), i
