@@ -198,32 +198,40 @@ __device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b) {
   return r;
 }
 
+// Inclusive sum over the lanes up to this one (DPP: within rows of 16, then
+// each row's last lane to the next row, then lane 31 to the upper half).
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xA, 0xF, false);
+  v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xC, 0xF, false);
+  return v;
+}
+
 // A workgroup's share [pos, end) of the tiles laid end to end, sequence b
 // beginning at `base` (in tiles of one unit; a sequence has `units` of them).
+// All counts fit 32 bits: the host bounds them.
 struct Share {
-  uint64_t pos, end, base;
-  uint32_t share, b;
+  uint32_t pos, end, base, share, b;
 };
 __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
   const uint32_t lane = threadIdx.x & 63u, B = (uint32_t)a.batch;
   const uint32_t each = (B + 63u) / 64u, b0 = lane * each;  // sequences of a lane
-  uint64_t mine = 0u;
+  uint32_t mine = 0u;
   for (uint32_t i = 0u; i < each; ++i)
     if (b0 + i < B) mine += range_of(a, b0 + i).counted();
-  uint64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint64_t o = __shfl_up((unsigned long long)upto, d);
-    if (lane >= (uint32_t)d) upto += o;
-  }
+  const uint32_t upto = wave_scan(mine);
   Share s;
-  const uint64_t total = __shfl((unsigned long long)upto, 63) * units;
-  s.share = (uint32_t)((total + kGrain * gridDim.x - 1u) / (kGrain * gridDim.x)) * kGrain;
-  s.pos = (uint64_t)blockIdx.x * s.share;
-  s.end = min(s.pos + s.share, total);
+  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
+  const uint32_t grains = total / kGrain;
+  s.share = (grains / gridDim.x + (grains % gridDim.x != 0u ? 1u : 0u)) * kGrain;
+  s.pos = min(blockIdx.x * s.share, total);
+  s.end = s.pos + min(s.share, total - s.pos);
   const uint64_t past = __ballot(upto * units > s.pos);
   const int at = past == 0u ? 0 : (int)__builtin_ctzll(past);
-  s.base = __shfl((unsigned long long)(upto - mine), at);
+  s.base = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), at);
   s.b = (uint32_t)at * each;
   while (s.pos < s.end) {
     const uint32_t v = range_of(a, s.b).counted();
@@ -231,16 +239,6 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
     s.base += v;
     ++s.b;
   }
-  // The same in every lane; said so, for scalar registers.
-  const auto uniform = [](uint64_t x) {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)x) |
-           (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(x >> 32)) << 32;
-  };
-  s.pos = uniform(s.pos);
-  s.end = uniform(s.end);
-  s.base = uniform(s.base);
-  s.share = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.share);
-  s.b = (uint32_t)__builtin_amdgcn_readfirstlane((int)s.b);
   return s;
 }
 
@@ -270,43 +268,24 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   // The share's next piece: tiles [t_begin, t_end) of unit `unit` of sequence b.
   const uint32_t b = w.b;
   const Range r = range_of(a, b);
-  const uint32_t counted = r.counted(), unit = (uint32_t)((w.pos - w.base * units) / counted);
-  const uint64_t unit0 = w.base * units + (uint64_t)unit * counted;
-  const uint32_t t_begin = (uint32_t)(w.pos - unit0);
-  const uint32_t t_upto = (uint32_t)min((uint64_t)counted, (uint64_t)t_begin + (w.end - w.pos));
+  const uint32_t counted = r.counted(), unit = (w.pos - w.base * units) / counted;
+  const uint32_t unit0 = w.base * units + unit * counted;
+  const uint32_t t_begin = w.pos - unit0, t_upto = min(counted, t_begin + (w.end - w.pos));
   const uint32_t t_end = min(t_upto, r.tiles);
   // The workgroups that have a piece of the unit.
-  const uint32_t wg0 = (uint32_t)(unit0 / w.share), pieces = (uint32_t)((unit0 + counted - 1u) / w.share) - wg0 + 1u;
+  const uint32_t wg0 = unit0 / w.share, pieces = (unit0 + counted - 1u) / w.share - wg0 + 1u;
   const uint32_t h = unit / (uint32_t)a.head_tiles, ht = unit % (uint32_t)a.head_tiles;
   const uint32_t heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
   const uint32_t head0 = h * (uint32_t)a.group + ht * kHeadTile;  // first query head
 
-  // Q: head c's elements g D/4 + 8 s .. + 7 in step s; zero for heads past the group.
-  v8bf q[kQTerms][kSteps];
+  // Q: head c's elements g D/4 + 8 s .. + 7 in step s; zero for heads past
+  // the group.  Asked for here, looked at once K and V are asked for too.
+  const size_t q_at = (size_t)b * (size_t)a.q_stride + (size_t)(head0 + (c < heads ? c : 0u)) * D + g * (D / 4);
+  u32x4 q_raw[kSteps];
+  if constexpr (!EX) {
 #pragma unroll
-  for (int s = 0; s < kSteps; ++s) {
-    const size_t at =
-        (size_t)b * (size_t)a.q_stride + (size_t)(head0 + (c < heads ? c : 0u)) * D + g * (D / 4) + 8 * s;
-    if constexpr (EX) {
-      float v[8];
-      if (a.q_f32) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = static_cast<const float*>(a.q)[at + i];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = u2f((uint32_t) static_cast<const uint16_t*>(a.q)[at + i] << 16);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c < heads ? v[i] : 0.0f;
-      uint32_t t[3][4];
-      split_terms<3>(v, t);
-#pragma unroll
-      for (int k = 0; k < 3; ++k) q[k][s] = frag(t[k][0], t[k][1], t[k][2], t[k][3]);
-    } else {
-      u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + at);
-      if (c >= heads) v = u32x4{0u, 0u, 0u, 0u};
-      q[0][s] = __builtin_bit_cast(v8bf, v);
-    }
+    for (int s = 0; s < kSteps; ++s)
+      q_raw[s] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.q) + q_at + 8 * s);
   }
 
   v4f o[EV];
@@ -364,6 +343,27 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     next[1] = half_row(tile + kWaves, 1);
     load_k(row);
     load_v(row);
+  }
+  v8bf q[kQTerms][kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if constexpr (EX) {
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const size_t at = q_at + 8 * s + i;
+        v[i] = a.q_f32 ? static_cast<const float*>(a.q)[at]
+                       : u2f((uint32_t) static_cast<const uint16_t*>(a.q)[at] << 16);
+        v[i] = c < heads ? v[i] : 0.0f;
+      }
+      uint32_t t[3][4];
+      split_terms<3>(v, t);
+#pragma unroll
+      for (int k = 0; k < 3; ++k) q[k][s] = frag(t[k][0], t[k][1], t[k][2], t[k][3]);
+    } else {
+      if (c >= heads) q_raw[s] = u32x4{0u, 0u, 0u, 0u};
+      q[0][s] = __builtin_bit_cast(v8bf, q_raw[s]);
+    }
   }
   for (; tile < t_end; tile += kWaves) {
     const bool more = tile + kWaves < t_end;

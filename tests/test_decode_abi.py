@@ -213,3 +213,12 @@ def test_plain_rows():
     codes = np.array([[0x21] + [0] * 15], np.uint8)
     assert list(ref.row_values(codes, np.array([[128]]), "mxfp4")[0, :3]) == [1.0, 2.0, 0.0]
     assert ref.row_values(np.array([[0x38] + [0] * 31], np.uint8), np.array([[126]]), "mxfp8")[0, 0] == 0.5
+
+
+def test_attention_counts_fit():
+    """The bound on sequences x heads x tiles that the kernel counts in 32 bits."""
+    c = cache(kv_heads=64, page_size=4096, head_dim=64)
+    big = dict(B=65535, Hq=64, qs=4096, width=1 << 15)
+    assert attn(c, max_len=1 << 20, **big) == SHAPE
+    assert fp4.fp4_attn_decode_workspace(c, 65535, 64, 1 << 20, 0) == 0
+    assert fp4.fp4_attn_decode_workspace(c, 65535, 64, 1 << 14, 0) > 0
