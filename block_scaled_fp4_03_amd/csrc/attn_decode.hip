@@ -112,6 +112,33 @@ __device__ __forceinline__ void load_bytes(const uint8_t* __restrict__ p, uint32
   }
 }
 
+// BYTES (a multiple of 8) of scales from p, 8-byte aligned.
+typedef uint32_t u32x4_by8 __attribute__((ext_vector_type(4), aligned(8)));
+template <int BYTES>
+__device__ __forceinline__ void load_scales(const uint8_t* __restrict__ p, uint32_t (&w)[BYTES / 4]) {
+  constexpr int kQuads = BYTES / 16;
+#pragma unroll
+  for (int i = 0; i < kQuads; ++i) {
+    const u32x4 v = reinterpret_cast<const u32x4_by8*>(p)[i];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[4 * i + k] = v[k];
+  }
+  if constexpr (BYTES % 16 != 0) {
+    const u32x2 v = *reinterpret_cast<const u32x2*>(p + 16 * kQuads);
+    w[4 * kQuads] = v[0];
+    w[4 * kQuads + 1] = v[1];
+  }
+}
+
+// Byte blk of token i's BLOCKS scale bytes in the dwords of four tokens.
+template <int BLOCKS>
+__device__ __forceinline__ uint32_t scale_byte(const uint32_t (&w)[BLOCKS], int i, uint32_t blk) {
+  const int at = i * BLOCKS;  // the token's first byte
+  if constexpr (BLOCKS <= 4) return (w[at / 4] >> (8u * (at % 4) + 8u * blk)) & 0xFFu;
+  const uint64_t both = (uint64_t)w[at / 4] | (uint64_t)w[at / 4 + 1] << 32;
+  return (uint32_t)(both >> (8u * (at % 4) + 8u * blk)) & 0xFFu;
+}
+
 __device__ __forceinline__ float e8m0(uint32_t byte) { return u2f(byte << 23); }
 
 // Elements 2i, 2i + 1 of a lane's piece of a row (its dwords w) times s, as a BF16 pair.
@@ -179,24 +206,38 @@ __device__ __forceinline__ void store_out2(const AttnArgs& a, size_t i, float x,
     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + i) = bf16_pair(x, y);
 }
 
+// p[i] for an index that is the same in the whole wavefront, by a scalar load
+// (page tables and lengths do not change while the kernel runs, which the
+// constant address space says).  A vector load here would be the youngest in
+// flight, and waiting for it would wait for all of K and V: 3.6 instead of
+// 4.5 TB/s over an MXFP4 cache.
+__device__ __forceinline__ int32_t load_uniform(const int32_t* p, size_t i) {
+  typedef const __attribute__((address_space(4))) int32_t* constant_ptr;
+  return ((constant_ptr)(uintptr_t)p)[i];
+}
+
 // The tokens of a sequence that the call attends to, in tiles of 32 aligned
 // to the pages (a page is at least 16 tokens).
 struct Range {
   uint32_t first, len;    // tokens [first, len)
   uint32_t tile0, tiles;  // tiles of the sequence from tile0 on
   // Tiles the work is counted in: whole grains, and one at least (an empty
-  // sequence's result has to be written too).
-  __device__ __forceinline__ uint32_t counted() const { return max((tiles + kGrain - 1u) / kGrain, 1u) * kGrain; }
+  // sequence's result has to be written too), and `more` for the time that
+  // changing from one unit to the next takes.
+  __device__ __forceinline__ uint32_t counted(uint32_t more) const {
+    return max((tiles + kGrain - 1u) / kGrain, 1u) * kGrain + more;
+  }
 };
-__device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b) {
+__device__ __forceinline__ Range range_at(const AttnArgs& a, int64_t l) {
   Range r;
-  const int64_t l = a.lens[b];
   r.len = (uint32_t)(l < 0 ? 0 : l < a.max_len ? l : a.max_len);
   r.first = a.window > 0 && a.window < (int64_t)r.len ? r.len - (uint32_t)a.window : 0u;
   r.tile0 = r.first / kTile;
   r.tiles = a.c.pages > 0 ? (r.len + kTile - 1) / kTile - r.tile0 : 0u;  // an empty pool has nothing to read
   return r;
 }
+
+__device__ __forceinline__ Range range_of(const AttnArgs& a, uint32_t b) { return range_at(a, a.lens[b]); }
 
 // Inclusive sum over the lanes up to this one (DPP: within rows of 16, then
 // each row's last lane to the next row, then lane 31 to the upper half).
@@ -214,19 +255,31 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // beginning at `base` (in tiles of one unit; a sequence has `units` of them).
 // All counts fit 32 bits: the host bounds them.
 struct Share {
-  uint32_t pos, end, base, share, b;
+  uint32_t pos, end, base, share, b, more;
 };
 __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
   const uint32_t lane = threadIdx.x & 63u, B = (uint32_t)a.batch;
   const uint32_t each = (B + 63u) / 64u, b0 = lane * each;  // sequences of a lane
   uint32_t mine = 0u;
   for (uint32_t i = 0u; i < each; ++i)
-    if (b0 + i < B) mine += range_of(a, b0 + i).counted();
-  const uint32_t upto = wave_scan(mine);
+    if (b0 + i < B) mine += range_of(a, b0 + i).counted(0u);
+  uint32_t upto = wave_scan(mine);
   Share s;
-  const uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
-  const uint32_t grains = total / kGrain;
-  s.share = (grains / gridDim.x + (grains % gridDim.x != 0u ? 1u : 0u)) * kGrain;
+  uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
+  const auto per_group = [](uint32_t tiles) {
+    const uint32_t n = tiles / kGrain;
+    return (n / gridDim.x + (n % gridDim.x != 0u ? 1u : 0u)) * kGrain;
+  };
+  s.share = per_group(total);
+  // Changing units takes about as long as a grain (4 us).  It is counted
+  // where shares are long enough not to be cut because of it.
+  s.more = s.share >= 8u * kGrain ? kGrain : 0u;
+  if (s.more > 0u) {
+    mine += s.more * (b0 < B ? min(each, B - b0) : 0u);
+    upto = wave_scan(mine);
+    total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
+    s.share = per_group(total);
+  }
   s.pos = min(blockIdx.x * s.share, total);
   s.end = s.pos + min(s.share, total - s.pos);
   const uint64_t past = __ballot(upto * units > s.pos);
@@ -234,7 +287,7 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
   s.base = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), at);
   s.b = (uint32_t)at * each;
   while (s.pos < s.end) {
-    const uint32_t v = range_of(a, s.b).counted();
+    const uint32_t v = range_at(a, load_uniform(a.lens, s.b)).counted(s.more);
     if ((s.base + v) * units > s.pos) break;
     s.base += v;
     ++s.b;
@@ -267,8 +320,8 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   for (; w.pos < w.end;) {
   // The share's next piece: tiles [t_begin, t_end) of unit `unit` of sequence b.
   const uint32_t b = w.b;
-  const Range r = range_of(a, b);
-  const uint32_t counted = r.counted(), unit = (w.pos - w.base * units) / counted;
+  const Range r = range_at(a, load_uniform(a.lens, b));
+  const uint32_t counted = r.counted(w.more), unit = (w.pos - w.base * units) / counted;
   const uint32_t unit0 = w.base * units + unit * counted;
   const uint32_t t_begin = w.pos - unit0, t_upto = min(counted, t_begin + (w.end - w.pos));
   const uint32_t t_end = min(t_upto, r.tiles);
@@ -299,13 +352,16 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   // Row number of a half tile's first token, or ~0 where its page is not in the pool.
   const auto half_row = [&](uint32_t tile, uint32_t j) -> uint64_t {
     const uint32_t t = (r.tile0 + tile) * kTile + 16u * j, p = t >> shift;
-    const int32_t page = tile < t_end && p < pages_used ? table[p] : -1;
+    const int32_t page = tile < t_end && p < pages_used ? load_uniform(table, p) : -1;
     if (page < 0 || page >= a.c.pages) return ~0ull;
     return (((uint64_t)(uint32_t)page * (uint32_t)a.c.kv_heads + h) << shift) + (t & in_page);
   };
 
   uint32_t kw[2][kKW], vw[8][kVW];
-  uint32_t kb[2][2], vb[8][2];  // MX: the scale bytes (two where a lane's elements touch two blocks)
+  // MX: K's scale bytes (two where a lane's elements touch two blocks), and
+  // all of V's of the lane's four consecutive tokens of each half: few wide
+  // loads, since every load is a request to the caches however narrow.
+  uint32_t kb[2][2], vb[2][kBlocks];
   const uint32_t k_off = c * kRow + g * kKB, v_off = 4u * g * kRow + c * kVB;
   constexpr int kKScales = D <= 128 ? 1 : 2, kVScales = 32 % EV == 0 ? 1 : 2;
   const uint32_t k_blk = g * (D / 4) / 32u, v_blk = c * EV / 32u;
@@ -326,10 +382,12 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     for (int j = 0; j < 8; ++j) {
       const uint64_t at = row[j >> 2] == ~0ull ? 0u : row[j >> 2];
       load_bytes<kVB>(static_cast<const uint8_t*>(a.c.v) + at * kRow + v_off + (j & 3) * kRow, vw[j]);
-      if constexpr (MX) {
+    }
+    if constexpr (MX) {
 #pragma unroll
-        for (int i = 0; i < kVScales; ++i)
-          vb[j][i] = (a.c.vs + at * kBlocks)[(4u * g + (j & 3)) * kBlocks + min(v_blk + i, (uint32_t)kBlocks - 1u)];
+      for (int j = 0; j < 2; ++j) {
+        const uint64_t at = row[j] == ~0ull ? 0u : row[j];
+        load_scales<4 * kBlocks>(a.c.vs + at * kBlocks + 4u * g * kBlocks, vb[j]);
       }
     }
   };
@@ -437,7 +495,8 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       float vs[2] = {1.0f, 1.0f};
       if constexpr (MX) {
 #pragma unroll
-        for (int i = 0; i < kVScales; ++i) vs[i] = e8m0(vb[j][i]);
+        for (int i = 0; i < kVScales; ++i)
+          vs[i] = e8m0(scale_byte<kBlocks>(vb[j >> 2], j & 3, min(v_blk + i, (uint32_t)kBlocks - 1u)));
       }
 #pragma unroll
       for (int i = 0; i < EV / 2; ++i) {
@@ -564,36 +623,35 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     if (last_arrival) {
       // Place of piece p, and its head hd.
       const auto place = [&](uint32_t p, uint32_t hd) { return (2u * (wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile + hd; };
-      // Maximum and sum of every head over the pieces; then 64 pieces at a
-      // time, factors 2^(m_p - M) / L in the red array, free now.
-      for (uint32_t hd = wave; hd < heads; hd += kWaves) {
-        float mx = -INFINITY, s = 0.0f;
-        for (uint32_t p = lane; p < pieces; p += 64u) {
-          const v2f ms = load2_agent(a.stats + 2u * place(p, hd));
-          const float to = fmaxf(mx, ms[0]);
-          s = (mx == -INFINITY ? 0.0f : s * exp2_fast(mx - to)) + (ms[0] == -INFINITY ? 0.0f : ms[1] * exp2_fast(ms[0] - to));
-          mx = to;
-        }
-        const float all = wave_fmax(mx);
-        s = wave_fsum(mx == -INFINITY ? 0.0f : s * exp2_fast(mx - all));
-        if (lane == 0u) {
-          wave_m[0][hd] = all;
-          wave_l[0][hd] = s == 0.0f ? 0.0f : 1.0f / s;
-          finish_head(hd, all, s);
-        }
-      }
-      __syncthreads();
+      // 64 pieces at a time: running maximum M and sum of every head, the
+      // factors 2^(m_p - M) of its pieces (in the red array, free now) and
+      // that of what was summed before.
       float* factor = &red[0][0][0];  // 16 x 64
       static_assert(kHeadTile * 64 <= 2 * kHeadTile * kPad, "factors fit in the array they reuse");
       constexpr uint32_t kItems = kHeadTile * (D / 2) / 256;  // pairs of elements of a thread, at most
       float x[kItems], y[kItems];
 #pragma unroll
       for (uint32_t k = 0; k < kItems; ++k) x[k] = y[k] = 0.0f;
+      if (threadIdx.x < kHeadTile) {
+        wave_m[0][threadIdx.x] = -INFINITY;
+        wave_l[0][threadIdx.x] = 0.0f;
+      }
+      __syncthreads();
       for (uint32_t p0 = 0u; p0 < pieces; p0 += 64u) {
         const uint32_t here = min(pieces - p0, 64u);
         for (uint32_t hd = wave; hd < heads; hd += kWaves) {
-          const float m_p = lane < here ? load2_agent(a.stats + 2u * place(p0 + lane, hd))[0] : -INFINITY;
-          factor[hd * 64u + lane] = m_p == -INFINITY ? 0.0f : exp2_fast(m_p - wave_m[0][hd]) * wave_l[0][hd];
+          v2f ms = v2f{-INFINITY, 0.0f};
+          if (lane < here) ms = load2_agent(a.stats + 2u * place(p0 + lane, hd));
+          const float old = wave_m[0][hd], to = fmaxf(old, wave_fmax(ms[0]));
+          const float f = ms[0] == -INFINITY ? 0.0f : exp2_fast(ms[0] - to);
+          const float f_old = old == -INFINITY ? 0.0f : exp2_fast(old - to);
+          const float s = wave_fsum(ms[1] * f);
+          factor[hd * 64u + lane] = f;
+          if (lane == 0u) {
+            wave_m[0][hd] = to;
+            wave_l[0][hd] = wave_l[0][hd] * f_old + s;
+            wave_m[1][hd] = f_old;
+          }
         }
         __syncthreads();
 #pragma unroll
@@ -601,13 +659,15 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
           const uint32_t i = k * 256u + threadIdx.x;
           if (i < heads * (D / 2)) {
             const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-            for (uint32_t q0 = 0u; q0 < here; q0 += 8u) {
-              v2f v[8];
+            x[k] *= wave_m[1][hd];
+            y[k] *= wave_m[1][hd];
+            for (uint32_t q0 = 0u; q0 < here; q0 += 4u) {
+              v2f v[4];
 #pragma unroll
-              for (uint32_t j = 0; j < 8u; ++j)
+              for (uint32_t j = 0; j < 4u; ++j)
                 v[j] = load2_agent(a.part + (size_t)place(p0 + min(q0 + j, here - 1u), hd) * D + d);
 #pragma unroll
-              for (uint32_t j = 0; j < 8u; ++j) {
+              for (uint32_t j = 0; j < 4u; ++j) {
                 if (q0 + j >= here) continue;
                 x[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][0], x[k]);
                 y[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][1], y[k]);
@@ -620,9 +680,13 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
       for (uint32_t k = 0; k < kItems; ++k) {
         const uint32_t i = k * 256u + threadIdx.x;
-        if (i < heads * (D / 2))
-          store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + i / (D / 2)) * D + 2u * (i % (D / 2)), x[k], y[k]);
+        if (i < heads * (D / 2)) {
+          const uint32_t hd = i / (D / 2);
+          const float s = wave_l[0][hd], inv = s == 0.0f ? 0.0f : 1.0f / s;
+          store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + 2u * (i % (D / 2)), x[k] * inv, y[k] * inv);
+        }
       }
+      if (threadIdx.x < heads) finish_head(threadIdx.x, wave_m[0][threadIdx.x], wave_l[0][threadIdx.x]);
     }
   }
   w.pos += t_upto - t_begin;
