@@ -204,7 +204,9 @@ struct EvictArgs {
 };
 
 // Copies the rows of kept tokens [from, to) of sequence b, head h to their
-// places: 16 bytes a thread, K and V of kRows tokens at a time in flight.
+// places: 16 bytes a thread, K and V of kRows tokens at a time in flight,
+// loads and stores marked as used once (16 x 8 heads of 4096 MXFP8 tokens: 97
+// us without, 81 us with).
 template <uint32_t THREADS>
 __device__ __forceinline__ void copy_rows(const EvictArgs& a, uint32_t b, uint32_t h, uint32_t from, uint32_t to) {
   constexpr uint32_t kRows = 4;
@@ -231,16 +233,18 @@ __device__ __forceinline__ void copy_rows(const EvictArgs& a, uint32_t b, uint32
 #pragma unroll
     for (uint32_t k = 0; k < kRows; ++k) {
       // (Row 0 stands in for one that is not copied; a pool without pages has none to copy.)
+      const uint64_t at = s[k] * a.row_bytes + piece * 16u;
       if (a.src.pages > 0) {
-        x[k] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.k) + s[k] * a.row_bytes + piece * 16u);
-        y[k] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.v) + s[k] * a.row_bytes + piece * 16u);
+        x[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.k) + at));
+        y[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.src.v) + at));
       }
     }
 #pragma unroll
     for (uint32_t k = 0; k < kRows; ++k) {
       if (!ok[k]) continue;
-      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.k) + d[k] * a.row_bytes + piece * 16u) = x[k];
-      *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.v) + d[k] * a.row_bytes + piece * 16u) = y[k];
+      const uint64_t at = d[k] * a.row_bytes + piece * 16u;
+      __builtin_nontemporal_store(x[k], reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.k) + at));
+      __builtin_nontemporal_store(y[k], reinterpret_cast<u32x4*>(static_cast<uint8_t*>(a.dst.v) + at));
       if (a.src.fmt != kKvBf16) {
         for (uint32_t i = piece; i < pairs; i += pieces) {
           reinterpret_cast<uint16_t*>(a.dst.ks)[d[k] * pairs + i] =

@@ -66,7 +66,8 @@ struct Row {
   }
   // Block j, which does, as it lies in memory; and as values.
   __device__ __forceinline__ u32x4 raw(uint32_t j) const {
-    return *reinterpret_cast<const u32x4*>(p + ((int64_t)j * kElem<DT> - head) * (DT == kDtF32 ? 4 : 2));
+    const uint8_t* at = p + ((int64_t)j * kElem<DT> - head) * (DT == kDtF32 ? 4 : 2);
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at));  // a logit is read once
   }
   static __device__ __forceinline__ void values(u32x4 w, float (&v)[kElem<DT>]) {
     if constexpr (DT == kDtF32) {
@@ -599,8 +600,9 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
 #pragma unroll
         for (int k = 0; k < 4; ++k) w[k] = bf16_pair(d[2 * k], d[2 * k + 1]);
       }
-      // (The output's rows may be aligned otherwise than the input's.)
-      *reinterpret_cast<u32x4_any*>(out + i0 * (DT == kDtF32 ? 4 : 2)) = w;
+      // (The output's rows may be aligned otherwise than the input's.  Marked
+      // as not read again here: 4096 x 100003 BF16 299 us without, 273 us with.)
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(out + i0 * (DT == kDtF32 ? 4 : 2)));
     } else {
 #pragma unroll
       for (uint32_t e = 0; e < E; ++e) {
