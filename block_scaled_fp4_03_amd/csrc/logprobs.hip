@@ -385,15 +385,12 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       }
     }
     if (s0 + kStepBlocks < b1 && whole(s0 + kStepBlocks)) fetch(s0 + kStepBlocks);
-    float hi[kUnroll], top = -INFINITY, low = INFINITY;
+    float hi[kUnroll], top = -INFINITY;
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u) {
       hi[u] = v[u][0];
 #pragma unroll
-      for (uint32_t e = 0; e < E; ++e) {
-        if (e > 0u) hi[u] = fmaxf(hi[u], v[u][e]);
-        low = fminf(low, v[u][e]);
-      }
+      for (uint32_t e = 1; e < E; ++e) hi[u] = fmaxf(hi[u], v[u][e]);
       top = fmaxf(top, hi[u]);
     }
     mine = fmaxf(mine, top);
@@ -403,27 +400,33 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       st.s *= f;
       st.r = r;
     }
-    const float ref = st.r == -INFINITY ? 0.0f : st.r;
-    if (__any(!(low - ref > -1e30f))) {
-      // Masked logits (-inf, the type's lowest): e^t = 0, and t e^t is 0 too.
+    const float ref = st.r == -INFINITY ? 0.0f : st.r, ref2 = -ref * c2;
+    float s = st.s, w = st.w;
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u)
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) {
+        const float t = __builtin_fmaf(v[u][e], c2, ref2), p = exp2_fast(t);
+        s += p;
+        w = __builtin_fmaf(t, p, w);
+      }
+    if (__any(w != w)) {
+      // A masked logit (-inf, or so low that t is): e^t is 0, and t e^t has
+      // to be too.  (Or a NaN, which stays one in s.)  Again, with care, and
+      // with differences first, since x log2 e may overflow.
+      s = st.s;
+      w = st.w;
 #pragma unroll
       for (uint32_t u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) {
           const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
-          st.s += p;
-          st.w = __builtin_fmaf(fmaxf(t, -1000.0f), p, st.w);
-        }
-    } else {
-#pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u)
-#pragma unroll
-        for (uint32_t e = 0; e < E; ++e) {
-          const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
-          st.s += p;
-          st.w = __builtin_fmaf(t, p, st.w);
+          s += p;
+          w = __builtin_fmaf(fmaxf(t, -1000.0f), p, w);
         }
     }
+    st.s = s;
+    st.w = w;
     if (k > 0u) {
       if (s0 == b0) tau = threshold(sh, mine, k);
 #pragma unroll
