@@ -11,19 +11,25 @@
 // base 2 (t times log2 e), FP32.
 //
 // The top k in the same pass: the first 16 KB give a threshold with at least
-// k elements at or above it (the k-th largest of 64 groups' maxima), and from
-// then on only elements above it are looked at: k V / 8192 of them in the
-// mean, collected in LDS and ranked at the end.  Elements equal to the
-// threshold are needed only if fewer than k lie above it, and then the first
-// ones in order; they lie in the first 16 KB.  A row that overflows the
-// buffer (a rising row) is collected again above the k-th largest of the
-// groups' maxima over everything; one that overflows again, or holds a NaN,
-// is searched k times.
+// k elements at or above it (the k-th largest of 64 groups' maxima).  16-byte
+// blocks that reach it, and later blocks that pass it, are noted in LDS (one
+// ballot; looking at their elements there and then cost a quarter of the
+// kernel's time).  The threshold rises as the row goes on (after 5, 17, 65,
+// ... steps, from the groups' maxima so far): the number of blocks noted grows
+// with the logarithm of V.  At the end the noted blocks are read once more,
+// their elements at or above the last threshold ranked.  An element equal to
+// the threshold in a later block is never among the k: k elements before it
+// are as large.  A row that overflows a buffer (a rising row, or one of few
+// values) is read again for elements above the k-th largest of the groups'
+// maxima over everything, and filled up with the first elements equal to
+// that; one that overflows again, or holds a NaN, is searched k times.
 //
 // Few rows are split over workgroups; the last to arrive joins them.
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
+
+#include <cfloat>
 
 namespace fp4 {
 namespace {
@@ -33,7 +39,8 @@ constexpr uint32_t kThreads = 256, kWaves = 4;
 constexpr uint32_t kUnroll = 4;                      // 16-byte blocks of a thread's step
 constexpr uint32_t kStepBlocks = kThreads * kUnroll;  // 16 KB
 constexpr uint32_t kGroups = 64;                     // groups of four threads
-constexpr uint32_t kCand = 1024;                     // candidates a workgroup can hold
+constexpr uint32_t kNoted = 512;                     // blocks a wave can note
+constexpr uint32_t kFew = 1024;                      // elements a workgroup can hold to rank them
 constexpr uint32_t kMaxSplits = 64, kMaxTop = 32;
 constexpr float kLazy = 8.0f;
 
@@ -49,27 +56,34 @@ __device__ __forceinline__ float logit(const void* x, size_t i) {
 }
 
 // A row as aligned 16-byte blocks: block j holds elements j E - head .. (the
-// first and the last block may be partly outside the row).
+// first and the last block may be partly outside the row).  Blocks are loaded
+// whole, also those that reach into the rows beside, as long as they lie
+// within the matrix; at most the first of its first row and the last of its
+// last do not.
 template <int DT>
 struct Row {
+  static constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u, E = kElem<DT>;
   const uint8_t* p;  // the row's first element
   uint32_t V, head, blocks;
-  __device__ __forceinline__ Row(const void* x, size_t at, uint32_t V_) : V(V_) {
-    constexpr uint32_t size = DT == kDtF32 ? 4u : 2u;
-    p = static_cast<const uint8_t*>(x) + at * size;
-    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / size;
-    blocks = (V + head + kElem<DT> - 1u) / kElem<DT>;
+  uint32_t lo, hi;   // blocks [lo, hi) can be loaded whole
+  __device__ __forceinline__ Row(const void* x, int64_t stride, size_t n, size_t rows, uint32_t V_) : V(V_) {
+    p = static_cast<const uint8_t*>(x) + n * (size_t)stride * kSize;
+    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / kSize;
+    blocks = (V + head + E - 1u) / E;
+    const uint32_t tail = blocks * E - head - V;  // elements of the last block past the row
+    lo = n == 0u && head > 0u ? 1u : 0u;
+    hi = n + 1u == rows && tail > 0u ? blocks - 1u : blocks;
   }
   // Whether blocks [j, j + n) lie wholly inside the row.
   __device__ __forceinline__ bool inside(uint32_t j, uint32_t n) const {
-    return (j > 0u || head == 0u) && (uint64_t)(j + n) * kElem<DT> <= (uint64_t)V + head;
+    return (j > 0u || head == 0u) && (uint64_t)(j + n) * E <= (uint64_t)V + head;
   }
-  // Block j, which does, as it lies in memory; and as values.
+  // Block j as it lies in memory, or the nearest that can be loaded (lo < hi).
   __device__ __forceinline__ u32x4 raw(uint32_t j) const {
-    const uint8_t* at = p + ((int64_t)j * kElem<DT> - head) * (DT == kDtF32 ? 4 : 2);
+    const uint8_t* at = p + ((int64_t)min(max(j, lo), hi - 1u) * E - head) * kSize;
     return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at));  // a logit is read once
   }
-  static __device__ __forceinline__ void values(u32x4 w, float (&v)[kElem<DT>]) {
+  static __device__ __forceinline__ void values(u32x4 w, float (&v)[E]) {
     if constexpr (DT == kDtF32) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) v[k] = u2f(w[k]);
@@ -81,18 +95,18 @@ struct Row {
       }
     }
   }
-  // Elements of any block j; -inf for those outside the row.
-  __device__ __forceinline__ void load(uint32_t j, float (&v)[kElem<DT>]) const {
-    constexpr uint32_t E = kElem<DT>;
-    if (inside(j, 1u)) {
-      values(raw(j), v);
-      return;
-    }
-    const int64_t i0 = (int64_t)j * E - head;
+  // Element i counted from the row's first; -inf for those outside the row.
+  __device__ __forceinline__ int64_t first(uint32_t j) const { return (int64_t)j * E - head; }
+  // Elements of any block j < end from what raw(j) gave.
+  __device__ __forceinline__ void edge_values(u32x4 w, uint32_t j, uint32_t end, float (&v)[E]) const {
+    values(w, v);
+    const int64_t i0 = first(j);
+    const bool direct = j < end && (j < lo || j >= hi);
 #pragma unroll
-    for (uint32_t k = 0; k < E; ++k) {
-      const int64_t i = i0 + k;
-      v[k] = i >= 0 && i < V ? logit<DT>(p, (size_t)i) : -INFINITY;
+    for (uint32_t e = 0; e < E; ++e) {
+      const bool in = j < end && i0 + e >= 0 && i0 + e < V;
+      v[e] = in ? v[e] : -INFINITY;
+      if (direct && in) v[e] = at((uint32_t)(i0 + e));
     }
   }
   __device__ __forceinline__ float at(uint32_t i) const { return logit<DT>(p, i); }
@@ -128,6 +142,7 @@ __device__ __forceinline__ Stats wave_join(Stats a, float c2) {
 struct Args {
   const void* x;
   int64_t stride;
+  uint32_t rows;
   uint32_t V;
   float scale;
   const int32_t* tokens;
@@ -144,52 +159,69 @@ struct Args {
 };
 
 struct Shared {
-  uint64_t cand[kCand];  // candidates, in no order
-  uint64_t few[kCand];   // those that can still be among the k largest
+  uint32_t noted[kWaves][kNoted];  // a wave's blocks, in no order
+  uint64_t few[kFew];              // keys to rank, in no order
   uint64_t best[kMaxTop];
   uint64_t group_key[kGroups];
   float group[kGroups];
   float tau;
   uint64_t tau_key;
-  uint32_t count, few_count, flag;
+  uint32_t wave_count[kWaves], few_count, flag;
   Stats part[kWaves];
   uint64_t wave_key[kWaves];
 };
 
-// The k-th largest of the 64 groups' maxima (each thread gives its own; a
-// lane ranks one group against all).  Every thread of the workgroup calls it.
-__device__ __forceinline__ float threshold(Shared& sh, float mine, uint32_t k) {
-  mine = fmaxf(mine, lane_xor1(mine));
-  mine = fmaxf(mine, lane_xor2(mine));
-  if ((threadIdx.x & 3u) == 0u) sh.group[threadIdx.x >> 2] = mine;
-  __syncthreads();
-  const uint32_t lane = threadIdx.x & 63u;
-  if (threadIdx.x < 64u) {
-    const float v = sh.group[lane];
-    uint32_t rank = 0u;
-#pragma unroll 16
-    for (uint32_t i = 0u; i < kGroups; ++i) {
-      const float u = sh.group[i];
-      rank += (u > v || (u == v && i < lane)) ? 1u : 0u;
-    }
-    if (rank == k - 1u) sh.tau = v;
-  }
-  __syncthreads();
-  return sh.tau;
-}
-
-__device__ __forceinline__ void push(Shared& sh, float v, uint32_t i) {
-  const uint32_t at = atomicAdd(&sh.count, 1u);
-  if (at < kCand) sh.cand[at] = top_key(v, i);
-}
-
-// The larger of a lane's key and its neighbour's (lane ^ 1, lane ^ 2), by DPP.
+// The larger of a lane's key and its neighbour's (lane ^ 1, lane ^ 2), by DPP;
+// the sum of a lane's count and its neighbour's.
 template <int CTRL>
 __device__ __forceinline__ uint64_t max_key_dpp(uint64_t a) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)a, CTRL, 0xF, 0xF, false);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(a >> 32), CTRL, 0xF, 0xF, false);
   const uint64_t b = ((uint64_t)hi << 32) | lo;
   return a > b ? a : b;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t add_dpp(uint32_t a) {
+  return a + (uint32_t)__builtin_amdgcn_mov_dpp((int)a, CTRL, 0xF, 0xF, false);
+}
+
+// The k-th largest of the 64 groups' maxima: every group of four threads gives
+// its own (`mine` in all four) and counts the groups above it, a quarter each.
+// Every thread of the workgroup calls it.
+template <typename T>
+__device__ __forceinline__ T kth_of_groups(T (&group)[kGroups], T& result, T mine, uint32_t k) {
+  const uint32_t g = threadIdx.x >> 2, q0 = (threadIdx.x & 3u) * (kGroups / 4u);
+  if ((threadIdx.x & 3u) == 0u) group[g] = mine;
+  __syncthreads();
+  uint32_t above = 0u;
+#pragma unroll
+  for (uint32_t i = 0u; i < kGroups / 4u; ++i) {
+    const T u = group[q0 + i];
+    above += (u > mine || (u == mine && q0 + i < g)) ? 1u : 0u;
+  }
+  above = add_dpp<0x4E>(add_dpp<0xB1>(above));
+  if (above == k - 1u && (threadIdx.x & 3u) == 0u) result = mine;
+  __syncthreads();
+  return result;
+}
+__device__ __forceinline__ float threshold(Shared& sh, float mine, uint32_t k) {
+  mine = fmaxf(mine, lane_xor1(mine));
+  mine = fmaxf(mine, lane_xor2(mine));
+  return kth_of_groups(sh.group, sh.tau, mine, k);
+}
+
+// Notes the lane's block j where `is`; `count` goes on past their number.
+__device__ __forceinline__ void note(Shared& sh, bool is, uint32_t j, uint32_t& count) {
+  const uint64_t all = __ballot(is);
+  const uint32_t at = count + (uint32_t)__popcll(all & ((1ull << (threadIdx.x & 63u)) - 1ull));
+  if (is && at < kNoted) sh.noted[threadIdx.x >> 6][at] = j;
+  count += (uint32_t)__popcll(all);
+}
+
+// Adds a key to those to rank; their number goes on past the array.
+__device__ __forceinline__ void push(Shared& sh, uint64_t key) {
+  const uint32_t at = atomicAdd(&sh.few_count, 1u);
+  if (at < kFew) sh.few[at] = key;
 }
 
 // The value a key stands for (-0 as +0).
@@ -198,58 +230,39 @@ __device__ __forceinline__ float key_value(uint64_t key) {
   return u == 0xFFFFFFFFu ? NAN : u2f((u & 0x80000000u) ? u & 0x7FFFFFFFu : ~u);
 }
 
-// Ranks keys[0 .. n) into best by counting for each how many are above it.
-__device__ __forceinline__ void rank_keys(Shared& sh, const uint64_t* keys, uint32_t n, uint32_t k) {
-  for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-    const uint64_t v = keys[i];
-    uint32_t rank = 0u;
-#pragma unroll 8
-    for (uint32_t j = 0u; j < n; ++j) rank += keys[j] > v ? 1u : 0u;
-    if (rank < k) sh.best[rank] = v;
-  }
-  __syncthreads();
-}
-
-// The largest k of cand[0 .. n) into best, in order (fewer: the rest 0).
-// Many: the k-th largest of 64 groups' maxima bounds the k-th largest from
-// below first, which leaves little more than k to rank.
-__device__ __forceinline__ void rank_candidates(Shared& sh, uint32_t n, uint32_t k) {
+// The largest k of few[0 .. n), n <= kFew, into best, in order (fewer: the
+// rest 0).  Many: the k-th largest of 64 groups' maxima bounds the k-th
+// largest from below first, which leaves little more than k; each of those is
+// then ranked by counting the ones above it.
+__device__ __forceinline__ void rank_few(Shared& sh, uint32_t n, uint32_t k) {
   const uint32_t tid = threadIdx.x;
-  if (n <= 64u) {
-    if (tid < k) sh.best[tid] = 0ull;
-    __syncthreads();
-    rank_keys(sh, sh.cand, n, k);
-    return;
-  }
-  uint64_t key[kCand / kThreads], mine = 0ull;
-#pragma unroll
-  for (uint32_t i = 0; i < kCand / kThreads; ++i) {
-    key[i] = i * kThreads + tid < n ? sh.cand[i * kThreads + tid] : 0ull;
-    mine = key[i] > mine ? key[i] : mine;
-  }
-  mine = max_key_dpp<0xB1>(mine);
-  mine = max_key_dpp<0x4E>(mine);
-  if ((tid & 3u) == 0u) sh.group_key[tid >> 2] = mine;
-  if (tid == 0u) sh.few_count = 0u;
   if (tid < k) sh.best[tid] = 0ull;
   __syncthreads();
-  if (tid < 64u) {
-    const uint64_t v = sh.group_key[tid];
-    uint32_t rank = 0u;
-#pragma unroll 16
-    for (uint32_t i = 0u; i < kGroups; ++i) {
-      const uint64_t u = sh.group_key[i];
-      rank += (u > v || (u == v && i < tid)) ? 1u : 0u;
+  if (n > 64u) {
+    uint64_t key[kFew / kThreads], mine = 0ull;
+#pragma unroll
+    for (uint32_t i = 0; i < kFew / kThreads; ++i) {
+      key[i] = i * kThreads + tid < n ? sh.few[i * kThreads + tid] : 0ull;
+      mine = key[i] > mine ? key[i] : mine;
     }
-    if (rank == k - 1u) sh.tau_key = v;
+    mine = max_key_dpp<0xB1>(mine);
+    mine = max_key_dpp<0x4E>(mine);
+    if (tid == 0u) sh.few_count = 0u;
+    const uint64_t kth = kth_of_groups(sh.group_key, sh.tau_key, mine, k);
+#pragma unroll
+    for (uint32_t i = 0; i < kFew / kThreads; ++i)
+      if (key[i] != 0ull && key[i] >= kth) push(sh, key[i]);
+    __syncthreads();
+    n = sh.few_count;
+  }
+  for (uint32_t i = tid; i < n; i += kThreads) {
+    const uint64_t v = sh.few[i];
+    uint32_t rank = 0u;
+#pragma unroll 8
+    for (uint32_t j = 0u; j < n; ++j) rank += sh.few[j] > v ? 1u : 0u;
+    if (v != 0ull && rank < k) sh.best[rank] = v;
   }
   __syncthreads();
-  const uint64_t tau = sh.tau_key;
-#pragma unroll
-  for (uint32_t i = 0; i < kCand / kThreads; ++i)
-    if (key[i] != 0ull && key[i] >= tau) sh.few[atomicAdd(&sh.few_count, 1u)] = key[i];
-  __syncthreads();
-  rank_keys(sh, sh.few, sh.few_count, k);
 }
 
 // k searches of blocks [b0, b1) for the largest key below the last.
@@ -354,37 +367,32 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   __shared__ Shared sh;
   const uint32_t split = blockIdx.x, splits = gridDim.x, tid = threadIdx.x;
   const size_t n = blockIdx.y;
-  const Row<DT> row(a.x, n * (size_t)a.stride, a.V);
+  const Row<DT> row(a.x, a.stride, n, a.rows, a.V);
   const uint32_t per = (row.blocks + splits - 1u) / splits;
   const uint32_t b0 = min(split * per, row.blocks), b1 = min(b0 + per, row.blocks);
   const uint32_t k = (uint32_t)a.top_k;
   const float c2 = a.scale * kLog2e;
 
-  if (tid == 0u) sh.count = 0u;
   Stats st = {-INFINITY, 0.0f, 0.0f};
   float mine = -INFINITY, tau = INFINITY;  // this thread's largest; nothing passes until the threshold is known
-  u32x4 next[kUnroll];
-  const auto whole = [&](uint32_t s0) { return s0 + kStepBlocks <= b1 && row.inside(s0, kStepBlocks); };
-  const auto fetch = [&](uint32_t s0) {
+  uint32_t count = 0u;                     // blocks this wave has noted
+  u32x4 next[kUnroll] = {};
+  const auto fetch = [&](uint32_t s0) __attribute__((always_inline)) {
+    if (row.lo >= row.hi) return;  // (a matrix without a whole block)
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u) next[u] = row.raw(s0 + u * kThreads + tid);
   };
-  if (b0 < b1 && whole(b0)) fetch(b0);
+  if (b0 < b1) fetch(b0);
   for (uint32_t s0 = b0; s0 < b1; s0 += kStepBlocks) {
     float v[kUnroll][E];
-    if (whole(s0)) {
+    if (s0 + kStepBlocks <= b1 && row.inside(s0, kStepBlocks)) {
 #pragma unroll
       for (uint32_t u = 0; u < kUnroll; ++u) Row<DT>::values(next[u], v[u]);
     } else {
 #pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u) {
-        const uint32_t j = s0 + u * kThreads + tid;
-#pragma unroll
-        for (uint32_t e = 0; e < E; ++e) v[u][e] = -INFINITY;
-        if (j < b1) row.load(j, v[u]);
-      }
+      for (uint32_t u = 0; u < kUnroll; ++u) row.edge_values(next[u], s0 + u * kThreads + tid, b1, v[u]);
     }
-    if (s0 + kStepBlocks < b1 && whole(s0 + kStepBlocks)) fetch(s0 + kStepBlocks);
+    if (s0 + kStepBlocks < b1) fetch(s0 + kStepBlocks);
     float hi[kUnroll], top = -INFINITY;
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u) {
@@ -428,49 +436,71 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     st.s = s;
     st.w = w;
     if (k > 0u) {
-      if (s0 == b0) tau = threshold(sh, mine, k);
+      const uint32_t step = (s0 - b0) / kStepBlocks;
+      if (step == 0u) {
+        // (Masked logits, -inf, are not noted; fill_ties finds the first where they are needed.)
+        tau = threshold(sh, mine, k);
 #pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u) {
-        if (hi[u] > tau) {
-          const uint32_t i0 = (s0 + u * kThreads + tid) * E - row.head;
+        for (uint32_t u = 0; u < kUnroll; ++u)
+          note(sh, hi[u] >= tau && hi[u] > -INFINITY, s0 + u * kThreads + tid, count);
+      } else {
 #pragma unroll
-          for (uint32_t e = 0; e < E; ++e)
-            if (v[u][e] > tau) push(sh, v[u][e], i0 + e);
-        }
+        for (uint32_t u = 0; u < kUnroll; ++u)
+          if (__any(hi[u] > tau)) note(sh, hi[u] > tau, s0 + u * kThreads + tid, count);
+        if (step == 4u || step == 16u || step == 64u || step == 256u) tau = threshold(sh, mine, k);
       }
     }
   }
 
   // The workgroup's statistics, in a fixed order.
   st = wave_join(st, c2);
-  if ((tid & 63u) == 0u) sh.part[tid >> 6] = st;
+  if ((tid & 63u) == 0u) {
+    sh.part[tid >> 6] = st;
+    sh.wave_count[tid >> 6] = count;
+  }
+  if (tid == 0u) sh.few_count = 0u;
   __syncthreads();
   st = join(join(sh.part[0], sh.part[1], c2), join(sh.part[2], sh.part[3], c2), c2);
 
   if (k > 0u) {
-    uint32_t n_cand = sh.count;
     const bool special = !(st.s == st.s) || st.r == INFINITY;
-    if (!special && n_cand > kCand) {
-      // Too many: again, above the k-th largest of the groups' maxima over all.
+    const uint32_t most = max(max(sh.wave_count[0], sh.wave_count[1]), max(sh.wave_count[2], sh.wave_count[3]));
+    bool over = special || most > kNoted;
+    if (!over) {
+      // The noted blocks' elements.
+      const float least = fmaxf(tau, -FLT_MAX);
+      for (uint32_t i = tid & 63u; i < count; i += 64u) {
+        const uint32_t j = sh.noted[tid >> 6][i];
+        float v[E];
+        row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, b1, v);
+#pragma unroll
+        for (uint32_t e = 0; e < E; ++e)
+          if (v[e] >= least) push(sh, top_key(v[e], j * E - row.head + e));
+      }
       __syncthreads();
-      tau = threshold(sh, mine, k);
-      if (tid == 0u) sh.count = 0u;
+      over = sh.few_count > kFew;
+    }
+    if (over && !special) {
+      // Too many: again, above the k-th largest of the groups' maxima over all.
+      tau = threshold(sh, mine, k);  // (its barriers end the reading of few_count)
+      if (tid == 0u) sh.few_count = 0u;
       __syncthreads();
       for (uint32_t j = b0 + tid; j < b1; j += kThreads) {
         float v[E];
-        row.load(j, v);
+        row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, b1, v);
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e)
-          if (v[e] > tau) push(sh, v[e], j * E - row.head + e);
+          if (v[e] > tau) push(sh, top_key(v[e], j * E - row.head + e));
       }
       __syncthreads();
-      n_cand = sh.count;
+      over = sh.few_count > kFew;
     }
-    if (special || n_cand > kCand) {
+    if (over) {
       search<DT>(sh, row, b0, b1, k);
     } else {
-      rank_candidates(sh, n_cand, k);
-      if (n_cand < k) fill_ties<DT>(sh, row, b0, b1, tau, n_cand, k);
+      const uint32_t n_few = sh.few_count;
+      rank_few(sh, n_few, k);
+      if (n_few < k) fill_ties<DT>(sh, row, b0, b1, tau, n_few, k);
     }
   }
   float x0 = 0.0f;
@@ -507,13 +537,11 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   }
   all = wave_join(all, c2);
   if (k > 0u) {
-    // splits x k <= kCand keys (the host's choice of splits); those of splits
-    // with fewer than k elements are 0, below all.
+    // splits x k <= kFew (the host's choice of splits); those of splits with
+    // fewer than k elements are 0, none.
     for (uint32_t i = tid; i < splits * k; i += kThreads)
-      sh.cand[i] = __hip_atomic_load(a.keys + part * k + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    // Equal keys are only the zeros of short splits, and V >= 1 others rank first.
-    rank_candidates(sh, splits * k, k);
+      sh.few[i] = __hip_atomic_load(a.keys + part * k + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    rank_few(sh, splits * k, k);
   }
   write_row<DT>(a, sh, row, n, all, x0, is0);
 }
@@ -529,26 +557,20 @@ template <int DT>
 __global__ __launch_bounds__(256) void logprobs_backward_kernel(
     const void* __restrict__ x, int64_t stride, uint32_t V, float scale, const int32_t* __restrict__ tokens, int32_t M,
     const float* __restrict__ lse, const float* __restrict__ entropy, const float* __restrict__ g_logp,
-    const float* __restrict__ g_entropy, void* __restrict__ dx, int64_t dx_stride) {
+    const float* __restrict__ g_entropy, void* __restrict__ dx, int64_t dx_stride, uint32_t rows) {
   constexpr uint32_t E = kElem<DT>;
   __shared__ uint32_t marked[kStepBlocks / 32u];
   __shared__ float sums[kWaves];
   const size_t n = blockIdx.y;
   const uint32_t tid = threadIdx.x;
-  const Row<DT> row(x, n * (size_t)stride, V);
+  const Row<DT> row(x, stride, n, rows, V);
   const uint32_t b0 = blockIdx.x * kStepBlocks;
   if (b0 >= row.blocks) return;
   float v[kUnroll][E];
-  if (row.inside(b0, kStepBlocks)) {
-    u32x4 w[kUnroll];
+  u32x4 raw[kUnroll] = {};
+  if (row.lo < row.hi) {
 #pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) w[u] = row.raw(b0 + u * kThreads + tid);
-#pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) Row<DT>::values(w[u], v[u]);
-  } else {
-#pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u)
-      if (b0 + u * kThreads + tid < row.blocks) row.load(b0 + u * kThreads + tid, v[u]);
+    for (uint32_t u = 0; u < kUnroll; ++u) raw[u] = row.raw(b0 + u * kThreads + tid);
   }
   if (tid < kStepBlocks / 32u) marked[tid] = 0u;
   __syncthreads();
@@ -571,6 +593,14 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
   // A row of -inf logits: every p is 0 (its lse of -inf would give NaN).
   const float ls = lse[n] == -INFINITY ? INFINITY : lse[n];
   const float A = -(g + ge * h), B = -ge;
+  const bool whole = row.inside(b0, kStepBlocks);
+#pragma unroll
+  for (uint32_t u = 0; u < kUnroll; ++u) {
+    if (whole)
+      Row<DT>::values(raw[u], v[u]);
+    else
+      row.edge_values(raw[u], b0 + u * kThreads + tid, row.blocks, v[u]);
+  }
   uint8_t* out = static_cast<uint8_t*>(dx) + n * (size_t)dx_stride * (DT == kDtF32 ? 4u : 2u);
 #pragma unroll
   for (uint32_t u = 0; u < kUnroll; ++u) {
@@ -632,7 +662,7 @@ uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
   const int64_t most = (V + 2047) / 2048;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;
-  if (top_k > 0 && s > (int64_t)kCand / top_k) s = kCand / top_k;
+  if (top_k > 0 && s > (int64_t)kFew / top_k) s = kFew / top_k;
   return (uint32_t)(s < 1 ? 1 : s);
 }
 
@@ -649,7 +679,7 @@ hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, 
                            float* top_logp, int32_t* top_index, void* workspace, hipStream_t stream) {
   const uint32_t s = splits_of(N, V, top_k);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  Args a{x, stride, (uint32_t)V, scale, tokens, M, logp, entropy, lse, top_k, top_logp, top_index, nullptr, nullptr,
+  Args a{x, stride, 0u, (uint32_t)V, scale, tokens, M, logp, entropy, lse, top_k, top_logp, top_index, nullptr, nullptr,
          nullptr};
   if (s > 1) {
     a.done = reinterpret_cast<uint32_t*>(ws);
@@ -661,6 +691,7 @@ hipError_t launch_logprobs(const void* x, int dtype, int64_t stride, int64_t N, 
     const int64_t rows = N - n0 < 65535 ? N - n0 : 65535;
     Args b = a;
     b.x = static_cast<const uint8_t*>(x) + (size_t)n0 * (size_t)stride * (dtype == kDtF32 ? 4 : 2);
+    b.rows = (uint32_t)rows;
     b.tokens = tokens + n0 * M;
     b.logp = logp + n0 * M;
     b.entropy = entropy ? entropy + n0 : nullptr;
@@ -695,10 +726,12 @@ hipError_t launch_logprobs_backward(const void* x, int dtype, int64_t stride, in
     const float* ge = g_entropy ? g_entropy + n0 : nullptr;
     if (dtype == kDtF32)
       logprobs_backward_kernel<kDtF32><<<grid, kThreads, 0, stream>>>(
-          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride);
+          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride,
+          (uint32_t)rows);
     else
       logprobs_backward_kernel<kDtBF16><<<grid, kThreads, 0, stream>>>(
-          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride);
+          xr, stride, (uint32_t)V, scale, tokens + n0 * M, M, lse + n0, ent, g_logp + n0 * M, ge, dr, dx_stride,
+          (uint32_t)rows);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
