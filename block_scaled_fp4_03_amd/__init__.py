@@ -563,32 +563,34 @@ def gemm_nvfp4_act(x, w, tensor_scale=None, ts_out=None, out_dtype=None, out=Non
 # ---- decode-step operators: cache, attention, eviction, log probabilities ------
 # These calls take microseconds on the GPU, so their wrappers are kept short:
 # one test for a well-formed tensor, with _need naming the fault of any other.
-def _is(t, dtype, ndim, device):
-    torch = _torch()
-    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == ndim and t.device == device
-            and t.is_contiguous())
-
-
 def _want(t, name, dtype, ndim, device, numel=None):
     """_need for one dtype and dimension count, quickly."""
-    if not _is(t, dtype, ndim, device) or (numel is not None and t.numel() < numel):
-        _need(t, name, (dtype,), numel, device, ndim)
+    try:
+        if (t.dtype is dtype and t.ndim == ndim and t.device == device and t.is_contiguous()
+                and (numel is None or t.numel() >= numel)):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, (dtype,), numel, device, ndim)
 
 
-def _want_rows(t, name, dtypes, ndim, device=None, shape=None):
-    """Check a tensor whose dimensions after the first are dense and whose
-    first may have any stride (columns of a wider matrix).  Returns that
+def _want_rows(t, name, ndim, device=None, like=None):
+    """Check a float32 or bfloat16 tensor (with `like`: of its dtype and shape)
+    whose dimensions after the first are dense and whose first may have any
+    stride (columns of a wider matrix).  Returns its fp4_dtype and that
     stride."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor, got %s" % (name, type(t).__name__))
-    if t.dtype not in dtypes:
-        raise TypeError("%s must be %s, got %s" % (name, " or ".join(str(d) for d in dtypes), t.dtype))
+    code = F32 if t.dtype is torch.float32 else BF16 if t.dtype is torch.bfloat16 else None
+    if code is None or (like is not None and t.dtype is not like.dtype):
+        raise TypeError("%s must be %s, got %s"
+                        % (name, "float32 or bfloat16" if like is None else like.dtype, t.dtype))
     sizes, strides = t.shape, t.stride()
     if len(sizes) != ndim:
         raise ValueError("%s must have %d dimensions, got shape %s" % (name, ndim, tuple(sizes)))
-    if shape is not None and sizes != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(sizes)))
+    if like is not None and sizes != like.shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(like.shape), tuple(sizes)))
     width = 1
     for i in range(ndim - 1, 0, -1):
         if strides[i] != width and sizes[i] != 1:
@@ -599,10 +601,10 @@ def _want_rows(t, name, dtypes, ndim, device=None, shape=None):
     if device is not None and t.device != device:
         raise ValueError("%s is on %s, the call's operands on %s" % (name, t.device, device))
     if sizes[0] <= 1:
-        return width
+        return code, width
     if strides[0] < width:
         raise ValueError("%s has overlapping rows (strides %s)" % (name, strides))
-    return strides[0]
+    return code, strides[0]
 
 
 def _run_on(stream, device):
@@ -663,6 +665,7 @@ class KVCache:
         self.device = dev
         self.struct = KVCacheStruct(_ptr(k), _ptr(v), _ptr(k_scales), _ptr(v_scales), pages, page_size, heads, dim,
                                     fmt)
+        self.ref = ctypes.byref(self.struct)
 
     @classmethod
     def empty(cls, pages, page_size, kv_heads, head_dim, fmt=KV_BF16, device="cuda"):
@@ -691,19 +694,19 @@ def kv_append(cache, k, v, table, seq, pos, stream=None):
     fp4_kv_append in include/fp4.h."""
     torch = _torch()
     dev = _need_cache(cache)
-    ks = _want_rows(k, "k", (torch.float32, torch.bfloat16), 3, dev)
+    code, ks = _want_rows(k, "k", 3, dev)
     shape = k.shape
     n = shape[0]
     if shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
         raise ValueError("k must have shape %s, got %s" % ((n, cache.kv_heads, cache.head_dim), tuple(shape)))
-    vs = _want_rows(v, "v", (k.dtype,), 3, dev, shape)
+    vs = _want_rows(v, "v", 3, dev, k)[1]
     i32 = torch.int32
     _want(table, "table", i32, 2, dev)
     _want(seq, "seq", i32, 1, dev, n)
     _want(pos, "pos", i32, 1, dev, n)
     seqs, width = table.shape
-    rc = lib().fp4_kv_append(cache.struct, k.data_ptr(), v.data_ptr(), _dtype_code(k), ks, vs, table.data_ptr(), width,
-                             seqs, seq.data_ptr(), pos.data_ptr(), n, _run_on(stream, dev))
+    rc = lib().fp4_kv_append(cache.ref, k.data_ptr(), v.data_ptr(), code, ks, vs, table.data_ptr(), width, seqs,
+                             seq.data_ptr(), pos.data_ptr(), n, _run_on(stream, dev))
     if rc != 0:
         _check(rc, "fp4_kv_append")
     return cache
@@ -732,7 +735,7 @@ def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, 
     None).  Returns out (dtype of q, or out_dtype)."""
     torch = _torch()
     dev = _need_cache(cache)
-    qs = _want_rows(q, "q", (torch.float32, torch.bfloat16), 3, dev)
+    code, qs = _want_rows(q, "q", 3, dev)
     shape = q.shape
     B, heads, dim = shape
     if dim != cache.head_dim:
@@ -746,6 +749,7 @@ def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, 
         max_len = width * cache.page_size
     if out is None:
         out = _alloc(stream, torch.empty, shape, dtype=q.dtype if out_dtype is None else out_dtype, device=dev)
+        _dtype_code(out)
     else:
         _need_out(out, "out", shape, (torch.float32, torch.bfloat16), dev)
     if lse is not None:
@@ -763,9 +767,10 @@ def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, 
         ws = _alloc(stream, attention_workspace, cache, B, heads, max_len, weights_out is not None)
     else:
         _want(ws, "ws", torch.uint8, 1, dev)
-    rc = lib().fp4_attn_decode(cache.struct, q.data_ptr(), _dtype_code(q), qs, table.data_ptr(), width,
+    rc = lib().fp4_attn_decode(cache.ref, q.data_ptr(), code, qs, table.data_ptr(), width,
                                lens.data_ptr(), B, heads, max_len, window, dim ** -0.5 if scale is None else scale,
-                               out.data_ptr(), _dtype_code(out), _ptr(lse), _ptr(weights), _ptr(weights_out), stride,
+                               out.data_ptr(), code if out.dtype is q.dtype else 1 - code, _ptr(lse), _ptr(weights),
+                               _ptr(weights_out), stride,
                                _ptr(ws), 0 if ws is None else ws.numel(), _run_on(stream, dev))
     if rc != 0:
         _check(rc, "fp4_attn_decode")
@@ -818,8 +823,8 @@ def kv_evict(cache, table, lens, weights, budget, recent, out_table, out_cache=N
         ws = _alloc(stream, evict_workspace, cache, B, cap, budget)
     else:
         _want(ws, "ws", torch.uint8, 1, dev)
-    rc = lib().fp4_kv_evict(cache.struct, table.data_ptr(), width, lens.data_ptr(), weights.data_ptr(),
-                            weights.shape[2], out_cache.struct, out_table.data_ptr(), out_width, out_lens.data_ptr(),
+    rc = lib().fp4_kv_evict(cache.ref, table.data_ptr(), width, lens.data_ptr(), weights.data_ptr(),
+                            weights.shape[2], out_cache.ref, out_table.data_ptr(), out_width, out_lens.data_ptr(),
                             out_weights.data_ptr(), room, kept.data_ptr(), B, cap, budget, recent, _ptr(ws),
                             0 if ws is None else ws.numel(), _run_on(stream, dev))
     if rc != 0:
@@ -849,7 +854,7 @@ def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
     largest alternatives; see fp4_logprobs in include/fp4.h.  ws:
     logprobs_workspace's tensor (one is allocated here if None)."""
     torch = _torch()
-    xs = _want_rows(x, "x", (torch.float32, torch.bfloat16), 2)
+    code, xs = _want_rows(x, "x", 2)
     dev = x.device
     N, V = x.shape
     _want(tokens, "tokens", torch.int32, 2, dev)
@@ -868,7 +873,7 @@ def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
         ws = _alloc(stream, logprobs_workspace, N, V, top_k, dev)
     else:
         _want(ws, "ws", torch.uint8, 1, dev)
-    rc = lib().fp4_logprobs(x.data_ptr(), _dtype_code(x), xs, N, V, scale, tokens.data_ptr(), M, logp.data_ptr(),
+    rc = lib().fp4_logprobs(x.data_ptr(), code, xs, N, V, scale, tokens.data_ptr(), M, logp.data_ptr(),
                             entropy.data_ptr(), lse.data_ptr(), top_k, _ptr(top), _ptr(index), _ptr(ws),
                             0 if ws is None else ws.numel(), _run_on(stream, dev))
     if rc != 0:
@@ -882,7 +887,7 @@ def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scal
     entropy as logprobs returned them; see fp4_logprobs_backward in
     include/fp4.h.  Returns dx of x's dtype."""
     torch = _torch()
-    xs = _want_rows(x, "x", (torch.float32, torch.bfloat16), 2)
+    code, xs = _want_rows(x, "x", 2)
     dev = x.device
     N, V = x.shape
     _want(tokens, "tokens", torch.int32, 2, dev)
@@ -903,8 +908,8 @@ def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scal
         out = _alloc(stream, torch.empty, (N, V), dtype=x.dtype, device=dev)
         os_ = V
     else:
-        os_ = _want_rows(out, "out", (x.dtype,), 2, dev, x.shape)
-    rc = lib().fp4_logprobs_backward(x.data_ptr(), _dtype_code(x), xs, N, V, scale, tokens.data_ptr(), M,
+        os_ = _want_rows(out, "out", 2, dev, x)[1]
+    rc = lib().fp4_logprobs_backward(x.data_ptr(), code, xs, N, V, scale, tokens.data_ptr(), M,
                                      lse.data_ptr(), _ptr(entropy), g_logp.data_ptr(), _ptr(g_entropy),
                                      out.data_ptr(), os_, _run_on(stream, dev))
     if rc != 0:

@@ -376,6 +376,8 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   Stats st = {-INFINITY, 0.0f, 0.0f};
   float mine = -INFINITY, tau = INFINITY;  // this thread's largest; nothing passes until the threshold is known
   uint32_t count = 0u;                     // blocks this wave has noted
+  const bool only = b1 - b0 <= kStepBlocks;
+  if (tid == 0u) sh.few_count = 0u;
   u32x4 next[kUnroll] = {};
   const auto fetch = [&](uint32_t s0) __attribute__((always_inline)) {
     if (row.lo >= row.hi) return;  // (a matrix without a whole block)
@@ -440,6 +442,19 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       if (step == 0u) {
         // (Masked logits, -inf, are not noted; fill_ties finds the first where they are needed.)
         tau = threshold(sh, mine, k);
+        if (only) {
+          // A workgroup's one step: its elements are still at hand.
+          const float least = fmaxf(tau, -FLT_MAX);
+#pragma unroll
+          for (uint32_t u = 0; u < kUnroll; ++u) {
+            if (!(hi[u] >= least)) continue;
+            const uint32_t i0 = (s0 + u * kThreads + tid) * E - row.head;
+#pragma unroll
+            for (uint32_t e = 0; e < E; ++e)
+              if (v[u][e] >= least) push(sh, top_key(v[u][e], i0 + e));
+          }
+          continue;
+        }
 #pragma unroll
         for (uint32_t u = 0; u < kUnroll; ++u)
           note(sh, hi[u] >= tau && hi[u] > -INFINITY, s0 + u * kThreads + tid, count);
@@ -458,7 +473,6 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     sh.part[tid >> 6] = st;
     sh.wave_count[tid >> 6] = count;
   }
-  if (tid == 0u) sh.few_count = 0u;
   __syncthreads();
   st = join(join(sh.part[0], sh.part[1], c2), join(sh.part[2], sh.part[3], c2), c2);
 
