@@ -605,8 +605,8 @@ int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, int i
   if (rows < 0 || rows > kMaxDim || seqs < 0 || seqs > kMaxDim || table_width < 0 || table_width > kMaxDim)
     return FP4_ERR_SHAPE;
   if (k_stride < width || v_stride < width || k_stride > kMaxDim || v_stride > kMaxDim) return FP4_ERR_SHAPE;
-  // One thread per 8 values of a row.
-  if (rows * (width / 8) + 255 > kMaxWorkItems) return FP4_ERR_SHAPE;
+  // One thread per 16 values of a row.
+  if (rows * (width / 16) + 255 > kMaxWorkItems) return FP4_ERR_SHAPE;
   if (rows == 0 || seqs == 0 || table_width == 0 || cache->pages == 0) return FP4_OK;
   if ((rc = kv_check_buffers(*cache)) != FP4_OK) return rc;
   if (!k || !v || !page_table || !seq || !pos) return FP4_ERR_NULL;

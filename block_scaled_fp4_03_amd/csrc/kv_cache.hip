@@ -8,61 +8,77 @@ namespace fp4 {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Append.  One thread per 8 values of a new key row and the same 8 of the
-// value row; in the MX formats the four threads of a 32-value block share its
+// Append.  One thread per 16 values of a new key row and the same 16 of the
+// value row; in the MX formats the two threads of a 32-value block share its
 // maximum by DPP (blocks never straddle a wave: a row is a multiple of 64
-// values).
+// values).  Bound by the bytes: 16384 rows of 8 x 128 to MXFP8 take 18.0 us
+// (5.7 TB/s); with 8 values a thread 20.4, and with stores not marked as
+// streaming 20.9 (loads marked so made it slower).
 // ---------------------------------------------------------------------------
+constexpr uint32_t kPiece = 16;  // values of a thread
 template <int DT>
-__device__ __forceinline__ void load8(const void* x, size_t i, float (&v)[8]) {
+__device__ __forceinline__ void load_piece(const void* x, size_t i, float (&v)[kPiece]) {
   if (DT == kDtF32) {
     const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const float*>(x) + i);
-    const u32x4 a = p[0], b = p[1];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = u2f(a[k]);
-      v[4 + k] = u2f(b[k]);
+    for (int q = 0; q < 4; ++q) {
+      const u32x4 a = p[q];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * q + k] = u2f(a[k]);
     }
   } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + i);
+    const u32x4* p = reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(x) + i);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[2 * k] = u2f(a[k] << 16);
-      v[2 * k + 1] = u2f(a[k] & 0xFFFF0000u);
+    for (int q = 0; q < 2; ++q) {
+      const u32x4 a = p[q];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[8 * q + 2 * k] = u2f(a[k] << 16);
+        v[8 * q + 2 * k + 1] = u2f(a[k] & 0xFFFF0000u);
+      }
     }
   }
 }
 
-// The 8 values of `v` as elements d0 .. d0 + 7 of cache row `row`.  Every
+// The 16 values of `v` as elements d0 .. d0 + 15 of cache row `row`.  Every
 // lane of the wavefront takes part (the block maximum); `valid` writes.
 template <int FMT>
-__device__ __forceinline__ void store8(void* pool, uint8_t* scales, uint64_t row, uint32_t D, uint32_t d0,
-                                       const float (&v)[8], bool valid) {
+__device__ __forceinline__ void store_piece(void* pool, uint8_t* scales, uint64_t row, uint32_t D, uint32_t d0,
+                                            const float (&v)[kPiece], bool valid) {
+  uint8_t* out = static_cast<uint8_t*>(pool) + row * kv_row_bytes(FMT, D) + kv_row_bytes(FMT, d0);
   if (FMT == kKvBf16) {
-    u32x4 w;
+    u32x4 w[2];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
-    if (valid) *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(pool) + (row * D + d0) * 2u) = w;
+    for (int k = 0; k < 8; ++k) w[k / 4][k % 4] = bf16_pair(v[2 * k], v[2 * k + 1]);
+    if (valid) {
+      __builtin_nontemporal_store(w[0], reinterpret_cast<u32x4*>(out));
+      __builtin_nontemporal_store(w[1], reinterpret_cast<u32x4*>(out) + 1);
+    }
     return;
   }
   float am = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) am = fmaxf(am, fabsf(v[k]));
+  for (uint32_t k = 0; k < kPiece; ++k) am = fmaxf(am, fabsf(v[k]));
   am = fmaxf(am, lane_xor1(am));
-  am = fmaxf(am, lane_xor2(am));
   const uint32_t byte = FMT == kKvMx8 ? mx8_scale_byte<kFmtMX8>(am) : mx_scale_byte<kFmtMX>(am);
-  const float inv = u2f((254u - byte) << 23);  // 2^(127 - byte), exact
-  float y[8];
+  const float inv = u2f((254u - byte) << 23);
+  float y[kPiece];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) y[k] = v[k] * inv;
+  for (uint32_t k = 0; k < kPiece; ++k) y[k] = v[k] * inv;
   if (!valid) return;
   if (FMT == kKvMx8) {
-    u32x2 w;
-    w[0] = e4m3x4_sat(y[0], y[1], y[2], y[3]);
-    w[1] = e4m3x4_sat(y[4], y[5], y[6], y[7]);
-    *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(pool) + row * D + d0) = w;
+    u32x4 w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = e4m3x4_sat(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(out));
   } else {
-    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(pool) + (row * D + d0) / 2u) = pack8(y);
+    float lo[8], hi[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      lo[k] = y[k];
+      hi[k] = y[8 + k];
+    }
+    __builtin_nontemporal_store(u32x2{pack8(lo), pack8(hi)}, reinterpret_cast<u32x2*>(out));
   }
   if ((d0 & 31u) == 0u) scales[row * (D / 32u) + d0 / 32u] = (uint8_t)byte;
 }
@@ -76,11 +92,11 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvPool c, const void* __
                                                         uint32_t total) {
   const uint32_t at = blockIdx.x * 256u + threadIdx.x;
   const bool in = at < total;
-  const uint32_t i = (in ? at : 0u) / per_row, e = ((in ? at : 0u) % per_row) * 8u;
+  const uint32_t i = (in ? at : 0u) / per_row, e = ((in ? at : 0u) % per_row) * kPiece;
   const uint32_t D = (uint32_t)c.head_dim, h = e / D, d0 = e % D;
-  float a[8], b[8];
-  load8<DT>(k, (size_t)i * (size_t)k_stride + e, a);
-  load8<DT>(v, (size_t)i * (size_t)v_stride + e, b);
+  float a[kPiece], b[kPiece];
+  load_piece<DT>(k, (size_t)i * (size_t)k_stride + e, a);
+  load_piece<DT>(v, (size_t)i * (size_t)v_stride + e, b);
   const int32_t s = seq[i], t = pos[i];
   const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)c.page_size);
   bool ok = in && s >= 0 && s < seqs && t >= 0 && (int64_t)(t >> shift) < width;
@@ -88,15 +104,15 @@ __global__ __launch_bounds__(256) void kv_append_kernel(KvPool c, const void* __
   ok = ok && page >= 0 && page < c.pages;
   const uint64_t row =
       ok ? (((uint64_t)(uint32_t)page * (uint32_t)c.kv_heads + h) << shift) + ((uint32_t)t & (c.page_size - 1u)) : 0u;
-  store8<FMT>(c.k, c.ks, row, D, d0, a, ok);
-  store8<FMT>(c.v, c.vs, row, D, d0, b, ok);
+  store_piece<FMT>(c.k, c.ks, row, D, d0, a, ok);
+  store_piece<FMT>(c.v, c.vs, row, D, d0, b, ok);
 }
 
 template <int FMT>
 hipError_t append_fmt(const KvPool& c, const void* k, const void* v, int in_dtype, int64_t k_stride, int64_t v_stride,
                       const int32_t* table, int64_t width, int64_t seqs, const int32_t* seq, const int32_t* pos,
                       int64_t rows, hipStream_t stream) {
-  const uint32_t per_row = (uint32_t)(c.kv_heads * c.head_dim / 8);
+  const uint32_t per_row = (uint32_t)(c.kv_heads * c.head_dim / (int)kPiece);
   const uint32_t total = (uint32_t)(rows * per_row), grid = (total + 255u) / 256u;
   if (in_dtype == kDtF32)
     kv_append_kernel<FMT, kDtF32><<<grid, 256, 0, stream>>>(c, k, v, k_stride, v_stride, table, width, seqs, seq, pos,

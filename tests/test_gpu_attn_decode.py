@@ -146,6 +146,14 @@ def test_attention_f32(fmt, lens, Hkv, G, D, page):
     run_case(sum(lens) + 31 * G, fmt, lens, Hkv, G, D, page, f32=True)
 
 
+@pytest.mark.parametrize("fmt,B,most", [("bf16", 130, 40), ("mxfp8", 65, 700), ("mxfp4", 600, 9)])
+def test_attention_many_sequences(fmt, B, most):
+    """More sequences than lanes, many of them empty: the shares' search over the lengths."""
+    lens = np.random.default_rng(B).integers(-2, most, B)
+    lens[lens < most // 4] = 0
+    run_case(B, fmt, [int(n) for n in lens], 1, 2, 64, 16, weights=True)
+
+
 def test_attention_mixed_dtypes():
     run_case(51, "bf16", [200, 33], 2, 4, 128, 16, f32=False, out_f32=True)
     run_case(52, "mxfp8", [200, 33], 2, 4, 128, 16, f32=True, out_f32=False)

@@ -110,6 +110,21 @@ def test_logprobs(dtype, N, V, M, k, pad, scale):
     check_forward(vals, scale, tokens, res, k, what)
 
 
+def test_logprobs_more_rows_than_a_grid_holds():
+    """70001 rows take two launches: every row's results and gradient."""
+    import block_scaled_fp4_03_amd as fp4
+    rng = np.random.default_rng(12)
+    x = rng.standard_normal((70001, 9)).astype(np.float32)
+    tokens = rng.integers(0, 9, (70001, 1)).astype(np.int32)
+    say("logprobs of 70001 rows")
+    res = fp4.logprobs(to_dev(x), to_dev(tokens), top_k=3)
+    check_forward(x, 1.0, tokens, res, 3, "70001 rows")
+    g = rng.standard_normal((70001, 1)).astype(np.float32)
+    dx = to_host(fp4.logprobs_backward(to_dev(x), to_dev(tokens), res.lse, to_dev(g)))
+    rows = np.r_[0:50, 65500:65600, 69951:70001]
+    check_grad(x[rows], 1.0, tokens[rows], g[rows], None, dx[rows].astype(np.float64), "f32", "70001 rows")
+
+
 @pytest.mark.parametrize("dtype", ("f32", "bf16"))
 @pytest.mark.parametrize("kind", ["ascending", "descending", "equal", "ties", "peaked", "masked", "lowest", "one",
                                   "zeros", "large"])
