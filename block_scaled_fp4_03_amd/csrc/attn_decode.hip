@@ -297,8 +297,113 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units) {
   return s;
 }
 
+// A workgroup's shared memory.
+template <int D>
+struct Shared {
+  float red[2][kHeadTile][D + 4];  // sums of two waves (rows padded against bank conflicts); in a join, factors
+  float wave_m[kWaves][kHeadTile], wave_l[kWaves][kHeadTile];
+  uint32_t last_arrival;
+};
+
+// A workgroup's piece of a unit: tiles [t_begin, t_end) (those past the
+// sequence's last only count) for the query heads head0 .. head0 + heads - 1,
+// which read kv head h of sequence b.  `pieces` workgroups from wg0 on have one.
+struct Piece {
+  Range r;
+  uint32_t b, h, head0, heads, t_begin, t_end, wg0, pieces;
+};
+
+// Element pairs of a piece's results, 256 at a time: f(head, d).
+template <int D, typename F>
+__device__ __forceinline__ void each_pair(uint32_t heads, F f) {
+  for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) f(i / (D / 2), 2u * (i % (D / 2)));
+}
+
+// Head hd's output elements d, d + 1.
+template <int D>
+__device__ __forceinline__ void write_out(const AttnArgs& a, const Piece& pc, uint32_t hd, uint32_t d, float x,
+                                          float y) {
+  store_out2(a, ((size_t)pc.b * (uint32_t)a.q_heads + pc.head0 + hd) * D + d, x, y);
+}
+
+// Head hd's maximum and sum to where they are wanted (one thread a head).
+__device__ __forceinline__ void write_stats(const AttnArgs& a, const Piece& pc, uint32_t hd, float mx, float s) {
+  const size_t at = (size_t)pc.b * (uint32_t)a.q_heads + pc.head0 + hd;
+  if (a.lse) a.lse[at] = s == 0.0f ? -INFINITY : (mx + __builtin_log2f(s)) * kLn2;
+  if (a.final_stats) *reinterpret_cast<v2f*>(a.final_stats + 2 * at) = v2f{mx, s == 0.0f ? 0.0f : 1.0f / s};
+}
+
+// The unit's result from its pieces' (a.part, a.stats), by the workgroup that
+// arrived last.  64 pieces at a time: the running maximum and sum of every
+// head, the factors 2^(m_p - M) of the pieces and that of what came before.
+template <int D>
+__device__ __forceinline__ void join_pieces(const AttnArgs& a, const Piece& pc, Shared<D>& sh) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  float* factor = &sh.red[0][0][0];  // 16 x 64
+  static_assert(kHeadTile * 64 * sizeof(float) <= sizeof(sh.red), "factors fit in the array they reuse");
+  constexpr uint32_t kItems = kHeadTile * (D / 2) / 256;  // pairs of elements of a thread, at most
+  // Where piece p keeps head hd: a workgroup's place for a unit it begins, or for one begun before.
+  const auto place = [&](uint32_t p, uint32_t hd) { return (2u * (pc.wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile + hd; };
+  float x[kItems], y[kItems];
+#pragma unroll
+  for (uint32_t k = 0; k < kItems; ++k) x[k] = y[k] = 0.0f;
+  if (tid < kHeadTile) {
+    sh.wave_m[0][tid] = -INFINITY;
+    sh.wave_l[0][tid] = 0.0f;
+  }
+  __syncthreads();
+  for (uint32_t p0 = 0u; p0 < pc.pieces; p0 += 64u) {
+    const uint32_t here = min(pc.pieces - p0, 64u);
+    for (uint32_t hd = wave; hd < pc.heads; hd += kWaves) {
+      v2f ms = v2f{-INFINITY, 0.0f};
+      if (lane < here) ms = load2_agent(a.stats + 2u * place(p0 + lane, hd));
+      const float old = sh.wave_m[0][hd], to = fmaxf(old, wave_fmax(ms[0]));
+      const float f = ms[0] == -INFINITY ? 0.0f : exp2_fast(ms[0] - to);
+      const float f_old = old == -INFINITY ? 0.0f : exp2_fast(old - to);
+      const float s = wave_fsum(ms[1] * f);
+      factor[hd * 64u + lane] = f;
+      if (lane == 0u) {
+        sh.wave_m[0][hd] = to;
+        sh.wave_l[0][hd] = sh.wave_l[0][hd] * f_old + s;
+        sh.wave_m[1][hd] = f_old;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (uint32_t k = 0; k < kItems; ++k) {
+      const uint32_t i = k * 256u + tid, hd = i / (D / 2), d = 2u * (i % (D / 2));
+      if (hd >= pc.heads) continue;
+      x[k] *= sh.wave_m[1][hd];
+      y[k] *= sh.wave_m[1][hd];
+      for (uint32_t q0 = 0u; q0 < here; q0 += 4u) {
+        v2f v[4];
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j)
+          v[j] = load2_agent(a.part + (size_t)place(p0 + min(q0 + j, here - 1u), hd) * D + d);
+#pragma unroll
+        for (uint32_t j = 0; j < 4u; ++j) {
+          if (q0 + j >= here) continue;
+          x[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][0], x[k]);
+          y[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][1], y[k]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (uint32_t k = 0; k < kItems; ++k) {
+    const uint32_t i = k * 256u + tid, hd = i / (D / 2), d = 2u * (i % (D / 2));
+    if (hd >= pc.heads) continue;
+    const float s = sh.wave_l[0][hd], inv = s == 0.0f ? 0.0f : 1.0f / s;
+    write_out<D>(a, pc, hd, d, x[k] * inv, y[k] * inv);
+  }
+  if (tid < pc.heads) write_stats(a, pc, tid, sh.wave_m[0][tid], sh.wave_l[0][tid]);
+}
+
+// One piece: the attention to its tokens, and the unit's result if it is the
+// only one, else its part of it.
 template <int FMT, int D, bool EX>
-__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
+__device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc, Shared<D>& sh) {
   constexpr int kRow = (int)kv_row_bytes(FMT, D);
   constexpr int kSteps = D / 32;               // matrix instructions along D for 16 tokens
   constexpr int EV = D / 16;                   // elements of V per lane and token
@@ -307,31 +412,12 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   constexpr bool MX = FMT != kKvBf16;
   constexpr int kBlocks = D / 32;
   constexpr int kQTerms = EX ? 3 : 1, kPTerms = EX ? 3 : 2;
-  constexpr int kPad = D + 4;
-
-  __shared__ float red[2][kHeadTile][kPad];
-  __shared__ float wave_m[kWaves][kHeadTile], wave_l[kWaves][kHeadTile];
-  __shared__ uint32_t last_arrival;
 
   const uint32_t lane = threadIdx.x & 63u, c = lane & 15u, g = lane >> 4;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const uint32_t shift = (uint32_t)__builtin_ctz((uint32_t)a.c.page_size), in_page = (uint32_t)a.c.page_size - 1u;
-  const uint32_t units = (uint32_t)a.c.kv_heads * (uint32_t)a.head_tiles;
-  Share w = share_of(a, units);
-
-  for (; w.pos < w.end;) {
-  // The share's next piece: tiles [t_begin, t_end) of unit `unit` of sequence b.
-  const uint32_t b = w.b;
-  const Range r = range_at(a, load_uniform(a.lens, b));
-  const uint32_t counted = r.counted(w.more), unit = (w.pos - w.base * units) / counted;
-  const uint32_t unit0 = w.base * units + unit * counted;
-  const uint32_t t_begin = w.pos - unit0, t_upto = min(counted, t_begin + (w.end - w.pos));
-  const uint32_t t_end = min(t_upto, r.tiles);
-  // The workgroups that have a piece of the unit.
-  const uint32_t wg0 = unit0 / w.share, pieces = (unit0 + counted - 1u) / w.share - wg0 + 1u;
-  const uint32_t h = unit / (uint32_t)a.head_tiles, ht = unit % (uint32_t)a.head_tiles;
-  const uint32_t heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
-  const uint32_t head0 = h * (uint32_t)a.group + ht * kHeadTile;  // first query head
+  const Range r = pc.r;
+  const uint32_t b = pc.b, h = pc.h, head0 = pc.head0, heads = pc.heads, t_end = min(pc.t_end, r.tiles);
 
   // Q: head c's elements g D/4 + 8 s .. + 7 in step s; zero for heads past
   // the group.  Asked for here, looked at once K and V are asked for too.
@@ -394,7 +480,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     }
   };
 
-  uint32_t tile = t_begin + wave;
+  uint32_t tile = pc.t_begin + wave;
   uint64_t row[2] = {~0ull, ~0ull}, next[2] = {~0ull, ~0ull};
   if (tile < t_end) {
     row[0] = half_row(tile, 0);
@@ -525,8 +611,8 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       constexpr uint32_t kLo = 0x05040100u, kHi = 0x07060302u;
       const uint32_t sel = (e & 1) ? kHi : kLo;
       const int i = e >> 1;
-      const v8bf vf = frag(__builtin_amdgcn_perm(vp[1][i], vp[0][i], sel), __builtin_amdgcn_perm(vp[3][i], vp[2][i], sel),
-                           __builtin_amdgcn_perm(vp[5][i], vp[4][i], sel), __builtin_amdgcn_perm(vp[7][i], vp[6][i], sel));
+      const auto two = [&](int j) { return __builtin_amdgcn_perm(vp[j + 1][i], vp[j][i], sel); };
+      const v8bf vf = frag(two(0), two(2), two(4), two(6));
 #pragma unroll
       for (int k = 0; k < kPTerms; ++k) o[e] = mfma(vf, frag(pt[k][0], pt[k][1], pt[k][2], pt[k][3]), o[e]);
     }
@@ -545,158 +631,104 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   l += __shfl_xor(l, 16);
   l += __shfl_xor(l, 32);
   if (lane < 16u) {
-    wave_m[wave][c] = m;
-    wave_l[wave][c] = l;
+    sh.wave_m[wave][c] = m;
+    sh.wave_l[wave][c] = l;
   }
   __syncthreads();
-  float M = wave_m[0][c];
+  float M = sh.wave_m[0][c];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) M = fmaxf(M, wave_m[w][c]);
+  for (int w = 1; w < kWaves; ++w) M = fmaxf(M, sh.wave_m[w][c]);
   const float f = m == -INFINITY ? 0.0f : exp2_fast(m - M);
   // Lane (c, g) holds head c, d = (4g + i) EV + e of o[e][i].
   if (wave < 2u && c < heads) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < EV; ++e) red[wave][c][(4 * g + i) * EV + e] = o[e][i] * f;
+      for (int e = 0; e < EV; ++e) sh.red[wave][c][(4 * g + i) * EV + e] = o[e][i] * f;
   }
   __syncthreads();
   if (wave >= 2u && c < heads) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int e = 0; e < EV; ++e) red[wave - 2u][c][(4 * g + i) * EV + e] += o[e][i] * f;
+      for (int e = 0; e < EV; ++e) sh.red[wave - 2u][c][(4 * g + i) * EV + e] += o[e][i] * f;
   }
   __syncthreads();
 
-  // Sum of head hd over the waves, with the workgroup's maximum.
+  // Head hd's sum over the waves, for the workgroup's maximum mx.
   const auto head_sum = [&](uint32_t hd, float& mx) {
-    mx = wave_m[0][hd];
+    mx = sh.wave_m[0][hd];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, wave_m[w][hd]);
+    for (int w = 1; w < kWaves; ++w) mx = fmaxf(mx, sh.wave_m[w][hd]);
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
-      s += wave_m[w][hd] == -INFINITY ? 0.0f : wave_l[w][hd] * exp2_fast(wave_m[w][hd] - mx);
+      s += sh.wave_m[w][hd] == -INFINITY ? 0.0f : sh.wave_l[w][hd] * exp2_fast(sh.wave_m[w][hd] - mx);
     return s;
   };
-  const auto finish_head = [&](uint32_t hd, float mx, float s) {  // one thread per head
-    const size_t at = (size_t)b * (uint32_t)a.q_heads + head0 + hd;
-    if (a.lse) a.lse[at] = s == 0.0f ? -INFINITY : (mx + __builtin_log2f(s)) * kLn2;
-    if (a.final_stats) *reinterpret_cast<v2f*>(a.final_stats + 2 * at) = v2f{mx, s == 0.0f ? 0.0f : 1.0f / s};
-  };
-
-  if (pieces == 1u) {
-    for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
-      const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-      float mx;
+  float mx;
+  if (pc.pieces == 1u) {
+    each_pair<D>(heads, [&](uint32_t hd, uint32_t d) {
       const float s = head_sum(hd, mx), inv = s == 0.0f ? 0.0f : 1.0f / s;
-      store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + d, (red[0][hd][d] + red[1][hd][d]) * inv,
-                 (red[0][hd][d + 1] + red[1][hd][d + 1]) * inv);
-    }
+      write_out<D>(a, pc, hd, d, (sh.red[0][hd][d] + sh.red[1][hd][d]) * inv,
+                   (sh.red[0][hd][d + 1] + sh.red[1][hd][d + 1]) * inv);
+    });
     if (threadIdx.x < heads) {
-      float mx;
       const float s = head_sum(threadIdx.x, mx);
-      finish_head(threadIdx.x, mx, s);
+      write_stats(a, pc, threadIdx.x, mx, s);
     }
-  } else {
-    // ---- the pieces' results: written through, then the last to arrive joins ----
-    // A workgroup has two places: for a unit it begins, and for one begun before.
-    const uint32_t mine = (2u * blockIdx.x + (t_begin == 0u ? 1u : 0u)) * kHeadTile;
-    for (uint32_t i = threadIdx.x; i < heads * (D / 2); i += 256u) {
-      const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-      store2_agent(a.part + (size_t)(mine + hd) * D + d, red[0][hd][d] + red[1][hd][d],
-                   red[0][hd][d + 1] + red[1][hd][d + 1]);
-    }
-    if (threadIdx.x < heads) {
-      float mx;
-      const float s = head_sum(threadIdx.x, mx);
-      store2_agent(a.stats + 2u * (mine + threadIdx.x), mx, s);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
-    __syncthreads();
-    if (threadIdx.x == 0u) {
-      uint32_t* done = a.done + wg0;  // of the units a workgroup begins only the last is cut
-      const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      last_arrival = before == pieces - 1u;
-      if (last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (last_arrival) {
-      // Place of piece p, and its head hd.
-      const auto place = [&](uint32_t p, uint32_t hd) { return (2u * (wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile + hd; };
-      // 64 pieces at a time: running maximum M and sum of every head, the
-      // factors 2^(m_p - M) of its pieces (in the red array, free now) and
-      // that of what was summed before.
-      float* factor = &red[0][0][0];  // 16 x 64
-      static_assert(kHeadTile * 64 <= 2 * kHeadTile * kPad, "factors fit in the array they reuse");
-      constexpr uint32_t kItems = kHeadTile * (D / 2) / 256;  // pairs of elements of a thread, at most
-      float x[kItems], y[kItems];
-#pragma unroll
-      for (uint32_t k = 0; k < kItems; ++k) x[k] = y[k] = 0.0f;
-      if (threadIdx.x < kHeadTile) {
-        wave_m[0][threadIdx.x] = -INFINITY;
-        wave_l[0][threadIdx.x] = 0.0f;
-      }
-      __syncthreads();
-      for (uint32_t p0 = 0u; p0 < pieces; p0 += 64u) {
-        const uint32_t here = min(pieces - p0, 64u);
-        for (uint32_t hd = wave; hd < heads; hd += kWaves) {
-          v2f ms = v2f{-INFINITY, 0.0f};
-          if (lane < here) ms = load2_agent(a.stats + 2u * place(p0 + lane, hd));
-          const float old = wave_m[0][hd], to = fmaxf(old, wave_fmax(ms[0]));
-          const float f = ms[0] == -INFINITY ? 0.0f : exp2_fast(ms[0] - to);
-          const float f_old = old == -INFINITY ? 0.0f : exp2_fast(old - to);
-          const float s = wave_fsum(ms[1] * f);
-          factor[hd * 64u + lane] = f;
-          if (lane == 0u) {
-            wave_m[0][hd] = to;
-            wave_l[0][hd] = wave_l[0][hd] * f_old + s;
-            wave_m[1][hd] = f_old;
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (uint32_t k = 0; k < kItems; ++k) {
-          const uint32_t i = k * 256u + threadIdx.x;
-          if (i < heads * (D / 2)) {
-            const uint32_t hd = i / (D / 2), d = 2u * (i % (D / 2));
-            x[k] *= wave_m[1][hd];
-            y[k] *= wave_m[1][hd];
-            for (uint32_t q0 = 0u; q0 < here; q0 += 4u) {
-              v2f v[4];
-#pragma unroll
-              for (uint32_t j = 0; j < 4u; ++j)
-                v[j] = load2_agent(a.part + (size_t)place(p0 + min(q0 + j, here - 1u), hd) * D + d);
-#pragma unroll
-              for (uint32_t j = 0; j < 4u; ++j) {
-                if (q0 + j >= here) continue;
-                x[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][0], x[k]);
-                y[k] = __builtin_fmaf(factor[hd * 64u + q0 + j], v[j][1], y[k]);
-              }
-            }
-          }
-        }
-        __syncthreads();
-      }
-#pragma unroll
-      for (uint32_t k = 0; k < kItems; ++k) {
-        const uint32_t i = k * 256u + threadIdx.x;
-        if (i < heads * (D / 2)) {
-          const uint32_t hd = i / (D / 2);
-          const float s = wave_l[0][hd], inv = s == 0.0f ? 0.0f : 1.0f / s;
-          store_out2(a, ((size_t)b * (uint32_t)a.q_heads + head0 + hd) * D + 2u * (i % (D / 2)), x[k] * inv, y[k] * inv);
-        }
-      }
-      if (threadIdx.x < heads) finish_head(threadIdx.x, wave_m[0][threadIdx.x], wave_l[0][threadIdx.x]);
-    }
+    return;
   }
-  w.pos += t_upto - t_begin;
-  if (t_upto == counted && unit + 1u == units) {
-    w.base += counted;
-    ++w.b;
+
+  // ---- a part of the unit: written through, and the last to arrive joins them ----
+  const uint32_t mine = (2u * blockIdx.x + (pc.t_begin == 0u ? 1u : 0u)) * kHeadTile;
+  each_pair<D>(heads, [&](uint32_t hd, uint32_t d) {
+    store2_agent(a.part + (size_t)(mine + hd) * D + d, sh.red[0][hd][d] + sh.red[1][hd][d],
+                 sh.red[0][hd][d + 1] + sh.red[1][hd][d + 1]);
+  });
+  if (threadIdx.x < heads) {
+    const float s = head_sum(threadIdx.x, mx);
+    store2_agent(a.stats + 2u * (mine + threadIdx.x), mx, s);
   }
-  __syncthreads();  // the shared arrays are free for the next piece
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
+  __syncthreads();
+  if (threadIdx.x == 0u) {
+    uint32_t* done = a.done + pc.wg0;  // of the units a workgroup begins only the last is cut
+    const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    sh.last_arrival = before == pc.pieces - 1u;
+    if (sh.last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (sh.last_arrival) join_pieces<D>(a, pc, sh);
+}
+
+template <int FMT, int D, bool EX>
+__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
+  __shared__ Shared<D> sh;
+  const uint32_t units = (uint32_t)a.c.kv_heads * (uint32_t)a.head_tiles;
+  Share w = share_of(a, units);
+  while (w.pos < w.end) {
+    // The share's next piece, of unit `unit` of sequence w.b.
+    Piece pc;
+    pc.b = w.b;
+    pc.r = range_at(a, load_uniform(a.lens, w.b));
+    const uint32_t counted = pc.r.counted(w.more), unit = (w.pos - w.base * units) / counted;
+    const uint32_t unit0 = w.base * units + unit * counted;
+    pc.t_begin = w.pos - unit0;
+    pc.t_end = min(counted, pc.t_begin + (w.end - w.pos));
+    pc.wg0 = unit0 / w.share;
+    pc.pieces = (unit0 + counted - 1u) / w.share - pc.wg0 + 1u;
+    const uint32_t ht = unit % (uint32_t)a.head_tiles;
+    pc.h = unit / (uint32_t)a.head_tiles;
+    pc.heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
+    pc.head0 = pc.h * (uint32_t)a.group + ht * kHeadTile;
+    attend_piece<FMT, D, EX>(a, pc, sh);
+    w.pos += pc.t_end - pc.t_begin;
+    if (pc.t_end == counted && unit + 1u == units) {
+      w.base += counted;
+      ++w.b;
+    }
+    __syncthreads();  // the shared memory is free for the next piece
   }
 }
 
