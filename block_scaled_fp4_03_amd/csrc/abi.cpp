@@ -636,10 +636,10 @@ static int attn_check_shape(const fp4_kv_cache* cache, int64_t B, int64_t q_head
   // Grid: sequences in z, kv heads x tiles of 16 query heads in y.
   if (B < 0 || B > 65535 || q_heads < 0 || q_heads % cache->kv_heads != 0 || q_heads > 65535) return FP4_ERR_SHAPE;
   if (max_len < 0 || max_len > kMaxDim) return FP4_ERR_SHAPE;
-  // The kernel counts all sequences' and heads' tiles of 32 tokens, each
-  // sequence's up to a multiple of 8, in 32 bits.
+  // The kernel counts all sequences' and heads' tiles of 32 tokens, rounded up
+  // and with up to 24 more for each, in 32 bits.
   const int64_t units = (q_heads / cache->kv_heads + 15) / 16 * cache->kv_heads;
-  if ((max_len / 32 + 9) * B * units > kMaxRange) return FP4_ERR_SHAPE;
+  if ((max_len / 32 + 32) * B * units > kMaxRange) return FP4_ERR_SHAPE;
   return FP4_OK;
 }
 

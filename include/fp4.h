@@ -485,7 +485,7 @@ size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q
  *   FP32 or NULL.  q_heads a multiple of kv_heads.
  *   lens: B device int32 (negative reads as 0).  max_len <= table_width *
  *   page_size bounds the lengths (and sizes the workspace); B * kv_heads *
- *   ceil(q_heads / kv_heads / 16) * (max_len / 32 + 9) < 2^32, B < 2^16.  window: 0 for
+ *   ceil(q_heads / kv_heads / 16) * (max_len / 32 + 32) < 2^32, B < 2^16.  window: 0 for
  *   none.
  *   weights_out (optional): FP32 B x kv_heads x weights_stride, receives for
  *   every t < len  weights_in[b,kv,t] + sum over the kv head's query heads of
