@@ -55,28 +55,29 @@ __device__ __forceinline__ float logit(const void* x, size_t i) {
   return u2f((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
 }
 
-// A row as aligned 16-byte blocks: block j holds elements j E - head .. (the
-// first and the last block may be partly outside the row).  Blocks are loaded
-// whole, also those that reach into the rows beside, as long as they lie
-// within the matrix; at most the first of its first row and the last of its
-// last do not.
+// A row as 16-byte blocks from its first 128-byte line on: block j holds
+// elements j E - head .. (the first blocks and the last may be partly or
+// wholly outside the row).  Blocks are loaded whole, also those that reach into
+// the rows beside, as long as they lie within the matrix; the first of its
+// first rows and the last of its last may not.  (A wavefront's 1 KB is then
+// eight whole lines.)
 template <int DT>
 struct Row {
-  static constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u, E = kElem<DT>;
+  static constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u, E = kElem<DT>, kLine = 128u / kSize;
   const uint8_t* p;  // the row's first element
   uint32_t V, head, blocks;
   uint32_t lo, hi;   // blocks [lo, hi) can be loaded whole
   __device__ __forceinline__ Row(const void* x, int64_t stride, size_t n, size_t rows, uint32_t V_) : V(V_) {
     p = static_cast<const uint8_t*>(x) + n * (size_t)stride * kSize;
-    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15u) / kSize;
+    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 127u) / kSize;
     blocks = (V + head + E - 1u) / E;
-    const uint32_t tail = blocks * E - head - V;  // elements of the last block past the row
-    lo = n == 0u && head > 0u ? 1u : 0u;
-    hi = n + 1u == rows && tail > 0u ? blocks - 1u : blocks;
+    const uint32_t before = (uint32_t)min(n * (size_t)stride, (size_t)kLine);  // elements of earlier rows
+    lo = head > before ? (head - before + E - 1u) / E : 0u;
+    hi = n + 1u == rows && blocks * E > head + V ? blocks - 1u : blocks;
   }
   // Whether blocks [j, j + n) lie wholly inside the row.
   __device__ __forceinline__ bool inside(uint32_t j, uint32_t n) const {
-    return (j > 0u || head == 0u) && (uint64_t)(j + n) * E <= (uint64_t)V + head;
+    return j * E >= head && (uint64_t)(j + n) * E <= (uint64_t)V + head;
   }
   // Block j as it lies in memory, or the nearest that can be loaded (lo < hi).
   __device__ __forceinline__ u32x4 raw(uint32_t j) const {
@@ -729,8 +730,8 @@ hipError_t launch_logprobs_backward(const void* x, int dtype, int64_t stride, in
                                     hipStream_t stream) {
   const size_t size = dtype == kDtF32 ? 4 : 2;
   const int64_t step = kStepBlocks * (16 / (int64_t)size);
-  // One more step than the row's length where its start is not aligned.
-  const uint32_t steps = (uint32_t)((V + (int64_t)(16 / size) - 1 + step - 1) / step);
+  // A row that does not begin a line may reach into one step more than its length takes.
+  const uint32_t steps = (uint32_t)((V + (int64_t)(128 / size) - 1 + step - 1) / step);
   for (int64_t n0 = 0; n0 < N; n0 += 65535) {
     const int64_t rows = N - n0 < 65535 ? N - n0 : 65535;
     const void* xr = static_cast<const uint8_t*>(x) + (size_t)n0 * (size_t)stride * size;
