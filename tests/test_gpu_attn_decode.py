@@ -351,3 +351,29 @@ def test_decode_calls_share_one_workspace():
     for i in list(range(len(calls))) * 2 + list(range(len(calls)))[::-1] * 2:
         for got, w in zip(calls[i][1](ws), want[i]):
             assert torch.equal(got, w), i
+
+
+@pytest.mark.parametrize("fmt,f32", [("bf16", False), ("mxfp8", False), ("mxfp4", False), ("bf16", True)])
+@pytest.mark.parametrize("lens,G,D", [([13405], 12, 128), ([33000], 16, 256), ([9000, 5, 7100], 3, 192),
+                                      ([66000, 70, 2300], 1, 64), ([2180], 2, 64)])
+def test_units_in_many_pieces(fmt, f32, lens, G, D):
+    """17 pieces of a unit and more are joined in two or three levels, with one
+    kept workspace (its counters zero again after each call) and the same bits
+    each time."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    run_case(len(lens) + D, fmt, lens, 1, G, D, 64, f32=f32)
+    rng = np.random.default_rng(D)
+    width = -(-max(lens) // 64)
+    cache = cache_of(make(3, fmt, width, 1, 64, D))
+    table = to_dev(np.stack([rng.permutation(width) for _ in lens]).astype(np.int32))
+    q = torch.from_numpy(rng.standard_normal((len(lens), G, D)).astype(np.float32)).cuda()
+    q = q if f32 else q.bfloat16()
+    ws = fp4.attention_workspace(cache, len(lens), G, width * 64)
+    first = None
+    for n in (0, 1, 2):
+        out = fp4.decode_attention(q, cache, table, to_dev(np.array(lens, np.int32)), ws=ws)
+        torch.cuda.synchronize()
+        assert not ws[:2048].any()
+        first = out if first is None else first
+        assert torch.equal(out, first)
