@@ -6,9 +6,11 @@
 //   entropy = log S - W / S.
 // Moving r to r' multiplies S by f = e^(scale (r - r')) and turns W into
 // f (W + scale (r - r') S).  Each thread keeps its own (r, S, W) and moves r
-// only when a logit passes it by 2^kLazy, so the common step is five VALU
-// operations and one exponential an element, below the memory's time.  All in
-// base 2 (t times log2 e), FP32.
+// only when a logit passes it by 2^kLazy, so the common step is six VALU
+// operations, one of them the exponential, for an element.  All in base 2 (t
+// times log2 e), FP32.  Their issue (about 100 us) and the memory (130 us at
+// 6.3 TB/s) bound it together: 4096 rows of 100003 BF16 take 141 us with the
+// top 8 (5.8 TB/s), 133 us without; 1024 rows of 131072 FP32 86 us (6.2 TB/s).
 //
 // The top k in the same pass: the first 16 KB give a threshold with at least
 // k elements at or above it (the k-th largest of 64 groups' maxima).  16-byte
@@ -18,8 +20,8 @@
 // ... steps, from the groups' maxima so far): the number of blocks noted grows
 // with the logarithm of V.  At the end the noted blocks' elements at or above
 // the last threshold are ranked, a wave's first 64 blocks' from LDS (read once
-// more they take 142 instead of 139 us for 6413 rows of 39381 BF16), later ones'
-// from memory.  An element equal to
+// more they cost 2% for 6413 rows of 39381 BF16, which take 107 us), later
+// ones' from memory.  An element equal to
 // the threshold in a later block is never among the k: k elements before it
 // are as large.  A row that overflows a buffer (a rising row, or one of few
 // values) is read again for elements above the k-th largest of the groups'
@@ -87,6 +89,18 @@ struct Row {
     const uint8_t* at = p + ((int64_t)min(max(j, lo), hi - 1u) * E - head) * kSize;
     return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at));  // a logit is read once
   }
+  // A step's blocks from j0 on, a thread's every 256th, as raw() gives them
+  // (offsets in 32 bits from the step's first).
+  __device__ __forceinline__ void raw_step(uint32_t j0, u32x4 (&w)[kUnroll]) const {
+    if (lo >= hi) return;  // a matrix without a whole block
+    const uint32_t from = min(j0, hi - 1u), least = max(lo, from) - from, most = hi - 1u - from;
+    const uint8_t* at = p - head * kSize + (size_t)from * 16u;
+#pragma unroll
+    for (uint32_t u = 0; u < kUnroll; ++u) {
+      const uint32_t j = min(max(u * kThreads + threadIdx.x, least), most);
+      w[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at + j * 16u));
+    }
+  }
   static __device__ __forceinline__ void values(u32x4 w, float (&v)[E]) {
     if constexpr (DT == kDtF32) {
 #pragma unroll
@@ -111,18 +125,22 @@ struct Row {
     }
     return w;
   }
-  // Element i counted from the row's first; -inf for those outside the row.
-  __device__ __forceinline__ int64_t first(uint32_t j) const { return (int64_t)j * E - head; }
-  // Elements of any block j < end from what raw(j) gave.
-  __device__ __forceinline__ void edge_values(u32x4 w, uint32_t j, uint32_t end, float (&v)[E]) const {
+  // Elements that blocks before `end` hold, counted from the row's first.
+  __device__ __forceinline__ uint32_t limit(uint32_t end) const { return end == blocks ? V : end * E - head; }
+  // Elements of block j from what raw(j) gave; -inf for those before the row
+  // (their numbers wrap) and from `limit` on.
+  __device__ __forceinline__ void edge_values(u32x4 w, uint32_t j, uint32_t limit, float (&v)[E]) const {
     values(w, v);
-    const int64_t i0 = first(j);
-    const bool direct = j < end && (j < lo || j >= hi);
+    const uint32_t i0 = j * E - head;
 #pragma unroll
-    for (uint32_t e = 0; e < E; ++e) {
-      const bool in = j < end && i0 + e >= 0 && i0 + e < V;
-      v[e] = in ? v[e] : -INFINITY;
-      if (direct && in) v[e] = at((uint32_t)(i0 + e));
+    for (uint32_t e = 0; e < E; ++e) v[e] = i0 + e < limit ? v[e] : -INFINITY;
+    if (j < lo || j >= hi) {
+#pragma unroll
+      for (uint32_t e = 0; e < E; ++e) {
+        const bool in = i0 + e < limit;
+        const float x = at(in ? i0 + e : 0u);
+        v[e] = in ? x : -INFINITY;
+      }
     }
   }
   __device__ __forceinline__ float at(uint32_t i) const { return logit<DT>(p, i); }
@@ -179,8 +197,8 @@ struct Shared {
   u32x4 kept[kWaves][kKept];       // the first of them
   uint64_t few[kFew];              // keys to rank, in no order
   uint64_t best[kMaxTop];
-  uint64_t group_key[kGroups];
-  float group[kGroups];
+  alignas(16) uint64_t group_key[kGroups];
+  alignas(16) float group[kGroups];
   float tau;
   uint64_t tau_key;
   uint32_t wave_count[kWaves], few_count, flag;
@@ -203,21 +221,25 @@ __device__ __forceinline__ uint32_t add_dpp(uint32_t a) {
 }
 
 // The k-th largest of the 64 groups' maxima: every group of four threads gives
-// its own (`mine` in all four) and counts the groups above it, a quarter each.
-// Every thread of the workgroup calls it.
+// its own (`mine` in all four) and counts those above it and those not below
+// it, a quarter each.  (The largest with fewer than k above and k or more not
+// below: every group that holds it writes it.)  Every thread of the workgroup
+// calls it.
 template <typename T>
 __device__ __forceinline__ T kth_of_groups(T (&group)[kGroups], T& result, T mine, uint32_t k) {
   const uint32_t g = threadIdx.x >> 2, q0 = (threadIdx.x & 3u) * (kGroups / 4u);
   if ((threadIdx.x & 3u) == 0u) group[g] = mine;
   __syncthreads();
-  uint32_t above = 0u;
+  uint32_t above = 0u, upto = 0u;
 #pragma unroll
   for (uint32_t i = 0u; i < kGroups / 4u; ++i) {
     const T u = group[q0 + i];
-    above += (u > mine || (u == mine && q0 + i < g)) ? 1u : 0u;
+    above += u > mine ? 1u : 0u;
+    upto += u >= mine ? 1u : 0u;
   }
   above = add_dpp<0x4E>(add_dpp<0xB1>(above));
-  if (above == k - 1u && (threadIdx.x & 3u) == 0u) result = mine;
+  upto = add_dpp<0x4E>(add_dpp<0xB1>(upto));
+  if (above < k && k <= upto && (threadIdx.x & 3u) == 0u) result = mine;
   __syncthreads();
   return result;
 }
@@ -398,22 +420,19 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
   const bool only = b1 - b0 <= kStepBlocks;
   if (tid == 0u) sh.few_count = 0u;
   u32x4 next[kUnroll] = {};
-  const auto fetch = [&](uint32_t s0) __attribute__((always_inline)) {
-    if (row.lo >= row.hi) return;  // (a matrix without a whole block)
-#pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) next[u] = row.raw(s0 + u * kThreads + tid);
-  };
-  if (b0 < b1) fetch(b0);
+  const uint32_t limit = row.limit(b1);
+  if (b0 < b1) row.raw_step(b0, next);
   for (uint32_t s0 = b0; s0 < b1; s0 += kStepBlocks) {
     float v[kUnroll][E];
+    const uint32_t used = min((b1 - s0 + kThreads - 1u) / kThreads, kUnroll);  // blocks of a thread
     if (s0 + kStepBlocks <= b1 && row.inside(s0, kStepBlocks)) {
 #pragma unroll
       for (uint32_t u = 0; u < kUnroll; ++u) Row<DT>::values(next[u], v[u]);
     } else {
 #pragma unroll
-      for (uint32_t u = 0; u < kUnroll; ++u) row.edge_values(next[u], s0 + u * kThreads + tid, b1, v[u]);
+      for (uint32_t u = 0; u < kUnroll; ++u) row.edge_values(next[u], s0 + u * kThreads + tid, limit, v[u]);
     }
-    if (s0 + kStepBlocks < b1) fetch(s0 + kStepBlocks);
+    if (s0 + kStepBlocks < b1) row.raw_step(s0 + kStepBlocks, next);
     float hi[kUnroll], top = -INFINITY;
 #pragma unroll
     for (uint32_t u = 0; u < kUnroll; ++u) {
@@ -432,17 +451,21 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     const float ref = st.r == -INFINITY ? 0.0f : st.r, ref2 = -ref * c2;
     float s = st.s, w = st.w;
 #pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u)
+    for (uint32_t u = 0; u < kUnroll; ++u) {
+      if (u >= used) continue;  // (also parts the code so that it takes 92 registers, not 141)
 #pragma unroll
       for (uint32_t e = 0; e < E; ++e) {
         const float t = __builtin_fmaf(v[u][e], c2, ref2), p = exp2_fast(t);
         s += p;
         w = __builtin_fmaf(t, p, w);
       }
-    if (__any(w != w)) {
+    }
+    constexpr int kNanOrInf = 0x207;
+    if (__any(__builtin_amdgcn_classf(w, kNanOrInf) || fabsf(ref2) > 65536.0f)) {
       // A masked logit (-inf, or so low that t is): e^t is 0, and t e^t has
-      // to be too.  (Or a NaN, which stays one in s.)  Again, with care, and
-      // with differences first, since x log2 e may overflow.
+      // to be too.  (Or a NaN, which stays one in s.)  Or logits so large that
+      // ref2's rounding, 2^-24 of it, shows in t (or that it overflows).
+      // Again, with care, and with differences first.
       s = st.s;
       w = st.w;
 #pragma unroll
@@ -508,7 +531,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
         if (i < kKept)
           Row<DT>::values(sh.kept[tid >> 6][i], v);
         else
-          row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, b1, v);
+          row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, limit, v);
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e)
           if (v[e] >= least) push(sh, top_key(v[e], j * E - row.head + e));
@@ -523,7 +546,7 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       __syncthreads();
       for (uint32_t j = b0 + tid; j < b1; j += kThreads) {
         float v[E];
-        row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, b1, v);
+        row.edge_values(row.lo < row.hi ? row.raw(j) : u32x4{}, j, limit, v);
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e)
           if (v[e] > tau) push(sh, top_key(v[e], j * E - row.head + e));
@@ -584,7 +607,8 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
 
 // ---------------------------------------------------------------------------
 // Gradient: dx_i = scale (hot_i - p_i (G + ge (log p_i + H))), one pass, 16
-// bytes a step.  The tokens' own terms are rare: a bitmap marks the blocks
+// bytes a step, bound by the memory (4096 rows of 100003 BF16: 264 us, 6.2 TB/s
+// read and written; 256 rows of 32768 FP32 12.5 us, 5.3 TB/s).  The tokens' own terms are rare: a bitmap marks the blocks
 // that hold one, and only those look through the row's tokens.
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
@@ -604,10 +628,7 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
   if (b0 >= row.blocks) return;
   float v[kUnroll][E];
   u32x4 raw[kUnroll] = {};
-  if (row.lo < row.hi) {
-#pragma unroll
-    for (uint32_t u = 0; u < kUnroll; ++u) raw[u] = row.raw(b0 + u * kThreads + tid);
-  }
+  row.raw_step(b0, raw);
   if (tid < kStepBlocks / 32u) marked[tid] = 0u;
   __syncthreads();
   const int32_t* tok = tokens + n * (size_t)M;
@@ -635,7 +656,7 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
     if (whole)
       Row<DT>::values(raw[u], v[u]);
     else
-      row.edge_values(raw[u], b0 + u * kThreads + tid, row.blocks, v[u]);
+      row.edge_values(raw[u], b0 + u * kThreads + tid, V, v[u]);
   }
   uint8_t* out = static_cast<uint8_t*>(dx) + n * (size_t)dx_stride * (DT == kDtF32 ? 4u : 2u);
 #pragma unroll
@@ -670,7 +691,7 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
         for (int k = 0; k < 4; ++k) w[k] = bf16_pair(d[2 * k], d[2 * k + 1]);
       }
       // (The output's rows may be aligned otherwise than the input's.  Marked
-      // as not read again here: 4096 x 100003 BF16 299 us without, 273 us with.)
+      // as not read again here, which takes 9% off 4096 x 100003 BF16.)
       __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(out + i0 * (DT == kDtF32 ? 4 : 2)));
     } else {
 #pragma unroll
@@ -687,7 +708,9 @@ __global__ __launch_bounds__(256) void logprobs_backward_kernel(
 
 // Workgroups of a row: one where the rows alone fill the chip, else pieces of
 // at least 2048 logits (8 a thread), as many as give about 512 workgroups,
-// with all their top keys within one workgroup's candidates.
+// with all their top keys within one workgroup's candidates.  (64 rows of
+// 131072 FP32, top 20: 17 us in 512 workgroups, 18 in 256 or 1024; 300 rows of
+// 131072 BF16, top 8: 23 us, 27 in 300, 25 in 1200.)
 constexpr int64_t kRowGroups = 512;
 // The counters take the same place whatever the sizes, so that no other
 // call's data ever lies where a call expects zeros.  (Rows are split only

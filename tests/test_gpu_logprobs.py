@@ -323,3 +323,27 @@ def test_logprobs_backward_against_differences():
                     ref.logprobs_loss(xm, tokens[n], scale, g[n], ge[n])) / (2 * d)
             tol = 8 * d * d * scale ** 3 * size + 1e-11 / d + 64 * 2 * U * size * scale
             assert abs(dx[n, i] - diff) <= tol, (n, i, dx[n, i], diff)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("value", ["lowest", "largest", "half"])
+def test_logprobs_of_equal_extreme_rows(dtype, value):
+    """Whole rows of the type's lowest or largest value (times log2 e it is not
+    finite), among ordinary ones, in rows that are not split and have no ragged
+    step: lse = x + log V rounds to x, the entropy is log V (sums of ones are
+    exact; the logarithm, the product and the difference round: 2^-20)."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    N, V = 520, 16384
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    big = torch.finfo(dt).min if value == "lowest" else torch.finfo(dt).max * (0.5 if value == "half" else 1.0)
+    x = torch.randn((N, V), device="cuda").to(dt)
+    x[::7] = big
+    tokens = torch.full((N, 1), 5, dtype=torch.int32, device="cuda")
+    say("logprobs of rows of %s %s" % (dtype, value))
+    r = fp4.logprobs(x, tokens, top_k=4)
+    torch.cuda.synchronize()
+    assert torch.equal(r.lse[::7], torch.full_like(r.lse[::7], float(torch.tensor(big).to(dt).float())))
+    assert ((r.entropy[::7] - np.log(V)).abs() <= 2.0 ** -20 * np.log(V)).all()
+    assert torch.isfinite(r.lse).all() and torch.isfinite(r.entropy).all()
+    assert torch.equal(r.top_index[::7].cpu(), torch.arange(4, dtype=torch.int32).expand(len(range(0, N, 7)), 4))
