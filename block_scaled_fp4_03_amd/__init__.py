@@ -3,7 +3,8 @@ for AMD Instinct MI355X (gfx950).
 
 The C ABI (include/fp4.h) is exposed under the same names (``fp4_quantize``,
 ``fp4_dequantize``, ``fp4_gemm``, ``fp4_gemm_ex``, ``fp4_gemm_grouped``, ``fp4_gemm_w4a8``, ``fp4_scale_bytes``,
-``fp4_workspace_size``, ``fp4_status_string``), taking raw device pointers as
+``fp4_workspace_size``, ``fp4_status_string``; the decode step's ``fp4_kv_append``, ``fp4_attn_decode``,
+``fp4_kv_evict``, ``fp4_logprobs``, ``fp4_logprobs_backward``), taking raw device pointers as
 integers.  The tensor helpers below only allocate outputs with torch and
 marshal ``data_ptr()`` / the current stream into those calls: every step of the
 computation runs in the HIP kernels of libfp4.so.  There is no fallback -- if

@@ -29,6 +29,12 @@
 //     begin another.  The units that are cut are joined from the workgroups'
 //     partial results by the last of them to arrive.  (A fixed number of
 //     splits per sequence leaves the chip waiting for the longest.)
+//   - Whole long caches run at what the memory gives: 4 x 131071 MXFP8 tokens
+//     (1.1 GB) 183 us, 6.0 TB/s; 8 x 16000 BF16 tokens, 8 kv heads of 128, 92
+//     us, 5.7 TB/s; 32 ragged MXFP4 sequences (293 MB) 59 us, 5.0 TB/s.  What a
+//     call adds is 8 to 10 us of waits one after the other: lengths, page
+//     table, first rows, the waves' sums, results to the coherence point, the
+//     join.
 //   - Softmax statistics are FP32 and running.  The reference maximum of a
 //     head moves only when a score passes it by 2^kLazy, so most tiles need
 //     no reduction across lanes and no rescaling.
@@ -92,7 +98,7 @@ struct AttnArgs {
 // ---- loads ----
 // BYTES bytes of a cache row from p (aligned to their largest power of two,
 // at most 16) as dwords.  Rows are read once: without the hint that says so 4
-// x 131071 MXFP8 tokens take 199 us, with it 184 us.
+// x 131071 MXFP8 tokens take 199 us, with it 183 us.
 template <int BYTES, int STEP = 0>
 __device__ __forceinline__ void load_bytes(const uint8_t* __restrict__ p, uint32_t (&w)[(BYTES + 3) / 4]) {
   constexpr int kAlign = BYTES & -BYTES, kStep = STEP ? STEP : kAlign >= 16 ? 16 : kAlign;
@@ -220,8 +226,8 @@ __device__ __forceinline__ void store_out2(const AttnArgs& a, size_t i, float x,
 // p[i] for an index that is the same in the whole wavefront, by a scalar load
 // (page tables and lengths do not change while the kernel runs, which the
 // constant address space says).  A vector load here would be the youngest in
-// flight, and waiting for it would wait for all of K and V: 3.6 instead of
-// 4.5 TB/s over an MXFP4 cache.
+// flight, and waiting for it would wait for all of K and V (a fifth of the
+// rate over an MXFP4 cache).
 __device__ __forceinline__ int32_t load_uniform(const int32_t* p, size_t i) {
   typedef const __attribute__((address_space(4))) int32_t* constant_ptr;
   return ((constant_ptr)(uintptr_t)p)[i];
@@ -752,7 +758,7 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
   // place of its first piece.  The unit's counter is that of the workgroup that
   // begins it; the others are those of workgroups wholly inside the unit, which
   // begin none.  (One workgroup for all: 131000 tokens of one kv head of 256
-  // BF16, 512 pieces, 479 us; so, 94 us.)
+  // BF16, in 512 pieces, 479 us; so, 94 us, and in today's 256 pieces 52.)
   uint32_t step = 1u, left = pc.pieces, level = 0u;
   for (;;) {
     const bool whole = left <= kDirect;
@@ -827,7 +833,10 @@ __global__ __launch_bounds__(256, groups_of(D, EX) / 256u) void attn_decode_kern
 }
 
 // weights_out = weights_in + sum over the kv head's query heads of p, from the
-// stored scores: p = 2^(x - M) / L.  Four tokens a thread.
+// stored scores: p = 2^(x - M) / L.  Four tokens a thread.  The scores cross
+// memory once more (FP32, a fifth of the rows' bytes for 64 BF16 elements and 8
+// heads), since M and L are known only at the end: 48 ragged sequences of up to
+// 4099 tokens, 64 heads, 7.7 us after the attention's 56.
 __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
   const uint32_t h = blockIdx.y, b = blockIdx.z, t = (blockIdx.x * 256u + threadIdx.x) * 4u;
   const Range r = range_of(a, b);

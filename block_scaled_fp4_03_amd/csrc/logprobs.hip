@@ -9,8 +9,8 @@
 // only when a logit passes it by 2^kLazy, so the common step is six VALU
 // operations, one of them the exponential, for an element.  All in base 2 (t
 // times log2 e), FP32.  Their issue (about 100 us) and the memory (130 us at
-// 6.3 TB/s) bound it together: 4096 rows of 100003 BF16 take 141 us with the
-// top 8 (5.8 TB/s), 133 us without; 1024 rows of 131072 FP32 86 us (6.2 TB/s).
+// 6.3 TB/s) bound it together: 4096 rows of 100003 BF16 take 138 us with the
+// top 8 (5.9 TB/s), 133 us without; 1024 rows of 131072 FP32 86 us (6.2 TB/s).
 //
 // The top k in the same pass: the first 16 KB give a threshold with at least
 // k elements at or above it (the k-th largest of 64 groups' maxima).  16-byte
@@ -608,8 +608,9 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
 // ---------------------------------------------------------------------------
 // Gradient: dx_i = scale (hot_i - p_i (G + ge (log p_i + H))), one pass, 16
 // bytes a step, bound by the memory (4096 rows of 100003 BF16: 264 us, 6.2 TB/s
-// read and written; 256 rows of 32768 FP32 12.5 us, 5.3 TB/s).  The tokens' own terms are rare: a bitmap marks the blocks
-// that hold one, and only those look through the row's tokens.
+// read and written; 256 rows of 32768 FP32 12.5 us, 5.3 TB/s).  The tokens' own
+// terms are rare: a bitmap marks the blocks that hold one, and only those look
+// through the row's tokens.
 // ---------------------------------------------------------------------------
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 
