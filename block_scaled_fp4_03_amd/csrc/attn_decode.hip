@@ -38,6 +38,7 @@
 //   - Softmax statistics are FP32 and running.  The reference maximum of a
 //     head moves only when a score passes it by 2^kLazy, so most tiles need
 //     no reduction across lanes and no rescaling.
+#include "attn_split.h"
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
@@ -46,21 +47,7 @@ namespace fp4 {
 namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
-constexpr int kTile = 32;             // tokens of a wave's step
 constexpr int kWaves = 4;             // waves of a workgroup, taking every fourth tile
-constexpr uint32_t kGrain = 4;        // shares and units are whole multiples of this many tiles
-// Workgroups: as many as fit at once, two a CU, or one where a row's
-// accumulators, or three terms of a query, fill the registers.
-//   32 ragged MXFP4 sequences of 128-element rows: 61 us in 512, 89, 80 and 72
-//   in 256, 768 and 1024; 4 x 131071 MXFP8 tokens 190 us, 190, 227, 200.
-//   8 x 16000 MXFP4 tokens of 256-element rows: 48 us in 256, 65 in 512 of
-//   which 256 fit, 66 in 512 with the registers cut so that they fit.
-constexpr uint32_t kGroups = 512;
-constexpr uint32_t groups_of(int64_t D, bool exact) {
-  return D > 128 || (exact && D > 64) ? kGroups / 2u : kGroups;
-}
-constexpr int kHeadTile = 16;         // query heads of a workgroup
-constexpr uint32_t kDirect = 16;      // pieces of a unit that are joined at once
 // Scores may pass the reference maximum by this much (in powers of two)
 // before it moves: probabilities up to 2^8, no loss in FP32 or BF16.
 constexpr float kLazy = 8.0f;
@@ -84,6 +71,7 @@ struct AttnArgs {
   float* lse;
   int32_t q_f32, out_f32;
   int32_t batch;
+  bool join;           // the workspace has room for the pieces of cut units
   uint32_t* done;      // arrival counters, one for each workgroup that begins a unit
   float* part;         // partial sums: workgroups x 2 x 16 heads x D
   float* stats;        // (maximum, sum): workgroups x 2 x 16 heads x 2
@@ -238,12 +226,7 @@ __device__ __forceinline__ int32_t load_uniform(const int32_t* p, size_t i) {
 struct Range {
   uint32_t first, len;    // tokens [first, len)
   uint32_t tile0, tiles;  // tiles of the sequence from tile0 on
-  // Tiles the work is counted in: whole grains, and one at least (an empty
-  // sequence's result has to be written too), and `more` for the time that
-  // changing from one unit to the next takes.
-  __device__ __forceinline__ uint32_t counted(uint32_t more) const {
-    return max((tiles + kGrain - 1u) / kGrain, 1u) * kGrain + more;
-  }
+  __device__ __forceinline__ uint32_t counted(uint32_t more) const { return counted_tiles(tiles, more); }
 };
 __device__ __forceinline__ Range range_at(const AttnArgs& a, int64_t l) {
   Range r;
@@ -283,18 +266,13 @@ __device__ __forceinline__ Share share_of(const AttnArgs& a, uint32_t units, uin
   uint32_t upto = wave_scan(mine);
   Share s;
   uint32_t total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
-  const auto per_group = [](uint32_t tiles) {
-    const uint32_t n = tiles / kGrain;
-    return (n / gridDim.x + (n % gridDim.x != 0u ? 1u : 0u)) * kGrain;
-  };
-  s.share = per_group(total);
-  // The change of units is counted where shares are long enough not to be cut because of it.
-  s.more = s.share >= 4u * change ? change : 0u;
+  s.share = share_tiles(total, gridDim.x);
+  s.more = counted_change(s.share, change, a.join);
   if (s.more > 0u) {
     mine += s.more * (b0 < B ? min(each, B - b0) : 0u);
     upto = wave_scan(mine);
     total = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63) * units;
-    s.share = per_group(total);
+    s.share = share_tiles(total, gridDim.x);
   }
   s.pos = min(blockIdx.x * s.share, total);
   s.end = s.pos + min(s.share, total - s.pos);
@@ -319,12 +297,11 @@ struct Shared {
   uint32_t last_arrival;
 };
 
-// A workgroup's piece of a unit: tiles [t_begin, t_end) (those past the
-// sequence's last only count) for the query heads head0 .. head0 + heads - 1,
-// which read kv head h of sequence b.  `pieces` workgroups from wg0 on have one.
-struct Piece {
+// A workgroup's piece of a unit (tiles past the sequence's last only count) for
+// the query heads head0 .. head0 + heads - 1, which read kv head h of sequence b.
+struct Piece : Cut {
   Range r;
-  uint32_t b, h, head0, heads, t_begin, t_end, wg0, pieces;
+  uint32_t b, h, head0, heads;
 };
 
 // Element pairs of a piece's results, 256 at a time: f(head, d).
@@ -347,12 +324,6 @@ __device__ __forceinline__ void write_stats(const AttnArgs& a, const Piece& pc, 
   if (a.final_stats) *reinterpret_cast<v2f*>(a.final_stats + 2 * at) = v2f{mx, s == 0.0f ? 0.0f : 1.0f / s};
 }
 
-// Where the unit's piece p keeps its results: a workgroup's place for a unit
-// it begins, or for one begun before.
-__device__ __forceinline__ uint32_t place_of(const Piece& pc, uint32_t p) {
-  return (2u * (pc.wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile;
-}
-
 // The results of n <= 16 pieces, first, first + step, .., joined by one
 // workgroup: every head's maximum and sum into sh.wave_m[0], sh.wave_l[0], its
 // sums of V to result(head, d, x, y), ITEMS pairs of elements a thread, BATCH
@@ -370,14 +341,14 @@ __device__ __forceinline__ void join_items(const AttnArgs& a, const Piece& pc, S
   for (int k = 0; k < kHeadTile / kWaves; ++k) {
     const uint32_t hd = k * kWaves + wave;
     ms[k] = v2f{-INFINITY, 0.0f};
-    if (hd < pc.heads && lane < n) ms[k] = load2_agent(a.stats + 2u * (place_of(pc, first + lane * step) + hd));
+    if (hd < pc.heads && lane < n) ms[k] = load2_agent(a.stats + 2u * (place_of(pc.wg0, first + lane * step) + hd));
   }
   v2f v[(uint32_t)BATCH][ITEMS];
   const auto ask = [&](uint32_t q0) __attribute__((always_inline)) {
 #pragma unroll
     for (uint32_t j = 0; j < (uint32_t)BATCH; ++j) {
       if (q0 + j >= n) continue;
-      const float* from = a.part + (size_t)place_of(pc, first + (q0 + j) * step) * D;
+      const float* from = a.part + (size_t)place_of(pc.wg0, first + (q0 + j) * step) * D;
 #pragma unroll
       for (uint32_t k = 0; k < ITEMS; ++k)
         if ((k * 256u + tid) / (D / 2) < pc.heads) v[j][k] = load2_agent(from + 2u * (k * 256u + tid));
@@ -744,7 +715,7 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
   }
 
   // ---- a part of the unit: written through, and the last to arrive joins them ----
-  const uint32_t mine = (2u * blockIdx.x + (pc.t_begin == 0u ? 1u : 0u)) * kHeadTile;
+  const uint32_t mine = place_of(pc.wg0, blockIdx.x - pc.wg0);
   each_pair<D>(heads, [&](uint32_t hd, uint32_t d) {
     store2_agent(a.part + (size_t)(mine + hd) * D + d, sh.red[0][hd][d] + sh.red[1][hd][d],
                  sh.red[0][hd][d + 1] + sh.red[1][hd][d + 1]);
@@ -753,45 +724,36 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
     const float s = head_sum(threadIdx.x, mx);
     store2_agent(a.stats + 2u * (mine + threadIdx.x), mx, s);
   }
-  // Up to kDirect pieces are joined at once.  More are joined eight by eight
-  // first, and eight of those, each by the last to arrive of its own, into the
-  // place of its first piece.  The unit's counter is that of the workgroup that
-  // begins it; the others are those of workgroups wholly inside the unit, which
-  // begin none.  (One workgroup for all: 131000 tokens of one kv head of 256
-  // BF16, in 512 pieces, 479 us; so, 94 us, and in today's 256 pieces 52.)
   uint32_t step = 1u, left = pc.pieces, level = 0u;
   for (;;) {
-    const bool whole = left <= kDirect;
-    ++level;
-    const uint32_t at = (blockIdx.x - pc.wg0) / (8u * step), first = whole ? 0u : 8u * step * at;
-    const uint32_t n = whole ? left : min(left - 8u * at, 8u);
-    uint32_t* done = a.done + pc.wg0 + (whole ? 0u : at == 0u ? level : first - level);
+    const Join j = join_of(pc.wg0, blockIdx.x - pc.wg0, step, left, ++level);
+    uint32_t* done = a.done + j.done;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
     __syncthreads();
     if (threadIdx.x == 0u) {
       const uint32_t before = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      sh.last_arrival = before == n - 1u;
+      sh.last_arrival = before == j.n - 1u;
       if (sh.last_arrival) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
     if (!sh.last_arrival) return;
     const auto result = [&](uint32_t hd, uint32_t d, float x, float y) __attribute__((always_inline)) {
-      if (!whole) {
-        store2_agent(a.part + (size_t)(place_of(pc, first) + hd) * D + d, x, y);
+      if (!j.whole) {
+        store2_agent(a.part + (size_t)(place_of(pc.wg0, j.first) + hd) * D + d, x, y);
       } else {
         const float s = sh.wave_l[0][hd], inv = s == 0.0f ? 0.0f : 1.0f / s;
         write_out<D>(a, pc, hd, d, x * inv, y * inv);
       }
     };
-    join_pieces<D>(a, pc, sh, first, step, n, result);
+    join_pieces<D>(a, pc, sh, j.first, step, j.n, result);
     if (threadIdx.x < heads) {
       const float mx = sh.wave_m[0][threadIdx.x], s = sh.wave_l[0][threadIdx.x];
-      if (!whole)
-        store2_agent(a.stats + 2u * (place_of(pc, first) + threadIdx.x), mx, s);
+      if (!j.whole)
+        store2_agent(a.stats + 2u * (place_of(pc.wg0, j.first) + threadIdx.x), mx, s);
       else
         write_stats(a, pc, threadIdx.x, mx, s);
     }
-    if (whole) return;
+    if (j.whole) return;
     step *= 8u;
     left = (left + 7u) / 8u;
   }
@@ -801,11 +763,7 @@ template <int FMT, int D, bool EX>
 __global__ __launch_bounds__(256, groups_of(D, EX) / 256u) void attn_decode_kernel(AttnArgs a) {
   __shared__ Shared<D> sh;
   const uint32_t units = (uint32_t)a.c.kv_heads * (uint32_t)a.head_tiles;
-  // Changing units (the end of one, the first loads of the next) takes about
-  // as long as 48 KB of rows: in tiles, to whole grains.  With none counted 32
-  // ragged MXFP4 sequences take 66 us, with it 60 us.
-  constexpr uint32_t kTileBytes = 2u * kTile * kv_row_bytes(FMT, D);
-  constexpr uint32_t kChange = (49152u / kTileBytes + kGrain - 1u) / kGrain * kGrain;
+  constexpr uint32_t kChange = change_tiles(kv_row_bytes(FMT, D));
   Share w = share_of(a, units, kChange);
   while (w.pos < w.end) {
     // The share's next piece, of unit `unit` of sequence w.b.
@@ -814,10 +772,7 @@ __global__ __launch_bounds__(256, groups_of(D, EX) / 256u) void attn_decode_kern
     pc.r = range_at(a, load_uniform(a.lens, w.b));
     const uint32_t counted = pc.r.counted(w.more), unit = (w.pos - w.base * units) / counted;
     const uint32_t unit0 = w.base * units + unit * counted;
-    pc.t_begin = w.pos - unit0;
-    pc.t_end = min(counted, pc.t_begin + (w.end - w.pos));
-    pc.wg0 = unit0 / w.share;
-    pc.pieces = (unit0 + counted - 1u) / w.share - pc.wg0 + 1u;
+    static_cast<Cut&>(pc) = cut_at(w.pos, w.end, unit0, counted, w.share);
     const uint32_t ht = unit % (uint32_t)a.head_tiles;
     pc.h = unit / (uint32_t)a.head_tiles;
     pc.heads = min((uint32_t)a.group - ht * kHeadTile, (uint32_t)kHeadTile);
@@ -857,35 +812,6 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
 #pragma unroll
   for (uint32_t i = 0; i < 4u; ++i)
     if (i < n) a.w_out[at + i] = (a.w_in ? a.w_in[at + i] : 0.0f) + w[i];
-}
-
-size_t round16(size_t n) { return (n + 15) / 16 * 16; }
-
-// The workspace: arrival counters (zero between calls), then statistics, partial sums, scores.
-struct Layout {
-  uint32_t groups;
-  int64_t head_tiles, score_stride;
-  size_t done, stats, final_stats, part, scores, total;
-};
-Layout layout_of(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t D, int64_t max_len, bool weights) {
-  Layout w{};
-  w.head_tiles = (q_heads / kv_heads + kHeadTile - 1) / kHeadTile;
-  w.score_stride = (max_len + kTile - 1) / kTile * kTile;
-  const int64_t units = B * kv_heads * w.head_tiles;
-  const int64_t grains = max_len == 0 ? 1 : (max_len + kTile * kGrain - 1) / (kTile * kGrain);
-  const uint32_t most = groups_of(D, false);
-  w.groups = units > most || units * grains > most ? most : (uint32_t)(units * grains);
-  // Units of one grain each are never cut.
-  const bool join = grains > 1;
-  // The counters take the same place whatever the sizes, so that no other
-  // call's data ever lies where a call expects zeros.
-  w.done = 0;
-  w.stats = join || weights ? (size_t)kGroups * 4 : 0;
-  w.final_stats = w.stats + (join ? (size_t)w.groups * 2 * kHeadTile * 8 : 0);
-  w.part = w.final_stats + (weights ? round16((size_t)(B * q_heads) * 8) : 0);
-  w.scores = w.part + (join ? (size_t)w.groups * 2 * kHeadTile * (size_t)D * 4 : 0);
-  w.total = w.scores + (weights ? (size_t)(B * q_heads) * (size_t)w.score_stride * 4 : 0);
-  return w;
 }
 
 template <int FMT, int D>
@@ -932,6 +858,7 @@ hipError_t launch_attn_decode(const KvPool& c, const void* q, int q_dtype, int64
   a.group = (int32_t)(q_heads / c.kv_heads);
   a.head_tiles = (int32_t)w.head_tiles;
   a.batch = (int32_t)B;
+  a.join = w.join;
   a.max_len = max_len;
   a.window = window;
   a.scale_log2 = scale * kLog2e;
