@@ -4,15 +4,7 @@
 // compile this one source.  Internal header, of whole numbers only.
 #pragma once
 
-#include <cstddef>
-#include <cstdint>
-
-#if defined(__HIP__)
-#include <hip/hip_runtime.h>
-#define FP4_SPLIT_FN __host__ __device__ __forceinline__
-#else
-#define FP4_SPLIT_FN inline
-#endif
+#include "host_device.h"
 
 namespace fp4 {
 
@@ -27,7 +19,7 @@ constexpr uint32_t kDirect = 16;  // pieces of a unit that are joined at once
 //   8 x 16000 MXFP4 tokens of 256-element rows: 48 us in 256, 65 in 512 of
 //   which 256 fit, 66 in 512 with the registers cut so that they fit.
 constexpr uint32_t kGroups = 512;
-FP4_SPLIT_FN constexpr uint32_t groups_of(int64_t D, bool exact) {
+FP4_HOST_DEVICE constexpr uint32_t groups_of(int64_t D, bool exact) {
   return D > 128 || (exact && D > 64) ? kGroups / 2u : kGroups;
 }
 
@@ -35,7 +27,7 @@ FP4_SPLIT_FN constexpr uint32_t groups_of(int64_t D, bool exact) {
 // heads attend to) counts: whole grains, and one at least (an empty sequence's
 // result has to be written too), and `more` for the time that changing from
 // one unit to the next takes.
-FP4_SPLIT_FN uint32_t counted_tiles(uint32_t tiles, uint32_t more) {
+FP4_HOST_DEVICE uint32_t counted_tiles(uint32_t tiles, uint32_t more) {
   const uint32_t grains = tiles / kGrain + (tiles % kGrain != 0u ? 1u : 0u);
   return (grains > 1u ? grains : 1u) * kGrain + more;
 }
@@ -43,7 +35,7 @@ FP4_SPLIT_FN uint32_t counted_tiles(uint32_t tiles, uint32_t more) {
 // Changing units (the end of one, the first loads of the next) takes about as
 // long as 48 KB of rows: in tiles, to whole grains.  With none counted 32
 // ragged MXFP4 sequences take 66 us, with it 60 us.
-FP4_SPLIT_FN constexpr uint32_t change_tiles(uint32_t row_bytes) {
+FP4_HOST_DEVICE constexpr uint32_t change_tiles(uint32_t row_bytes) {
   return (49152u / (2u * kTile * row_bytes) + kGrain - 1u) / kGrain * kGrain;
 }
 
@@ -52,12 +44,12 @@ FP4_SPLIT_FN constexpr uint32_t change_tiles(uint32_t row_bytes) {
 // room for the pieces of a cut unit (`join` false: no sequence has more than a
 // grain).  Units of one grain with nothing more lie on whole shares' grains
 // and are never cut; with a change of units counted they would be.
-FP4_SPLIT_FN uint32_t counted_change(uint32_t share, uint32_t change, bool join) {
+FP4_HOST_DEVICE uint32_t counted_change(uint32_t share, uint32_t change, bool join) {
   return join && share >= 4u * change ? change : 0u;
 }
 
 // A workgroup's share of `total` tiles (whole grains) among `groups`.
-FP4_SPLIT_FN uint32_t share_tiles(uint32_t total, uint32_t groups) {
+FP4_HOST_DEVICE uint32_t share_tiles(uint32_t total, uint32_t groups) {
   const uint32_t n = total / kGrain;
   return (n / groups + (n % groups != 0u ? 1u : 0u)) * kGrain;
 }
@@ -68,7 +60,7 @@ FP4_SPLIT_FN uint32_t share_tiles(uint32_t total, uint32_t groups) {
 struct Cut {
   uint32_t t_begin, t_end, wg0, pieces;
 };
-FP4_SPLIT_FN Cut cut_at(uint32_t pos, uint32_t end, uint32_t unit0, uint32_t counted, uint32_t share) {
+FP4_HOST_DEVICE Cut cut_at(uint32_t pos, uint32_t end, uint32_t unit0, uint32_t counted, uint32_t share) {
   Cut c;
   c.t_begin = pos - unit0;
   c.t_end = c.t_begin + (end - pos) < counted ? c.t_begin + (end - pos) : counted;
@@ -80,7 +72,7 @@ FP4_SPLIT_FN Cut cut_at(uint32_t pos, uint32_t end, uint32_t unit0, uint32_t cou
 // Where piece p of a unit begun by workgroup wg0 keeps its results, in heads'
 // rows: a workgroup has a place for a unit it begins and one for a unit begun
 // before.
-FP4_SPLIT_FN uint32_t place_of(uint32_t wg0, uint32_t p) {
+FP4_HOST_DEVICE uint32_t place_of(uint32_t wg0, uint32_t p) {
   return (2u * (wg0 + p) + (p == 0u ? 1u : 0u)) * kHeadTile;
 }
 
@@ -97,7 +89,7 @@ struct Join {
   bool whole;  // what is left of the unit
   uint32_t first, n, done;
 };
-FP4_SPLIT_FN Join join_of(uint32_t wg0, uint32_t p, uint32_t step, uint32_t left, uint32_t level) {
+FP4_HOST_DEVICE Join join_of(uint32_t wg0, uint32_t p, uint32_t step, uint32_t left, uint32_t level) {
   Join j;
   j.whole = left <= kDirect;
   const uint32_t at = p / (8u * step);

@@ -32,6 +32,7 @@
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
+#include "logit_rows.h"
 
 #include <cfloat>
 
@@ -60,25 +61,15 @@ __device__ __forceinline__ float logit(const void* x, size_t i) {
   return u2f((uint32_t) static_cast<const uint16_t*>(x)[i] << 16);
 }
 
-// A row as 16-byte blocks from its first 128-byte line on: block j holds
-// elements j E - head .. (the first blocks and the last may be partly or
-// wholly outside the row).  Blocks are loaded whole, also those that reach into
-// the rows beside, as long as they lie within the matrix; the first of its
-// first rows and the last of its last may not.  (A wavefront's 1 KB is then
-// eight whole lines.)
+// A row and its 16-byte blocks (logit_rows.h says which can be loaded whole).
 template <int DT>
-struct Row {
-  static constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u, E = kElem<DT>, kLine = 128u / kSize;
+struct Row : RowBlocks {
+  static constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u, E = kElem<DT>;
   const uint8_t* p;  // the row's first element
-  uint32_t V, head, blocks;
-  uint32_t lo, hi;   // blocks [lo, hi) can be loaded whole
-  __device__ __forceinline__ Row(const void* x, int64_t stride, size_t n, size_t rows, uint32_t V_) : V(V_) {
-    p = static_cast<const uint8_t*>(x) + n * (size_t)stride * kSize;
-    head = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 127u) / kSize;
-    blocks = (V + head + E - 1u) / E;
-    const uint32_t before = (uint32_t)min(n * (size_t)stride, (size_t)kLine);  // elements of earlier rows
-    lo = head > before ? (head - before + E - 1u) / E : 0u;
-    hi = n + 1u == rows && blocks * E > head + V ? blocks - 1u : blocks;
+  uint32_t V;
+  __device__ __forceinline__ Row(const void* x, int64_t stride, size_t n, uint32_t rows, uint32_t V_)
+      : p(static_cast<const uint8_t*>(x) + n * (size_t)stride * kSize), V(V_) {
+    static_cast<RowBlocks&>(*this) = row_blocks<kSize>(reinterpret_cast<uintptr_t>(p), (uint32_t)n, rows, (uint32_t)stride, V_);
   }
   // Whether blocks [j, j + n) lie wholly inside the row.
   __device__ __forceinline__ bool inside(uint32_t j, uint32_t n) const {
