@@ -297,12 +297,13 @@ __device__ __forceinline__ void rank_few(Shared& sh, uint32_t n, uint32_t k) {
   __syncthreads();
 }
 
-// k searches of blocks [b0, b1) for the largest key below the last.
+// k searches of blocks [b0, b1) for the largest key below the last (the first
+// takes any: a NaN at index 0 has the largest key there is).
 template <int DT>
 __device__ __forceinline__ void search(Shared& sh, const Row<DT>& row, uint32_t b0, uint32_t b1, uint32_t k) {
   constexpr uint32_t E = kElem<DT>;
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  uint64_t below = ~0ull;
+  uint64_t below = 0ull;
   for (uint32_t n = 0u; n < k; ++n) {
     uint64_t most = 0ull;
     for (uint32_t j = b0 + threadIdx.x; j < b1; j += kThreads) {
@@ -310,7 +311,7 @@ __device__ __forceinline__ void search(Shared& sh, const Row<DT>& row, uint32_t 
         const int64_t i = (int64_t)j * E + e - row.head;
         if (i < 0 || i >= row.V) continue;
         const uint64_t key = top_key(row.at((uint32_t)i), (uint32_t)i);
-        if (key < below && key > most) most = key;
+        if ((n == 0u || key < below) && key > most) most = key;
       }
     }
     for (int d = 32; d > 0; d >>= 1) {
