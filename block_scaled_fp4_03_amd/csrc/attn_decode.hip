@@ -689,7 +689,9 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
   }
   __syncthreads();
 
-  // Head hd's sum over the waves, for the workgroup's maximum mx.
+  // Head hd's sum over the waves, for the workgroup's maximum mx.  (A wave whose
+  // scores are all NaN has the maximum of one without tokens, but a NaN sum,
+  // which has to stay: 0 times it.)
   const auto head_sum = [&](uint32_t hd, float& mx) {
     mx = sh.wave_m[0][hd];
 #pragma unroll
@@ -697,7 +699,7 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
     float s = 0.0f;
 #pragma unroll
     for (int w = 0; w < kWaves; ++w)
-      s += sh.wave_m[w][hd] == -INFINITY ? 0.0f : sh.wave_l[w][hd] * exp2_fast(sh.wave_m[w][hd] - mx);
+      s += sh.wave_l[w][hd] * (sh.wave_m[w][hd] == -INFINITY ? 0.0f : exp2_fast(sh.wave_m[w][hd] - mx));
     return s;
   };
   float mx;
@@ -788,10 +790,11 @@ __global__ __launch_bounds__(256, groups_of(D, EX) / 256u) void attn_decode_kern
 }
 
 // weights_out = weights_in + sum over the kv head's query heads of p, from the
-// stored scores: p = 2^(x - M) / L.  Four tokens a thread.  The scores cross
-// memory once more (FP32, a fifth of the rows' bytes for 64 BF16 elements and 8
-// heads), since M and L are known only at the end: 48 ragged sequences of up to
-// 4099 tokens, 64 heads, 7.7 us after the attention's 56.
+// stored scores: p = 2^(x - M) / L, and 0 for a masked token (x = -inf) also
+// where a NaN among the others makes L one.  Four tokens a thread.  The scores
+// cross memory once more (FP32, a fifth of the rows' bytes for 64 BF16 elements
+// and 8 heads), since M and L are known only at the end: 48 ragged sequences of
+// up to 4099 tokens, 64 heads, 7.7 us after the attention's 56.
 __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
   const uint32_t h = blockIdx.y, b = blockIdx.z, t = (blockIdx.x * 256u + threadIdx.x) * 4u;
   const Range r = range_of(a, b);
@@ -806,7 +809,7 @@ __global__ __launch_bounds__(256) void attn_weights_kernel(AttnArgs a) {
       const v2f ms = *reinterpret_cast<const v2f*>(a.final_stats + 2 * (head0 + k));
       const float ref = ms[0] == -INFINITY ? 0.0f : ms[0];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] += exp2_fast(x[i] - ref) * ms[1];
+      for (int i = 0; i < 4; ++i) w[i] += x[i] == -INFINITY ? 0.0f : exp2_fast(x[i] - ref) * ms[1];
     }
   }
 #pragma unroll

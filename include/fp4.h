@@ -478,7 +478,8 @@ size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q
  *   out[b,h,:] = sum_t p_t V[t,:];  lse[b,h] = log sum_t exp s_t.
  *   A row with no tokens (length 0, or all pages masked) gives out = 0 and
  *   lse = -inf.  Slots outside the range never influence the result, whatever
- *   bits they hold.
+ *   bits they hold.  A NaN score in the range gives a NaN row, a NaN lse and NaN
+ *   weights of the tokens attended to; masked tokens' weights stay as they are.
  *   q: B x q_heads x head_dim of q_dtype, sequence b at element b * q_stride
  *   (heads dense; 16-byte aligned, stride a multiple of 16 bytes).  out: B x
  *   q_heads x head_dim of out_dtype, dense, 16-byte aligned.  lse: B x q_heads
