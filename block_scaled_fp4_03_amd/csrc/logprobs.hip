@@ -164,6 +164,18 @@ __device__ __forceinline__ Stats wave_join(Stats a, float c2) {
   return Stats{r, wave_fsum(a.s * f), wave_fsum(f == 0.0f ? 0.0f : (a.w + d * a.s) * f)};
 }
 
+// A step's t is v c2 + ref2 in one operation, ref2 = -r c2 rounded: (v - r) c2
+// and what that rounding leaves, which is the same for every logit until the
+// reference moves and is taken out then.  (Left in, threads whose references
+// differ would weigh differently: 2^-24 |ref2|, 3e-3 for logits of 4e4, and the
+// entropy is a mean over them.)  Beyond kFarRef, and where ref2 is not finite,
+// differences come first and nothing is left over.
+constexpr float kFarRef = 65536.0f;
+__device__ __forceinline__ float ref_rest(float r, float c2) {
+  const float ref = r == -INFINITY ? 0.0f : r, ref2 = -ref * c2;
+  return fabsf(ref2) > kFarRef ? 0.0f : __builtin_fmaf(ref, c2, ref2);
+}
+
 struct Args {
   const void* x;
   int64_t stride;
@@ -435,7 +447,8 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     }
     mine = fmaxf(mine, top);
     if (__any((top - st.r) * c2 > kLazy || st.r == -INFINITY)) {
-      const float r = fmaxf(st.r, top), d = st.r == r ? 0.0f : (st.r - r) * c2, f = exp2_fast(d);
+      const float r = fmaxf(st.r, top);
+      const float d = st.r == r ? 0.0f : (st.r - r) * c2 + (ref_rest(r, c2) - ref_rest(st.r, c2)), f = exp2_fast(d);
       st.w = f == 0.0f ? 0.0f : (st.w + d * st.s) * f;
       st.s *= f;
       st.r = r;
@@ -453,18 +466,19 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
       }
     }
     constexpr int kNanOrInf = 0x207;
-    if (__any(__builtin_amdgcn_classf(w, kNanOrInf) || fabsf(ref2) > 65536.0f)) {
+    if (__any(__builtin_amdgcn_classf(w, kNanOrInf) || fabsf(ref2) > kFarRef)) {
       // A masked logit (-inf, or so low that t is): e^t is 0, and t e^t has
       // to be too.  (Or a NaN, which stays one in s.)  Or logits so large that
-      // ref2's rounding, 2^-24 of it, shows in t (or that it overflows).
-      // Again, with care, and with differences first.
+      // the product's rounding shows in t (or that ref2 overflows).  Again, with
+      // care, and with differences first.
+      const float rest = ref_rest(st.r, c2);
       s = st.s;
       w = st.w;
 #pragma unroll
       for (uint32_t u = 0; u < kUnroll; ++u)
 #pragma unroll
         for (uint32_t e = 0; e < E; ++e) {
-          const float t = (v[u][e] - ref) * c2, p = exp2_fast(t);
+          const float t = __builtin_fmaf(v[u][e] - ref, c2, rest), p = exp2_fast(t);
           s += p;
           w = __builtin_fmaf(fmaxf(t, -1000.0f), p, w);
         }
@@ -501,7 +515,10 @@ __global__ __launch_bounds__(256) void logprobs_kernel(Args a) {
     }
   }
 
-  // The workgroup's statistics, in a fixed order.
+  // The workgroup's statistics, in a fixed order, relative to the references themselves.
+  const float rest = ref_rest(st.r, c2), less = exp2_fast(-rest);
+  st.w = (st.w - rest * st.s) * less;
+  st.s *= less;
   st = wave_join(st, c2);
   if ((tid & 63u) == 0u) {
     sh.part[tid >> 6] = st;

@@ -1,4 +1,5 @@
-"""fp4_logprobs on rows that hold a NaN at any place, against the definition."""
+"""fp4_logprobs on rows that hold a NaN at any place, and on logits far from
+zero, against the definition."""
 import numpy as np
 import pytest
 
@@ -41,3 +42,32 @@ def test_top_of_rows_with_nan(dtype, N, V, k):
     top = to_host(r.top_logp)
     assert np.isnan(top[special][:, :min(k, V)]).all() and np.isneginf(top[:, V:]).all()
     assert np.isfinite(top[~special][:, :min(k, V)]).all()
+
+
+@pytest.mark.parametrize("N,V", [(64, 50), (64, 1000), (9, 30011), (3, 200003), (600, 4100)])
+@pytest.mark.parametrize("offset", (0.0, 100.0, -3000.0, 20000.0, -40000.0, 60000.0, 1e7))
+def test_logits_with_a_common_offset(N, V, offset):
+    """softmax does not change when all logits move by the same amount.  With
+    scale 1 the differences of FP32 logits to their maximum lose nothing, so
+    the entropy's tolerance is test_gpu_logprobs.py's without the terms of y's
+    own size, and that of log-sum-exp has its last place's alone (u = 2^-24):
+    r = (V / 256 + 72 + 2 E|t|) 2u; |dH| <= r (1 + 2 E|t|) + 4u (E t^2 + |H|);
+    |d lse| <= r + 4u |lse|."""
+    import block_scaled_fp4_03_amd as fp4
+    U = 2.0 ** -24
+    rng = np.random.default_rng(V)
+    x = (3.0 * rng.standard_normal((N, V)) + offset).astype(np.float32)
+    say("logprobs at %g, N %d V %d" % (offset, N, V))
+    r = fp4.logprobs(to_dev(x), to_dev(np.zeros((N, 1), np.int32)))
+    y = x.astype(np.float64)
+    m = y.max(axis=1, keepdims=True)
+    t = y - m
+    e = np.exp(t)
+    s = e.sum(axis=1)
+    p = e / s[:, None]
+    lse, et, et2 = m[:, 0] + np.log(s), (p * -t).sum(axis=1), (p * t * t).sum(axis=1)
+    H = np.log(s) + et
+    rel = (V / 256 + 72 + 2 * et) * 2 * U
+    off = np.abs(to_host(r.lse) - lse) / (rel + 4 * U * np.abs(lse))
+    offH = np.abs(to_host(r.entropy) - H) / (rel * (1 + 2 * et) + 4 * U * (et2 + np.abs(H)))
+    assert off.max() <= 1 and offH.max() <= 1, "lse %.3g, entropy %.3g of the tolerance" % (off.max(), offH.max())
