@@ -433,7 +433,13 @@ __device__ __forceinline__ void attend_piece(const AttnArgs& a, const Piece& pc,
   const auto v_elem = [](uint32_t row, int e) __attribute__((always_inline)) {
     return (uint32_t)(e / kPart) * 16u * kPart + row * kPart + (uint32_t)(e % kPart);
   };
-  constexpr int kQTerms = EX ? 3 : 1, kPTerms = EX ? 3 : 2;
+  // BF16 terms of a query and of a probability: three hold FP32's 24 bits.  With
+  // BF16 q and out over an MX cache, whose values have 4 significant bits at
+  // most, probabilities take two (2^-17): the third costs 32 ragged MXFP4
+  // sequences 6% (59.4 to 63.1 us) and 8 x 16000 MXFP8 tokens 0.4% to 3% (heads
+  // of 128: 54.9 to 55.1 us, of 64: 29.6 to 30.6).  Over a BF16 cache it costs
+  // nothing (88.4 and 88.5 us, heads of 256 169.8 and 169.7).
+  constexpr int kQTerms = EX ? 3 : 1, kPTerms = EX || !MX ? 3 : 2;
 
   const uint32_t lane = threadIdx.x & 63u, c = lane & 15u, g = lane >> 4;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));

@@ -492,9 +492,9 @@ size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q
  *   every t < len  weights_in[b,kv,t] + sum over the kv head's query heads of
  *   p_t  (weights_in NULL: 0; it may equal weights_out); entries t >= len are
  *   left alone.  weights_stride >= max_len.
- *   Scores, softmax and sums in FP32.  With BF16 q and out the probabilities
- *   enter the product with V as two BF16 terms (relative error 2^-17); with
- *   either in FP32, q and the probabilities enter as three (FP32's 24 bits).
+ *   Scores, softmax and sums in FP32.  The probabilities enter the product with
+ *   V as three BF16 terms (FP32's 24 bits), with BF16 q and out over an MX
+ *   cache as two (relative error 2^-17); q in FP32, or with FP32 out, as three.
  *   Sums are in a fixed order: results do not depend on timing.
  * B == 0 or q_heads == 0 is a no-op; max_len == 0 writes the empty result. */
 int fp4_attn_decode(const fp4_kv_cache* cache, const void* q, int q_dtype, int64_t q_stride,
