@@ -7,7 +7,6 @@
 #include "fp4_launch.h"
 
 #include <atomic>
-#include <cfloat>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -629,6 +628,9 @@ int fp4_kv_append(const fp4_kv_cache* cache, const void* k, const void* v, int i
                 s);
 }
 
+// The kernels take exponentials in base 2: scale times log2 e has to be finite too.
+constexpr float kMaxScale = 0x1p127f;
+
 // Shapes of an attention call that the workspace's size and the call share.
 static int attn_check_shape(const fp4_kv_cache* cache, int64_t B, int64_t q_heads, int64_t max_len) {
   const int rc = kv_check_shape(cache);
@@ -659,6 +661,7 @@ int fp4_attn_decode(const fp4_kv_cache* cache, const void* q, int q_dtype, int64
   if (!dtype_ok(q_dtype) || !dtype_ok(out_dtype)) return FP4_ERR_DTYPE;
   if (table_width < 0 || table_width > kMaxDim || max_len > table_width * cache->page_size) return FP4_ERR_SHAPE;
   if (window < 0 || q_stride < q_heads * cache->head_dim || q_stride > kMaxDim) return FP4_ERR_SHAPE;
+  if (!(scale >= -kMaxScale && scale <= kMaxScale)) return FP4_ERR_SHAPE;
   if (weights_out && (weights_stride < max_len || weights_stride > kMaxDim)) return FP4_ERR_SHAPE;
   if (B == 0 || q_heads == 0) return FP4_OK;
   if ((rc = kv_check_buffers(*cache)) != FP4_OK) return rc;
@@ -767,7 +770,7 @@ int fp4_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V,
                  int32_t* top_index, void* workspace, size_t workspace_bytes, void* stream) {
   if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
   if (!logprobs_shape_ok(N, V) || stride < V || stride > kMaxDim || M < 0 || M > kMaxTokens || top_k < 0 ||
-      top_k > kMaxTopK || !(scale > 0.0f) || scale > FLT_MAX)
+      top_k > kMaxTopK || !(scale > 0.0f) || scale > kMaxScale)
     return FP4_ERR_SHAPE;
   if (N == 0) return FP4_OK;
   if (!x || (M > 0 && (!tokens || !logp)) || (top_k > 0 && (!top_logp || !top_index))) return FP4_ERR_NULL;
@@ -799,7 +802,7 @@ int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, i
                           const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride, void* stream) {
   if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
   if (!logprobs_shape_ok(N, V) || stride < V || stride > kMaxDim || dx_stride < V || dx_stride > kMaxDim || M < 0 ||
-      M > kMaxTokens || !(scale > 0.0f) || scale > FLT_MAX)
+      M > kMaxTokens || !(scale > 0.0f) || scale > kMaxScale)
     return FP4_ERR_SHAPE;
   if (N == 0) return FP4_OK;
   if (!x || !dx || !lse || (M > 0 && (!tokens || !g_logp)) || (g_entropy && !entropy)) return FP4_ERR_NULL;

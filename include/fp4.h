@@ -487,7 +487,7 @@ size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q
  *   lens: B device int32 (negative reads as 0).  max_len <= table_width *
  *   page_size bounds the lengths (and sizes the workspace); B * kv_heads *
  *   ceil(q_heads / kv_heads / 16) * (max_len / 32 + 32) < 2^32, B < 2^16.  window: 0 for
- *   none.
+ *   none.  scale: of magnitude 2^127 at most (0 and below 0 too).
  *   weights_out (optional): FP32 B x kv_heads x weights_stride, receives for
  *   every t < len  weights_in[b,kv,t] + sum over the kv head's query heads of
  *   p_t  (weights_in NULL: 0; it may equal weights_out); entries t >= len are
@@ -547,7 +547,8 @@ size_t fp4_logprobs_workspace(int64_t N, int64_t V, int32_t top_k);
  *   +inf logit gives NaN.
  *   x: N rows of V values of dtype, row n at element n * stride (stride >= V),
  *   aligned to its element size only.  tokens: int32 N x M, dense (M <= 1024).  entropy
- *   and lse may be NULL; top_k 0..32; scale finite, > 0.  All sums in FP32.
+ *   and lse may be NULL; top_k 0..32; 0 < scale <= 2^127.  All sums in
+ *   FP32.
  * N == 0 is a no-op; V >= 1. */
 int fp4_logprobs(const void* x, int dtype, int64_t stride, int64_t N, int64_t V, float scale, const int32_t* tokens,
                  int32_t M, float* logp, float* entropy, float* lse, int32_t top_k, float* top_logp,

@@ -3,6 +3,7 @@ zero, against the definition."""
 import numpy as np
 import pytest
 
+import test_gpu_logprobs as lp
 from gpu_helpers import say, to_dev, to_host
 
 pytestmark = pytest.mark.gpu
@@ -71,3 +72,17 @@ def test_logits_with_a_common_offset(N, V, offset):
     off = np.abs(to_host(r.lse) - lse) / (rel + 4 * U * np.abs(lse))
     offH = np.abs(to_host(r.entropy) - H) / (rel * (1 + 2 * et) + 4 * U * (et2 + np.abs(H)))
     assert off.max() <= 1 and offH.max() <= 1, "lse %.3g, entropy %.3g of the tolerance" % (off.max(), offH.max())
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+def test_largest_and_smallest_scale(dtype):
+    """2^127 on logits of 2^-126 and 2^-100 on logits of 2^100: the same softmax."""
+    import block_scaled_fp4_03_amd as fp4
+    rng = np.random.default_rng(3)
+    for at, scale in ((-126, 2.0 ** 127), (101, 2.0 ** -100)):
+        x = np.ldexp(rng.integers(-8, 9, (4, 3001)), at).astype(np.float32)
+        xd, vals = lp._dev(x, dtype)
+        tokens = rng.integers(0, 3001, (4, 2)).astype(np.int32)
+        say("logprobs at scale %g, %s" % (scale, dtype))
+        res = fp4.logprobs(xd, to_dev(tokens), top_k=5, scale=scale)
+        lp.check_forward(vals, scale, tokens, res, 5, "scale %g" % scale)
