@@ -853,7 +853,9 @@ def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
     padding, 0) under softmax(scale * x), x: N x V float32/bfloat16 logits
     (any row stride), with the entropy, the log-sum-exp and the top_k <= 32
     largest alternatives; see fp4_logprobs in include/fp4.h.  ws:
-    logprobs_workspace's tensor (one is allocated here if None)."""
+    logprobs_workspace's tensor (one is allocated here if None).  The results
+    carry no autograd history, also where x requires a gradient:
+    logprobs_backward gives that of logp and the entropy."""
     torch = _torch()
     code, xs = _want_rows(x, "x", 2)
     dev = x.device

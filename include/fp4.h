@@ -495,7 +495,9 @@ size_t fp4_attn_decode_workspace(const fp4_kv_cache* cache, int64_t B, int64_t q
  *   Scores, softmax and sums in FP32.  The probabilities enter the product with
  *   V as three BF16 terms (FP32's 24 bits), with BF16 q and out over an MX
  *   cache as two (relative error 2^-17); q in FP32, or with FP32 out, as three.
- *   Sums are in a fixed order: results do not depend on timing.
+ *   Sums are in a fixed order: results do not depend on timing.  The order
+ *   follows the lengths of all sequences of the call, so a sequence's last bits
+ *   may differ beside other sequences.
  * B == 0 or q_heads == 0 is a no-op; max_len == 0 writes the empty result. */
 int fp4_attn_decode(const fp4_kv_cache* cache, const void* q, int q_dtype, int64_t q_stride,
                     const int32_t* page_table, int64_t table_width, const int32_t* lens, int64_t B, int64_t q_heads,
