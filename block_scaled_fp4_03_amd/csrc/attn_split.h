@@ -43,7 +43,9 @@ FP4_HOST_DEVICE constexpr uint32_t change_tiles(uint32_t row_bytes) {
 // are long enough not to be cut because of it, and none where the call has no
 // room for the pieces of a cut unit (`join` false: no sequence has more than a
 // grain).  Units of one grain with nothing more lie on whole shares' grains
-// and are never cut; with a change of units counted they would be.
+// and are never cut; with a change of units counted they would be, which is
+// slower too (193 sequences of 128 BF16 tokens, 8 kv heads of 128: 29.7 us whole,
+// 32.4 cut and joined; 1500 of MXFP8 134 and 139).
 FP4_HOST_DEVICE uint32_t counted_change(uint32_t share, uint32_t change, bool join) {
   return join && share >= 4u * change ? change : 0u;
 }
