@@ -4,7 +4,8 @@ for AMD Instinct MI355X (gfx950).
 The C ABI (include/fp4.h) is exposed under the same names (``fp4_quantize``,
 ``fp4_dequantize``, ``fp4_gemm``, ``fp4_gemm_ex``, ``fp4_gemm_grouped``, ``fp4_gemm_w4a8``, ``fp4_scale_bytes``,
 ``fp4_workspace_size``, ``fp4_status_string``; the decode step's ``fp4_kv_append``, ``fp4_attn_decode``,
-``fp4_kv_evict``, ``fp4_logprobs``, ``fp4_logprobs_backward``), taking raw device pointers as
+``fp4_kv_evict``, ``fp4_logprobs``, ``fp4_logprobs_backward``, ``fp4_qk_norm_rope``, ``fp4_moe_route``,
+``fp4_moe_sort``, ``fp4_moe_gather``, ``fp4_moe_combine``, ``fp4_verify_drafts`` and gradients), taking raw device pointers as
 integers.  The tensor helpers below only allocate outputs with torch and
 marshal ``data_ptr()`` / the current stream into those calls: every step of the
 computation runs in the HIP kernels of libfp4.so.  There is no fallback -- if
@@ -29,6 +30,8 @@ OUT_F32, OUT_BF16, OUT_MXFP4, OUT_MXFP4_OCP, OUT_NVFP4 = 0, 1, 2, 3, 4
 ACT_NONE, ACT_RELU = 0, 1
 # enum fp4_kv_fmt (cache rows)
 KV_BF16, KV_MXFP8, KV_MXFP4 = 0, 1, 2
+# flags of struct fp4_rope
+ROPE_INTERLEAVED, ROPE_CYCLIC = 1, 2
 
 FUNCTIONS = ("fp4_scale_bytes", "fp4_workspace_size", "fp4_quantize", "fp4_quantize_noalloc", "fp4_quantize_sr",
              "fp4_quantize_ex",
@@ -36,7 +39,9 @@ FUNCTIONS = ("fp4_scale_bytes", "fp4_workspace_size", "fp4_quantize", "fp4_quant
              "fp4_gemm_grouped", "fp4_gemm_nvfp4_act", "fp4_gemm_nvfp4_act_supported", "fp4_gemm_w4a8",
              "fp4_status_string", "fp4_set_debug", "fp4_kv_append", "fp4_attn_decode_workspace", "fp4_attn_decode",
              "fp4_kv_evict_workspace", "fp4_kv_evict", "fp4_logprobs_workspace", "fp4_logprobs",
-             "fp4_logprobs_backward")
+             "fp4_logprobs_backward", "fp4_qk_norm_rope", "fp4_qk_norm_rope_workspace", "fp4_qk_norm_rope_backward",
+             "fp4_moe_route", "fp4_moe_route_backward", "fp4_moe_sort_workspace", "fp4_moe_sort", "fp4_moe_gather",
+             "fp4_moe_combine", "fp4_moe_combine_backward", "fp4_verify_drafts_workspace", "fp4_verify_drafts")
 
 
 class KVCacheStruct(ctypes.Structure):
@@ -44,6 +49,12 @@ class KVCacheStruct(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
                 ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("fmt", ctypes.c_int32)]
+
+
+class RopeStruct(ctypes.Structure):
+    """struct fp4_rope of include/fp4.h."""
+    _fields_ = [("freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("axes", ctypes.c_int32),
+                ("sections", ctypes.c_int32 * 4), ("flags", ctypes.c_uint32)]
 
 
 class Fp4Error(RuntimeError):
@@ -72,7 +83,7 @@ def lib():
             pass
         L = ctypes.CDLL(LIB_PATH)
         P, I64, I32, U32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
-        F32C, CACHE = ctypes.c_float, ctypes.POINTER(KVCacheStruct)
+        F32C, CACHE, ROPE = ctypes.c_float, ctypes.POINTER(KVCacheStruct), ctypes.POINTER(RopeStruct)
         sig = {
             "fp4_scale_bytes": (I64, [I32, I64, I64]),
             "fp4_workspace_size": (SZ, [I32, I32, I64, I64, I64, I32]),
@@ -100,6 +111,20 @@ def lib():
             "fp4_logprobs_workspace": (SZ, [I64, I64, I32]),
             "fp4_logprobs": (I32, [P, I32, I64, I64, I64, F32C, P, I32, P, P, P, I32, P, P, P, SZ, P]),
             "fp4_logprobs_backward": (I32, [P, I32, I64, I64, I64, F32C, P, I32, P, P, P, P, P, I64, P]),
+            "fp4_qk_norm_rope": (I32, [ROPE, P, P, I64, I64, P, I64, I64, I64, I32, P, P, F32C, P, I64, P, I64, I64,
+                                       P]),
+            "fp4_qk_norm_rope_workspace": (SZ, [I64, I64, I64, I64]),
+            "fp4_qk_norm_rope_backward": (I32, [ROPE, P, P, I64, P, I64, P, I64, I64, P, I64, I64, I64, I32, P, P,
+                                                F32C, P, I64, P, I64, P, P, I64, P, SZ, P]),
+            "fp4_moe_route": (I32, [P, I32, I64, I64, I64, I32, I32, P, P, P]),
+            "fp4_moe_route_backward": (I32, [P, I32, I64, I64, I64, I32, I32, P, P, P, P]),
+            "fp4_moe_sort_workspace": (SZ, [I64, I32, I64]),
+            "fp4_moe_sort": (I32, [P, I64, I32, I64, P, P, P, P, SZ, P]),
+            "fp4_moe_gather": (I32, [P, I32, I64, P, I64, I32, I64, I64, P, P]),
+            "fp4_moe_combine": (I32, [P, I32, P, P, I64, I32, I64, I64, P, I64, P]),
+            "fp4_moe_combine_backward": (I32, [P, I64, P, I32, P, P, I64, I32, I64, I64, P, P, P]),
+            "fp4_verify_drafts_workspace": (SZ, [I64, I64, I64]),
+            "fp4_verify_drafts": (I32, [P, I64, I64, P, I64, I64, I32, I64, I64, I64, P, P, P, P, P, P, P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -225,6 +250,63 @@ def fp4_logprobs_backward(x, dtype, stride_, N, V, scale, tokens, M, lse, entrop
                           stream):
     return lib().fp4_logprobs_backward(x, dtype, stride_, N, V, scale, tokens, M, lse, entropy, g_logp, g_entropy, dx,
                                        dx_stride, stream)
+
+
+def fp4_qk_norm_rope(rope, pos, q, q_stride, q_heads, k, k_stride, k_heads, head_dim, dtype, q_weight, k_weight, eps,
+                     q_out, q_out_stride, k_out, k_out_stride, rows, stream):
+    return lib().fp4_qk_norm_rope(rope, pos, q, q_stride, q_heads, k, k_stride, k_heads, head_dim, dtype, q_weight,
+                                  k_weight, eps, q_out, q_out_stride, k_out, k_out_stride, rows, stream)
+
+
+def fp4_qk_norm_rope_workspace(rows, q_heads, k_heads, head_dim):
+    return lib().fp4_qk_norm_rope_workspace(rows, q_heads, k_heads, head_dim)
+
+
+def fp4_qk_norm_rope_backward(rope, pos, gq, gq_stride, gk, gk_stride, q, q_stride, q_heads, k, k_stride, k_heads,
+                              head_dim, dtype, q_weight, k_weight, eps, dq, dq_stride, dk, dk_stride, dq_weight,
+                              dk_weight, rows, workspace, workspace_bytes, stream):
+    return lib().fp4_qk_norm_rope_backward(rope, pos, gq, gq_stride, gk, gk_stride, q, q_stride, q_heads, k, k_stride,
+                                           k_heads, head_dim, dtype, q_weight, k_weight, eps, dq, dq_stride, dk,
+                                           dk_stride, dq_weight, dk_weight, rows, workspace, workspace_bytes, stream)
+
+
+def fp4_moe_route(logits, dtype, stride_, T, E, top_k, renormalise, ids, weights, stream):
+    return lib().fp4_moe_route(logits, dtype, stride_, T, E, top_k, renormalise, ids, weights, stream)
+
+
+def fp4_moe_route_backward(logits, dtype, stride_, T, E, top_k, renormalise, ids, g, dlogits, stream):
+    return lib().fp4_moe_route_backward(logits, dtype, stride_, T, E, top_k, renormalise, ids, g, dlogits, stream)
+
+
+def fp4_moe_sort_workspace(T, top_k, E):
+    return lib().fp4_moe_sort_workspace(T, top_k, E)
+
+
+def fp4_moe_sort(ids, T, top_k, E, group_off, row_idx, pos, workspace, workspace_bytes, stream):
+    return lib().fp4_moe_sort(ids, T, top_k, E, group_off, row_idx, pos, workspace, workspace_bytes, stream)
+
+
+def fp4_moe_gather(x, dtype, stride_, pos, T, top_k, H, rows, out, stream):
+    return lib().fp4_moe_gather(x, dtype, stride_, pos, T, top_k, H, rows, out, stream)
+
+
+def fp4_moe_combine(y, dtype, pos, weights, T, top_k, H, rows, out, stride_, stream):
+    return lib().fp4_moe_combine(y, dtype, pos, weights, T, top_k, H, rows, out, stride_, stream)
+
+
+def fp4_moe_combine_backward(g, stride_, y, dtype, pos, weights, T, top_k, H, rows, dy, dweights, stream):
+    return lib().fp4_moe_combine_backward(g, stride_, y, dtype, pos, weights, T, top_k, H, rows, dy, dweights, stream)
+
+
+def fp4_verify_drafts_workspace(B, G, V):
+    return lib().fp4_verify_drafts_workspace(B, G, V)
+
+
+def fp4_verify_drafts(target, target_seq_stride, target_row_stride, draft, draft_seq_stride, draft_row_stride, dtype,
+                      B, G, V, tokens, u, temperature, out, accepted, chance, workspace, workspace_bytes, stream):
+    return lib().fp4_verify_drafts(target, target_seq_stride, target_row_stride, draft, draft_seq_stride,
+                                   draft_row_stride, dtype, B, G, V, tokens, u, temperature, out, accepted, chance,
+                                   workspace, workspace_bytes, stream)
 
 
 # ---- torch helpers: allocation + pointer/stream marshalling only -------------
@@ -918,3 +1000,379 @@ def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scal
     if rc != 0:
         _check(rc, "fp4_logprobs_backward")
     return out
+
+
+# ---- norms and rotary positions of queries and keys ---------------------------
+class Rope:
+    """Rotary positions (struct fp4_rope of include/fp4.h): pair i of a head's
+    first 2 * len(freq) values is turned by pos * freq[i] (float32 tensor,
+    radians a position; the object holds it).
+
+    sections: the number of pairs of each axis, for positions of two to four
+    axes, summing to len(freq) (default: one axis); the axes take the pairs one
+    after the other, or in turns (cyclic).  interleaved: pairs (2i, 2i + 1)
+    instead of (i, i + len(freq))."""
+
+    def __init__(self, freq, sections=None, interleaved=False, cyclic=False):
+        torch = _torch()
+        _need(freq, "freq", (torch.float32,), ndim=1)
+        pairs = freq.numel()
+        if pairs % 4 != 0 or pairs > 128:
+            raise ValueError("freq holds %d pairs: a multiple of 4 up to 128 is needed" % pairs)
+        sections = [pairs] if sections is None else [int(n) for n in sections]
+        if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != pairs:
+            raise ValueError("sections %s: one to four numbers that sum to the %d pairs of freq are needed"
+                             % (sections, pairs))
+        self.freq, self.axes, self.device = freq, len(sections), freq.device
+        flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_CYCLIC if cyclic else 0)
+        self.struct = RopeStruct(_ptr(freq), 2 * pairs, len(sections), (ctypes.c_int32 * 4)(*sections), flags)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _want_pos(rope, pos, rows, dev):
+    """The rope's struct and the positions' pointer, checked (None, None: no rotation)."""
+    if rope is None:
+        return None, None
+    if not isinstance(rope, Rope):
+        raise TypeError("rope must be a Rope, got %s" % type(rope).__name__)
+    if rope.device != dev:
+        raise ValueError("rope is on %s, the call's operands on %s" % (rope.device, dev))
+    torch = _torch()
+    if isinstance(pos, torch.Tensor) and pos.ndim == 1 and rope.axes == 1:
+        pos = pos.view(1, -1)
+    _want(pos, "pos", torch.int32, 2, dev)
+    if pos.shape[0] != rope.axes or pos.shape[1] != rows:
+        raise ValueError("pos must have shape (%d, %d), got %s" % (rope.axes, rows, tuple(pos.shape)))
+    return rope.ref, pos.data_ptr()
+
+
+def _want_heads(q, k):
+    """q and k, rows x heads x head_dim of one dtype: its code, the device,
+    rows, head_dim and the row strides."""
+    code, qs = _want_rows(q, "q", 3)
+    dev = q.device
+    kcode, ks = _want_rows(k, "k", 3, dev)
+    rows, _, dim = q.shape
+    if kcode != code:
+        raise TypeError("k must be %s, got %s" % (q.dtype, k.dtype))
+    if k.shape[0] != rows or k.shape[2] != dim:
+        raise ValueError("k must have shape (%d, heads, %d), got %s" % (rows, dim, tuple(k.shape)))
+    return code, dev, rows, dim, qs, ks
+
+
+def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
+    """Norms of queries and keys for each head (over head_dim, times q_weight /
+    k_weight; left out where that is None) and the rotation of their positions,
+    in one pass; see fp4_qk_norm_rope in include/fp4.h.
+
+    q, k: rows x heads x head_dim float32/bfloat16, any row stride (columns of
+    one projection's output); pos: int32 axes x rows (or rows, with one axis);
+    rope: a Rope, or None for no rotation; weights: float32 head_dim.  q_out,
+    k_out may be q, k themselves.  Returns the two (new dense tensors unless
+    given)."""
+    torch = _torch()
+    code, dev, rows, dim, qs, ks = _want_heads(q, k)
+    ref, at = _want_pos(rope, pos, rows, dev)
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _want(t, name, torch.float32, 1, dev, dim)
+    if q_out is None:
+        q_out = _alloc(stream, torch.empty, q.shape, dtype=q.dtype, device=dev)
+        qos = q.shape[1] * dim
+    else:
+        qos = _want_rows(q_out, "q_out", 3, dev, q)[1]
+    if k_out is None:
+        k_out = _alloc(stream, torch.empty, k.shape, dtype=k.dtype, device=dev)
+        kos = k.shape[1] * dim
+    else:
+        kos = _want_rows(k_out, "k_out", 3, dev, k)[1]
+    rc = lib().fp4_qk_norm_rope(ref, at, q.data_ptr(), qs, q.shape[1], k.data_ptr(), ks, k.shape[1], dim, code,
+                                _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
+                                rows, _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_workspace(rows, q_heads, k_heads, head_dim, device="cuda"):
+    """A workspace tensor for qk_norm_rope_backward (or None)."""
+    n = fp4_qk_norm_rope_workspace(rows, q_heads, k_heads, head_dim)
+    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+
+
+def qk_norm_rope_backward(gq, gk, q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, dq=None, dk=None, ws=None,
+                          stream=None):
+    """Gradient of qk_norm_rope from the gradients gq, gk of its results (of
+    q's, k's shape and dtype) and its arguments; see fp4_qk_norm_rope_backward
+    in include/fp4.h.  dq may be gq or q, dk gk or k.  ws:
+    qk_norm_rope_workspace's tensor (one is allocated here if None).  Returns
+    (dq, dk, the gradients of q_weight and k_weight: float32, None for a weight
+    that is None)."""
+    torch = _torch()
+    code, dev, rows, dim, qs, ks = _want_heads(q, k)
+    gqs = _want_rows(gq, "gq", 3, dev, q)[1]
+    gks = _want_rows(gk, "gk", 3, dev, k)[1]
+    ref, at = _want_pos(rope, pos, rows, dev)
+    f32 = torch.float32
+    grads = []
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _want(t, name, f32, 1, dev, dim)
+        grads.append(None if t is None else _alloc(stream, torch.zeros, dim, dtype=f32, device=dev)
+                     if (q if name[0] == "q" else k).shape[1] == 0
+                     else _alloc(stream, torch.empty, dim, dtype=f32, device=dev))
+    if dq is None:
+        dq = _alloc(stream, torch.empty, q.shape, dtype=q.dtype, device=dev)
+        dqs = q.shape[1] * dim
+    else:
+        dqs = _want_rows(dq, "dq", 3, dev, q)[1]
+    if dk is None:
+        dk = _alloc(stream, torch.empty, k.shape, dtype=k.dtype, device=dev)
+        dks = k.shape[1] * dim
+    else:
+        dks = _want_rows(dk, "dk", 3, dev, k)[1]
+    if ws is not None:
+        _want(ws, "ws", torch.uint8, 1, dev)
+    elif q_weight is not None or k_weight is not None:
+        ws = _alloc(stream, qk_norm_rope_workspace, rows, q.shape[1], k.shape[1], dim, dev)
+    rc = lib().fp4_qk_norm_rope_backward(ref, at, gq.data_ptr(), gqs, gk.data_ptr(), gks, q.data_ptr(), qs,
+                                         q.shape[1], k.data_ptr(), ks, k.shape[1], dim, code, _ptr(q_weight),
+                                         _ptr(k_weight), eps, dq.data_ptr(), dqs, dk.data_ptr(), dks, _ptr(grads[0]),
+                                         _ptr(grads[1]), rows, _ptr(ws), 0 if ws is None else ws.numel(),
+                                         _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_qk_norm_rope_backward")
+    return dq, dk, grads[0], grads[1]
+
+
+# ---- around the grouped GEMM: routing, rows to the experts' order and back -----
+def moe_route(logits, top_k, renormalise=True, stream=None):
+    """The top_k <= 16 experts of each token (ties to the lowest) and their
+    weights: the softmax over the chosen logits, or with renormalise False that
+    over all at them; see fp4_moe_route in include/fp4.h.  logits: T x E
+    float32/bfloat16, any row stride, E <= 512.  Returns (ids int32, weights
+    float32, both T x top_k), without autograd history: moe_route_backward gives
+    the gradient."""
+    torch = _torch()
+    code, stride = _want_rows(logits, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    ids = _alloc(stream, torch.empty, (T, max(top_k, 0)), dtype=torch.int32, device=dev)
+    weights = _alloc(stream, torch.empty, (T, max(top_k, 0)), dtype=torch.float32, device=dev)
+    rc = lib().fp4_moe_route(logits.data_ptr(), code, stride, T, E, top_k, 1 if renormalise else 0, ids.data_ptr(),
+                             weights.data_ptr(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_route")
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, g, renormalise=True, stream=None):
+    """Gradient of moe_route's weights with respect to the logits, from theirs
+    (g, float32 T x top_k); see fp4_moe_route_backward in include/fp4.h.
+    Returns a dense T x E tensor of the logits' dtype."""
+    torch = _torch()
+    code, stride = _want_rows(logits, "logits", 2)
+    dev = logits.device
+    T, E = logits.shape
+    _want(ids, "ids", torch.int32, 2, dev)
+    _want(g, "g", torch.float32, 2, dev)
+    if ids.shape[0] != T or g.shape != ids.shape:
+        raise ValueError("ids and g must have shape (%d, top_k), got %s and %s" % (T, tuple(ids.shape), tuple(g.shape)))
+    out = _alloc(stream, torch.empty, (T, E), dtype=logits.dtype, device=dev)
+    rc = lib().fp4_moe_route_backward(logits.data_ptr(), code, stride, T, E, ids.shape[1], 1 if renormalise else 0,
+                                      ids.data_ptr(), g.data_ptr(), out.data_ptr(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_route_backward")
+    return out
+
+
+def moe_sort_workspace(tokens, top_k, experts, device="cuda"):
+    """A workspace tensor for moe_sort (or None)."""
+    n = fp4_moe_sort_workspace(tokens, top_k, experts)
+    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+
+
+def moe_sort(ids, experts, ws=None, stream=None):
+    """The entries of ids (int32 T x top_k) in the order of their experts; see
+    fp4_moe_sort in include/fp4.h.  An id outside [0, experts) is taken by no
+    expert.  ws: moe_sort_workspace's tensor (one is allocated here if None).
+    Returns int32 (group_off, row_idx) for gemm_grouped and pos, T x top_k: each
+    entry's row, or -1 - row where no expert takes it."""
+    torch = _torch()
+    i32 = torch.int32
+    _need(ids, "ids", (i32,), ndim=2)
+    dev = ids.device
+    T, k = ids.shape
+    off = _alloc(stream, torch.empty, max(experts, 0) + 1, dtype=i32, device=dev)
+    rows = _alloc(stream, torch.empty, T * k, dtype=i32, device=dev)
+    pos = _alloc(stream, torch.empty, (T, k), dtype=i32, device=dev)
+    if ws is None:
+        ws = _alloc(stream, moe_sort_workspace, T, k, experts, dev)
+    else:
+        _want(ws, "ws", torch.uint8, 1, dev)
+    rc = lib().fp4_moe_sort(ids.data_ptr(), T, k, experts, off.data_ptr(), rows.data_ptr(), pos.data_ptr(), _ptr(ws),
+                            0 if ws is None else ws.numel(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_sort")
+    return off, rows, pos
+
+
+def moe_gather(x, pos, out=None, stream=None):
+    """Rows of x (T x H float32/bfloat16, any row stride) in expert order: row
+    pos[t, j] of the result is x[t]; see fp4_moe_gather in include/fp4.h.  pos as
+    moe_sort gave it.  out: default a new (T * top_k) x H tensor.  The gradient
+    is moe_combine of the result's without weights."""
+    torch = _torch()
+    code, stride = _want_rows(x, "x", 2)
+    dev = x.device
+    T, H = x.shape
+    _want(pos, "pos", torch.int32, 2, dev)
+    k = pos.shape[1]
+    if pos.shape[0] != T:
+        raise ValueError("pos has %d rows, x %d" % (pos.shape[0], T))
+    if out is None:
+        out = _alloc(stream, torch.empty, (T * k, H), dtype=x.dtype, device=dev)
+    else:
+        _want(out, "out", x.dtype, 2, dev)
+        if out.shape[1] != H:
+            raise ValueError("out has rows of %d values, x of %d" % (out.shape[1], H))
+    rc = lib().fp4_moe_gather(x.data_ptr(), code, stride, pos.data_ptr(), T, k, H, out.shape[0], out.data_ptr(),
+                              _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_gather")
+    return out
+
+
+def _want_entries(y, pos, weights):
+    """y (rows x H), pos and weights (T x top_k), checked: dtype code, device, T, top_k, H."""
+    torch = _torch()
+    _need(y, "y", (torch.float32, torch.bfloat16), ndim=2)
+    dev = y.device
+    _want(pos, "pos", torch.int32, 2, dev)
+    if weights is not None:
+        _want(weights, "weights", torch.float32, 2, dev)
+        if weights.shape != pos.shape:
+            raise ValueError("weights must have shape %s, got %s" % (tuple(pos.shape), tuple(weights.shape)))
+    return _dtype_code(y), dev, pos.shape[0], pos.shape[1], y.shape[1]
+
+
+def moe_combine(y, pos, weights=None, out=None, stream=None):
+    """Rows of y (dense, in expert order) joined to tokens: sum over j of
+    weights[t, j] (float32; None: 1) times y[pos[t, j]]; see fp4_moe_combine in
+    include/fp4.h.  out: default a new T x H tensor; may have any row stride."""
+    torch = _torch()
+    code, dev, T, k, H = _want_entries(y, pos, weights)
+    if out is None:
+        out = _alloc(stream, torch.empty, (T, H), dtype=y.dtype, device=dev)
+        stride = H
+    else:
+        ocode, stride = _want_rows(out, "out", 2, dev)
+        if ocode != code or tuple(out.shape) != (T, H):
+            raise ValueError("out must have shape %s and y's dtype, got %s %s" % ((T, H), tuple(out.shape), out.dtype))
+    rc = lib().fp4_moe_combine(y.data_ptr(), code, pos.data_ptr(), _ptr(weights), T, k, H, y.shape[0], out.data_ptr(),
+                               stride, _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_combine")
+    return out
+
+
+def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
+    """Gradient of moe_combine from that of its result (g, T x H of y's dtype,
+    any row stride); see fp4_moe_combine_backward in include/fp4.h.  Returns
+    (dy, of y's shape, and the weights' gradient, float32 T x top_k)."""
+    torch = _torch()
+    if weights is None:
+        raise ValueError("without weights the gradient is moe_gather's")
+    code, dev, T, k, H = _want_entries(y, pos, weights)
+    gcode, stride = _want_rows(g, "g", 2, dev)
+    if gcode != code or tuple(g.shape) != (T, H):
+        raise ValueError("g must have shape %s and y's dtype, got %s %s" % ((T, H), tuple(g.shape), g.dtype))
+    if dy is None:
+        dy = _alloc(stream, torch.empty, y.shape, dtype=y.dtype, device=dev)
+    else:
+        _need_out(dy, "dy", y.shape, (y.dtype,), dev)
+    dw = _alloc(stream, torch.empty, (T, k), dtype=torch.float32, device=dev)
+    rc = lib().fp4_moe_combine_backward(g.data_ptr(), stride, y.data_ptr(), code, pos.data_ptr(), weights.data_ptr(),
+                                        T, k, H, y.shape[0], dy.data_ptr(), dw.data_ptr(), _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_moe_combine_backward")
+    return dy, dw
+
+
+# ---- drafted tokens -------------------------------------------------------------
+def verify_workspace(batch, drafts, vocab, device="cuda"):
+    """A workspace tensor for verify_drafts."""
+    n = fp4_verify_drafts_workspace(batch, drafts, vocab)
+    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+
+
+def _want_logits(t, name, rows, device=None, like=None):
+    """Check batch x rows x vocab logits with a dense last dimension: dtype
+    code and the other two strides."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor, got %s" % (name, type(t).__name__))
+    code = F32 if t.dtype is torch.float32 else BF16 if t.dtype is torch.bfloat16 else None
+    if code is None or (like is not None and t.dtype is not like.dtype):
+        raise TypeError("%s must be %s, got %s"
+                        % (name, "float32 or bfloat16" if like is None else like.dtype, t.dtype))
+    if t.ndim != 3 or t.shape[1] != rows or (like is not None and (t.shape[0], t.shape[2]) != (like.shape[0],
+                                                                                             like.shape[2])):
+        raise ValueError("%s must have shape %s, got %s"
+                         % (name, "batch x %d x vocab" % rows if like is None
+                            else (like.shape[0], rows, like.shape[2]), tuple(t.shape)))
+    if t.stride(2) != 1 and t.shape[2] > 1:
+        raise ValueError("%s must be dense in its last dimension, got strides %s" % (name, t.stride()))
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor, got device %s" % (name, t.device))
+    if device is not None and t.device != device:
+        raise ValueError("%s is on %s, the call's operands on %s" % (name, t.device, device))
+    return code, t.stride(0), t.stride(1)
+
+
+def verify_drafts(target, draft, tokens, u, temperature=None, ws=None, stream=None):
+    """Verify drafted tokens against the target's probabilities with given
+    random numbers, and draw the token that follows the last one kept; see
+    fp4_verify_drafts in include/fp4.h.
+
+    target: batch x (drafts + 1) x vocab float32/bfloat16 logits (any strides
+    but the last); draft: batch x drafts x vocab, or None for drafts that were not
+    drawn; tokens: int32 batch x drafts (one outside the vocabulary ends a
+    sequence's drafts); u: float32 batch x (drafts + 1) in [0, 1), the last for
+    the draw; temperature: float32 batch (default 1; 0 is greedy).  ws:
+    verify_workspace's tensor (one is allocated here if None).  Returns (int32
+    batch x (drafts + 1): the drafts kept, the token drawn, then -1; int32 batch:
+    the number kept; float32 batch x drafts: each draft's probability of being
+    kept)."""
+    torch = _torch()
+    if not isinstance(tokens, torch.Tensor) or tokens.ndim != 2:
+        raise ValueError("tokens must be a tensor of 2 dimensions")
+    B, G = tokens.shape
+    code, tseq, trow = _want_logits(target, "target", G + 1)
+    dev = target.device
+    if target.shape[0] != B:
+        raise ValueError("tokens has %d rows, target %d" % (B, target.shape[0]))
+    dseq = drow = 0
+    if draft is not None:
+        dseq, drow = _want_logits(draft, "draft", G, dev, target)[1:]
+    _want(tokens, "tokens", torch.int32, 2, dev)
+    _want(u, "u", torch.float32, 2, dev)
+    if tuple(u.shape) != (B, G + 1):
+        raise ValueError("u must have shape %s, got %s" % ((B, G + 1), tuple(u.shape)))
+    if temperature is not None:
+        _want(temperature, "temperature", torch.float32, 1, dev, B)
+    V = target.shape[2]
+    out = _alloc(stream, torch.empty, (B, G + 1), dtype=torch.int32, device=dev)
+    accepted = _alloc(stream, torch.empty, B, dtype=torch.int32, device=dev)
+    chance = _alloc(stream, torch.empty, (B, G), dtype=torch.float32, device=dev)
+    if ws is None:
+        ws = _alloc(stream, verify_workspace, B, G, V, dev)
+    else:
+        _want(ws, "ws", torch.uint8, 1, dev)
+    rc = lib().fp4_verify_drafts(target.data_ptr(), tseq, trow, _ptr(draft), dseq, drow, code, B, G, V,
+                                 tokens.data_ptr(), u.data_ptr(), _ptr(temperature), out.data_ptr(),
+                                 accepted.data_ptr(), chance.data_ptr(), _ptr(ws), 0 if ws is None else ws.numel(),
+                                 _run_on(stream, dev))
+    if rc != 0:
+        _check(rc, "fp4_verify_drafts")
+    return out, accepted, chance

@@ -825,6 +825,395 @@ int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, i
                 s);
 }
 
+// ---- norms and rotary positions of queries and keys ----
+
+// Values of dtype in 16 bytes.
+static int64_t per16(int dtype) { return dtype == FP4_F32 ? 4 : 8; }
+
+static bool qk_shape_ok(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim) {
+  // (A wave to a row at least.)
+  return rows >= 0 && rows <= kMaxDim && rows * 64 + 255 <= kMaxWorkItems && q_heads >= 0 && k_heads >= 0 && q_heads <= 65535 &&
+         k_heads <= 65535 && head_dim >= 32 && head_dim <= 256 && head_dim % 8 == 0;
+}
+
+// The axis of every pair, two bits each, from the sections.
+static int rope_axes(const fp4_rope& r, uint32_t (&axis)[8]) {
+  for (uint32_t& w : axis) w = 0u;
+  if (r.axes < 1 || r.axes > 4) return FP4_ERR_SHAPE;
+  if (r.axes == 1) return FP4_OK;
+  const int32_t pairs = r.rot_dim / 2;
+  int32_t left[4] = {0, 0, 0, 0};
+  int64_t sum = 0;
+  for (int32_t a = 0; a < r.axes; ++a) {
+    if (r.sections[a] < 0) return FP4_ERR_SHAPE;
+    left[a] = r.sections[a];
+    sum += r.sections[a];
+  }
+  if (sum != pairs) return FP4_ERR_SHAPE;
+  int32_t a = 0;
+  for (int32_t i = 0; i < pairs; ++i) {
+    while (left[a] == 0) a = (a + 1) % r.axes;
+    axis[i / 16] |= (uint32_t)a << (2 * (i % 16));
+    --left[a];
+    if (r.flags & FP4_ROPE_CYCLIC) a = (a + 1) % r.axes;
+  }
+  return FP4_OK;
+}
+
+// A tensor of rows x heads x head_dim, its rows `stride` apart.
+struct HeadRows {
+  const void* p;
+  int64_t stride, heads;
+};
+static int head_rows_check(std::initializer_list<HeadRows> all, int64_t head_dim, int dtype) {
+  for (const HeadRows& t : all)
+    if (t.heads > 0 && (t.stride < t.heads * head_dim || t.stride > kMaxDim)) return FP4_ERR_SHAPE;
+  for (const HeadRows& t : all)
+    if (t.heads > 0 && !t.p) return FP4_ERR_NULL;
+  for (const HeadRows& t : all)
+    if (t.heads > 0 && (!aligned(t.p, 16) || t.stride % per16(dtype) != 0)) return FP4_ERR_ALIGN;
+  return FP4_OK;
+}
+
+// What the two calls share; fills the rope's part of the arguments.
+static int rope_check(const fp4_rope* rope, const int32_t* pos, int64_t rows, int64_t q_heads, int64_t k_heads,
+                      int64_t head_dim, int dtype, const float* q_weight, const float* k_weight, float eps,
+                      fp4::QkRope& a) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!qk_shape_ok(rows, q_heads, k_heads, head_dim) || !(eps >= 0.0f) || eps > 0x1p127f) return FP4_ERR_SHAPE;
+  a.axes = 1;
+  if (rope) {
+    if (rope->flags & ~(FP4_ROPE_INTERLEAVED | FP4_ROPE_CYCLIC)) return FP4_ERR_FLAGS;
+    if (rope->rot_dim < 0 || rope->rot_dim > head_dim || rope->rot_dim % 8 != 0) return FP4_ERR_SHAPE;
+    const int rc = rope_axes(*rope, a.axis);
+    if (rc != FP4_OK) return rc;
+    a.R = rope->rot_dim;
+    a.axes = rope->axes;
+    a.interleaved = (rope->flags & FP4_ROPE_INTERLEAVED) != 0;
+    if (a.R > 0 && rows > 0 && (!rope->freq || !pos)) return FP4_ERR_NULL;
+    a.freq = rope->freq;
+    a.pos = pos;
+    if (a.R > 0 && (!aligned(a.freq, 4) || !aligned(pos, 4))) return FP4_ERR_ALIGN;
+  }
+  if (!aligned(q_weight, 4) || !aligned(k_weight, 4)) return FP4_ERR_ALIGN;
+  a.hq = q_heads;
+  a.hk = k_heads;
+  a.D = head_dim;
+  a.rows = rows;
+  a.dtype = dtype;
+  a.wq = q_heads > 0 ? q_weight : nullptr;
+  a.wk = k_heads > 0 ? k_weight : nullptr;
+  a.eps = eps;
+  return FP4_OK;
+}
+// Debug mode: the buffers of the rope, the weights and a few tensors of heads.
+static int rope_debug(const fp4::QkRope& a, std::initializer_list<HeadRows> tensors) {
+  int rc = debug_buffers({{a.R > 0 ? a.freq : nullptr, (uint64_t)a.R * 2u},
+                          {a.R > 0 ? a.pos : nullptr, (uint64_t)a.axes * (uint64_t)a.rows * 4u},
+                          {a.wq, (uint64_t)a.D * 4u},
+                          {a.wk, (uint64_t)a.D * 4u},
+                          {a.dwq, (uint64_t)a.D * 4u},
+                          {a.dwk, (uint64_t)a.D * 4u}});
+  for (const HeadRows& t : tensors)
+    if (rc == FP4_OK && t.heads > 0)
+      rc = debug_buffers({{t.p, strided(a.rows, t.stride, t.heads * a.D) * elem_bytes(a.dtype)}});
+  return rc;
+}
+
+int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, int64_t q_stride, int64_t q_heads,
+                     const void* k, int64_t k_stride, int64_t k_heads, int64_t head_dim, int dtype,
+                     const float* q_weight, const float* k_weight, float eps, void* q_out, int64_t q_out_stride,
+                     void* k_out, int64_t k_out_stride, int64_t rows, void* stream) {
+  fp4::QkRope a{};
+  int rc = rope_check(rope, pos, rows, q_heads, k_heads, head_dim, dtype, q_weight, k_weight, eps, a);
+  if (rc != FP4_OK) return rc;
+  if (rows == 0 || q_heads + k_heads == 0) return FP4_OK;
+  const std::initializer_list<HeadRows> tensors = {
+      {q, q_stride, q_heads}, {k, k_stride, k_heads}, {q_out, q_out_stride, q_heads}, {k_out, k_out_stride, k_heads}};
+  if ((rc = head_rows_check(tensors, head_dim, dtype)) != FP4_OK) return rc;
+  if (debug_on() && (rc = rope_debug(a, tensors)) != FP4_OK) return rc;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.oq = q_out;
+  a.oq_stride = q_out_stride;
+  a.ok = k_out;
+  a.ok_stride = k_out_stride;
+  hipStream_t s = as_stream(stream);
+  return finish(launched(fp4::launch_qk_rope(a, s)), s);
+}
+
+size_t fp4_qk_norm_rope_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim) {
+  if (!qk_shape_ok(rows, q_heads, k_heads, head_dim)) return 0;
+  return fp4::qk_rope_workspace(rows, q_heads + k_heads, head_dim);
+}
+
+int fp4_qk_norm_rope_backward(const fp4_rope* rope, const int32_t* pos, const void* gq, int64_t gq_stride,
+                              const void* gk, int64_t gk_stride, const void* q, int64_t q_stride, int64_t q_heads,
+                              const void* k, int64_t k_stride, int64_t k_heads, int64_t head_dim, int dtype,
+                              const float* q_weight, const float* k_weight, float eps, void* dq, int64_t dq_stride,
+                              void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight, int64_t rows,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  fp4::QkRope a{};
+  int rc = rope_check(rope, pos, rows, q_heads, k_heads, head_dim, dtype, q_weight, k_weight, eps, a);
+  if (rc != FP4_OK) return rc;
+  if (q_heads + k_heads == 0) return FP4_OK;
+  if ((a.wq && !dq_weight) || (a.wk && !dk_weight)) return FP4_ERR_NULL;
+  a.dwq = a.wq ? dq_weight : nullptr;
+  a.dwk = a.wk ? dk_weight : nullptr;
+  if (!aligned(a.dwq, 4) || !aligned(a.dwk, 4)) return FP4_ERR_ALIGN;
+  // (Inputs are read where there is a weight to norm with.)
+  const std::initializer_list<HeadRows> tensors = {{gq, gq_stride, q_heads},          {gk, gk_stride, k_heads},
+                                                   {q, q_stride, a.wq ? q_heads : 0}, {k, k_stride, a.wk ? k_heads : 0},
+                                                   {dq, dq_stride, q_heads},          {dk, dk_stride, k_heads}};
+  if (rows > 0 && (rc = head_rows_check(tensors, head_dim, dtype)) != FP4_OK) return rc;
+  const size_t need = a.wq || a.wk ? fp4::qk_rope_workspace(rows, q_heads + k_heads, head_dim) : 0u;
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  if (rows == 0 && !a.wq && !a.wk) return FP4_OK;
+  if (debug_on()) {
+    if ((rc = rope_debug(a, tensors)) != FP4_OK) return rc;
+    if ((rc = debug_buffers({{need ? workspace : nullptr, need}})) != FP4_OK) return rc;
+  }
+  a.gq = gq;
+  a.gq_stride = gq_stride;
+  a.gk = gk;
+  a.gk_stride = gk_stride;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.k = k;
+  a.k_stride = k_stride;
+  a.oq = dq;
+  a.oq_stride = dq_stride;
+  a.ok = dk;
+  a.ok_stride = dk_stride;
+  a.workspace = workspace;
+  hipStream_t s = as_stream(stream);
+  return finish(launched(fp4::launch_qk_rope_backward(a, s)), s);
+}
+
+// ---- routing to experts ----
+
+constexpr int32_t kMaxEntryK = 64;  // entries of a token that rows are moved for
+
+static bool route_shape_ok(int64_t T, int64_t E, int32_t top_k, int64_t stride) {
+  return T >= 0 && T <= kMaxDim && T * 16 + 255 <= kMaxWorkItems && E >= 1 && E <= fp4::kMaxExperts && top_k >= 1 && top_k <= E &&
+         top_k <= fp4::kMaxRouteTopK && stride >= E && stride <= kMaxDim;
+}
+
+int fp4_moe_route(const void* logits, int dtype, int64_t stride, int64_t T, int64_t E, int32_t top_k, int renormalise,
+                  int32_t* ids, float* weights, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!route_shape_ok(T, E, top_k, stride)) return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (!logits || !ids || !weights) return FP4_ERR_NULL;
+  if (!aligned(logits, elem_bytes(dtype)) || !aligned(ids, 4) || !aligned(weights, 4)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t entries = (uint64_t)T * (uint64_t)top_k;
+    const int rc = debug_buffers(
+        {{logits, strided(T, stride, E) * elem_bytes(dtype)}, {ids, entries * 4u}, {weights, entries * 4u}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_route(logits, dtype, stride, T, E, top_k, renormalise != 0, ids, weights, s)),
+                s);
+}
+
+int fp4_moe_route_backward(const void* logits, int dtype, int64_t stride, int64_t T, int64_t E, int32_t top_k,
+                           int renormalise, const int32_t* ids, const float* g, void* dlogits, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!route_shape_ok(T, E, top_k, stride)) return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (!logits || !ids || !g || !dlogits) return FP4_ERR_NULL;
+  if (!aligned(logits, elem_bytes(dtype)) || !aligned(dlogits, elem_bytes(dtype)) || !aligned(ids, 4) ||
+      !aligned(g, 4))
+    return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t entries = (uint64_t)T * (uint64_t)top_k;
+    const int rc = debug_buffers({{logits, strided(T, stride, E) * elem_bytes(dtype)},
+                                  {ids, entries * 4u},
+                                  {g, entries * 4u},
+                                  {dlogits, (uint64_t)T * (uint64_t)E * elem_bytes(dtype)}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_route_backward(logits, dtype, stride, T, E, top_k, renormalise != 0, ids, g,
+                                                        dlogits, s)),
+                s);
+}
+
+static bool sort_shape_ok(int64_t T, int32_t top_k, int64_t E) {
+  return T >= 0 && T <= kMaxDim && top_k >= 0 && top_k <= kMaxEntryK && T * top_k <= kMaxDim && E >= 1 &&
+         E <= fp4::kMaxExperts;
+}
+
+size_t fp4_moe_sort_workspace(int64_t T, int32_t top_k, int64_t E) {
+  return sort_shape_ok(T, top_k, E) ? fp4::moe_sort_workspace(T * top_k, E) : 0u;
+}
+
+int fp4_moe_sort(const int32_t* ids, int64_t T, int32_t top_k, int64_t E, int32_t* group_off, int32_t* row_idx,
+                 int32_t* pos, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!sort_shape_ok(T, top_k, E)) return FP4_ERR_SHAPE;
+  const uint64_t entries = (uint64_t)T * (uint64_t)top_k;
+  if (!group_off || (entries > 0 && (!ids || !row_idx || !pos))) return FP4_ERR_NULL;
+  if (!aligned(ids, 4) || !aligned(group_off, 4) || !aligned(row_idx, 4) || !aligned(pos, 4)) return FP4_ERR_ALIGN;
+  const size_t need = fp4::moe_sort_workspace((int64_t)entries, E);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP4_ERR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const int rc = debug_buffers({{ids, entries * 4u},
+                                  {group_off, ((uint64_t)E + 1u) * 4u},
+                                  {row_idx, entries * 4u},
+                                  {pos, entries * 4u},
+                                  {need ? workspace : nullptr, need}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_sort(ids, T, top_k, E, group_off, row_idx, pos, workspace, s)), s);
+}
+
+// Sizes of a call that moves rows of H values between T tokens and `rows` rows.
+static bool rows_shape_ok(int dtype, int64_t T, int32_t top_k, int64_t H, int64_t rows, int64_t stride) {
+  if (T < 0 || T > kMaxDim || top_k < 0 || top_k > kMaxEntryK || T * top_k > kMaxDim || rows < 0 || rows > kMaxDim)
+    return false;
+  if (H < 1 || H > kMaxDim || H % per16(dtype) != 0 || stride < H || stride > kMaxDim) return false;
+  // One wave to 64 vectors of 16 bytes.
+  return T * ((H / per16(dtype) + 63) / 64) * 64 + 255 <= kMaxWorkItems;
+}
+
+int fp4_moe_gather(const void* x, int dtype, int64_t stride, const int32_t* pos, int64_t T, int32_t top_k, int64_t H,
+                   int64_t rows, void* out, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!rows_shape_ok(dtype, T, top_k, H, rows, stride)) return FP4_ERR_SHAPE;
+  if (T == 0 || top_k == 0 || rows == 0) return FP4_OK;
+  if (!x || !pos || !out) return FP4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(out, 16) || stride % per16(dtype) != 0 || !aligned(pos, 4)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const int rc = debug_buffers({{x, strided(T, stride, H) * elem_bytes(dtype)},
+                                  {pos, (uint64_t)T * (uint64_t)top_k * 4u},
+                                  {out, (uint64_t)rows * (uint64_t)H * elem_bytes(dtype)}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_gather(x, dtype, stride, pos, T, top_k, H, rows, out, s)), s);
+}
+
+int fp4_moe_combine(const void* y, int dtype, const int32_t* pos, const float* weights, int64_t T, int32_t top_k,
+                    int64_t H, int64_t rows, void* out, int64_t stride, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!rows_shape_ok(dtype, T, top_k, H, rows, stride)) return FP4_ERR_SHAPE;
+  if (T == 0) return FP4_OK;
+  if (!out || (rows > 0 && !y) || (top_k > 0 && !pos)) return FP4_ERR_NULL;
+  if (!aligned(y, 16) || !aligned(out, 16) || stride % per16(dtype) != 0 || !aligned(pos, 4) || !aligned(weights, 4))
+    return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t entries = (uint64_t)T * (uint64_t)top_k;
+    const int rc = debug_buffers({{y, (uint64_t)rows * (uint64_t)H * elem_bytes(dtype)},
+                                  {pos, entries * 4u},
+                                  {weights, entries * 4u},
+                                  {out, strided(T, stride, H) * elem_bytes(dtype)}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_combine(y, dtype, pos, weights, T, top_k, H, rows, out, stride, s)), s);
+}
+
+int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int dtype, const int32_t* pos,
+                             const float* weights, int64_t T, int32_t top_k, int64_t H, int64_t rows, void* dy,
+                             float* dweights, void* stream) {
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!rows_shape_ok(dtype, T, top_k, H, rows, stride)) return FP4_ERR_SHAPE;
+  if (T == 0 || top_k == 0) return FP4_OK;
+  if (!g || !pos || !weights || !dweights || (rows > 0 && (!y || !dy))) return FP4_ERR_NULL;
+  if (!aligned(g, 16) || !aligned(y, 16) || !aligned(dy, 16) || stride % per16(dtype) != 0 || !aligned(pos, 4) ||
+      !aligned(weights, 4) || !aligned(dweights, 4))
+    return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const uint64_t entries = (uint64_t)T * (uint64_t)top_k, all = (uint64_t)rows * (uint64_t)H * elem_bytes(dtype);
+    const int rc = debug_buffers({{g, strided(T, stride, H) * elem_bytes(dtype)},
+                                  {y, all},
+                                  {pos, entries * 4u},
+                                  {weights, entries * 4u},
+                                  {dy, all},
+                                  {dweights, entries * 4u}});
+    if (rc != FP4_OK) return rc;
+  }
+  return finish(launched(fp4::launch_moe_combine_backward(g, stride, y, dtype, pos, weights, T, top_k, H, rows, dy,
+                                                          dweights, s)),
+                s);
+}
+
+// ---- drafted tokens ----
+
+static bool verify_shape_ok(int64_t B, int64_t G, int64_t V) {
+  if (B < 0 || B > 65535 || G < 0 || G > 32 || V < 1 || V > (int64_t(1) << 24)) return false;
+  // A workgroup of 256 to every 4096 logits of a row drawn from.
+  return B * ((V + 4095) / 4096) * 256 <= kMaxWorkItems;
+}
+
+size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V) {
+  return verify_shape_ok(B, G, V) ? fp4::verify_workspace(B, G, V) : 0u;
+}
+
+int fp4_verify_drafts(const void* target, int64_t target_seq_stride, int64_t target_row_stride, const void* draft,
+                      int64_t draft_seq_stride, int64_t draft_row_stride, int dtype, int64_t B, int64_t G, int64_t V,
+                      const int32_t* tokens, const float* u, const float* temperature, int32_t* out,
+                      int32_t* accepted, float* chance, void* workspace, size_t workspace_bytes, void* stream) {
+  constexpr int64_t kMaxStride = int64_t(1) << 40;
+  if (!dtype_ok(dtype)) return FP4_ERR_DTYPE;
+  if (!verify_shape_ok(B, G, V)) return FP4_ERR_SHAPE;
+  if (G == 0) draft = nullptr;
+  for (const int64_t st : {target_seq_stride, target_row_stride, draft ? draft_seq_stride : 0, draft ? draft_row_stride : 0})
+    if (st < 0 || st > kMaxStride) return FP4_ERR_SHAPE;
+  if (B == 0) return FP4_OK;
+  if (!target || !u || !out || !accepted || (G > 0 && (!tokens || !chance))) return FP4_ERR_NULL;
+  if (!aligned(target, elem_bytes(dtype)) || !aligned(draft, elem_bytes(dtype)) || !aligned(tokens, 4) ||
+      !aligned(u, 4) || !aligned(temperature, 4) || !aligned(out, 4) || !aligned(accepted, 4) || !aligned(chance, 4))
+    return FP4_ERR_ALIGN;
+  const size_t need = fp4::verify_workspace(B, G, V);
+  if (!workspace || workspace_bytes < need) return FP4_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return FP4_ERR_ALIGN;
+  hipStream_t s = as_stream(stream);
+  if (debug_on()) {
+    const auto span = [&](int64_t rows, int64_t seq, int64_t row) {
+      return ((uint64_t)(B - 1) * (uint64_t)seq + (uint64_t)(rows - 1) * (uint64_t)row + (uint64_t)V) *
+             elem_bytes(dtype);
+    };
+    const uint64_t drafts = (uint64_t)B * (uint64_t)G * 4u, all = (uint64_t)B * (uint64_t)(G + 1) * 4u;
+    const int rc = debug_buffers({{target, span(G + 1, target_seq_stride, target_row_stride)},
+                                  {draft, draft ? span(G, draft_seq_stride, draft_row_stride) : 0u},
+                                  {tokens, drafts},
+                                  {u, all},
+                                  {temperature, (uint64_t)B * 4u},
+                                  {out, all},
+                                  {accepted, (uint64_t)B * 4u},
+                                  {chance, drafts},
+                                  {workspace, need}});
+    if (rc != FP4_OK) return rc;
+  }
+  fp4::Verify a{};
+  a.target = target;
+  a.target_seq = target_seq_stride;
+  a.target_row = target_row_stride;
+  a.draft = draft;
+  a.draft_seq = draft_seq_stride;
+  a.draft_row = draft_row_stride;
+  a.dtype = dtype;
+  a.B = B;
+  a.G = G;
+  a.V = V;
+  a.tokens = tokens;
+  a.u = u;
+  a.temperature = temperature;
+  a.out = out;
+  a.accepted = accepted;
+  a.chance = chance;
+  a.workspace = workspace;
+  return finish(launched(fp4::launch_verify(a, s)), s);
+}
+
 const char* fp4_status_string(int status) {
   switch (status) {
     case FP4_OK: return "FP4_OK";

@@ -156,4 +156,76 @@ hipError_t launch_logprobs_backward(const void* x, int dtype, int64_t stride, in
                                     const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride,
                                     hipStream_t stream);
 
+// Norms and rotary positions of queries and keys, and their gradient
+// (qk_rope.hip).  Strides in elements; R 0: no rotation.  axis: two bits for
+// each pair, pair i in bits 2 (i % 16) of word i / 16.
+struct QkRope {
+  const float* freq;
+  const int32_t* pos;
+  int64_t R;
+  int32_t axes;
+  bool interleaved;
+  uint32_t axis[8];
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* gq;
+  int64_t gq_stride;
+  const void* gk;
+  int64_t gk_stride;
+  void* oq;
+  int64_t oq_stride;
+  void* ok;
+  int64_t ok_stride;
+  int64_t hq, hk, D, rows;
+  int dtype;
+  const float* wq;
+  const float* wk;
+  float eps;
+  float* dwq;
+  float* dwk;
+  void* workspace;
+};
+size_t qk_rope_workspace(int64_t rows, int64_t heads, int64_t D);
+hipError_t launch_qk_rope(const QkRope& a, hipStream_t stream);
+hipError_t launch_qk_rope_backward(const QkRope& a, hipStream_t stream);
+
+// Routing to experts, and rows to their order and back (moe.hip).
+constexpr int64_t kMaxExperts = 512, kMaxRouteTopK = 16;
+hipError_t launch_moe_route(const void* x, int dtype, int64_t stride, int64_t T, int64_t E, int32_t k,
+                            bool renormalise, int32_t* ids, float* weights, hipStream_t stream);
+hipError_t launch_moe_route_backward(const void* x, int dtype, int64_t stride, int64_t T, int64_t E, int32_t k,
+                                     bool renormalise, const int32_t* ids, const float* g, void* dx,
+                                     hipStream_t stream);
+size_t moe_sort_workspace(int64_t entries, int64_t E);
+hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int32_t k, int64_t E, int32_t* group_off, int32_t* row_idx,
+                           int32_t* pos, void* workspace, hipStream_t stream);
+hipError_t launch_moe_gather(const void* x, int dtype, int64_t stride, const int32_t* pos, int64_t T, int32_t k,
+                             int64_t H, int64_t rows, void* out, hipStream_t stream);
+hipError_t launch_moe_combine(const void* y, int dtype, const int32_t* pos, const float* weights, int64_t T, int32_t k,
+                              int64_t H, int64_t rows, void* out, int64_t stride, hipStream_t stream);
+hipError_t launch_moe_combine_backward(const void* g, int64_t stride, const void* y, int dtype, const int32_t* pos,
+                                       const float* weights, int64_t T, int32_t k, int64_t H, int64_t rows, void* dy,
+                                       float* dw, hipStream_t stream);
+
+// Verification of drafted tokens (verify.hip).
+struct Verify {
+  const void* target;
+  int64_t target_seq, target_row;  // elements between sequences, and between a sequence's rows
+  const void* draft;               // NULL: tokens drafted without a distribution
+  int64_t draft_seq, draft_row;
+  int dtype;
+  int64_t B, G, V;
+  const int32_t* tokens;
+  const float* u;
+  const float* temperature;
+  int32_t* out;
+  int32_t* accepted;
+  float* chance;
+  void* workspace;
+};
+size_t verify_workspace(int64_t B, int64_t G, int64_t V);
+hipError_t launch_verify(const Verify& a, hipStream_t stream);
+
 }  // namespace fp4

@@ -568,6 +568,164 @@ int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, i
                           const int32_t* tokens, int32_t M, const float* lse, const float* entropy,
                           const float* g_logp, const float* g_entropy, void* dx, int64_t dx_stride, void* stream);
 
+/* ---- Between the projections and the cache: norms of queries and keys for
+ * each head, and rotary positions. ---- */
+
+/* Pairs of values (2i, 2i + 1) are turned; otherwise (i, i + rot_dim / 2). */
+#define FP4_ROPE_INTERLEAVED 1u
+/* Several axes take the pairs in turns (0, 1, 2, 0, 1, 2, ...; one whose section
+ * is used up is passed over); otherwise axis 0 the first sections[0] pairs, axis 1
+ * the next, and so on. */
+#define FP4_ROPE_CYCLIC 2u
+
+/* Rotary positions (a host struct).  Pair i of a head's first rot_dim values is
+ * turned by the angle pos[axis(i)] * freq[i], worked out in FP64. */
+typedef struct fp4_rope {
+    const float* freq;   /* device, rot_dim / 2 radians a position           */
+    int32_t rot_dim;     /* a multiple of 8, 0 (no rotation) to head_dim     */
+    int32_t axes;        /* 1 to 4 (e.g. 3: time, height, width)             */
+    int32_t sections[4]; /* pairs of each axis, rot_dim / 2 together (axes > 1) */
+    uint32_t flags;      /* FP4_ROPE_INTERLEAVED, FP4_ROPE_CYCLIC            */
+} fp4_rope;
+
+/* For every row and head of q and k, with x its head_dim values:
+ *   y = x * (mean x^2 + eps)^-1/2 * weight   (weight NULL: y = x),
+ * then the rotation, (a, b) -> (a cos - b sin, b cos + a sin); FP32
+ * throughout, rounded once to dtype.
+ *   q, k: `rows` rows of q_heads (k_heads) x head_dim values of dtype, row i at
+ *   element i * q_stride (k_stride), the heads dense within a row; outputs
+ *   likewise.  16-byte aligned, strides multiples of 16 bytes and no less
+ *   than a row.  An output may be its input (same address and stride); it must
+ *   not overlap an input otherwise.  Either may have no heads.
+ *   head_dim: a multiple of 8 from 32 to 256.  q_weight, k_weight: head_dim FP32
+ *   or NULL.  eps >= 0.  pos: device int32, axes x rows, dense, any values.
+ *   rope NULL: no rotation.
+ * rows == 0 is a no-op. */
+int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, int64_t q_stride, int64_t q_heads,
+                     const void* k, int64_t k_stride, int64_t k_heads, int64_t head_dim, int dtype,
+                     const float* q_weight, const float* k_weight, float eps, void* q_out, int64_t q_out_stride,
+                     void* k_out, int64_t k_out_stride, int64_t rows, void* stream);
+
+/* Workspace bytes of fp4_qk_norm_rope_backward (0: none needed, also for
+ * invalid arguments).  It holds no control words: no zero-fill needed. */
+size_t fp4_qk_norm_rope_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim);
+
+/* Gradient of fp4_qk_norm_rope: from the gradients gq, gk of its outputs and
+ * its inputs q, k (strided as there), dq and dk (of dtype, rounded once) and,
+ * of each weight given, its gradient dq_weight, dk_weight (head_dim FP32,
+ * required; sums over rows and heads in a fixed order; 0 for rows == 0).  q (k)
+ * is not read without its weight.  dq may be gq or q, dk gk or k. */
+int fp4_qk_norm_rope_backward(const fp4_rope* rope, const int32_t* pos, const void* gq, int64_t gq_stride,
+                              const void* gk, int64_t gk_stride, const void* q, int64_t q_stride, int64_t q_heads,
+                              const void* k, int64_t k_stride, int64_t k_heads, int64_t head_dim, int dtype,
+                              const float* q_weight, const float* k_weight, float eps, void* dq, int64_t dq_stride,
+                              void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight, int64_t rows,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Around fp4_gemm_grouped: the choice of experts, the tokens' order by
+ * expert, and rows there and back. ---- */
+
+/* The top_k largest logits of each token, in order (ties to the lowest expert,
+ * NaN above all, +0 equal to -0), and their weights: the softmax over the
+ * chosen logits (renormalise != 0), or the softmax over all experts at them.
+ * FP32.  A logit of -inf has weight 0 (a row of them only: all weights 0); a NaN
+ * or +inf logit makes weights of the row NaN.
+ *   logits: T rows of E values of dtype, row t at element t * stride, aligned
+ *   to its element size.  1 <= top_k <= min(E, 16); E <= 512.  ids (int32),
+ *   weights (FP32): T x top_k, dense.
+ * T == 0 is a no-op. */
+int fp4_moe_route(const void* logits, int dtype, int64_t stride, int64_t T, int64_t E, int32_t top_k, int renormalise,
+                  int32_t* ids, float* weights, void* stream);
+
+/* Gradient of fp4_moe_route's weights with respect to the logits, given the ids
+ * it returned and the weights' gradient g (T x top_k FP32):
+ *   dlogits_e = p_e (G_e - sum_i p_i G_i),
+ * p the softmax over the chosen experts (renormalise; 0 elsewhere) or over all,
+ * G_e the sum of g at e's places in ids.  dlogits: T x E of dtype, dense, every
+ * element written.  Ids outside [0, E) count for nothing. */
+int fp4_moe_route_backward(const void* logits, int dtype, int64_t stride, int64_t T, int64_t E, int32_t top_k,
+                           int renormalise, const int32_t* ids, const float* g, void* dlogits, void* stream);
+
+/* Workspace bytes of fp4_moe_sort (0: none needed, also for invalid
+ * arguments).  No zero-fill needed. */
+size_t fp4_moe_sort_workspace(int64_t T, int32_t top_k, int64_t E);
+
+/* The T * top_k entries of ids (T x top_k, device int32) in the order of their
+ * experts, equal ids in the order of the entries:
+ *   group_off (int32, E + 1) and row_idx (int32, T * top_k: the token of every
+ *   row) as fp4_gemm_grouped takes them;
+ *   pos (int32, T x top_k): the row of every entry.
+ * An entry whose id is outside [0, E) (-1 pads a batch) is taken by no expert:
+ * its row r lies behind all the others and pos has -1 - r.  So that group_off[E]
+ * is T * top_k, those rows count to the last group; the calls below leave
+ * them out.
+ *   1 <= E <= 512, 0 <= top_k <= 64, T * top_k <= 2^30. */
+int fp4_moe_sort(const int32_t* ids, int64_t T, int32_t top_k, int64_t E, int32_t* group_off, int32_t* row_idx,
+                 int32_t* pos, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Rows in expert order: out[r] = x[t] for every entry (t, j), r = pos[t,j] (or
+ * -1 - pos[t,j] where that is negative: every row is written).
+ *   x: T rows of H values of dtype, row t at element t * stride; out: `rows` rows
+ *   of H, dense.  16-byte aligned, H and stride multiples of 16 bytes.  An entry
+ *   whose r is no row (r >= rows) is skipped; two entries for one row race.
+ *   0 <= top_k <= 64.  Its gradient is fp4_moe_combine without weights.
+ * T == 0 is a no-op. */
+int fp4_moe_gather(const void* x, int dtype, int64_t stride, const int32_t* pos, int64_t T, int32_t top_k, int64_t H,
+                   int64_t rows, void* out, void* stream);
+
+/* Rows joined back: out[t] = sum_j weights[t,j] * y[pos[t,j]], j in order, FP32
+ * sums, rounded once to dtype.  Entries with pos outside [0, rows) count for
+ * nothing (a token without any: 0).  weights: T x top_k FP32, or NULL for 1.
+ *   y: `rows` rows of H values of dtype, dense; out: T rows of H, row t at element
+ *   t * stride.  Alignment as above.  out must not overlap y.
+ * T == 0 is a no-op. */
+int fp4_moe_combine(const void* y, int dtype, const int32_t* pos, const float* weights, int64_t T, int32_t top_k,
+                    int64_t H, int64_t rows, void* out, int64_t stride, void* stream);
+
+/* Gradient of fp4_moe_combine (with weights) from that of its output, g (T rows
+ * of H values of dtype, row t at element t * stride): dy[pos[t,j]] =
+ * weights[t,j] * g[t] (rows of dtype, dense), dweights[t,j] = g[t] . y[pos[t,j]]
+ * (T x top_k FP32).  An entry that no expert takes (pos negative) has dweights 0
+ * and its row -1 - pos in dy zeros; one that names no row of y has dweights 0.
+ * dy must not overlap y or g. */
+int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int dtype, const int32_t* pos,
+                             const float* weights, int64_t T, int32_t top_k, int64_t H, int64_t rows, void* dy,
+                             float* dweights, void* stream);
+
+/* ---- Behind the head: drafted tokens. ---- */
+
+/* Workspace bytes of fp4_verify_drafts (0 for invalid arguments).  No
+ * zero-fill needed. */
+size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V);
+
+/* Verify up to G drafted tokens of each of B sequences against the target's
+ * distribution, from given random numbers.  p_i, q_i: the softmaxes of the
+ * target's and the draft's logits of position i over the sequence's temperature.
+ *   tokens[b,i] is kept while u[b,i] * q_i(token) < p_i(token).  At the first
+ *   position i that is not kept one token is drawn from max(p_i - q_i, 0) (from
+ *   p_i where that is 0 everywhere), past the last draft (i = G, or a token
+ *   outside [0, V), which ends a sequence's drafts) from p_i: the smallest t with
+ *   sum_{s <= t} r_s > u[b,G] * sum_s r_s.
+ *   draft NULL: q_i is 1 at tokens[b,i] (drafts that were not drawn).
+ *   temperature[b] (FP32, or NULL for 1) 0, below or NaN: greedy; a token is kept
+ *   if it is p_i's largest logit (ties to the lowest), else that one is emitted.
+ *   out (int32 B x (G + 1)): the drafts kept, the token drawn, then -1.
+ *   accepted (int32 B): the number of drafts kept.  chance (FP32 B x G): the
+ *   probability of keeping each draft were it reached, min(1, p_i / q_i); 0
+ *   where there is none.
+ *   A target row without a distribution (a NaN or +inf logit, or all -inf) ends
+ *   the drafts before it and draws nothing (-1); with such a draft row a token
+ *   is never kept, and q_i counts as 0.
+ *   target: B x (G + 1) rows, draft: B x G rows of V values of dtype, row i of
+ *   sequence b at element b * seq_stride + i * row_stride, aligned to the element
+ *   size.  tokens: int32 B x G, u: FP32 B x (G + 1), in [0, 1), dense.
+ *   0 <= G <= 32, 1 <= V <= 2^24.  Exponentials and sums in FP64.
+ * B == 0 is a no-op. */
+int fp4_verify_drafts(const void* target, int64_t target_seq_stride, int64_t target_row_stride, const void* draft,
+                      int64_t draft_seq_stride, int64_t draft_row_stride, int dtype, int64_t B, int64_t G, int64_t V,
+                      const int32_t* tokens, const float* u, const float* temperature, int32_t* out,
+                      int32_t* accepted, float* chance, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static string naming a status code. */
 const char* fp4_status_string(int status);
 
