@@ -1301,9 +1301,9 @@ def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
 
 # ---- drafted tokens -------------------------------------------------------------
 def verify_workspace(batch, drafts, vocab, device="cuda"):
-    """A workspace tensor for verify_drafts."""
+    """A zero-filled workspace tensor for verify_drafts (or None)."""
     n = fp4_verify_drafts_workspace(batch, drafts, vocab)
-    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+    return _torch().zeros(n, dtype=_torch().uint8, device=device) if n else None
 
 
 def _want_logits(t, name, rows, device=None, like=None):

@@ -10,8 +10,10 @@
 // FP32's 2^-24 would move one draw in a hundred at V = 131072.  2^z from a table
 // of 2^(j / 256) and a cubic (relative error 2e-13).
 //
-// Three launches: the sums of every row's splits; of the row drawn from, the
-// sums of chunks of r; and the token, found among the chunks, then within one.
+// Two launches.  The sums of every row's parts, a wave each: the last workgroup of
+// a sequence to arrive joins them and decides.  Then, of the row drawn from, the
+// sums of chunks of r, a wave each: the last workgroup to arrive finds the token
+// among the chunks, and within one.
 #include "fp4_device.h"
 #include "fp4_launch.h"
 
@@ -21,20 +23,19 @@ namespace fp4 {
 namespace {
 
 constexpr uint32_t kThreads = 256, kWaves = 4;
-constexpr uint32_t kTable = 256;              // 2^(j / 256)
-constexpr uint32_t kRounds = 16;              // tokens of a chunk a thread has
-constexpr uint32_t kChunk = kThreads * kRounds;
-constexpr uint32_t kMaxSplits = 64, kMaxDrafts = 32;
+constexpr uint32_t kRounds = 8;               // tokens of a chunk a lane has
+constexpr uint32_t kChunk = 64u * kRounds;
+constexpr uint32_t kMaxSplits = 32;           // workgroups of a row
+constexpr uint32_t kLaneParts = kMaxSplits * kWaves / 64u;  // a row's parts that a lane joins
+constexpr uint32_t kMaxDrafts = 32;
+constexpr int64_t kWantedGroups = 2048, kWantedWaves = 4096;
 constexpr double kLog2e = 1.4426950408889634074;
 
-// A split's part of a row: sum of 2^(c (x - r)) / 256, r a logit; the largest
-// logit's key where the sequence is greedy.
+// A wave's part of a row: the sum of 2^(c (x - r) / 256), r a logit; where the
+// sequence is greedy, the largest logit's key.
 struct Part {
-  double sum;
-  float r;
-  uint32_t bad;  // a NaN or +inf
-  uint64_t key;
-  uint64_t unused;
+  uint64_t value;   // the sum's bits, or the key
+  uint64_t r_bad;   // r's bits; above them, whether there is a NaN
 };
 
 // What the draw needs of the row drawn from.
@@ -49,9 +50,11 @@ constexpr int32_t kQNone = -1, kQDraft = -2, kNoDraw = -3;
 struct Args {
   Verify v;
   uint32_t B, G, V, rows, splits, chunks;
-  Part* parts;     // B x rows x splits; rows: G + 1 of the target, G of the draft
-  double* sums;    // B x chunks
-  Chosen* chosen;  // B
+  uint32_t per, groups;  // chunks of a wave, and workgroups of a sequence, in the draw
+  Part* parts;       // B x rows x splits x kWaves; rows: G + 1 of the target, G of the draft
+  double* sums;      // B x chunks
+  Chosen* chosen;    // B
+  uint32_t* arrived; // 2 x B counters, zero before and after each call
 };
 
 template <int DT>
@@ -76,41 +79,87 @@ __device__ __forceinline__ uint64_t order_key(float v, uint32_t i) {
   return ((uint64_t)((u & 0x80000000u) ? ~u : u | 0x80000000u) << 32) | (uint32_t)~i;
 }
 
-// 256 log2 e / temperature; 0 where the sequence is greedy.
+// 256 log2 e / temperature; -1 where the sequence is greedy.
 __device__ __forceinline__ double units_of(const Args& a, uint32_t b) {
   const float t = a.v.temperature ? a.v.temperature[b] : 1.0f;
-  return t > 0.0f ? (double)kTable * kLog2e / (double)t : -1.0;
+  return t > 0.0f ? 256.0 * kLog2e / (double)t : -1.0;
 }
 
-__device__ __forceinline__ void fill_table(double (&table)[kTable]) {
-  table[threadIdx.x] = exp2((double)threadIdx.x / (double)kTable);
+// 2^(j / 256), less j in the upper word's bits from 12 on: with k << 12 added
+// there, entry k % 256 gives 2^(k / 256) at once.
+constexpr uint32_t kTable = 256;
+struct Table {
+  uint64_t v[kTable];
+};
+constexpr Table make_table() {
+  Table t{};
+  for (uint32_t j = 0; j < kTable; ++j) {
+    const double x = 0.69314718055994530942 * j / kTable;
+    double sum = 0.0;
+    for (int n = 1; n < 24; ++n) {  // e^x - 1, the small terms first
+      double p = 1.0;
+      for (int m = 24 - n; m > 0; --m) p *= x / m;
+      sum += p;
+    }
+    t.v[j] = __builtin_bit_cast(uint64_t, 1.0 + sum) - ((uint64_t)j << 44);
+  }
+  return t;
+}
+__constant__ const Table kPowers = make_table();
+typedef u32x2 Powers[kTable];
+
+// 2^(k / 256).
+__device__ __forceinline__ double power(const Powers& table, uint32_t k) {
+  const u32x2 e = table[k & (kTable - 1u)];
+  return __builtin_bit_cast(double, u32x2{e[0], e[1] + (k << 12)});
+}
+
+__device__ __forceinline__ void fill_table(Powers& table) {
+  static_assert(kTable == kThreads, "a thread fills one entry");
+  table[threadIdx.x] = __builtin_bit_cast(u32x2, kPowers.v[threadIdx.x]);
   __syncthreads();
 }
-static_assert(kTable == kThreads, "a thread fills one entry");
+
+// 2^(f / 256) = 1 + kC1 f + kC2 f^2 + kC3 f^3 for |f| <= 1/2.
+constexpr double kC1 = 0.69314718055994530942 / kTable, kC2 = kC1 * kC1 / 2.0, kC3 = kC1 * kC1 * kC1 / 6.0;
 
 // 2^(y / 256), y <= 256 * 512; below -256 * 1000, and for a NaN, 2^-1000.
-__device__ __forceinline__ double exp_units(double y, const double (&table)[kTable]) {
+__device__ __forceinline__ double exp_units(double y, const Powers& table) {
   constexpr double kRound = 0x1.8p52;  // its last place is 1
-  constexpr double kC1 = 0.69314718055994530942 / kTable, kC2 = kC1 * kC1 / 2.0, kC3 = kC1 * kC1 * kC1 / 6.0;
   y = __builtin_fmax(y, -256.0 * 1000.0);
   const double t = y + kRound;
-  const int32_t k = (int32_t)(uint32_t)__builtin_bit_cast(uint64_t, t);
   const double f = y - (t - kRound);
   const double p = f * __builtin_fma(f, __builtin_fma(f, kC3, kC2), kC1);
-  const double e = table[(uint32_t)k & (kTable - 1u)];
-  const uint64_t v = __builtin_bit_cast(uint64_t, __builtin_fma(e, p, e));
-  return __builtin_bit_cast(double, v + ((uint64_t)(uint32_t)((k >> 8) << 20) << 32));
+  const double e = power(table, (uint32_t)__builtin_bit_cast(uint64_t, t));
+  return __builtin_fma(e, p, e);
 }
 // The same, 0 below.
-__device__ __forceinline__ double weight(float x, float r, double c, const double (&table)[kTable]) {
+__device__ __forceinline__ double weight(float x, float r, double c, const Powers& table) {
   const double y = ((double)x - (double)r) * c, v = exp_units(y, table);
   return y > -256.0 * 1000.0 ? v : 0.0;
 }
 
+// Sum over the wavefront, in every lane and in a fixed order: rotations inside
+// each row of 16 lanes (DPP), then the four rows' results.
+template <int CTRL>
+__device__ __forceinline__ double ror(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double from_lane(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  v += ror<0x121>(v);
+  v += ror<0x122>(v);
+  v += ror<0x124>(v);
+  v += ror<0x128>(v);
+  return (from_lane(v, 0) + from_lane(v, 16)) + (from_lane(v, 32) + from_lane(v, 48));
 }
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
 #pragma unroll
@@ -121,123 +170,29 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
   return v;
 }
 
-// ---- the rows' sums ----------------------------------------------------------
-struct Running {
-  double sum;
-  float r;  // reference, moved when a logit passes it by 2^500
-  bool bad;
-  uint64_t key;
-};
-
-template <int N>
-__device__ __forceinline__ void take(Running& a, const float (&v)[N], double c, float c32,
-                                     const double (&table)[kTable]) {
-  float m = v[0];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    m = fmaxf(m, v[i]);
-    a.bad |= v[i] != v[i];
-  }
-  if ((m - a.r) * c32 > 256.0f * 500.0f || a.r == -INFINITY) {
-    a.sum = a.r == -INFINITY ? 0.0 : a.sum * weight(a.r, m, c, table);
-    a.r = m;
-  }
-  const double r = (double)a.r;
-#pragma unroll
-  for (int i = 0; i < N; ++i) a.sum += exp_units(((double)v[i] - r) * c, table);
+// What one workgroup hands to another is written through to the coherence point,
+// and read from there.
+template <typename T>
+__device__ __forceinline__ void put(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-
-template <int N>
-__device__ __forceinline__ void take_best(Running& a, const float (&v)[N], uint32_t i0) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    a.bad |= v[i] != v[i];
-    const uint64_t k = order_key(v[i], i0 + i);
-    a.key = k > a.key ? k : a.key;
-  }
+template <typename T>
+__device__ __forceinline__ T get(const T* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void stats_kernel(Args a) {
-  constexpr uint32_t E = 16u / kSize<DT>, U = 4u;
-  __shared__ double table[kTable];
-  __shared__ Running part[kWaves];
-  const uint32_t split = blockIdx.x % a.splits, n = blockIdx.x / a.splits, b = n / a.rows, row = n - b * a.rows;
-  const double c = units_of(a, b);
-  const bool greedy = c < 0.0;
-  if (greedy && row > a.G) return;  // the draft's distribution is not asked for
-  fill_table(table);
-  const uint8_t* p = row_at<DT>(a, b, row);
-  // Blocks of 16 bytes that lie wholly in the row, and the elements beside them.
-  const uint32_t head = min((uint32_t)(-reinterpret_cast<intptr_t>(p) & 15) / kSize<DT>, a.V);
-  const uint32_t blocks = (a.V - head) / E;
-  const uint32_t b0 = (uint32_t)((uint64_t)blocks * split / a.splits);
-  const uint32_t b1 = (uint32_t)((uint64_t)blocks * (split + 1u) / a.splits);
-  const u32x4* from = reinterpret_cast<const u32x4*>(p + (size_t)head * kSize<DT>);
-  const float c32 = (float)c;
-  Running s{0.0, -INFINITY, false, 0ull};
-  const auto one = [&](const u32x4& w, uint32_t j) __attribute__((always_inline)) {
-    float v[E];
-    if constexpr (DT == kDtF32) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = u2f(w[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = u2f(w[i] << 16);
-        v[2 * i + 1] = u2f(w[i] & 0xFFFF0000u);
-      }
-    }
-    if (greedy)
-      take_best(s, v, head + j * E);
-    else
-      take(s, v, c, c32, table);
-  };
-  uint32_t j = b0 + threadIdx.x;
-  for (; j + (U - 1u) * kThreads < b1; j += U * kThreads) {
-    u32x4 w[U];
-#pragma unroll
-    for (uint32_t u = 0; u < U; ++u) w[u] = from[j + u * kThreads];
-#pragma unroll
-    for (uint32_t u = 0; u < U; ++u) one(w[u], j + u * kThreads);
-  }
-  for (; j < b1; j += kThreads) one(from[j], j);
-  // The elements before the first block and behind the last: split 0's threads.
-  const uint32_t tail = head + blocks * E;
-  if (split == 0u && threadIdx.x < head + (a.V - tail)) {
-    const uint32_t i = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
-    const float v[1] = {logit<DT>(p, i)};
-    if (greedy)
-      take_best(s, v, i);
-    else
-      take(s, v, c, c32, table);
-  }
-  // Joined over the workgroup.
-  const float r = wave_fmax(s.r);
-  double sum = s.r == -INFINITY ? 0.0 : s.r == r ? s.sum : s.sum * weight(s.r, r, c, table);
-  sum = wave_sum(sum);
-  const uint64_t key = wave_max(s.key);
-  const bool bad = __ballot(s.bad) != 0ull;
-  if ((threadIdx.x & 63u) == 0u) {
-    Running& w = part[threadIdx.x >> 6];
-    w.r = r;
-    w.sum = sum;
-    w.bad = bad;
-    w.key = key;
+// Whether this workgroup is the last of n to come here (which resets the counter).
+__device__ __forceinline__ bool last_of(uint32_t* arrived, uint32_t n, uint32_t& flag) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's results have reached the coherence point
+  __syncthreads();
+  if (threadIdx.x == 0u) {
+    const uint32_t before = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    flag = before == n - 1u;
+    if (flag) put(arrived, 0u);
   }
   __syncthreads();
-  if (threadIdx.x != 0u) return;
-  Part out{};
-  out.r = fmaxf(fmaxf(part[0].r, part[1].r), fmaxf(part[2].r, part[3].r));
-  for (uint32_t w = 0; w < kWaves; ++w) {
-    if (part[w].r != -INFINITY) out.sum += part[w].sum * weight(part[w].r, out.r, c, table);
-    out.bad |= part[w].bad ? 1u : 0u;
-    out.key = part[w].key > out.key ? part[w].key : out.key;
-  }
-  a.parts[(size_t)n * a.splits + split] = out;
+  return flag != 0u;
 }
 
-// ---- the decision ------------------------------------------------------------
 struct RowSum {
   double inv;  // 1 / sum of the row
   float r;
@@ -245,133 +200,335 @@ struct RowSum {
   uint32_t best;
 };
 struct Shared {
-  double table[kTable];
+  Powers table;
   RowSum row[2 * kMaxDrafts + 1];
-  Chosen chosen;
-  double part[kRounds * kWaves];
-  uint32_t found;
+  uint32_t flag;
+};
+struct Running {
+  double sum;
+  float r;
+  bool bad;
+  uint64_t key;
 };
 
-// Every row's sum, a wave a row, a lane a split.
-__device__ __forceinline__ void join_rows(const Args& a, Shared& sh, uint32_t b, double c) {
-  const uint32_t lane = threadIdx.x & 63u;
-  for (uint32_t row = threadIdx.x >> 6; row < a.rows; row += kWaves) {
-    if (c < 0.0 && row > a.G) break;
-    Part p{};
-    p.r = -INFINITY;
-    if (lane < a.splits) p = a.parts[((size_t)b * a.rows + row) * a.splits + lane];
-    const float r = wave_fmax(p.r);
-    const double sum = wave_sum(p.r == -INFINITY ? 0.0 : p.sum * weight(p.r, r, c, sh.table));
-    const uint64_t key = wave_max(p.key);
-    const bool bad = __ballot(p.bad != 0u) != 0ull;
-    if (lane == 0u) {
-      RowSum& s = sh.row[row];
-      s.inv = 1.0 / sum;
-      s.r = r;
-      s.best = ~(uint32_t)key;
-      const uint32_t top = (uint32_t)(key >> 32);  // the keys of -inf and +inf bound those of finite values
-      s.ok = !bad && (c < 0.0 ? top > 0x007FFFFFu && top < 0xFF800000u : r > -INFINITY && r < INFINITY);
-    }
+// ---- the rows' sums ----------------------------------------------------------
+// A wave's sum against a reference r that its lanes share, moved (to the lanes'
+// largest logit) when a logit passes it by 2^500.  Of each logit, with R the
+// whole number nearest c r:
+//   t = c x - R to the nearest whole number, f = c x - R - t,
+// both from an FMA's exact product.  Logits far below r are first raised to one
+// whose term is 2^-900.  Where |c r| reaches 2^38 (a temperature near 0) and where
+// c vanishes, differences come first instead.
+struct WaveSum {
+  static constexpr double kRound = 0x1.8p52;
+  double sum = 0.0, c, shift = 0.0;  // shift: kRound - R
+  float r = -INFINITY, passes, low = 0.0f, c_passes;
+  bool fast = false, bad = false;
+
+  __device__ __forceinline__ explicit WaveSum(double c_) : c(c_), passes(-INFINITY) {
+    c_passes = (float)(256.0 * 500.0 / c_);
   }
-  __syncthreads();
-}
-
-// Decides over a sequence's drafts (wave 0, a lane a position) and, in its first
-// workgroup, writes all but a drawn token.
-template <int DT>
-__device__ __forceinline__ void decide(const Args& a, Shared& sh, uint32_t b, double c, bool first) {
-  const bool greedy = c < 0.0;
-  const int32_t* tokens = a.v.tokens + (size_t)b * a.G;
-  if (threadIdx.x < 64u) {
-    const uint32_t i = threadIdx.x;
-    bool keep = false;
-    double odds = 0.0;
-    int32_t d = -1;
-    if (i < a.G) {
-      d = tokens[i];
-      const RowSum& p = sh.row[i];
-      if (p.ok && (uint32_t)d < a.V) {
-        if (greedy) {
-          keep = (uint32_t)d == p.best;
-          odds = keep ? 1.0 : 0.0;
-        } else {
-          const double pd = weight(logit<DT>(row_at<DT>(a, b, i), (uint32_t)d), p.r, c, sh.table) * p.inv;
-          double qd = 1.0;
-          bool ok = true;
-          if (a.v.draft) {
-            const RowSum& q = sh.row[a.G + 1u + i];
-            ok = q.ok;
-            if (ok) qd = weight(logit<DT>(row_at<DT>(a, b, a.G + 1u + i), (uint32_t)d), q.r, c, sh.table) * q.inv;
-          }
-          if (ok) {
-            keep = (double)a.v.u[(size_t)b * (a.G + 1u) + i] * qd < pd;
-            odds = pd >= qd ? (pd > 0.0 ? 1.0 : 0.0) : pd / qd;
-          }
-        }
-      }
-    }
-    const uint32_t n = (uint32_t)__builtin_ctzll(__ballot(!keep));  // drafts kept (lane G keeps none)
-    if (first) {
-      if (i < a.G) a.v.chance[(size_t)b * a.G + i] = (float)odds;
-      const int32_t last = greedy && sh.row[n].ok ? (int32_t)sh.row[n].best : -1;
-      if (i <= a.G) a.v.out[(size_t)b * (a.G + 1u) + i] = i < n ? d : i == n ? last : -1;
-      if (i == 0u) a.v.accepted[b] = (int32_t)n;
-    }
-    if (i == 0u) {
-      const RowSum& p = sh.row[n];
-      Chosen& s = sh.chosen;
-      s.row = n;
-      s.inv_p = p.inv;
-      s.rp = p.r;
-      s.q = kQNone;
-      if (n < a.G && (uint32_t)tokens[n] < a.V) {
-        if (!a.v.draft) {
-          s.q = tokens[n];
-        } else if (!greedy && sh.row[a.G + 1u + n].ok) {
-          s.q = kQDraft;
-          s.inv_q = sh.row[a.G + 1u + n].inv;
-          s.rq = sh.row[a.G + 1u + n].r;
-        }
-      }
-      if (!p.ok || greedy) s.q = kNoDraw;
-      if (first) a.chosen[b] = s;
-    }
+  // Factor from sums against R to sums against r.
+  __device__ __forceinline__ double rest(const Powers& table) const {
+    return fast ? exp_units(__builtin_fma(-(double)r, c, kRound - shift), table) : 1.0;
   }
-  __syncthreads();
-}
-
-// r of token t.
-template <int DT>
-__device__ __forceinline__ double residual(const Args& a, const Chosen& s, const uint8_t* p, const uint8_t* q,
-                                           uint32_t t, double c, const double (&table)[kTable]) {
-  if (t >= a.V) return 0.0;
-  const double w = weight(logit<DT>(p, t), s.rp, c, table) * s.inv_p;
-  if (s.q == kQNone) return w;
-  const double o = s.q == kQDraft ? weight(logit<DT>(q, t), s.rq, c, table) * s.inv_q : (uint32_t)s.q == t ? 1.0 : 0.0;
-  return w > o ? w - o : 0.0;
-}
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void sums_kernel(Args a) {
-  __shared__ Shared sh;
-  const uint32_t chunk = blockIdx.x % a.chunks, b = blockIdx.x / a.chunks;
-  const double c = units_of(a, b);
-  if (c < 0.0 && chunk != 0u) return;
-  fill_table(sh.table);
-  join_rows(a, sh, b, c);
-  decide<DT>(a, sh, b, c, chunk == 0u);
-  const Chosen s = sh.chosen;
-  if (s.q == kNoDraw) return;
-  const uint8_t* p = row_at<DT>(a, b, s.row);
-  const uint8_t* q = s.q == kQDraft ? row_at<DT>(a, b, a.G + 1u + s.row) : nullptr;
-  double sum = 0.0;
+  __device__ __forceinline__ void move(float m, const Powers& table) {
+    bad |= m != m;
+    m = wave_fmax(m);  // (a NaN left out)
+    if (!(m > r)) return;
+    if (r != -INFINITY) sum *= rest(table) * weight(r, m, c, table);
+    r = m;
+    passes = r + c_passes;
+    const double rc = (double)r * c;
+    fast = c > 1e-30 && __builtin_fabs(rc) < 0x1p38;
+    if (!fast) return;
+    shift = kRound - __builtin_rint(rc);
+    low = (float)((double)r - 256.0 * 900.0 / c);  // (FP32's rounding is 2^14 of those units at most)
+  }
+  template <int N>
+  __device__ __forceinline__ void add_fast(const float (&v)[N], const Powers& table) {
+    double f[N], e[N];
 #pragma unroll
-  for (uint32_t r = 0; r < kRounds; ++r)
-    sum += residual<DT>(a, s, p, q, chunk * kChunk + r * kThreads + threadIdx.x, c, sh.table);
-  sum = wave_sum(sum);
-  if ((threadIdx.x & 63u) == 0u) sh.part[threadIdx.x >> 6] = sum;
+    for (int i = 0; i < N; ++i) {
+      const double x = (double)__builtin_amdgcn_fmed3f(v[i], low, INFINITY);  // (a NaN gives low)
+      const double t = __builtin_fma(x, c, shift);
+      e[i] = power(table, (uint32_t)__builtin_bit_cast(uint64_t, t));
+      f[i] = __builtin_fma(x, c, shift - t);  // t - shift: the whole number nearest c x
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      sum += __builtin_fma(e[i], f[i] * __builtin_fma(f[i], __builtin_fma(f[i], kC3, kC2), kC1), e[i]);
+  }
+  __device__ __forceinline__ void add(float v, const Powers& table) {
+    if (v != -INFINITY) sum += exp_units(fast ? __builtin_fma((double)v, c, shift - kRound) : ((double)v - (double)r) * c, table);
+  }
+};
+
+// The largest; a NaN if there is one.
+template <int N>
+__device__ __forceinline__ float largest(const float (&v)[N]) {
+  float m = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) m = __builtin_elementwise_maximum(m, v[i]);
+  return m;
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void values(const u32x4& w, float (&v)[N]) {
+  if constexpr (DT == kDtF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = u2f(w[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = u2f(w[i] << 16);
+      v[2 * i + 1] = u2f(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+// A wave's part of a split: blocks [b0, b1) of 16 bytes that lie wholly in the
+// row, every fourth 1 KB of them, and, in split 0, the elements beside them.
+template <int DT>
+__device__ __forceinline__ Running row_part(const uint8_t* p, uint32_t V, uint32_t split, uint32_t splits, double c,
+                                            const Powers& table) {
+  constexpr uint32_t E = 16u / kSize<DT>, U = 2u;
+  const uint32_t head = min((uint32_t)(-reinterpret_cast<intptr_t>(p) & 15) / kSize<DT>, V);
+  const uint32_t blocks = (V - head) / E, tail = head + blocks * E;
+  constexpr uint32_t kStep = U * kThreads;  // a split has whole steps, but the last
+  const uint32_t steps = (blocks + kStep - 1u) / kStep;
+  const uint32_t b0 = steps * split / splits * kStep, b1 = min(steps * (split + 1u) / splits * kStep, blocks);
+  const u32x4* from = reinterpret_cast<const u32x4*>(p + (size_t)head * kSize<DT>);
+  const bool edge = split == 0u && threadIdx.x < head + (V - tail);
+  const uint32_t edge_at = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+  Running s{0.0, -INFINITY, false, 0ull};
+  constexpr uint32_t kLowest = DT == kDtF32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+  // Blocks of the step at j0 (those past the end: the last one).
+  const auto load = [&](uint32_t j0, u32x4 (&w)[U]) __attribute__((always_inline)) {
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) w[u] = from[min(j0 + u * kThreads + threadIdx.x, b1 - 1u)];
+  };
+  if (c < 0.0) {
+    float best = -INFINITY;
+    uint32_t at = 0u;
+    for (uint32_t j0 = b0; j0 < b1; j0 += U * kThreads) {
+      u32x4 w[U];
+      load(j0, w);
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) {
+        float v[E];
+        values<DT, E>(w[u], v);
+        const float m = largest(v);
+        if (!(m <= best)) {  // (rarely)
+          s.bad |= m != m;
+          best = m;
+#pragma unroll
+          for (int i = (int)E - 1; i >= 0; --i)
+            at = v[i] == m ? head + min(j0 + u * kThreads + threadIdx.x, b1 - 1u) * E + i : at;
+        }
+      }
+    }
+    if (best > -INFINITY) s.key = order_key(best, at);
+    if (edge) {
+      const float v = logit<DT>(p, edge_at);
+      const uint64_t key = order_key(v, edge_at);
+      s.bad |= v != v;
+      s.key = key > s.key ? key : s.key;
+    }
+    return s;
+  }
+  WaveSum sum(c);
+  uint32_t j0 = b0;
+  u32x4 next[U];
+  if (b0 < b1) load(b0, next);
+  for (; j0 < b1; j0 += U * kThreads) {  // (the same steps for every lane)
+    u32x4 w[U];
+    float m = -INFINITY;  // the lane's largest logit of this step
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) w[u] = next[u];
+    load(j0 + U * kThreads, next);  // (past the end: the last block)
+    if (j0 + U * kThreads > b1) {
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u)
+        if (j0 + u * kThreads + threadIdx.x >= b1) w[u] = u32x4{kLowest, kLowest, kLowest, kLowest};
+    }
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      float v[E];
+      values<DT, E>(w[u], v);
+      m = __builtin_elementwise_maximum(m, largest(v));
+    }
+    if (__any(!(m <= sum.passes))) {
+      sum.move(m, table);
+      if (!sum.fast && sum.r > -INFINITY) break;
+    }
+    if (!sum.fast) continue;  // nothing but masked logits so far
+#pragma unroll
+    for (uint32_t u = 0; u < U; ++u) {
+      float v[E];
+      values<DT, E>(w[u], v);
+      if constexpr (DT == kDtF32) {
+        sum.add_fast(v, table);
+      } else {  // (four at a time: fewer registers, more waves)
+        const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+        sum.add_fast(lo, table);
+        sum.add_fast(hi, table);
+      }
+    }
+  }
+  // Temperatures at the edge of their range: from the step that showed it on.
+  for (; j0 < b1; j0 += kThreads) {
+    const bool in = j0 + threadIdx.x < b1;
+    const u32x4 w = from[min(j0 + threadIdx.x, b1 - 1u)];
+    float v[E];
+    values<DT, E>(w, v);
+    const float m = in ? largest(v) : -INFINITY;
+    if (__any(!(m <= sum.passes))) sum.move(m, table);
+#pragma unroll 1
+    for (uint32_t i = 0; i < E; ++i)
+      if (in) sum.add(logit<DT>(from + j0 + threadIdx.x, i), table);
+  }
+  if (split == 0u) {
+    const float v = edge ? logit<DT>(p, edge_at) : -INFINITY;
+    if (__any(!(v <= sum.passes))) sum.move(v, table);
+    sum.add(v, table);
+  }
+  s.sum = sum.sum * sum.rest(table);
+  s.r = sum.r;
+  s.bad = sum.bad;
+  return s;
+}
+
+// ---- the decision ------------------------------------------------------------
+// Every row's sum, a wave a row at a time; a lane has kLaneParts of its parts.
+__device__ __forceinline__ void join_rows(const Args& a, Shared& sh, uint32_t b, double c) {
+  constexpr uint32_t kAhead = 4;  // rows whose parts are asked for together
+  const uint32_t lane = threadIdx.x & 63u, rows = c < 0.0 ? a.G + 1u : a.rows, parts = a.splits * kWaves;
+  for (uint32_t row0 = threadIdx.x >> 6; row0 < rows; row0 += kWaves * kAhead) {
+    uint64_t value[kAhead][kLaneParts], r_bad[kAhead][kLaneParts];
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      const Part* from = a.parts + ((size_t)b * a.rows + row0 + i * kWaves) * parts;
+#pragma unroll
+      for (uint32_t k = 0; k < kLaneParts; ++k) {
+        const bool in = row0 + i * kWaves < rows && lane + 64u * k < parts;
+        value[i][k] = in ? get(&from[lane + 64u * k].value) : 0ull;
+        r_bad[i][k] = in ? get(&from[lane + 64u * k].r_bad) : (uint64_t)0xFF800000u;  // -inf
+      }
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      if (row0 + i * kWaves >= rows) break;
+      bool bad = false;
+      RowSum s{};
+      if (c < 0.0) {
+        uint64_t key = 0ull;
+#pragma unroll
+        for (uint32_t k = 0; k < kLaneParts; ++k) {
+          key = value[i][k] > key ? value[i][k] : key;
+          bad |= (r_bad[i][k] >> 32) != 0ull;
+        }
+        key = wave_max(key);
+        const uint32_t top = (uint32_t)(key >> 32);  // the keys of -inf and +inf bound those of finite values
+        s.best = ~(uint32_t)key;
+        s.ok = __ballot(bad) == 0ull && top > 0x007FFFFFu && top < 0xFF800000u;
+      } else {
+        float r[kLaneParts], m = -INFINITY;
+#pragma unroll
+        for (uint32_t k = 0; k < kLaneParts; ++k) {
+          r[k] = u2f((uint32_t)r_bad[i][k]);
+          m = fmaxf(m, r[k]);
+          bad |= (r_bad[i][k] >> 32) != 0ull;
+        }
+        s.r = wave_fmax(m);
+        double sum = 0.0;
+#pragma unroll
+        for (uint32_t k = 0; k < kLaneParts; ++k)
+          if (r[k] != -INFINITY) sum += __builtin_bit_cast(double, value[i][k]) * weight(r[k], s.r, c, sh.table);
+        s.inv = 1.0 / wave_sum(sum);
+        s.ok = __ballot(bad) == 0ull && s.r > -INFINITY && s.r < INFINITY;
+      }
+      if (lane == 0u) sh.row[row0 + i * kWaves] = s;
+    }
+  }
   __syncthreads();
-  if (threadIdx.x == 0u) a.sums[(size_t)b * a.chunks + chunk] = (sh.part[0] + sh.part[1]) + (sh.part[2] + sh.part[3]);
+}
+
+// Decides over a sequence's drafts (wave 0, a lane a position) and writes all
+// but a drawn token.  d: the lane's draft; xp, xq: its logits.
+__device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t b, double c, int32_t d, float xp,
+                                       float xq, float u) {
+  const bool greedy = c < 0.0;
+  const uint32_t i = threadIdx.x;
+  bool keep = false;
+  double odds = 0.0;
+  if (i < a.G && (uint32_t)d < a.V && sh.row[i].ok) {
+    const RowSum& p = sh.row[i];
+    if (greedy) {
+      keep = (uint32_t)d == p.best;
+      odds = keep ? 1.0 : 0.0;
+    } else if (!a.v.draft || sh.row[a.G + 1u + i].ok) {
+      const RowSum& q = sh.row[a.v.draft ? a.G + 1u + i : i];
+      const double pd = weight(xp, p.r, c, sh.table) * p.inv;
+      const double qd = a.v.draft ? weight(xq, q.r, c, sh.table) * q.inv : 1.0;
+      keep = (double)u * qd < pd;
+      odds = pd >= qd ? (pd > 0.0 ? 1.0 : 0.0) : pd / qd;
+    }
+  }
+  const uint32_t n = (uint32_t)__builtin_ctzll(__ballot(!keep));  // drafts kept (lane G keeps none)
+  const RowSum& p = sh.row[n];
+  if (i < a.G) a.v.chance[(size_t)b * a.G + i] = (float)odds;
+  if (i <= a.G) a.v.out[(size_t)b * (a.G + 1u) + i] = i < n ? d : i == n && greedy && p.ok ? (int32_t)p.best : -1;
+  const int32_t dn = __shfl(d, (int)n);
+  if (i != 0u) return;
+  a.v.accepted[b] = (int32_t)n;
+  Chosen s{p.inv, 0.0, p.r, 0.0f, n, kQNone};
+  if (n < a.G && (uint32_t)dn < a.V) {
+    if (!a.v.draft) {
+      s.q = dn;
+    } else if (!greedy && sh.row[a.G + 1u + n].ok) {
+      s.q = kQDraft;
+      s.inv_q = sh.row[a.G + 1u + n].inv;
+      s.rq = sh.row[a.G + 1u + n].r;
+    }
+  }
+  if (!p.ok || greedy) s.q = kNoDraw;
+  a.chosen[b] = s;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void stats_kernel(Args a) {
+  __shared__ Shared sh;
+  const uint32_t split = blockIdx.x % a.splits, n = blockIdx.x / a.splits, b = n / a.rows, row = n - b * a.rows;
+  const double c = units_of(a, b);
+  const bool greedy = c < 0.0;
+  if (greedy && row > a.G) return;  // the draft's distribution is not asked for
+  fill_table(sh.table);
+  const Running s = row_part<DT>(row_at<DT>(a, b, row), a.V, split, a.splits, c, sh.table);
+  {
+    const uint64_t value = greedy ? wave_max(s.key) : __builtin_bit_cast(uint64_t, wave_sum(s.sum));  // (lanes share r)
+    const uint64_t bad = __ballot(s.bad) != 0ull ? 1ull : 0ull;
+    if ((threadIdx.x & 63u) == 0u) {
+      Part* to = a.parts + ((size_t)n * a.splits + split) * kWaves + (threadIdx.x >> 6);
+      put(&to->value, value);
+      put(&to->r_bad, bad << 32 | f2u(s.r));
+    }
+  }
+  if (!last_of(a.arrived + b, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
+  // The drafts' own logits are asked for before the rows are joined.
+  int32_t d = -1;
+  float xp = 0.0f, xq = 0.0f, u = 0.0f;
+  if (threadIdx.x < a.G) {
+    const uint32_t i = threadIdx.x;
+    d = a.v.tokens[(size_t)b * a.G + i];
+    u = a.v.u[(size_t)b * (a.G + 1u) + i];
+    if ((uint32_t)d < a.V) {
+      xp = logit<DT>(row_at<DT>(a, b, i), (uint32_t)d);
+      if (a.v.draft) xq = logit<DT>(row_at<DT>(a, b, a.G + 1u + i), (uint32_t)d);
+    }
+  }
+  join_rows(a, sh, b, c);
+  if (threadIdx.x < 64u) decide(a, sh, b, c, d, xp, xq, u);
 }
 
 // ---- the draw ----------------------------------------------------------------
@@ -384,103 +541,122 @@ __device__ __forceinline__ double scan(double v, uint32_t lane) {
   return v;
 }
 
-// The token of chunk `chunk` at which the sum (`before` it) first passes `border`; the
-// last that has any weight, if rounding leaves none; -1 if none has.
+// r of a chunk's tokens, 64 apart in a lane, and its sum.  The logits are all asked
+// for before the first is used (tokens past the end: the last one, without weight).
 template <int DT>
-__device__ __forceinline__ int32_t pick(const Args& a, Shared& sh, const Chosen& s, const uint8_t* p, const uint8_t* q,
-                                        uint32_t chunk, double before, double border, double c) {
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, t0 = chunk * kChunk + threadIdx.x;
-  double w[kRounds];
+__device__ __forceinline__ double chunk_sum(const Args& a, const Chosen& s, const uint8_t* p, const uint8_t* q,
+                                            uint32_t chunk, double c, const Powers& table,
+                                            double (&w)[kRounds]) {
+  const uint32_t t0 = chunk * kChunk + (threadIdx.x & 63u);
+  float x[kRounds], y[kRounds];
 #pragma unroll
-  for (uint32_t r = 0; r < kRounds; ++r) w[r] = residual<DT>(a, s, p, q, t0 + r * kThreads, c, sh.table);
-  if (threadIdx.x == 0u) sh.found = 0u;
+  for (uint32_t r = 0; r < kRounds; ++r) x[r] = logit<DT>(p, min(t0 + 64u * r, a.V - 1u));
+  if (s.q == kQDraft) {
+#pragma unroll
+    for (uint32_t r = 0; r < kRounds; ++r) y[r] = logit<DT>(q, min(t0 + 64u * r, a.V - 1u));
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < kRounds; ++r) w[r] = weight(x[r], s.rp, c, table) * s.inv_p;
+  if (s.q == kQDraft) {
+#pragma unroll
+    for (uint32_t r = 0; r < kRounds; ++r) w[r] = __builtin_fmax(w[r] - weight(y[r], s.rq, c, table) * s.inv_q, 0.0);
+  }
+  double sum = 0.0;
 #pragma unroll
   for (uint32_t r = 0; r < kRounds; ++r) {
-    const double sum = wave_sum(w[r]);
-    if (lane == 0u) sh.part[r * kWaves + wave] = sum;
+    const uint32_t t = t0 + 64u * r;
+    // (A token that holds all of q has p < 1 there, or no weight is left in any.)
+    if (t >= a.V || (s.q >= 0 && (uint32_t)s.q == t)) w[r] = 0.0;
+    sum += w[r];
   }
-  __syncthreads();
-  static_assert(kRounds * kWaves == 64u, "a lane of the scan for each segment");
-  const double upto = before + scan(sh.part[lane], lane);  // every wave alike
-  const uint64_t some = __ballot(sh.part[lane] > 0.0), past = __ballot(upto > border) & some;
-  if (some == 0ull) return -1;
-  const uint32_t seg = past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(some);
-  const double start = __shfl(upto - sh.part[lane], (int)seg);
-  if (seg % kWaves == wave) {
-    double mine = 0.0;
+  return wave_sum(sum);
+}
+
+// The token of a chunk at which the sum (`before` it) first passes `border`; the
+// last that has any weight, if rounding leaves none; -1 if none has.
+__device__ __forceinline__ int32_t pick(const double (&w)[kRounds], uint32_t chunk, double before, double border) {
+  const uint32_t lane = threadIdx.x & 63u;
+  int32_t token = -1;
+  bool found = false;
 #pragma unroll
-    for (uint32_t r = 0; r < kRounds; ++r) mine = seg / kWaves == r ? w[r] : mine;
-    const double at = start + scan(mine, lane);
-    const uint64_t hit = __ballot(at > border && mine > 0.0), any = __ballot(mine > 0.0);
-    const uint32_t l = hit ? (uint32_t)__builtin_ctzll(hit) : any ? 63u - (uint32_t)__builtin_clzll(any) : 0u;
-    if (lane == 0u) sh.found = chunk * kChunk + seg * 64u + l;
+  for (uint32_t r = 0; r < kRounds; ++r) {
+    const double upto = before + scan(w[r], lane);
+    const uint64_t some = __ballot(w[r] > 0.0), past = __ballot(upto > border) & some;
+    if (some && !found) {
+      token = (int32_t)(chunk * kChunk + 64u * r + (past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(some)));
+      found = past != 0ull;
+    }
+    before = from_lane(upto, 63);
   }
-  __syncthreads();
-  return (int32_t)sh.found;
+  return token;
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void pick_kernel(Args a) {
+__global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   __shared__ Shared sh;
-  const uint32_t b = blockIdx.x, lane = threadIdx.x & 63u;
-  const double c = units_of(a, b);
+  const uint32_t group = blockIdx.x % a.groups, b = blockIdx.x / a.groups, lane = threadIdx.x & 63u;
+  const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   Chosen s = a.chosen[b];
   if (s.q == kNoDraw) return;
+  const double c = units_of(a, b);
   fill_table(sh.table);
   const uint8_t* p = row_at<DT>(a, b, s.row);
   const uint8_t* q = s.q == kQDraft ? row_at<DT>(a, b, a.G + 1u + s.row) : nullptr;
-  const double* sums = a.sums + (size_t)b * a.chunks;
-  double total = 0.0;
-  for (uint32_t i = 0; i < a.chunks; i += 64u) total += wave_sum(i + lane < a.chunks ? sums[i + lane] : 0.0);
-  const double border = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G] * total;
-  // The chunk that passes the border; the last with any weight, if none does.
-  uint32_t chunk = 0u;
-  double before = 0.0, chunk_before = 0.0;
-  bool found = false;
-  for (uint32_t i = 0; i < a.chunks && !found; i += 64u) {
-    const double mine = i + lane < a.chunks ? sums[i + lane] : 0.0, upto = before + scan(mine, lane);
-    const uint64_t some = __ballot(mine > 0.0), past = __ballot(upto > border) & some;
-    if (some) {
-      const uint32_t l = past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(some);
-      chunk = i + l;
-      chunk_before = __shfl(upto - mine, (int)l);
-      found = past != 0ull;
-    }
-    before = __shfl(upto, 63);
+  double* sums = a.sums + (size_t)b * a.chunks;
+  double w[kRounds];
+  const uint32_t c0 = (group * kWaves + wave) * a.per, c1 = min(c0 + a.per, a.chunks);
+  for (uint32_t i = c0; i < c1; ++i) {
+    const double sum = chunk_sum<DT>(a, s, p, q, i, c, sh.table, w);
+    if (lane == 0u) put(sums + i, sum);
   }
+  if (!last_of(a.arrived + a.B + b, a.groups, sh.flag)) return;
+  if (wave != 0u) return;
+  const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
+  // A lane has a run of the chunks: the run, then the chunk, that passes the border;
+  // the last with any weight, if none does.
+  const uint32_t run = (a.chunks + 63u) / 64u, i0 = min(lane * run, a.chunks), i1 = min(i0 + run, a.chunks);
+  double mine = 0.0;
+  for (uint32_t i = i0; i < i1; ++i) mine += get(sums + i);
+  double upto = scan(mine, lane);
+  const double total = from_lane(upto, 63), border = u * total;
   int32_t token = -1;
   if (total > 0.0) {
-    token = pick<DT>(a, sh, s, p, q, chunk, chunk_before, border, c);
+    const uint64_t some = __ballot(mine > 0.0), past = __ballot(upto > border) & some;
+    const uint32_t l = past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(some);
+    double before = __shfl(upto - mine, (int)l), chunk_before = before;
+    uint32_t chunk = l * run;
+    const uint32_t end = min((l + 1u) * run, a.chunks);
+    for (uint32_t i = l * run; i < end; i += 64u) {
+      const double part = i + lane < end ? get(sums + i + lane) : 0.0;
+      upto = before + scan(part, lane);
+      const uint64_t any = __ballot(part > 0.0), hit = __ballot(upto > border) & any;
+      if (any) {
+        const uint32_t at = hit ? (uint32_t)__builtin_ctzll(hit) : 63u - (uint32_t)__builtin_clzll(any);
+        chunk = i + at;
+        chunk_before = __shfl(upto - part, (int)at);
+        if (hit) break;
+      }
+      before = from_lane(upto, 63);
+    }
+    chunk_sum<DT>(a, s, p, q, chunk, c, sh.table, w);
+    token = pick(w, chunk, chunk_before, border);
   } else {
     // p and q alike to the last bit: nothing is left over, and p itself is drawn from.
     s.q = kQNone;
-    const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
-    double upto = 0.0;
+    double before = 0.0;
     for (uint32_t i = 0; i < a.chunks; ++i) {
-      double sum = 0.0;
-#pragma unroll
-      for (uint32_t r = 0; r < kRounds; ++r)
-        sum += residual<DT>(a, s, p, q, i * kChunk + r * kThreads + threadIdx.x, c, sh.table);
-      sum = wave_sum(sum);
-      __syncthreads();
-      if (lane == 0u) sh.part[threadIdx.x >> 6] = sum;
-      __syncthreads();
-      sum = (sh.part[0] + sh.part[1]) + (sh.part[2] + sh.part[3]);
-      __syncthreads();
-      const bool last = upto + sum > u;
-      if (sum > 0.0 && (last || i + 1u == a.chunks)) {
-        token = pick<DT>(a, sh, s, p, q, i, upto, u, c);
-        break;
-      }
-      upto += sum;
+      const double sum = chunk_sum<DT>(a, s, p, q, i, c, sh.table, w);
+      if (sum > 0.0) token = pick(w, i, before, u);
+      if (before + sum > u) break;
+      before += sum;
     }
   }
-  if (threadIdx.x == 0u) a.v.out[(size_t)b * (a.G + 1u) + s.row] = token;
+  if (lane == 0u) a.v.out[(size_t)b * (a.G + 1u) + s.row] = token;
 }
 
-// Splits of a row: enough workgroups for the chip, each with 4096 logits or more.
+// Workgroups of a row: enough for the chip, each with 4096 logits or more.
 uint32_t splits_of(int64_t B, int64_t rows, int64_t V) {
-  const int64_t n = B * rows, wanted = (2048 + n - 1) / n, most = std::max<int64_t>(V / 4096, 1);
+  const int64_t n = B * rows, wanted = (kWantedGroups + n - 1) / n, most = std::max<int64_t>(V / 4096, 1);
   return (uint32_t)std::min<int64_t>({wanted, most, kMaxSplits});
 }
 uint32_t chunks_of(int64_t V) { return (uint32_t)((V + kChunk - 1) / kChunk); }
@@ -488,21 +664,22 @@ uint32_t chunks_of(int64_t V) { return (uint32_t)((V + kChunk - 1) / kChunk); }
 template <int DT>
 hipError_t launch(const Args& a, hipStream_t stream) {
   stats_kernel<DT><<<dim3(a.B * a.rows * a.splits), dim3(kThreads), 0, stream>>>(a);
-  hipError_t e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  sums_kernel<DT><<<dim3(a.B * a.chunks), dim3(kThreads), 0, stream>>>(a);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  pick_kernel<DT><<<dim3(a.B), dim3(kThreads), 0, stream>>>(a);
+  draw_kernel<DT><<<dim3(a.B * a.groups), dim3(kThreads), 0, stream>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// For a call with draft logits; one without needs less.
+// The counters come first; a whole number of 16 bytes of them.
+static size_t counter_bytes(int64_t B) { return ((size_t)B * 8u + 15u) & ~(size_t)15u; }
+
+// For calls with and without draft logits.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
   const int64_t with = B * (2 * G + 1) * splits_of(B, 2 * G + 1, V), without = B * (G + 1) * splits_of(B, G + 1, V);
-  return (size_t)std::max(with, without) * sizeof(Part) + (size_t)B * chunks_of(V) * 8u + (size_t)B * sizeof(Chosen);
+  return counter_bytes(B) + (size_t)std::max(with, without) * kWaves * sizeof(Part) + (size_t)B * chunks_of(V) * 8u +
+         (size_t)B * sizeof(Chosen);
 }
 
 hipError_t launch_verify(const Verify& v, hipStream_t stream) {
@@ -514,7 +691,11 @@ hipError_t launch_verify(const Verify& v, hipStream_t stream) {
   a.rows = (uint32_t)(v.draft ? 2 * v.G + 1 : v.G + 1);
   a.splits = splits_of(v.B, a.rows, v.V);
   a.chunks = chunks_of(v.V);
-  a.chosen = static_cast<Chosen*>(v.workspace);
+  // A wave has one chunk while the chip has room, and more in a large batch.
+  a.per = std::max<uint32_t>(1u, (uint32_t)((int64_t)a.B * a.chunks / kWantedWaves));
+  a.groups = (a.chunks + a.per * kWaves - 1u) / (a.per * kWaves);
+  a.arrived = static_cast<uint32_t*>(v.workspace);
+  a.chosen = reinterpret_cast<Chosen*>(static_cast<uint8_t*>(v.workspace) + counter_bytes(v.B));
   a.sums = reinterpret_cast<double*>(a.chosen + a.B);
   a.parts = reinterpret_cast<Part*>(a.sums + (size_t)a.B * a.chunks);
   return v.dtype == kDtF32 ? launch<kDtF32>(a, stream) : launch<kDtBF16>(a, stream);
