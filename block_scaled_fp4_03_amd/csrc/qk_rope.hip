@@ -4,11 +4,12 @@
 //   y = x r w,  r = (mean x^2 + eps)^-1/2 over a head's D values;
 //   pair i of the first R values turned by pos freq_i.
 //
-// A lane holds P pairs of a head: with the halves of a pair R / 2 apart, P
-// values at two places, so that no pair crosses lanes; G lanes make a head (a
-// DPP sum), 64 / G heads a wave's step.  Values that are not rotated lie in
-// pairs of their own with cos 1 and sin 0.  A wave keeps to one row while it
-// can: the angles are worked out once for all its heads.
+// A lane holds N consecutive values of a head (16 bytes where the halves divide
+// into them: whole lines in one load); G lanes make a head (a DPP sum), 64 / G
+// heads a wave's step.  Where the halves of a pair lie R / 2 apart, the other
+// half comes from another lane.  A wave keeps to one row of q or of k while it
+// can; its lanes work out one pair's angle each and share them in LDS, from where
+// each takes the factors of its values, w cos and w' sin.
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
@@ -21,28 +22,33 @@ namespace {
 
 constexpr uint32_t kWaves = 4;
 constexpr uint32_t kMaxGroups = 1024;  // workgroups of the gradient, each with a partial sum
+constexpr uint64_t kWantedWaves = 8192;
 
 struct Tensor {
   const void* p;
   int64_t stride;  // elements between rows
 };
 
-struct Args {
-  Tensor q, k, gq, gk;       // inputs; gradients of the outputs
-  Tensor oq, ok;             // outputs (written)
-  const float* wq;
-  const float* wk;
-  const float* freq;
-  const int32_t* pos;
-  float* partial;
-  float eps;
-  uint32_t rows, hq, heads;  // heads: q's and then k's
-  uint32_t D, R, axes;
-  uint32_t steps, parts;     // a row's steps of 64 / G heads, and the waves they are cut to
-  uint32_t axis[8];          // two bits a pair
+// One of q and k.
+struct Heads {
+  Tensor x, g, out;    // input; gradient of the output; output (written)
+  const float* w;
+  float* partial;      // gradient: a row of D sums for each workgroup
+  uint32_t heads;
+  uint32_t steps, parts;  // a row's steps of 64 / G heads, and the waves they are cut to
+  uint32_t groups;     // workgroups
 };
 
-template <int DT, int P>
+struct Args {
+  Heads t[2];
+  const float* freq;
+  const int32_t* pos;
+  float eps;
+  uint32_t rows, D, R, axes;
+  uint32_t axis[8];    // two bits a pair
+};
+
+template <int DT, int N>
 struct Chunk;
 template <>
 struct Chunk<kDtF32, 4> {
@@ -57,29 +63,29 @@ struct Chunk<kDtBF16, 4> {
   typedef u32x2 T;
 };
 
-// P values of a chunk.
-template <int DT, int P>
-__device__ __forceinline__ void unpack(typename Chunk<DT, P>::T w, float* v) {
+// The N values of a chunk.
+template <int DT, int N>
+__device__ __forceinline__ void unpack(typename Chunk<DT, N>::T w, float (&v)[N]) {
   if constexpr (DT == kDtF32) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = u2f(w[i]);
+    for (int i = 0; i < N; ++i) v[i] = u2f(w[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < P / 2; ++i) {
+    for (int i = 0; i < N / 2; ++i) {
       v[2 * i] = u2f(w[i] << 16);
       v[2 * i + 1] = u2f(w[i] & 0xFFFF0000u);
     }
   }
 }
-template <int DT, int P>
-__device__ __forceinline__ typename Chunk<DT, P>::T pack(const float* v) {
-  typename Chunk<DT, P>::T w;
+template <int DT, int N>
+__device__ __forceinline__ typename Chunk<DT, N>::T pack(const float (&v)[N]) {
+  typename Chunk<DT, N>::T w;
   if constexpr (DT == kDtF32) {
 #pragma unroll
-    for (int i = 0; i < P; ++i) w[i] = f2u(v[i]);
+    for (int i = 0; i < N; ++i) w[i] = f2u(v[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < P / 2; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < N / 2; ++i) w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
   }
   return w;
 }
@@ -96,318 +102,344 @@ __device__ __forceinline__ float head_sum(float v) {
   if (G >= 8) v += moved<0x141>(v);  // 7 - lane of 8: the other four
   if (G >= 16) v += moved<0x140>(v); // 15 - lane of 16: the other eight
   if (G >= 32) v += __shfl_xor(v, 16);
+  if (G >= 64) v += __shfl_xor(v, 32);
   return v;
 }
 
 // A lane's place in its head.
-template <int P, int G, bool INTERLEAVED>
+template <int DT, int N, int G, bool INTERLEAVED>
 struct Lane {
-  uint32_t l, a, b;  // its two chunks' first values
-  bool live, turns;
-  uint32_t axis;     // its pairs' axes, two bits each
+  uint32_t e;      // its first value
+  uint32_t other;  // byte address (4 lane) of the lane that holds the other halves
+  bool live, turns, second;
   __device__ __forceinline__ explicit Lane(const Args& s) {
-    l = threadIdx.x & (G - 1u);
-    live = l * 2u * P < s.D;
-    turns = l * 2u * P < s.R;
-    if (INTERLEAVED) {
-      a = l * 2u * P;
-      b = a + P;
-    } else {
-      const uint32_t m = turns ? l : l - s.R / (2u * P);
-      a = (turns ? 0u : s.R) + m * P;
-      b = a + (turns ? s.R : s.D - s.R) / 2u;
-    }
-    uint32_t word = 0u;
-#pragma unroll
-    for (uint32_t i = 0; i < 8u; ++i) word = (l * P) >> 4 == i ? s.axis[i] : word;
-    axis = word >> (2u * ((l * P) & 15u));
+    const uint32_t l = threadIdx.x & (G - 1u), half = s.R / 2u;
+    e = l * N;
+    live = e < s.D;
+    turns = e < s.R;
+    second = !INTERLEAVED && turns && e >= half;
+    const uint32_t o = !turns ? l : second ? l - half / N : l + half / N;
+    other = ((threadIdx.x & 63u & ~(G - 1u)) + o) * 4u;
   }
-  // Cosines and sines of the lane's pairs at a row's positions.  The angle in
-  // turns, in FP64: its whole part goes before it is rounded (pos freq in
-  // FP32 would be off by 2^-24 pos).
-  __device__ __forceinline__ void angles(const Args& s, uint32_t row, const float (&freq)[P], float (&c)[P],
-                                         float (&n)[P]) const {
-    constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
-    if (s.R == 0u) {
+  // The other half of every value's pair (0 where there is none: an infinity that
+  // is not turned stays one).
+  __device__ __forceinline__ typename Chunk<DT, N>::T others(typename Chunk<DT, N>::T w) const {
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        c[i] = 1.0f;
-        n[i] = 0.0f;
-      }
-      return;
+    for (uint32_t i = 0; i < sizeof(w) / 4u; ++i) {
+      if (!INTERLEAVED) w[i] = (uint32_t)__builtin_amdgcn_ds_bpermute((int)other, (int)w[i]);
+      w[i] = turns ? w[i] : 0u;
     }
+    return w;
+  }
+  // v's other halves among what others() gave of its chunk.
+  static __device__ __forceinline__ float half_of(const float (&o)[N], int i) { return o[INTERLEAVED ? i ^ 1 : i]; }
+};
+
+// A wave's cosines and sines, one row's at a time.
+struct alignas(16) Turns {
+  float c[128], s[128];
+};
+// What a lane needs of its pairs, lane and lane + 64, for any row.
+struct Angles {
+  float freq[2];
+  uint32_t axis[2];
+  __device__ __forceinline__ explicit Angles(const Args& s) {
+#pragma unroll
+    for (uint32_t h = 0; h < 2u; ++h) {
+      const uint32_t i = (threadIdx.x & 63u) + 64u * h;
+      freq[h] = 2u * i < s.R ? s.freq[i] : 0.0f;
+      uint32_t word = 0u;
+#pragma unroll
+      for (uint32_t k = 0; k < 8u; ++k) word = i >> 4 == k ? s.axis[k] : word;
+      axis[h] = (word >> (2u * (i & 15u))) & 3u;
+    }
+  }
+  // Of the row's positions.  The angle in turns, in FP64: its whole part goes
+  // before it is rounded (pos freq in FP32 would be off by 2^-24 pos).
+  __device__ __forceinline__ void fill(const Args& s, uint32_t row, Turns& to) const {
+    constexpr double kTurn = 0.15915494309189533577;  // 1 / (2 pi)
+    if (s.R == 0u) return;
     int32_t at[4];
 #pragma unroll
     for (uint32_t x = 0; x < 4u; ++x) at[x] = x < s.axes ? s.pos[(size_t)x * s.rows + row] : 0;
+    __builtin_amdgcn_wave_barrier();  // (the row before has been read)
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const uint32_t x = (axis >> (2 * i)) & 3u;
+    for (uint32_t h = 0; h < 2u; ++h) {
+      if (h == 1u && s.R <= 128u) break;
+      const uint32_t x = axis[h];
       const int32_t p = x == 0u ? at[0] : x == 1u ? at[1] : x == 2u ? at[2] : at[3];
-      double t = (double)p * (double)freq[i] * kTurn;
+      double t = (double)p * (double)freq[h] * kTurn;
       t -= __builtin_rint(t);
       float sn, cs;
       sincospif(2.0f * (float)t, &sn, &cs);
-      c[i] = turns ? cs : 1.0f;
-      n[i] = turns ? sn : 0.0f;
+      to.c[(threadIdx.x & 63u) + 64u * h] = cs;
+      to.s[(threadIdx.x & 63u) + 64u * h] = sn;
     }
+    // The wave's own LDS writes before its reads: in order, once they are issued.
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   }
-  // Index of the first and the second value of pair i among a lane's 2 P.
-  static __device__ __forceinline__ constexpr int first(int i) { return INTERLEAVED ? 2 * i : i; }
-  static __device__ __forceinline__ constexpr int second(int i) { return INTERLEAVED ? 2 * i + 1 : P + i; }
 };
-
-template <int P>
-__device__ __forceinline__ void load_floats(const float* p, uint32_t at, bool live, float otherwise, float* v) {
+// Factors of a lane's values: turned, value i is v_i c_i + (its other half) n_i.
+template <int DT, int N, int G, bool INTERLEAVED>
+__device__ __forceinline__ void read_turns(const Lane<DT, N, G, INTERLEAVED>& lane, const Args& s, const Turns& from,
+                                           float (&c)[N], float (&n)[N]) {
+  const uint32_t pair = INTERLEAVED ? lane.e / 2u : lane.second ? lane.e - s.R / 2u : lane.e;
 #pragma unroll
-  for (int i = 0; i < P; ++i) v[i] = p && live ? p[at + i] : otherwise;
+  for (int i = 0; i < N; ++i) {
+    const uint32_t at = (pair + (INTERLEAVED ? i / 2 : i)) & 127u;
+    const bool minus = INTERLEAVED ? i % 2 == 0 : !lane.second;
+    c[i] = lane.turns ? from.c[at] : 1.0f;
+    n[i] = !lane.turns ? 0.0f : minus ? -from.s[at] : from.s[at];
+  }
+}
+template <int N>
+__device__ __forceinline__ void load_floats(const float* p, uint32_t at, bool live, float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = p && live ? p[at + i] : 1.0f;
 }
 
 // A wave's share of a row: steps [s0, s1).
 struct Unit {
   uint32_t row, s0, s1;
 };
-__device__ __forceinline__ Unit unit_of(const Args& s, uint32_t u) {
-  const uint32_t row = u / s.parts, part = u - row * s.parts;
-  return Unit{row, part * s.steps / s.parts, (part + 1u) * s.steps / s.parts};
+__device__ __forceinline__ Unit unit_of(const Heads& t, uint32_t u) {
+  const uint32_t row = u / t.parts, part = u - row * t.parts;
+  return Unit{row, part * t.steps / t.parts, (part + 1u) * t.steps / t.parts};
+}
+// Whether this workgroup has q or k, and its number among those (q's come first).
+__device__ __forceinline__ uint32_t which(const Args& s, uint32_t& group) {
+  const uint32_t t = blockIdx.x >= s.t[0].groups ? 1u : 0u;
+  group = blockIdx.x - (t ? s.t[0].groups : 0u);
+  return t;
 }
 
-template <int DT, int P, int G, bool INTERLEAVED>
-__device__ __forceinline__ size_t at_head(const Tensor& q, const Tensor& k, const Args& s, uint32_t row, uint32_t head,
-                                          const void** base) {
-  const bool is_q = head < s.hq;
-  *base = is_q ? q.p : k.p;
-  return (size_t)row * (size_t)(is_q ? q.stride : k.stride) + (size_t)(is_q ? head : head - s.hq) * s.D;
+template <int DT>
+__device__ __forceinline__ const uint8_t* head_at(const Tensor& x, uint32_t row, uint32_t value) {
+  return static_cast<const uint8_t*>(x.p) + ((size_t)row * (size_t)x.stride + value) * (DT == kDtF32 ? 4u : 2u);
+}
+template <int DT, int N>
+__device__ __forceinline__ typename Chunk<DT, N>::T load(const uint8_t* p) {
+  return *reinterpret_cast<const typename Chunk<DT, N>::T*>(p);
+}
+template <int DT, int N>
+__device__ __forceinline__ void store(const uint8_t* p, const float (&v)[N]) {
+  *reinterpret_cast<typename Chunk<DT, N>::T*>(const_cast<uint8_t*>(p)) = pack<DT, N>(v);
 }
 
-template <int DT, int P>
-__device__ __forceinline__ typename Chunk<DT, P>::T load(const void* base, size_t at) {
-  constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u;
-  return *reinterpret_cast<const typename Chunk<DT, P>::T*>(static_cast<const uint8_t*>(base) + at * kSize);
-}
-template <int DT, int P>
-__device__ __forceinline__ void store(const void* base, size_t at, const float* v) {
-  constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u;
-  *reinterpret_cast<typename Chunk<DT, P>::T*>(const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) + at * kSize) =
-      pack<DT, P>(v);
-}
-
-template <int DT, int P, int G, bool INTERLEAVED>
+template <int DT, int N, int G, bool INTERLEAVED>
 __global__ __launch_bounds__(64 * kWaves) void forward_kernel(Args s) {
   constexpr uint32_t kHeads = 64u / G;
+  __shared__ Turns turns[kWaves];
+  uint32_t group;
+  const Heads t = s.t[which(s, group)];
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const uint32_t u = blockIdx.x * kWaves + wave;
-  if (u >= s.rows * s.parts) return;
-  const Unit unit = unit_of(s, u);
-  const Lane<P, G, INTERLEAVED> lane(s);
-  float freq[P], c[P], n[P], wq[2 * P], wk[2 * P];
-  load_floats<P>(s.freq, lane.l * P, lane.turns, 0.0f, freq);
-  load_floats<P>(s.wq, lane.a, lane.live, 1.0f, wq);
-  load_floats<P>(s.wq, lane.b, lane.live, 1.0f, wq + P);
-  load_floats<P>(s.wk, lane.a, lane.live, 1.0f, wk);
-  load_floats<P>(s.wk, lane.b, lane.live, 1.0f, wk + P);
-  lane.angles(s, unit.row, freq, c, n);
+  const uint32_t u = group * kWaves + wave;
+  if (u >= s.rows * t.parts) return;
+  const Unit unit = unit_of(t, u);
+  const Lane<DT, N, G, INTERLEAVED> lane(s);
+  float c[N], n[N];
+  {
+    float w[N], o[N];
+    load_floats(t.w, lane.e, lane.live, w);
+    Angles(s).fill(s, unit.row, turns[wave]);
+    read_turns(lane, s, turns[wave], c, n);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      o[i] = INTERLEAVED ? w[i] : u2f((uint32_t)__builtin_amdgcn_ds_bpermute((int)lane.other, (int)f2u(w[i])));
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      c[i] *= w[i];
+      n[i] *= lane.half_of(o, i);
+    }
+  }
   const float inv_d = 1.0f / (float)s.D;
   for (uint32_t step = unit.s0; step < unit.s1; ++step) {
     const uint32_t head = step * kHeads + (threadIdx.x & 63u) / G;
-    const bool live = lane.live && head < s.heads, is_q = head < s.hq;
-    const void* base;
-    const size_t at = at_head<DT, P, G, INTERLEAVED>(s.q, s.k, s, unit.row, head, &base);
-    float v[2 * P] = {};
-    if (live) {
-      unpack<DT, P>(load<DT, P>(base, at + lane.a), v);
-      unpack<DT, P>(load<DT, P>(base, at + lane.b), v + P);
-    }
-    float sum = 0.0f;
+    const bool live = lane.live && head < t.heads;
+    typename Chunk<DT, N>::T raw{};
+    if (live) raw = load<DT, N>(head_at<DT>(t.x, unit.row, head * s.D + lane.e));
+    float v[N], o[N];
+    unpack<DT, N>(raw, v);
+    unpack<DT, N>(lane.others(raw), o);
+    float r = 1.0f;
+    if (t.w) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 2 * P; ++i) sum = __builtin_fmaf(v[i], v[i], sum);
-    sum = head_sum<G>(sum);
-    const bool norm = (is_q ? s.wq : s.wk) != nullptr;
-    const float r = norm ? __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv_d, s.eps)) : 1.0f;
-    float y[2 * P];
-#pragma unroll
-    for (int i = 0; i < 2 * P; ++i) v[i] = v[i] * r * (is_q ? wq[i] : wk[i]);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const int a = lane.first(i), b = lane.second(i);
-      y[a] = __builtin_fmaf(v[a], c[i], -(v[b] * n[i]));
-      y[b] = __builtin_fmaf(v[b], c[i], v[a] * n[i]);
+      for (int i = 0; i < N; ++i) sum = __builtin_fmaf(v[i], v[i], sum);
+      r = __builtin_amdgcn_rsqf(__builtin_fmaf(head_sum<G>(sum), inv_d, s.eps));
     }
-    if (live) {
-      const size_t to = at_head<DT, P, G, INTERLEAVED>(s.oq, s.ok, s, unit.row, head, &base);
-      store<DT, P>(base, to + lane.a, y);
-      store<DT, P>(base, to + lane.b, y + P);
-    }
+    float y[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) y[i] = r * __builtin_fmaf(v[i], c[i], lane.half_of(o, i) * n[i]);
+    if (live) store<DT, N>(head_at<DT>(t.out, unit.row, head * s.D + lane.e), y);
   }
 }
 
 // g' = the output's gradient turned back; dx = r (w g' - x r^2 mean(x w g'));
 // dw = sum of g' x r: in registers over a wave's rows and heads, then over the
 // workgroup, then (sum_kernel) over the workgroups, all in a fixed order.
-template <int DT, int P, int G, bool INTERLEAVED>
+template <int DT, int N, int G, bool INTERLEAVED>
 __global__ __launch_bounds__(64 * kWaves) void backward_kernel(Args s) {
   constexpr uint32_t kHeads = 64u / G;
-  __shared__ float part[kWaves][2][256];
+  __shared__ union {
+    Turns turns[kWaves];
+    float part[kWaves][256];
+  } sh;
+  uint32_t group;
+  const Heads t = s.t[which(s, group)];
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-  const Lane<P, G, INTERLEAVED> lane(s);
-  float freq[P], c[P], n[P], wq[2 * P], wk[2 * P], dq[2 * P] = {}, dk[2 * P] = {};
-  load_floats<P>(s.freq, lane.l * P, lane.turns, 0.0f, freq);
-  load_floats<P>(s.wq, lane.a, lane.live, 1.0f, wq);
-  load_floats<P>(s.wq, lane.b, lane.live, 1.0f, wq + P);
-  load_floats<P>(s.wk, lane.a, lane.live, 1.0f, wk);
-  load_floats<P>(s.wk, lane.b, lane.live, 1.0f, wk + P);
+  const Lane<DT, N, G, INTERLEAVED> lane(s);
+  const Angles angles(s);
+  float c[N], n[N], w[N], dw[N] = {};
+  load_floats(t.w, lane.e, lane.live, w);
   const float inv_d = 1.0f / (float)s.D;
-  for (uint32_t u = blockIdx.x * kWaves + wave; u < s.rows * s.parts; u += gridDim.x * kWaves) {
-    const Unit unit = unit_of(s, u);
-    lane.angles(s, unit.row, freq, c, n);
+  for (uint32_t u = group * kWaves + wave; u < s.rows * t.parts; u += t.groups * kWaves) {
+    const Unit unit = unit_of(t, u);
+    angles.fill(s, unit.row, sh.turns[wave]);
+    read_turns(lane, s, sh.turns[wave], c, n);
     for (uint32_t step = unit.s0; step < unit.s1; ++step) {
       const uint32_t head = step * kHeads + (threadIdx.x & 63u) / G;
-      const bool live = lane.live && head < s.heads, is_q = head < s.hq;
-      const bool norm = (is_q ? s.wq : s.wk) != nullptr;
-      const void* base;
-      float g[2 * P] = {}, x[2 * P] = {}, t[2 * P];
-      if (live) {
-        const size_t at = at_head<DT, P, G, INTERLEAVED>(s.gq, s.gk, s, unit.row, head, &base);
-        unpack<DT, P>(load<DT, P>(base, at + lane.a), g);
-        unpack<DT, P>(load<DT, P>(base, at + lane.b), g + P);
-      }
-      if (live && norm) {
-        const size_t at = at_head<DT, P, G, INTERLEAVED>(s.q, s.k, s, unit.row, head, &base);
-        unpack<DT, P>(load<DT, P>(base, at + lane.a), x);
-        unpack<DT, P>(load<DT, P>(base, at + lane.b), x + P);
-      }
-      float sum = 0.0f, dot = 0.0f;
+      const bool live = lane.live && head < t.heads;
+      typename Chunk<DT, N>::T raw_g{}, raw_x{};
+      if (live) raw_g = load<DT, N>(head_at<DT>(t.g, unit.row, head * s.D + lane.e));
+      if (live && t.w) raw_x = load<DT, N>(head_at<DT>(t.x, unit.row, head * s.D + lane.e));
+      float g[N], o[N], d[N];
+      unpack<DT, N>(raw_g, g);
+      unpack<DT, N>(lane.others(raw_g), o);
 #pragma unroll
-      for (int i = 0; i < 2 * P; ++i) sum = __builtin_fmaf(x[i], x[i], sum);
+      for (int i = 0; i < N; ++i) d[i] = __builtin_fmaf(g[i], c[i], -(lane.half_of(o, i) * n[i]));
+      if (t.w) {
+        float x[N], sum = 0.0f, dot = 0.0f;
+        unpack<DT, N>(raw_x, x);
 #pragma unroll
-      for (int i = 0; i < P; ++i) {
-        const int a = lane.first(i), b = lane.second(i);
-        t[a] = __builtin_fmaf(g[a], c[i], g[b] * n[i]);
-        t[b] = __builtin_fmaf(g[b], c[i], -(g[a] * n[i]));
-      }
-      sum = head_sum<G>(sum);
-      const float r = norm ? __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv_d, s.eps)) : 1.0f;
+        for (int i = 0; i < N; ++i) sum = __builtin_fmaf(x[i], x[i], sum);
+        sum = head_sum<G>(sum);
+        const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(sum, inv_d, s.eps));
 #pragma unroll
-      for (int i = 0; i < 2 * P; ++i) {
-        x[i] *= r;
-        const float d = t[i] * x[i];
-        if (live && is_q) dq[i] += d;
-        if (live && !is_q) dk[i] += d;
-        t[i] *= is_q ? wq[i] : wk[i];
-        dot = __builtin_fmaf(x[i], t[i], dot);
-      }
-      dot = head_sum<G>(dot) * inv_d;
+        for (int i = 0; i < N; ++i) {
+          x[i] *= r;
+          const float p = d[i] * x[i];
+          dw[i] += live ? p : 0.0f;
+          d[i] *= w[i];
+          dot = __builtin_fmaf(p, w[i], dot);
+        }
+        dot = head_sum<G>(dot) * inv_d;
 #pragma unroll
-      for (int i = 0; i < 2 * P; ++i) t[i] = norm ? r * __builtin_fmaf(-x[i], dot, t[i]) : t[i];
-      if (live) {
-        const size_t to = at_head<DT, P, G, INTERLEAVED>(s.oq, s.ok, s, unit.row, head, &base);
-        store<DT, P>(base, to + lane.a, t);
-        store<DT, P>(base, to + lane.b, t + P);
+        for (int i = 0; i < N; ++i) d[i] = r * __builtin_fmaf(-x[i], dot, d[i]);
       }
+      if (live) store<DT, N>(head_at<DT>(t.out, unit.row, head * s.D + lane.e), d);
     }
   }
-  if (!s.partial) return;
+  if (!t.w) return;
+  __syncthreads();  // (the turns have been read)
 #pragma unroll
-  for (int i = 0; i < 2 * P; ++i) {
+  for (int i = 0; i < N; ++i) {
 #pragma unroll
-    for (int d = G; d < 64; d <<= 1) {
-      dq[i] += __shfl_xor(dq[i], d);
-      dk[i] += __shfl_xor(dk[i], d);
-    }
-    if ((threadIdx.x & 63u) < G && lane.live) {
-      const uint32_t e = (i < P ? lane.a : lane.b - P) + i;
-      part[wave][0][e] = dq[i];
-      part[wave][1][e] = dk[i];
-    }
+    for (int k = G; k < 64; k <<= 1) dw[i] += __shfl_xor(dw[i], k);
+    if ((threadIdx.x & 63u) < G && lane.live) sh.part[wave][lane.e + i] = dw[i];
   }
   __syncthreads();
-  for (uint32_t e = threadIdx.x; e < 2u * s.D; e += 64u * kWaves) {
-    const uint32_t w = e >= s.D, at = e - w * s.D;
-    float sum = 0.0f;
-#pragma unroll
-    for (uint32_t i = 0; i < kWaves; ++i) sum += part[i][w][at];
-    s.partial[(size_t)blockIdx.x * 2u * s.D + e] = sum;
-  }
+  const uint32_t e = threadIdx.x;
+  if (e < s.D)
+    t.partial[(size_t)group * s.D + e] = (sh.part[0][e] + sh.part[1][e]) + (sh.part[2][e] + sh.part[3][e]);
 }
 
-// Sums of the workgroups' partial sums: 16 columns a workgroup, 16 threads each.
-__global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ partial, uint32_t groups, uint32_t D,
-                                                  float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ float part[16][16];
-  const uint32_t c = threadIdx.x & 15u, seg = threadIdx.x >> 4, e = blockIdx.x * 16u + c;
+// Sums of the workgroups' partial sums: 16 columns a workgroup, 16 threads
+// each.
+__global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ partial_q,
+                                                  const float* __restrict__ partial_k, uint32_t groups_q,
+                                                  uint32_t groups_k, uint32_t D, float* __restrict__ dwq,
+                                                  float* __restrict__ dwk) {
+  __shared__ float part[16][17];
+  const uint32_t columns = (D + 15u) / 16u;
+  const bool is_q = blockIdx.x < columns;
+  const float* partial = is_q ? partial_q : partial_k;
+  float* out = is_q ? dwq : dwk;
+  if (!out) return;
+  const uint32_t groups = is_q ? groups_q : groups_k;
+  const uint32_t c = threadIdx.x & 15u, seg = threadIdx.x >> 4, e = (is_q ? blockIdx.x : blockIdx.x - columns) * 16u + c;
   float sum = 0.0f;
-  if (e < 2u * D)
-    for (uint32_t g = seg; g < groups; g += 16u) sum += partial[(size_t)g * 2u * D + e];
+  if (e < D) {
+    uint32_t g = seg;
+    for (; g + 112u < groups; g += 128u) {  // eight loads at a time
+      float v[8];
+#pragma unroll
+      for (uint32_t i = 0; i < 8u; ++i) v[i] = partial[(size_t)(g + 16u * i) * D + e];
+#pragma unroll
+      for (uint32_t i = 0; i < 8u; ++i) sum += v[i];
+    }
+    for (; g < groups; g += 16u) sum += partial[(size_t)g * D + e];
+  }
   part[seg][c] = sum;
   __syncthreads();
-  if (seg != 0u || e >= 2u * D) return;
+  if (seg != 0u || e >= D) return;
   for (uint32_t i = 1; i < 16u; ++i) sum += part[i][c];
-  float* out = e < D ? dwq : dwk;
-  if (out) out[e < D ? e : e - D] = sum;
+  out[e] = sum;
 }
 
-uint32_t group_lanes(uint32_t D, uint32_t P) {
-  uint32_t g = 2u;
-  while (g * 2u * P < D) g *= 2u;
+uint32_t group_lanes(uint32_t D, uint32_t N) {
+  uint32_t g = 4u;
+  while (g * N < D) g *= 2u;
   return g;
 }
 
-// Pairs of a lane: 16-byte chunks, if the halves divide into them.
-int lane_pairs(const QkRope& a) {
-  return a.dtype == kDtBF16 && a.R % 16 == 0 && a.D % 16 == 0 ? 8 : 4;
-}
+// Values of a lane: 16 bytes, if the halves divide into them.
+int lane_values(const QkRope& a) { return a.dtype == kDtBF16 && (a.interleaved || a.R % 16 == 0) ? 8 : 4; }
 
-template <bool BACKWARD, int DT, int P, int G, bool INTERLEAVED>
+template <bool BACKWARD, int DT, int N, int G, bool INTERLEAVED>
 hipError_t launch_one(Args& s, const QkRope& a, hipStream_t stream) {
-  s.steps = (s.heads + 64u / G - 1u) / (64u / G);
-  // Enough waves to fill the chip; beyond that a wave keeps a whole row.
-  const uint64_t wanted = 8192u;
-  s.parts = (uint32_t)std::min<uint64_t>(s.steps, (wanted + s.rows - 1u) / std::max(s.rows, 1u));
-  const uint64_t units = (uint64_t)s.rows * s.parts;
-  uint32_t grid = (uint32_t)((units + kWaves - 1u) / kWaves);
-  if (BACKWARD) grid = std::min(grid, kMaxGroups);
-  if (grid > 0u) {  // (no rows: the weights' gradients are 0)
+  uint32_t grid = 0u;
+  const uint32_t all = s.t[0].heads + s.t[1].heads;
+  for (Heads& t : s.t) {
+    if (t.heads == 0u || s.rows == 0u) continue;
+    t.steps = (t.heads + 64u / G - 1u) / (64u / G);
+    // Enough waves to fill the chip; beyond that a wave keeps a whole row.
+    t.parts = (uint32_t)std::min<uint64_t>(t.steps, (kWantedWaves + s.rows - 1u) / s.rows);
+    t.groups = (uint32_t)(((uint64_t)s.rows * t.parts + kWaves - 1u) / kWaves);
+    // (The gradient's keep their sums over many rows.)
+    if (BACKWARD) t.groups = std::min(t.groups, std::max(kMaxGroups * t.heads / all, 1u));
+    grid += t.groups;
+  }
+  s.t[1].partial = s.t[0].partial + (size_t)s.t[0].groups * s.D;
+  if (grid > 0u) {
     if (BACKWARD)
-      backward_kernel<DT, P, G, INTERLEAVED><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(s);
+      backward_kernel<DT, N, G, INTERLEAVED><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(s);
     else
-      forward_kernel<DT, P, G, INTERLEAVED><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(s);
+      forward_kernel<DT, N, G, INTERLEAVED><<<dim3(grid), dim3(64 * kWaves), 0, stream>>>(s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  if (!BACKWARD || !(s.wq || s.wk)) return hipSuccess;
-  sum_kernel<<<dim3((2u * s.D + 15u) / 16u), dim3(256), 0, stream>>>(s.partial, grid, s.D, a.dwq, a.dwk);
+  if (!BACKWARD || !(s.t[0].w || s.t[1].w)) return hipSuccess;
+  // (Without rows the weights' gradients are 0.)
+  sum_kernel<<<dim3(2u * ((s.D + 15u) / 16u)), dim3(256), 0, stream>>>(s.t[0].partial, s.t[1].partial, s.t[0].groups,
+                                                                      s.t[1].groups, s.D, a.dwq, a.dwk);
   return hipGetLastError();
 }
 
-template <bool BACKWARD, int DT, int P, bool INTERLEAVED>
+template <bool BACKWARD, int DT, int N, bool INTERLEAVED>
 hipError_t launch_lanes(Args& s, const QkRope& a, hipStream_t stream) {
-  const uint32_t g = group_lanes(s.D, P);
-  if constexpr (P == 8)
-    if (g == 2u) return launch_one<BACKWARD, DT, P, 2, INTERLEAVED>(s, a, stream);
-  if (g == 4u) return launch_one<BACKWARD, DT, P, 4, INTERLEAVED>(s, a, stream);
-  if (g == 8u) return launch_one<BACKWARD, DT, P, 8, INTERLEAVED>(s, a, stream);
-  if (g == 16u) return launch_one<BACKWARD, DT, P, 16, INTERLEAVED>(s, a, stream);  // (heads of 32 to 256 values)
-  if constexpr (P == 4) return launch_one<BACKWARD, DT, P, 32, INTERLEAVED>(s, a, stream);
+  const uint32_t g = group_lanes(s.D, N);  // (heads of 32 to 256 values)
+  if constexpr (N == 8)
+    if (g == 4u) return launch_one<BACKWARD, DT, N, 4, INTERLEAVED>(s, a, stream);
+  if (g == 8u) return launch_one<BACKWARD, DT, N, 8, INTERLEAVED>(s, a, stream);
+  if (g == 16u) return launch_one<BACKWARD, DT, N, 16, INTERLEAVED>(s, a, stream);
+  if (g == 32u) return launch_one<BACKWARD, DT, N, 32, INTERLEAVED>(s, a, stream);
+  if constexpr (N == 4) return launch_one<BACKWARD, DT, N, 64, INTERLEAVED>(s, a, stream);
   return hipErrorInvalidValue;
 }
 
 template <bool BACKWARD>
 hipError_t launch(const QkRope& a, hipStream_t stream) {
   Args s{};
-  s.q = Tensor{a.q, a.q_stride};
-  s.k = Tensor{a.k, a.k_stride};
-  s.gq = Tensor{a.gq, a.gq_stride};
-  s.gk = Tensor{a.gk, a.gk_stride};
-  s.oq = Tensor{a.oq, a.oq_stride};
-  s.ok = Tensor{a.ok, a.ok_stride};
-  s.wq = a.wq;
-  s.wk = a.wk;
+  s.t[0] = Heads{{a.q, a.q_stride}, {a.gq, a.gq_stride}, {a.oq, a.oq_stride}, a.wq,
+                 static_cast<float*>(a.workspace), (uint32_t)a.hq, 0u, 0u, 0u};
+  s.t[1] = Heads{{a.k, a.k_stride}, {a.gk, a.gk_stride}, {a.ok, a.ok_stride}, a.wk, nullptr, (uint32_t)a.hk, 0u, 0u, 0u};
   s.freq = a.freq;
   s.pos = a.pos;
-  s.partial = BACKWARD && (a.wq || a.wk) ? static_cast<float*>(a.workspace) : nullptr;
   s.eps = a.eps;
   s.rows = (uint32_t)a.rows;
-  s.hq = (uint32_t)a.hq;
-  s.heads = (uint32_t)(a.hq + a.hk);
   s.D = (uint32_t)a.D;
   s.R = (uint32_t)a.R;
   s.axes = (uint32_t)a.axes;
@@ -415,7 +447,7 @@ hipError_t launch(const QkRope& a, hipStream_t stream) {
   const auto go = [&](auto interleaved) {
     constexpr bool I = decltype(interleaved)::value;
     if (a.dtype == kDtF32) return launch_lanes<BACKWARD, kDtF32, 4, I>(s, a, stream);
-    if (lane_pairs(a) == 8) return launch_lanes<BACKWARD, kDtBF16, 8, I>(s, a, stream);
+    if (lane_values(a) == 8) return launch_lanes<BACKWARD, kDtBF16, 8, I>(s, a, stream);
     return launch_lanes<BACKWARD, kDtBF16, 4, I>(s, a, stream);
   };
   return a.interleaved ? go(std::true_type{}) : go(std::false_type{});
@@ -423,6 +455,8 @@ hipError_t launch(const QkRope& a, hipStream_t stream) {
 
 }  // namespace
 
+// (Workgroups: no more than heads of all rows, and kMaxGroups and one more of q or
+// of k where that would have none.)
 size_t qk_rope_workspace(int64_t rows, int64_t heads, int64_t D) {
   return (size_t)std::min<int64_t>(rows * heads, kMaxGroups) * 2u * (size_t)D * 4u;
 }
