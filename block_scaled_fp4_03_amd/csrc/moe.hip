@@ -4,7 +4,8 @@
 //
 // Route.  The k largest logits of a token (ties to the lower expert) and their
 // softmax.  16 lanes hold a token (one DPP row), expert e in lane e % 16: the
-// largest of a lane's keys, then of the 16, k times.
+// largest of a lane's keys, then of the 16, k times.  A BF16 key and its expert
+// fit one word; of an FP32 key the expert is found after the largest.
 //
 // Sort.  A stable counting sort.  A wave ranks 64 entries at a time among
 // equal ids by one ballot for each bit of the id, and adds their number to its
@@ -43,20 +44,23 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return k == 0xFFFFFFFFu ? NAN : u2f((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// Rotations inside each row of 16 lanes (DPP row_ror): the largest key and the
-// sum over the row, in every lane.
+// Rotations inside each row of 16 lanes (DPP row_ror): the largest and the least
+// word and the sum over the row, in every lane.
 template <int CTRL>
-__device__ __forceinline__ uint64_t max_key_ror(uint64_t a) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)a, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(a >> 32), CTRL, 0xF, 0xF, false);
-  const uint64_t b = ((uint64_t)hi << 32) | lo;
-  return a > b ? a : b;
+__device__ __forceinline__ uint32_t ror_word(uint32_t a) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)a, CTRL, 0xF, 0xF, false);
 }
-__device__ __forceinline__ uint64_t row_max(uint64_t a) {
-  a = max_key_ror<0x121>(a);
-  a = max_key_ror<0x122>(a);
-  a = max_key_ror<0x124>(a);
-  return max_key_ror<0x128>(a);
+__device__ __forceinline__ uint32_t row_max(uint32_t a) {
+  a = max(a, ror_word<0x121>(a));
+  a = max(a, ror_word<0x122>(a));
+  a = max(a, ror_word<0x124>(a));
+  return max(a, ror_word<0x128>(a));
+}
+__device__ __forceinline__ uint32_t row_min(uint32_t a) {
+  a = min(a, ror_word<0x121>(a));
+  a = min(a, ror_word<0x122>(a));
+  a = min(a, ror_word<0x124>(a));
+  return min(a, ror_word<0x128>(a));
 }
 template <int CTRL>
 __device__ __forceinline__ float ror(float v) {
@@ -78,6 +82,18 @@ __device__ __forceinline__ float row_fmax(float v) {
 // e^(v - m), 0 for v = -inf whatever m is.
 __device__ __forceinline__ float weight_of(float v, float m) { return v == -INFINITY ? 0.0f : expf(v - m); }
 
+// The key of expert e's logit v; of BF16 the upper half (all there is) and, so
+// that the lower expert of equals is first, e's complement below.
+template <int DT>
+__device__ __forceinline__ uint32_t choice_key(float v, uint32_t e) {
+  const uint32_t k = order_key(v);
+  return DT == kDtF32 ? k : (k & 0xFFFF0000u) | (0xFFFFu - e);
+}
+template <int DT>
+__device__ __forceinline__ float choice_value(uint32_t k) {
+  return key_value(DT == kDtF32 ? k : (k & 0x80000000u) ? k & 0xFFFF0000u : k | 0xFFFFu);
+}
+
 // N: values a lane holds (16 N >= E).
 template <int DT, int N>
 __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ x, int64_t stride, uint32_t T, uint32_t E,
@@ -85,39 +101,48 @@ __global__ __launch_bounds__(256) void route_kernel(const void* __restrict__ x, 
                                                     float* __restrict__ weights) {
   const uint32_t lane = threadIdx.x & 15u, t = blockIdx.x * 16u + (threadIdx.x >> 4);
   const uint32_t row = t < T ? t : T - 1u;  // (every lane takes part in the moves)
-  uint32_t key[N];
+  uint32_t key[N];  // 0: none, or chosen already
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const uint32_t e = 16u * i + lane;
-    key[i] = e < E ? order_key(element<DT>(x, (size_t)row * (size_t)stride + e)) : 0u;
+    key[i] = e < E ? choice_key<DT>(element<DT>(x, (size_t)row * (size_t)stride + e), e) : 0u;
   }
-  float rest = 0.0f, top = 0.0f;
+  float rest = 0.0f, top = 0.0f, value = -INFINITY;
   uint32_t mine = 0u;       // lane j keeps the j-th choice
-  float value = -INFINITY;
   for (uint32_t j = 0; j < k; ++j) {
-    uint32_t best = 0u, at = 0u;
+    uint32_t best = key[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      at = key[i] > best ? 16u * i + lane : at;
-      best = key[i] > best ? key[i] : best;
+    for (int i = 1; i < N; ++i) best = max(best, key[i]);
+    best = row_max(best);
+    uint32_t e;
+    if (DT == kDtF32) {
+      e = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i) e = key[i] == best ? 16u * i + lane : e;
+      e = row_min(e);
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = 16u * i + lane == e ? 0u : key[i];
+    } else {
+      e = 0xFFFFu - (best & 0xFFFFu);
     }
-    const uint64_t first = row_max(((uint64_t)best << 32) | (uint32_t)~at);
-    const uint32_t e = ~(uint32_t)first;
-    const float v = key_value((uint32_t)(first >> 32));
+    const float v = choice_value<DT>(best);
     if (j == 0u) {
       top = v;
       if (!renormalise) {
+        rest = weight_of(DT == kDtF32 && (e & 15u) == lane ? v : -INFINITY, top);  // (gone from key[] already)
 #pragma unroll
         for (int i = 0; i < N; ++i)
-          if (key[i] != 0u) rest += weight_of(key_value(key[i]), top);
+          if (key[i] != 0u) rest += weight_of(choice_value<DT>(key[i]), top);
       }
     }
     if (lane == j) {
       mine = e;
       value = v;
     }
+    if (DT != kDtF32) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = 16u * i + lane == e ? 0u : key[i];
+      for (int i = 0; i < N; ++i) key[i] = key[i] == best ? 0u : key[i];
+    }
   }
   const float w = weight_of(value, top), sum = row_sum(renormalise ? w : rest);
   if (t < T && lane < k) {
@@ -230,9 +255,12 @@ struct RouteBackward {
 };
 
 // ---- sort ------------------------------------------------------------------
+// A chunk of entries is a workgroup's: small ones while their counters can be
+// summed where they are needed (64 chunks), large ones beyond, with a launch of
+// its own for the sums.
 constexpr uint32_t kSortWaves = 16, kSortThreads = 64 * kSortWaves;
-constexpr uint32_t kSortRounds = 8;                              // of 64 entries, a wave
-constexpr uint32_t kSortChunk = kSortThreads * kSortRounds;      // entries of a workgroup
+constexpr uint32_t kFewRounds = 2, kManyRounds = 8;              // of 64 entries, a wave
+constexpr uint32_t kFewChunks = 64;
 constexpr uint32_t kMaxBins = 512 + 2;                           // experts, unrouted, past the end
 
 // Bin of entry i: its expert, E for an id that is none, E + 1 past the end.
@@ -243,20 +271,47 @@ __device__ __forceinline__ uint32_t bin_of(const int32_t* ids, uint32_t i, uint3
 }
 
 // How many entries of each bin every chunk has: counts[chunk][E + 1].
+template <uint32_t ROUNDS>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* __restrict__ ids, uint32_t N,
                                                                   uint32_t E, uint32_t* __restrict__ counts) {
   __shared__ uint32_t count[kMaxBins];
+  const uint32_t base = blockIdx.x * (kSortThreads * ROUNDS) + threadIdx.x;
+  uint32_t bin[ROUNDS];
+#pragma unroll
+  for (uint32_t r = 0; r < ROUNDS; ++r) bin[r] = bin_of(ids, base + r * kSortThreads, N, E);
   for (uint32_t e = threadIdx.x; e < E + 2u; e += kSortThreads) count[e] = 0u;
   __syncthreads();
-  const uint32_t base = blockIdx.x * kSortChunk;
 #pragma unroll
-  for (uint32_t r = 0; r < kSortRounds; ++r) atomicAdd(&count[bin_of(ids, base + r * kSortThreads + threadIdx.x, N, E)], 1u);
+  for (uint32_t r = 0; r < ROUNDS; ++r) atomicAdd(&count[bin[r]], 1u);
   __syncthreads();
   for (uint32_t e = threadIdx.x; e < E + 1u; e += kSortThreads) counts[(size_t)blockIdx.x * (E + 1u) + e] = count[e];
 }
 
-// Places of a chunk's entries.  counts: sort_count_kernel's, or NULL where
-// there is one chunk.  Dynamic LDS: kSortWaves x (E + 2) counters.
+// counts[chunk][bin] to the sums over the chunks before, and row `chunks` to the
+// sums over all: 16 bins a workgroup, 64 runs of chunks each.
+__global__ __launch_bounds__(kSortThreads) void sort_scan_kernel(uint32_t* __restrict__ counts, uint32_t chunks,
+                                                                 uint32_t bins) {
+  __shared__ uint32_t run_sum[64][16];
+  const uint32_t e = blockIdx.x * 16u + (threadIdx.x & 15u), run = threadIdx.x >> 4, len = (chunks + 63u) / 64u;
+  const uint32_t b0 = min(run * len, chunks), b1 = e < bins ? min(b0 + len, chunks) : b0;
+  uint32_t sum = 0u;
+  for (uint32_t b = b0; b < b1; ++b) sum += counts[(size_t)b * bins + e];
+  run_sum[run][threadIdx.x & 15u] = sum;
+  __syncthreads();
+  uint32_t before = 0u;
+  for (uint32_t i = 0; i < run; ++i) before += run_sum[i][threadIdx.x & 15u];
+  for (uint32_t b = b0; b < b1; ++b) {
+    const uint32_t c = counts[(size_t)b * bins + e];
+    counts[(size_t)b * bins + e] = before;
+    before += c;
+  }
+  if (run == 63u && e < bins) counts[(size_t)chunks * bins + e] = before;
+}
+
+// Places of a chunk's entries.  counts: sort_count_kernel's (kFewRounds),
+// sort_scan_kernel's (kManyRounds), or NULL where there is one chunk.  Dynamic
+// LDS: kSortWaves x (E + 2) counters.
+template <uint32_t ROUNDS>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t* __restrict__ ids, uint32_t N,
                                                                   uint32_t k, uint32_t E, uint32_t bits,
                                                                   const uint32_t* __restrict__ counts,
@@ -264,16 +319,30 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
                                                                   int32_t* __restrict__ row_idx,
                                                                   int32_t* __restrict__ pos) {
   extern __shared__ uint32_t wave_count[];
-  __shared__ uint32_t start[kMaxBins], wave_sum[kSortWaves];
+  __shared__ uint32_t start[kMaxBins], wave_sum[kSortWaves], part[2][kSortThreads];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6, bins = E + 2u;
-  for (uint32_t i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) wave_count[i] = 0u;
-  const uint32_t base = blockIdx.x * kSortChunk + wave * 64u * kSortRounds + lane;
-  uint32_t bin[kSortRounds], rank[kSortRounds];
+  const uint32_t base = blockIdx.x * (kSortThreads * ROUNDS) + wave * 64u * ROUNDS + lane;
+  uint32_t bin[ROUNDS], rank[ROUNDS];
 #pragma unroll
-  for (uint32_t r = 0; r < kSortRounds; ++r) bin[r] = bin_of(ids, base + 64u * r, N, E);
+  for (uint32_t r = 0; r < ROUNDS; ++r) bin[r] = bin_of(ids, base + 64u * r, N, E);
+  for (uint32_t i = threadIdx.x; i < kSortWaves * bins; i += kSortThreads) wave_count[i] = 0u;
+  // Few chunks: a bin's counts of every `runs`-th chunk, all and those before this one.
+  const uint32_t runs = kSortThreads / (E + 1u), run = threadIdx.x / (E + 1u);
+  if (ROUNDS == kFewRounds && counts != nullptr && run < runs) {
+    const uint32_t at = threadIdx.x - run * (E + 1u);
+    uint32_t all = 0u, before = 0u;
+#pragma unroll 8
+    for (uint32_t b = run; b < gridDim.x; b += runs) {
+      const uint32_t c = counts[(size_t)b * (E + 1u) + at];
+      all += c;
+      before += b < blockIdx.x ? c : 0u;
+    }
+    part[0][threadIdx.x] = all;
+    part[1][threadIdx.x] = before;
+  }
   __syncthreads();
 #pragma unroll
-  for (uint32_t r = 0; r < kSortRounds; ++r) {
+  for (uint32_t r = 0; r < ROUNDS; ++r) {
     uint64_t same = ~0ull;  // lanes with this lane's bin
     for (uint32_t b = 0; b < bits; ++b) {
       const bool set = (bin[r] >> b) & 1u;
@@ -291,16 +360,24 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
   const uint32_t e = threadIdx.x;
   uint32_t total = 0u, mine = 0u;
   if (e <= E) {
+    uint32_t c[kSortWaves];
+#pragma unroll
+    for (uint32_t w = 0; w < kSortWaves; ++w) c[w] = wave_count[w * bins + e];
+#pragma unroll
     for (uint32_t w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = wave_count[w * bins + e];
       wave_count[w * bins + e] = total;
-      total += c;
+      total += c[w];
     }
     if (counts != nullptr) {
       total = 0u;
-      for (uint32_t b = 0; b < gridDim.x; ++b) {
-        if (b == blockIdx.x) mine = total;
-        total += counts[(size_t)b * (E + 1u) + e];
+      if (ROUNDS == kFewRounds) {
+        for (uint32_t i = 0; i < runs; ++i) {
+          total += part[0][i * (E + 1u) + e];
+          mine += part[1][i * (E + 1u) + e];
+        }
+      } else {
+        total = counts[(size_t)gridDim.x * (E + 1u) + e];
+        mine = counts[(size_t)blockIdx.x * (E + 1u) + e];
       }
     }
   }
@@ -319,7 +396,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
   if (blockIdx.x == 0u && e <= E) group_off[e] = (int32_t)(e < E ? at : N);
   __syncthreads();
 #pragma unroll
-  for (uint32_t r = 0; r < kSortRounds; ++r) {
+  for (uint32_t r = 0; r < ROUNDS; ++r) {
     const uint32_t i = base + 64u * r, b = bin[r];
     if (i >= N) continue;
     const uint32_t p = start[b] + wave_count[wave * bins + b] + rank[r];
@@ -530,29 +607,44 @@ hipError_t launch_moe_route_backward(const void* x, int dtype, int64_t stride, i
                                    ids, g, dx, s);
 }
 
-static uint32_t sort_chunks(int64_t entries) { return (uint32_t)((entries + kSortChunk - 1) / kSortChunk); }
+// Entries of a chunk, and the chunks.
+static bool sort_few(int64_t entries) { return entries <= (int64_t)kFewChunks * kSortThreads * kFewRounds; }
+static uint32_t sort_chunks(int64_t entries) {
+  const int64_t chunk = (int64_t)kSortThreads * (sort_few(entries) ? kFewRounds : kManyRounds);
+  return (uint32_t)((entries + chunk - 1) / chunk);
+}
 
 size_t moe_sort_workspace(int64_t entries, int64_t E) {
-  const uint32_t chunks = sort_chunks(entries);
-  return chunks <= 1u ? 0u : (size_t)chunks * (size_t)(E + 1) * 4u;
+  const size_t chunks = sort_chunks(entries);
+  return chunks <= 1u ? 0u : (chunks + 1u) * (size_t)(E + 1) * 4u;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int32_t k, int64_t E, int32_t* group_off, int32_t* row_idx,
                            int32_t* pos, void* workspace, hipStream_t s) {
   const int64_t entries = T * k;
-  const uint32_t chunks = sort_chunks(entries);
+  const uint32_t n = (uint32_t)entries, bins = (uint32_t)E + 1u, chunks = sort_chunks(entries);
   uint32_t* counts = chunks > 1u ? static_cast<uint32_t*>(workspace) : nullptr;
-  if (counts) {
-    sort_count_kernel<<<dim3(chunks), dim3(kSortThreads), 0, s>>>(ids, (uint32_t)entries, (uint32_t)E, counts);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   uint32_t bits = 1u;
   while ((1u << bits) < (uint32_t)E + 2u) ++bits;
   const size_t lds = kSortWaves * (size_t)(E + 2) * 4u;
-  sort_place_kernel<<<dim3(chunks ? chunks : 1u), dim3(kSortThreads), lds, s>>>(
-      ids, (uint32_t)entries, (uint32_t)k, (uint32_t)E, bits, counts, group_off, row_idx, pos);
-  return hipGetLastError();
+  const auto go = [&](auto rounds) {
+    constexpr uint32_t R = decltype(rounds)::value;
+    if (counts) {
+      sort_count_kernel<R><<<dim3(chunks), dim3(kSortThreads), 0, s>>>(ids, n, (uint32_t)E, counts);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (R == kManyRounds) {
+      sort_scan_kernel<<<dim3((bins + 15u) / 16u), dim3(kSortThreads), 0, s>>>(counts, chunks, bins);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    sort_place_kernel<R><<<dim3(chunks ? chunks : 1u), dim3(kSortThreads), lds, s>>>(
+        ids, n, (uint32_t)k, (uint32_t)E, bits, counts, group_off, row_idx, pos);
+    return hipGetLastError();
+  };
+  if (sort_few(entries)) return go(std::integral_constant<uint32_t, kFewRounds>{});
+  return go(std::integral_constant<uint32_t, kManyRounds>{});
 }
 
 // Workgroups of four waves, one wave to 64 vectors of a token.

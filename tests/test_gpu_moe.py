@@ -114,7 +114,8 @@ def _ids(T, k, E, seed, kind):
 
 @pytest.mark.parametrize("kind", ["random", "holes", "one", "none"])
 @pytest.mark.parametrize("T,k,E", [(0, 4, 8), (1, 1, 1), (1, 4, 32), (16, 4, 32), (63, 1, 3), (65, 2, 512), (1000, 8, 128),
-                                   (2048, 4, 60), (2049, 4, 60), (5000, 8, 256), (40000, 3, 512), (16384, 8, 128)])
+                                   (2048, 4, 60), (2049, 4, 60), (5000, 8, 256), (40000, 3, 512), (16384, 8, 128),
+                                   (32769, 4, 37), (70001, 8, 512), (300007, 2, 3)])
 def test_sort(T, k, E, kind):
     import block_scaled_fp4_03_amd as fp4
     say("sort %d x %d of %d, %s" % (T, k, E, kind))
