@@ -692,8 +692,13 @@ def _want_rows(t, name, ndim, device=None, like=None):
 
 def _run_on(stream, device):
     """The raw handle of the stream a call runs on: the given one, or the
-    device's current one."""
-    return stream.cuda_stream if stream is not None else _torch()._C._cuda_getCurrentRawStream(device.index)
+    device's current one.  The null stream is that of the current device, so
+    operands on another one are refused there (its other streams are its own)."""
+    C = _torch()._C
+    raw = stream.cuda_stream if stream is not None else C._cuda_getCurrentRawStream(device.index)
+    if raw == 0 and C._cuda_getDevice() != device.index:
+        raise ValueError("the operands are on %s, which is not the current device" % device)
+    return raw
 
 
 def _alloc(stream, make, *args, **kw):
@@ -709,6 +714,22 @@ def _alloc(stream, make, *args, **kw):
     if t is not None:
         t.record_stream(torch.cuda.current_stream())
     return t
+
+
+def _like(t, stream, dtype=None):
+    """A dense tensor of t's shape and device (and dtype) for the stream a call
+    runs on; half the time of torch.empty."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty_like(t, dtype=dtype, memory_format=torch.contiguous_format)
+    return _alloc(stream, torch.empty_like, t, dtype=dtype, memory_format=torch.contiguous_format)
+
+
+def _new(stream, shape, dtype, device):
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _alloc(stream, torch.empty, shape, dtype=dtype, device=device)
 
 
 class KVCache:
@@ -1038,17 +1059,26 @@ def _want_pos(rope, pos, rows, dev):
     if rope.device != dev:
         raise ValueError("rope is on %s, the call's operands on %s" % (rope.device, dev))
     torch = _torch()
-    if isinstance(pos, torch.Tensor) and pos.ndim == 1 and rope.axes == 1:
-        pos = pos.view(1, -1)
-    _want(pos, "pos", torch.int32, 2, dev)
-    if pos.shape[0] != rope.axes or pos.shape[1] != rows:
+    one = isinstance(pos, torch.Tensor) and pos.ndim == 1 and rope.axes == 1
+    _want(pos, "pos", torch.int32, 1 if one else 2, dev)
+    if pos.shape != ((rows,) if one else (rope.axes, rows)):
         raise ValueError("pos must have shape (%d, %d), got %s" % (rope.axes, rows, tuple(pos.shape)))
     return rope.ref, pos.data_ptr()
 
 
 def _want_heads(q, k):
     """q and k, rows x heads x head_dim of one dtype: its code, the device,
-    rows, head_dim and the row strides."""
+    their shapes and row strides."""
+    try:   # one test for two well-formed tensors; what follows names the fault of any others
+        dt, dev, qn, kn, qs, ks = q.dtype, q.device, q.shape, k.shape, q.stride(), k.stride()
+        rows, heads, dim = qn
+        if (k.dtype is dt and k.device == dev and dev.type == "cuda" and kn[0] == rows and kn[2] == dim and len(kn) == 3
+                and qs[2] == 1 == ks[2] and qs[1] == dim == ks[1] and qs[0] >= heads * dim and ks[0] >= kn[1] * dim):
+            torch = _torch()
+            if dt is torch.bfloat16 or dt is torch.float32:
+                return BF16 if dt is torch.bfloat16 else F32, dev, qn, kn, qs[0], ks[0]
+    except (AttributeError, IndexError, TypeError, ValueError):
+        pass
     code, qs = _want_rows(q, "q", 3)
     dev = q.device
     kcode, ks = _want_rows(k, "k", 3, dev)
@@ -1057,7 +1087,7 @@ def _want_heads(q, k):
         raise TypeError("k must be %s, got %s" % (q.dtype, k.dtype))
     if k.shape[0] != rows or k.shape[2] != dim:
         raise ValueError("k must have shape (%d, heads, %d), got %s" % (rows, dim, tuple(k.shape)))
-    return code, dev, rows, dim, qs, ks
+    return code, dev, q.shape, k.shape, qs, ks
 
 
 def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
@@ -1070,25 +1100,25 @@ def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=
     rope: a Rope, or None for no rotation; weights: float32 head_dim.  q_out,
     k_out may be q, k themselves.  Returns the two (new dense tensors unless
     given)."""
-    torch = _torch()
-    code, dev, rows, dim, qs, ks = _want_heads(q, k)
+    code, dev, (rows, qh, dim), (_, kh, _), qs, ks = _want_heads(q, k)
     ref, at = _want_pos(rope, pos, rows, dev)
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _want(t, name, torch.float32, 1, dev, dim)
+    f32 = _torch().float32
+    if q_weight is not None:
+        _want(q_weight, "q_weight", f32, 1, dev, dim)
+    if k_weight is not None:
+        _want(k_weight, "k_weight", f32, 1, dev, dim)
     if q_out is None:
-        q_out = _alloc(stream, torch.empty, q.shape, dtype=q.dtype, device=dev)
-        qos = q.shape[1] * dim
+        q_out, qos = _like(q, stream), qh * dim
     else:
         qos = _want_rows(q_out, "q_out", 3, dev, q)[1]
     if k_out is None:
-        k_out = _alloc(stream, torch.empty, k.shape, dtype=k.dtype, device=dev)
-        kos = k.shape[1] * dim
+        k_out, kos = _like(k, stream), kh * dim
     else:
         kos = _want_rows(k_out, "k_out", 3, dev, k)[1]
-    rc = lib().fp4_qk_norm_rope(ref, at, q.data_ptr(), qs, q.shape[1], k.data_ptr(), ks, k.shape[1], dim, code,
-                                _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), qos, k_out.data_ptr(), kos,
-                                rows, _run_on(stream, dev))
+    rc = lib().fp4_qk_norm_rope(ref, at, q.data_ptr(), qs, qh, k.data_ptr(), ks, kh, dim, code,
+                                None if q_weight is None else q_weight.data_ptr(),
+                                None if k_weight is None else k_weight.data_ptr(), eps, q_out.data_ptr(), qos,
+                                k_out.data_ptr(), kos, rows, _run_on(stream, dev))
     if rc != 0:
         _check(rc, "fp4_qk_norm_rope")
     return q_out, k_out
@@ -1109,37 +1139,34 @@ def qk_norm_rope_backward(gq, gk, q, k, rope, pos, q_weight=None, k_weight=None,
     (dq, dk, the gradients of q_weight and k_weight: float32, None for a weight
     that is None)."""
     torch = _torch()
-    code, dev, rows, dim, qs, ks = _want_heads(q, k)
+    code, dev, (rows, qh, dim), (_, kh, _), qs, ks = _want_heads(q, k)
     gqs = _want_rows(gq, "gq", 3, dev, q)[1]
     gks = _want_rows(gk, "gk", 3, dev, k)[1]
     ref, at = _want_pos(rope, pos, rows, dev)
-    f32 = torch.float32
     grads = []
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _want(t, name, f32, 1, dev, dim)
-        grads.append(None if t is None else _alloc(stream, torch.zeros, dim, dtype=f32, device=dev)
-                     if (q if name[0] == "q" else k).shape[1] == 0
-                     else _alloc(stream, torch.empty, dim, dtype=f32, device=dev))
+    for t, name, heads in ((q_weight, "q_weight", qh), (k_weight, "k_weight", kh)):
+        if t is None:
+            grads.append(None)
+            continue
+        _want(t, name, torch.float32, 1, dev, dim)
+        # (Without heads the call has no weight to give a gradient of.)
+        grads.append(_alloc(stream, torch.empty if heads else torch.zeros, dim, dtype=torch.float32, device=dev))
     if dq is None:
-        dq = _alloc(stream, torch.empty, q.shape, dtype=q.dtype, device=dev)
-        dqs = q.shape[1] * dim
+        dq, dqs = _like(q, stream), qh * dim
     else:
         dqs = _want_rows(dq, "dq", 3, dev, q)[1]
     if dk is None:
-        dk = _alloc(stream, torch.empty, k.shape, dtype=k.dtype, device=dev)
-        dks = k.shape[1] * dim
+        dk, dks = _like(k, stream), kh * dim
     else:
         dks = _want_rows(dk, "dk", 3, dev, k)[1]
     if ws is not None:
         _want(ws, "ws", torch.uint8, 1, dev)
     elif q_weight is not None or k_weight is not None:
-        ws = _alloc(stream, qk_norm_rope_workspace, rows, q.shape[1], k.shape[1], dim, dev)
-    rc = lib().fp4_qk_norm_rope_backward(ref, at, gq.data_ptr(), gqs, gk.data_ptr(), gks, q.data_ptr(), qs,
-                                         q.shape[1], k.data_ptr(), ks, k.shape[1], dim, code, _ptr(q_weight),
-                                         _ptr(k_weight), eps, dq.data_ptr(), dqs, dk.data_ptr(), dks, _ptr(grads[0]),
-                                         _ptr(grads[1]), rows, _ptr(ws), 0 if ws is None else ws.numel(),
-                                         _run_on(stream, dev))
+        ws = _alloc(stream, qk_norm_rope_workspace, rows, qh, kh, dim, dev)
+    rc = lib().fp4_qk_norm_rope_backward(ref, at, gq.data_ptr(), gqs, gk.data_ptr(), gks, q.data_ptr(), qs, qh,
+                                         k.data_ptr(), ks, kh, dim, code, _ptr(q_weight), _ptr(k_weight), eps,
+                                         dq.data_ptr(), dqs, dk.data_ptr(), dks, _ptr(grads[0]), _ptr(grads[1]), rows,
+                                         _ptr(ws), 0 if ws is None else ws.numel(), _run_on(stream, dev))
     if rc != 0:
         _check(rc, "fp4_qk_norm_rope_backward")
     return dq, dk, grads[0], grads[1]
@@ -1157,8 +1184,8 @@ def moe_route(logits, top_k, renormalise=True, stream=None):
     code, stride = _want_rows(logits, "logits", 2)
     dev = logits.device
     T, E = logits.shape
-    ids = _alloc(stream, torch.empty, (T, max(top_k, 0)), dtype=torch.int32, device=dev)
-    weights = _alloc(stream, torch.empty, (T, max(top_k, 0)), dtype=torch.float32, device=dev)
+    ids = _new(stream, (T, max(top_k, 0)), torch.int32, dev)
+    weights = _like(ids, stream, torch.float32)
     rc = lib().fp4_moe_route(logits.data_ptr(), code, stride, T, E, top_k, 1 if renormalise else 0, ids.data_ptr(),
                              weights.data_ptr(), _run_on(stream, dev))
     if rc != 0:
@@ -1203,9 +1230,9 @@ def moe_sort(ids, experts, ws=None, stream=None):
     _need(ids, "ids", (i32,), ndim=2)
     dev = ids.device
     T, k = ids.shape
-    off = _alloc(stream, torch.empty, max(experts, 0) + 1, dtype=i32, device=dev)
-    rows = _alloc(stream, torch.empty, T * k, dtype=i32, device=dev)
-    pos = _alloc(stream, torch.empty, (T, k), dtype=i32, device=dev)
+    off = _new(stream, max(experts, 0) + 1, i32, dev)
+    rows = _new(stream, T * k, i32, dev)
+    pos = _like(ids, stream)
     if ws is None:
         ws = _alloc(stream, moe_sort_workspace, T, k, experts, dev)
     else:
@@ -1231,7 +1258,7 @@ def moe_gather(x, pos, out=None, stream=None):
     if pos.shape[0] != T:
         raise ValueError("pos has %d rows, x %d" % (pos.shape[0], T))
     if out is None:
-        out = _alloc(stream, torch.empty, (T * k, H), dtype=x.dtype, device=dev)
+        out = _new(stream, (T * k, H), x.dtype, dev)
     else:
         _want(out, "out", x.dtype, 2, dev)
         if out.shape[1] != H:
@@ -1260,10 +1287,9 @@ def moe_combine(y, pos, weights=None, out=None, stream=None):
     """Rows of y (dense, in expert order) joined to tokens: sum over j of
     weights[t, j] (float32; None: 1) times y[pos[t, j]]; see fp4_moe_combine in
     include/fp4.h.  out: default a new T x H tensor; may have any row stride."""
-    torch = _torch()
     code, dev, T, k, H = _want_entries(y, pos, weights)
     if out is None:
-        out = _alloc(stream, torch.empty, (T, H), dtype=y.dtype, device=dev)
+        out = _new(stream, (T, H), y.dtype, dev)
         stride = H
     else:
         ocode, stride = _want_rows(out, "out", 2, dev)
@@ -1280,7 +1306,6 @@ def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
     """Gradient of moe_combine from that of its result (g, T x H of y's dtype,
     any row stride); see fp4_moe_combine_backward in include/fp4.h.  Returns
     (dy, of y's shape, and the weights' gradient, float32 T x top_k)."""
-    torch = _torch()
     if weights is None:
         raise ValueError("without weights the gradient is moe_gather's")
     code, dev, T, k, H = _want_entries(y, pos, weights)
@@ -1288,10 +1313,10 @@ def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
     if gcode != code or tuple(g.shape) != (T, H):
         raise ValueError("g must have shape %s and y's dtype, got %s %s" % ((T, H), tuple(g.shape), g.dtype))
     if dy is None:
-        dy = _alloc(stream, torch.empty, y.shape, dtype=y.dtype, device=dev)
+        dy = _like(y, stream)
     else:
         _need_out(dy, "dy", y.shape, (y.dtype,), dev)
-    dw = _alloc(stream, torch.empty, (T, k), dtype=torch.float32, device=dev)
+    dw = _like(weights, stream)
     rc = lib().fp4_moe_combine_backward(g.data_ptr(), stride, y.data_ptr(), code, pos.data_ptr(), weights.data_ptr(),
                                         T, k, H, y.shape[0], dy.data_ptr(), dw.data_ptr(), _run_on(stream, dev))
     if rc != 0:
@@ -1362,9 +1387,9 @@ def verify_drafts(target, draft, tokens, u, temperature=None, ws=None, stream=No
     if temperature is not None:
         _want(temperature, "temperature", torch.float32, 1, dev, B)
     V = target.shape[2]
-    out = _alloc(stream, torch.empty, (B, G + 1), dtype=torch.int32, device=dev)
-    accepted = _alloc(stream, torch.empty, B, dtype=torch.int32, device=dev)
-    chance = _alloc(stream, torch.empty, (B, G), dtype=torch.float32, device=dev)
+    out = _like(u, stream, torch.int32)
+    accepted = _new(stream, B, torch.int32, dev)
+    chance = _like(tokens, stream, torch.float32)
     if ws is None:
         ws = _alloc(stream, verify_workspace, B, G, V, dev)
     else:

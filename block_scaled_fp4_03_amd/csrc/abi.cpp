@@ -1149,8 +1149,7 @@ int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int d
 
 static bool verify_shape_ok(int64_t B, int64_t G, int64_t V) {
   if (B < 0 || B > 65535 || G < 0 || G > 32 || V < 1 || V > (int64_t(1) << 24)) return false;
-  // A workgroup of 256 to every 4096 logits of a row drawn from.
-  return B * ((V + 4095) / 4096) * 256 <= kMaxWorkItems;
+  return B * (2 * G + 1) * V <= int64_t(1) << 40;
 }
 
 size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V) {

@@ -54,7 +54,7 @@ struct Args {
   Part* parts;       // B x rows x splits x kWaves; rows: G + 1 of the target, G of the draft
   double* sums;      // B x chunks
   Chosen* chosen;    // B
-  uint32_t* arrived; // 2 x B counters, zero before and after each call
+  uint32_t* arrived; // 2 x B counters, zero before and after each launch
 };
 
 template <int DT>
@@ -672,33 +672,49 @@ hipError_t launch(const Args& a, hipStream_t stream) {
 
 }  // namespace
 
-// The counters come first; a whole number of 16 bytes of them.
-static size_t counter_bytes(int64_t B) { return ((size_t)B * 8u + 15u) & ~(size_t)15u; }
+// A launch takes at most kBatch sequences, whose counters come first: at one
+// place whatever the call, so that no call's data lie where another's counters do.
+static constexpr int64_t kBatch = 1024;
+static constexpr size_t kCounterBytes = kBatch * 8;
 
 // For calls with and without draft logits.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
-  const int64_t with = B * (2 * G + 1) * splits_of(B, 2 * G + 1, V), without = B * (G + 1) * splits_of(B, G + 1, V);
-  return counter_bytes(B) + (size_t)std::max(with, without) * kWaves * sizeof(Part) + (size_t)B * chunks_of(V) * 8u +
-         (size_t)B * sizeof(Chosen);
+  const int64_t n = std::min(B, kBatch);
+  const int64_t with = n * (2 * G + 1) * splits_of(n, 2 * G + 1, V), without = n * (G + 1) * splits_of(n, G + 1, V);
+  return kCounterBytes + (size_t)std::max(with, without) * kWaves * sizeof(Part) + (size_t)n * chunks_of(V) * 8u +
+         (size_t)n * sizeof(Chosen);
 }
 
 hipError_t launch_verify(const Verify& v, hipStream_t stream) {
   Args a{};
-  a.v = v;
-  a.B = (uint32_t)v.B;
+  const int64_t most = std::min(v.B, kBatch), size = v.dtype == kDtF32 ? 4 : 2;
   a.G = (uint32_t)v.G;
   a.V = (uint32_t)v.V;
   a.rows = (uint32_t)(v.draft ? 2 * v.G + 1 : v.G + 1);
-  a.splits = splits_of(v.B, a.rows, v.V);
+  a.splits = splits_of(most, a.rows, v.V);
   a.chunks = chunks_of(v.V);
   // A wave has one chunk while the chip has room, and more in a large batch.
-  a.per = std::max<uint32_t>(1u, (uint32_t)((int64_t)a.B * a.chunks / kWantedWaves));
+  a.per = std::max<uint32_t>(1u, (uint32_t)(most * a.chunks / kWantedWaves));
   a.groups = (a.chunks + a.per * kWaves - 1u) / (a.per * kWaves);
   a.arrived = static_cast<uint32_t*>(v.workspace);
-  a.chosen = reinterpret_cast<Chosen*>(static_cast<uint8_t*>(v.workspace) + counter_bytes(v.B));
-  a.sums = reinterpret_cast<double*>(a.chosen + a.B);
-  a.parts = reinterpret_cast<Part*>(a.sums + (size_t)a.B * a.chunks);
-  return v.dtype == kDtF32 ? launch<kDtF32>(a, stream) : launch<kDtBF16>(a, stream);
+  a.chosen = reinterpret_cast<Chosen*>(static_cast<uint8_t*>(v.workspace) + kCounterBytes);
+  a.sums = reinterpret_cast<double*>(a.chosen + most);
+  a.parts = reinterpret_cast<Part*>(a.sums + (size_t)most * a.chunks);
+  for (int64_t b = 0; b < v.B; b += kBatch) {
+    a.v = v;
+    a.B = (uint32_t)std::min(v.B - b, kBatch);
+    a.v.target = static_cast<const uint8_t*>(v.target) + b * v.target_seq * size;
+    if (v.draft) a.v.draft = static_cast<const uint8_t*>(v.draft) + b * v.draft_seq * size;
+    if (v.tokens) a.v.tokens = v.tokens + b * v.G;
+    a.v.u = v.u + b * (v.G + 1);
+    if (v.temperature) a.v.temperature = v.temperature + b;
+    a.v.out = v.out + b * (v.G + 1);
+    a.v.accepted = v.accepted + b;
+    if (v.chance) a.v.chance = v.chance + b * v.G;
+    const hipError_t e = v.dtype == kDtF32 ? launch<kDtF32>(a, stream) : launch<kDtBF16>(a, stream);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace fp4

@@ -56,6 +56,17 @@ def test_shapes(B, G, V, dtype):
     assert kept > 0 or G == 0
 
 
+def test_more_sequences_than_a_launch_takes():
+    import torch
+    say("verify, 2300 sequences")
+    for draft in (True, False):
+        kept = _check(_case(torch, 2300, 1, 37, "bf16", 21, draft=draft))
+        assert 0 < kept.sum() < 2300
+    s = _case(torch, 1025, 2, 5003, "f32", 22, draft=False)
+    s["temperature"] = None
+    _check(s)
+
+
 def test_every_outcome():
     """Over many sequences: none kept, some, all, and greedy ones of each."""
     import torch

@@ -242,6 +242,22 @@ def test_wrappers_refuse_before_the_library():
         fp4.verify_drafts(f((2, 4, 9), dtype=i32), None, f((2, 3), dtype=i32), f((2, 4)))
 
 
+def test_null_stream_of_another_device(monkeypatch):
+    """The null stream is the current device's: operands on another one are refused
+    there, and run on a stream of their own."""
+    torch = pytest.importorskip("torch")
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    assert fp4._run_on(None, torch.device("cuda", 0)) == 0
+    with pytest.raises(ValueError):
+        fp4._run_on(None, torch.device("cuda", 1))
+    assert fp4._run_on(Stream(), torch.device("cuda", 1)) == 77
+
+
 def test_struct_layout():
     assert ctypes.sizeof(fp4.RopeStruct) == 40
     assert fp4.RopeStruct.sections.offset == 16 and fp4.RopeStruct.flags.offset == 32
