@@ -79,11 +79,11 @@ __device__ __forceinline__ uint64_t order_key(float v, uint32_t i) {
   return ((uint64_t)((u & 0x80000000u) ? ~u : u | 0x80000000u) << 32) | (uint32_t)~i;
 }
 
-// 256 log2 e / temperature; -1 where the sequence is greedy.
-__device__ __forceinline__ double units_of(const Args& a, uint32_t b) {
-  const float t = a.v.temperature ? a.v.temperature[b] : 1.0f;
-  return t > 0.0f ? 256.0 * kLog2e / (double)t : -1.0;
+__device__ __forceinline__ float temperature_of(const Args& a, uint32_t b) {
+  return a.v.temperature ? a.v.temperature[b] : 1.0f;
 }
+// 256 log2 e / temperature; -1 where the sequence is greedy.
+__device__ __forceinline__ double units_of(float t) { return t > 0.0f ? 256.0 * kLog2e / (double)t : -1.0; }
 
 // 2^(j / 256), less j in the upper word's bits from 12 on: with k << 12 added
 // there, entry k % 256 gives 2^(k / 256) at once.
@@ -114,9 +114,13 @@ __device__ __forceinline__ double power(const Powers& table, uint32_t k) {
   return __builtin_bit_cast(double, u32x2{e[0], e[1] + (k << 12)});
 }
 
-__device__ __forceinline__ void fill_table(Powers& table) {
-  static_assert(kTable == kThreads, "a thread fills one entry");
-  table[threadIdx.x] = __builtin_bit_cast(u32x2, kPowers.v[threadIdx.x]);
+// A thread's entry, asked for before it is needed, and the table from them.
+__device__ __forceinline__ u32x2 table_entry() {
+  static_assert(kTable == kThreads, "a thread has one entry");
+  return __builtin_bit_cast(u32x2, kPowers.v[threadIdx.x]);
+}
+__device__ __forceinline__ void fill_table(Powers& table, u32x2 entry) {
+  table[threadIdx.x] = entry;
   __syncthreads();
 }
 
@@ -290,30 +294,46 @@ __device__ __forceinline__ void values(const u32x4& w, float (&v)[N]) {
 // A wave's part of a split: blocks [b0, b1) of 16 bytes that lie wholly in the
 // row, every fourth 1 KB of them, and, in split 0, the elements beside them.
 template <int DT>
-__device__ __forceinline__ Running row_part(const uint8_t* p, uint32_t V, uint32_t split, uint32_t splits, double c,
-                                            const Powers& table) {
-  constexpr uint32_t E = 16u / kSize<DT>, U = 2u;
-  const uint32_t head = min((uint32_t)(-reinterpret_cast<intptr_t>(p) & 15) / kSize<DT>, V);
-  const uint32_t blocks = (V - head) / E, tail = head + blocks * E;
-  constexpr uint32_t kStep = U * kThreads;  // a split has whole steps, but the last
-  const uint32_t steps = (blocks + kStep - 1u) / kStep;
-  const uint32_t b0 = steps * split / splits * kStep, b1 = min(steps * (split + 1u) / splits * kStep, blocks);
-  const u32x4* from = reinterpret_cast<const u32x4*>(p + (size_t)head * kSize<DT>);
-  const bool edge = split == 0u && threadIdx.x < head + (V - tail);
-  const uint32_t edge_at = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
-  Running s{0.0, -INFINITY, false, 0ull};
-  constexpr uint32_t kLowest = DT == kDtF32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+struct RowPart {
+  static constexpr uint32_t E = 16u / kSize<DT>, U = 2u;
+  static constexpr uint32_t kStep = U * kThreads;  // a split has whole steps, but the last
+  static constexpr uint32_t kLowest = DT == kDtF32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
+  const uint8_t* p;
+  const u32x4* from;
+  uint32_t head, b0, b1, edge_at;
+  bool first, edge;
+  u32x4 next[U];  // the first step's blocks, on their way
+
+  __device__ __forceinline__ RowPart(const uint8_t* p_, uint32_t V, uint32_t split, uint32_t splits) : p(p_) {
+    head = min((uint32_t)(-reinterpret_cast<intptr_t>(p) & 15) / kSize<DT>, V);
+    const uint32_t blocks = (V - head) / E, tail = head + blocks * E, steps = (blocks + kStep - 1u) / kStep;
+    b0 = steps * split / splits * kStep;
+    b1 = min(steps * (split + 1u) / splits * kStep, blocks);
+    from = reinterpret_cast<const u32x4*>(p + (size_t)head * kSize<DT>);
+    first = split == 0u;
+    edge = first && threadIdx.x < head + (V - tail);
+    edge_at = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+    if (b0 < b1) load(b0, next);
+  }
   // Blocks of the step at j0 (those past the end: the last one).
-  const auto load = [&](uint32_t j0, u32x4 (&w)[U]) __attribute__((always_inline)) {
+  __device__ __forceinline__ void load(uint32_t j0, u32x4 (&w)[U]) const {
 #pragma unroll
     for (uint32_t u = 0; u < U; ++u) w[u] = from[min(j0 + u * kThreads + threadIdx.x, b1 - 1u)];
-  };
+  }
+  __device__ __forceinline__ Running run(double c, const Powers& table);
+};
+
+template <int DT>
+__device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& table) {
+  Running s{0.0, -INFINITY, false, 0ull};
   if (c < 0.0) {
     float best = -INFINITY;
     uint32_t at = 0u;
     for (uint32_t j0 = b0; j0 < b1; j0 += U * kThreads) {
       u32x4 w[U];
-      load(j0, w);
+#pragma unroll
+      for (uint32_t u = 0; u < U; ++u) w[u] = next[u];
+      load(j0 + U * kThreads, next);
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u) {
         float v[E];
@@ -339,8 +359,6 @@ __device__ __forceinline__ Running row_part(const uint8_t* p, uint32_t V, uint32
   }
   WaveSum sum(c);
   uint32_t j0 = b0;
-  u32x4 next[U];
-  if (b0 < b1) load(b0, next);
   for (; j0 < b1; j0 += U * kThreads) {  // (the same steps for every lane)
     u32x4 w[U];
     float m = -INFINITY;  // the lane's largest logit of this step
@@ -388,7 +406,7 @@ __device__ __forceinline__ Running row_part(const uint8_t* p, uint32_t V, uint32
     for (uint32_t i = 0; i < E; ++i)
       if (in) sum.add(logit<DT>(from + j0 + threadIdx.x, i), table);
   }
-  if (split == 0u) {
+  if (first) {
     const float v = edge ? logit<DT>(p, edge_at) : -INFINITY;
     if (__any(!(v <= sum.passes))) sum.move(v, table);
     sum.add(v, table);
@@ -500,11 +518,14 @@ template <int DT>
 __global__ __launch_bounds__(kThreads) void stats_kernel(Args a) {
   __shared__ Shared sh;
   const uint32_t split = blockIdx.x % a.splits, n = blockIdx.x / a.splits, b = n / a.rows, row = n - b * a.rows;
-  const double c = units_of(a, b);
+  const float temperature = temperature_of(a, b);
+  const u32x2 entry = table_entry();
+  RowPart<DT> part(row_at<DT>(a, b, row), a.V, split, a.splits);
+  const double c = units_of(temperature);
   const bool greedy = c < 0.0;
   if (greedy && row > a.G) return;  // the draft's distribution is not asked for
-  fill_table(sh.table);
-  const Running s = row_part<DT>(row_at<DT>(a, b, row), a.V, split, a.splits, c, sh.table);
+  fill_table(sh.table, entry);
+  const Running s = part.run(c, sh.table);
   {
     const uint64_t value = greedy ? wave_max(s.key) : __builtin_bit_cast(uint64_t, wave_sum(s.sum));  // (lanes share r)
     const uint64_t bad = __ballot(s.bad) != 0ull ? 1ull : 0ull;
@@ -596,10 +617,12 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   __shared__ Shared sh;
   const uint32_t group = blockIdx.x % a.groups, b = blockIdx.x / a.groups, lane = threadIdx.x & 63u;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const float temperature = temperature_of(a, b);
+  const u32x2 entry = table_entry();
   Chosen s = a.chosen[b];
   if (s.q == kNoDraw) return;
-  const double c = units_of(a, b);
-  fill_table(sh.table);
+  const double c = units_of(temperature);
+  fill_table(sh.table, entry);
   const uint8_t* p = row_at<DT>(a, b, s.row);
   const uint8_t* q = s.q == kQDraft ? row_at<DT>(a, b, a.G + 1u + s.row) : nullptr;
   double* sums = a.sums + (size_t)b * a.chunks;
