@@ -12,6 +12,7 @@ computation runs in the HIP kernels of libfp4.so.  There is no fallback -- if
 the library is not built, or no GPU is present, the calls fail loudly.
 """
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -1076,6 +1077,8 @@ def _want_heads(q, k):
                 and qs[2] == 1 == ks[2] and qs[1] == dim == ks[1] and qs[0] >= heads * dim and ks[0] >= kn[1] * dim):
             torch = _torch()
             if dt is torch.bfloat16 or dt is torch.float32:
+                if rows <= 1:   # (then a stride is no more than a number)
+                    return BF16 if dt is torch.bfloat16 else F32, dev, qn, kn, heads * dim, kn[1] * dim
                 return BF16 if dt is torch.bfloat16 else F32, dev, qn, kn, qs[0], ks[0]
     except (AttributeError, IndexError, TypeError, ValueError):
         pass
@@ -1184,7 +1187,7 @@ def moe_route(logits, top_k, renormalise=True, stream=None):
     code, stride = _want_rows(logits, "logits", 2)
     dev = logits.device
     T, E = logits.shape
-    ids = _new(stream, (T, max(top_k, 0)), torch.int32, dev)
+    ids = _new(stream, (T, min(max(top_k, 0), E)), torch.int32, dev)   # (top_k > E is refused below)
     weights = _like(ids, stream, torch.float32)
     rc = lib().fp4_moe_route(logits.data_ptr(), code, stride, T, E, top_k, 1 if renormalise else 0, ids.data_ptr(),
                              weights.data_ptr(), _run_on(stream, dev))
@@ -1213,9 +1216,14 @@ def moe_route_backward(logits, ids, g, renormalise=True, stream=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _sort_bytes(tokens, top_k, experts):
+    return fp4_moe_sort_workspace(tokens, top_k, experts)
+
+
 def moe_sort_workspace(tokens, top_k, experts, device="cuda"):
     """A workspace tensor for moe_sort (or None)."""
-    n = fp4_moe_sort_workspace(tokens, top_k, experts)
+    n = _sort_bytes(tokens, top_k, experts)
     return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
 
 
@@ -1230,13 +1238,13 @@ def moe_sort(ids, experts, ws=None, stream=None):
     _need(ids, "ids", (i32,), ndim=2)
     dev = ids.device
     T, k = ids.shape
-    off = _new(stream, max(experts, 0) + 1, i32, dev)
-    rows = _new(stream, T * k, i32, dev)
+    off = _alloc(stream, ids.new_empty, max(experts, 0) + 1)
+    rows = _alloc(stream, ids.new_empty, T * k)
     pos = _like(ids, stream)
-    if ws is None:
-        ws = _alloc(stream, moe_sort_workspace, T, k, experts, dev)
-    else:
+    if ws is not None:
         _want(ws, "ws", torch.uint8, 1, dev)
+    elif _sort_bytes(T, k, experts):
+        ws = _alloc(stream, moe_sort_workspace, T, k, experts, dev)
     rc = lib().fp4_moe_sort(ids.data_ptr(), T, k, experts, off.data_ptr(), rows.data_ptr(), pos.data_ptr(), _ptr(ws),
                             0 if ws is None else ws.numel(), _run_on(stream, dev))
     if rc != 0:

@@ -831,8 +831,8 @@ int fp4_logprobs_backward(const void* x, int dtype, int64_t stride, int64_t N, i
 static int64_t per16(int dtype) { return dtype == FP4_F32 ? 4 : 8; }
 
 static bool qk_shape_ok(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim) {
-  // (A wave to a row at least.)
-  return rows >= 0 && rows <= kMaxDim && rows * 64 + 255 <= kMaxWorkItems && q_heads >= 0 && k_heads >= 0 && q_heads <= 65535 &&
+  // (A wave to a row of q and one to a row of k at least, four to a workgroup.)
+  return rows >= 0 && rows <= kMaxDim && rows * 128 + 511 <= kMaxWorkItems && q_heads >= 0 && k_heads >= 0 && q_heads <= 65535 &&
          k_heads <= 65535 && head_dim >= 32 && head_dim <= 256 && head_dim % 8 == 0;
 }
 
@@ -1078,8 +1078,9 @@ static bool rows_shape_ok(int dtype, int64_t T, int32_t top_k, int64_t H, int64_
   if (T < 0 || T > kMaxDim || top_k < 0 || top_k > kMaxEntryK || T * top_k > kMaxDim || rows < 0 || rows > kMaxDim)
     return false;
   if (H < 1 || H > kMaxDim || H % per16(dtype) != 0 || stride < H || stride > kMaxDim) return false;
-  // One wave to 64 vectors of 16 bytes.
-  return T * ((H / per16(dtype) + 63) / 64) * 64 + 255 <= kMaxWorkItems;
+  // One wave to 64 vectors of 16 bytes; in the gradient up to four to a token.
+  const int64_t waves = (H / per16(dtype) + 63) / 64;
+  return T * (waves > 4 ? waves : 4) * 64 + 255 <= kMaxWorkItems;
 }
 
 int fp4_moe_gather(const void* x, int dtype, int64_t stride, const int32_t* pos, int64_t T, int32_t top_k, int64_t H,

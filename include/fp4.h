@@ -599,7 +599,7 @@ typedef struct fp4_rope {
  *   not overlap an input otherwise.  Either may have no heads.
  *   head_dim: a multiple of 8 from 32 to 256.  q_weight, k_weight: head_dim FP32
  *   or NULL.  eps >= 0.  pos: device int32, axes x rows, dense, any values.
- *   rope NULL: no rotation.
+ *   rope NULL: no rotation.  rows < 2^25.
  * rows == 0 is a no-op. */
 int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, int64_t q_stride, int64_t q_heads,
                      const void* k, int64_t k_stride, int64_t k_heads, int64_t head_dim, int dtype,
@@ -668,7 +668,8 @@ int fp4_moe_sort(const int32_t* ids, int64_t T, int32_t top_k, int64_t E, int32_
  *   x: T rows of H values of dtype, row t at element t * stride; out: `rows` rows
  *   of H, dense.  16-byte aligned, H and stride multiples of 16 bytes.  An entry
  *   whose r is no row (r >= rows) is skipped; two entries for one row race.
- *   0 <= top_k <= 64.  Its gradient is fp4_moe_combine without weights.
+ *   0 <= top_k <= 64; T < 2^24 and T * (H rounded up to 1 KB) below 2^32 * 16 bytes,
+ *   for this call and the two below.  Its gradient is fp4_moe_combine without weights.
  * T == 0 is a no-op. */
 int fp4_moe_gather(const void* x, int dtype, int64_t stride, const int32_t* pos, int64_t T, int32_t top_k, int64_t H,
                    int64_t rows, void* out, void* stream);

@@ -167,6 +167,17 @@ def test_strides_and_in_place():
         assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and (rest[:, 7:] == 1).all()
 
 
+def test_one_row_of_any_stride():
+    """A single row's stride is no more than a number: an odd one is no obstacle."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    s = _case(torch, 1, 4, 2, 64, "bf16")
+    want = fp4.qk_norm_rope(s["q"], s["k"], s["rope"], s["pos"], s["wq"], s["wk"])
+    q, k = (s[n].as_strided(s[n].shape, (777, 64, 1), s[n].storage_offset()) for n in "qk")
+    got = fp4.qk_norm_rope(q, k, s["rope"], s["pos"], s["wq"], s["wk"])
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_no_rows():
     """No rows: empty outputs, and gradients of the weights that are 0."""
     import torch

@@ -60,6 +60,7 @@ def test_rope_faults(call, kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=2), DTYPE), (dict(D=24), SHAPE), (dict(D=68), SHAPE), (dict(D=264), SHAPE), (dict(hq=-1), SHAPE),
     (dict(hk=65536), SHAPE), (dict(rows=-1), SHAPE), (dict(rows=1 << 40), SHAPE), (dict(rows=1 << 62), SHAPE),
+    (dict(rows=1 << 25), SHAPE),
     (dict(qs=255), SHAPE), (dict(ks=127), SHAPE), (dict(eps=-1.0), SHAPE), (dict(eps=NAN), SHAPE),
     (dict(eps=INF), SHAPE), (dict(q=None), NULL), (dict(k=None), NULL), (dict(pos=None), NULL),
     (dict(pos=FAKE + 2), ALIGN), (dict(q=FAKE + 8), ALIGN), (dict(k=FAKE + 2), ALIGN), (dict(qs=260), ALIGN),
@@ -165,7 +166,7 @@ def combine_back(**kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(dt=2), DTYPE), (dict(T=-1), SHAPE), (dict(k=-1), SHAPE), (dict(k=65), SHAPE), (dict(H=0), SHAPE),
     (dict(H=60), SHAPE), (dict(dt=0, H=62), SHAPE), (dict(st=56), SHAPE), (dict(rows=-1), SHAPE),
-    (dict(T=1 << 26, H=1 << 16, st=1 << 16, k=1), SHAPE), (dict(T=1 << 30, k=2), SHAPE), (dict(x=None), NULL),
+    (dict(T=1 << 26, H=1 << 16, st=1 << 16, k=1), SHAPE), (dict(T=1 << 30, k=2), SHAPE), (dict(T=1 << 24, k=1), SHAPE), (dict(x=None), NULL),
     (dict(pos=None), NULL), (dict(out=None), NULL), (dict(x=FAKE + 8), ALIGN), (dict(out=FAKE + 4), ALIGN),
     (dict(st=68), ALIGN), (dict(pos=FAKE + 2), ALIGN), (dict(T=0, x=None), 0)])
 def test_row_arguments(call, kw, status):
