@@ -21,7 +21,9 @@ namespace fp4 {
 namespace {
 
 constexpr uint32_t kWaves = 4;
-constexpr uint32_t kMaxGroups = 1024;  // workgroups of the gradient, each with a partial sum
+// Workgroups of the gradient, each with a partial sum: as many as run at once (BF16
+// heads of 128: 94 registers, five a CU; 8192 x 40 of them take 57 us, 58 with 1024).
+constexpr uint32_t kMaxGroups = 1280;
 constexpr uint64_t kWantedWaves = 8192;
 
 struct Tensor {
@@ -363,13 +365,13 @@ __global__ __launch_bounds__(64 * kWaves) void backward_kernel(Args s) {
     t.partial[(size_t)group * s.D + e] = (sh.part[0][e] + sh.part[1][e]) + (sh.part[2][e] + sh.part[3][e]);
 }
 
-// Sums of the workgroups' partial sums: 16 columns a workgroup, 16 threads
+// Sums of the workgroups' partial sums: 16 columns a workgroup, 64 threads
 // each.
-__global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ partial_q,
+__global__ __launch_bounds__(1024) void sum_kernel(const float* __restrict__ partial_q,
                                                   const float* __restrict__ partial_k, uint32_t groups_q,
                                                   uint32_t groups_k, uint32_t D, float* __restrict__ dwq,
                                                   float* __restrict__ dwk) {
-  __shared__ float part[16][17];
+  __shared__ float part[64][17];
   const uint32_t columns = (D + 15u) / 16u;
   const bool is_q = blockIdx.x < columns;
   const float* partial = is_q ? partial_q : partial_k;
@@ -380,19 +382,20 @@ __global__ __launch_bounds__(256) void sum_kernel(const float* __restrict__ part
   float sum = 0.0f;
   if (e < D) {
     uint32_t g = seg;
-    for (; g + 112u < groups; g += 128u) {  // eight loads at a time
+    for (; g + 448u < groups; g += 512u) {  // eight loads at a time
       float v[8];
 #pragma unroll
-      for (uint32_t i = 0; i < 8u; ++i) v[i] = partial[(size_t)(g + 16u * i) * D + e];
+      for (uint32_t i = 0; i < 8u; ++i) v[i] = partial[(size_t)(g + 64u * i) * D + e];
 #pragma unroll
       for (uint32_t i = 0; i < 8u; ++i) sum += v[i];
     }
-    for (; g < groups; g += 16u) sum += partial[(size_t)g * D + e];
+    for (; g < groups; g += 64u) sum += partial[(size_t)g * D + e];
   }
   part[seg][c] = sum;
   __syncthreads();
   if (seg != 0u || e >= D) return;
-  for (uint32_t i = 1; i < 16u; ++i) sum += part[i][c];
+#pragma unroll
+  for (uint32_t i = 1; i < 64u; ++i) sum += part[i][c];
   out[e] = sum;
 }
 
@@ -430,7 +433,7 @@ hipError_t launch_one(Args& s, const QkRope& a, hipStream_t stream) {
   }
   if (!BACKWARD || !(s.t[0].w || s.t[1].w)) return hipSuccess;
   // (Without rows the weights' gradients are 0.)
-  sum_kernel<<<dim3(2u * ((s.D + 15u) / 16u)), dim3(256), 0, stream>>>(s.t[0].partial, s.t[1].partial, s.t[0].groups,
+  sum_kernel<<<dim3(2u * ((s.D + 15u) / 16u)), dim3(1024), 0, stream>>>(s.t[0].partial, s.t[1].partial, s.t[0].groups,
                                                                       s.t[1].groups, s.D, a.dwq, a.dwk);
   return hipGetLastError();
 }
@@ -472,10 +475,12 @@ hipError_t launch(const QkRope& a, hipStream_t stream) {
 
 }  // namespace
 
-// (Workgroups: no more than heads of all rows, and kMaxGroups and one more of q or
-// of k where that would have none.)
+// Room for a sum of each workgroup: they are no more than heads of all rows, nor than
+// kMaxGroups and one (of q or of k, where that would have none).
 size_t qk_rope_workspace(int64_t rows, int64_t heads, int64_t D) {
-  return (size_t)std::min<int64_t>(rows * heads, kMaxGroups) * 2u * (size_t)D * 4u;
+  constexpr int64_t kRoom = 1024;
+  static_assert(2 * kRoom >= kMaxGroups + 1);
+  return (size_t)std::min(rows * heads, kRoom) * 2u * (size_t)D * 4u;
 }
 hipError_t launch_qk_rope(const QkRope& a, hipStream_t stream) { return launch<false>(a, stream); }
 hipError_t launch_qk_rope_backward(const QkRope& a, hipStream_t stream) { return launch<true>(a, stream); }
