@@ -1266,7 +1266,7 @@ def moe_gather(x, pos, out=None, stream=None):
     if pos.shape[0] != T:
         raise ValueError("pos has %d rows, x %d" % (pos.shape[0], T))
     if out is None:
-        out = _new(stream, (T * k, H), x.dtype, dev)
+        out = _alloc(stream, x.new_empty, (T * k, H))
     else:
         _want(out, "out", x.dtype, 2, dev)
         if out.shape[1] != H:
@@ -1297,7 +1297,7 @@ def moe_combine(y, pos, weights=None, out=None, stream=None):
     include/fp4.h.  out: default a new T x H tensor; may have any row stride."""
     code, dev, T, k, H = _want_entries(y, pos, weights)
     if out is None:
-        out = _new(stream, (T, H), y.dtype, dev)
+        out = _alloc(stream, y.new_empty, (T, H))
         stride = H
     else:
         ocode, stride = _want_rows(out, "out", 2, dev)

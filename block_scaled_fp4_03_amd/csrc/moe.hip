@@ -261,6 +261,7 @@ struct RouteBackward {
 constexpr uint32_t kSortWaves = 16, kSortThreads = 64 * kSortWaves;
 constexpr uint32_t kFewRounds = 2, kManyRounds = 8;              // of 64 entries, a wave
 constexpr uint32_t kFewChunks = 64;
+constexpr uint32_t kAhead = 16;                                  // counts of chunks asked for together
 constexpr uint32_t kMaxBins = 512 + 2;                           // experts, unrouted, past the end
 
 // Bin of entry i: its expert, E for an id that is none, E + 1 past the end.
@@ -331,11 +332,15 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int32_t*
   if (ROUNDS == kFewRounds && counts != nullptr && run < runs) {
     const uint32_t at = threadIdx.x - run * (E + 1u);
     uint32_t all = 0u, before = 0u;
-#pragma unroll 8
-    for (uint32_t b = run; b < gridDim.x; b += runs) {
-      const uint32_t c = counts[(size_t)b * (E + 1u) + at];
-      all += c;
-      before += b < blockIdx.x ? c : 0u;
+    for (uint32_t b0 = run; b0 < gridDim.x; b0 += kAhead * runs) {
+      uint32_t c[kAhead];
+#pragma unroll
+      for (uint32_t i = 0; i < kAhead; ++i) c[i] = counts[(size_t)min(b0 + i * runs, gridDim.x - 1u) * (E + 1u) + at];
+#pragma unroll
+      for (uint32_t i = 0; i < kAhead; ++i) {
+        all += b0 + i * runs < gridDim.x ? c[i] : 0u;
+        before += b0 + i * runs < blockIdx.x ? c[i] : 0u;
+      }
     }
     part[0][threadIdx.x] = all;
     part[1][threadIdx.x] = before;
