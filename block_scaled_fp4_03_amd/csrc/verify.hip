@@ -22,13 +22,16 @@
 namespace fp4 {
 namespace {
 
-constexpr uint32_t kThreads = 256, kWaves = 4;
+constexpr uint32_t kThreads = 256, kWaves = 4;            // of the draw's workgroups
+constexpr uint32_t kRowThreads = 256, kRowWaves = 4;      // of the rows'
 constexpr uint32_t kRounds = 8;               // tokens of a chunk a lane has
 constexpr uint32_t kChunk = 64u * kRounds;
 constexpr uint32_t kMaxSplits = 32;           // workgroups of a row
-constexpr uint32_t kLaneParts = kMaxSplits * kWaves / 64u;  // a row's parts that a lane joins
+constexpr uint32_t kLaneParts = kMaxSplits * kRowWaves / 64u;  // a row's parts that a lane joins
 constexpr uint32_t kMaxDrafts = 32;
-constexpr int64_t kWantedGroups = 2048, kWantedWaves = 4096;
+// Workgroups for the rows and waves for the draw, of a launch (64 x 15 rows of
+// 100003 BF16: 3000 and 6000 workgroups +6% and +1%, 960 +10%; 4096 waves +3%).
+constexpr int64_t kWantedGroups = 2048, kWantedWaves = 16384;
 constexpr double kLog2e = 1.4426950408889634074;
 
 // A wave's part of a row: the sum of 2^(c (x - r) / 256), r a logit; where the
@@ -37,6 +40,11 @@ struct Part {
   uint64_t value;   // the sum's bits, or the key
   uint64_t r_bad;   // r's bits; above them, whether there is a NaN
 };
+
+// A sequence's counters lie in lines of their own: adds to one line are made one
+// after the other, 8 ns each (with 64 sequences' in two lines, 12000 small workgroups
+// took 139 us, 2880 at least 23).
+constexpr uint32_t kCounterWords = 32;
 
 // What the draw needs of the row drawn from.
 struct Chosen {
@@ -51,7 +59,7 @@ struct Args {
   Verify v;
   uint32_t B, G, V, rows, splits, chunks;
   uint32_t per, groups;  // chunks of a wave, and workgroups of a sequence, in the draw
-  Part* parts;       // B x rows x splits x kWaves; rows: G + 1 of the target, G of the draft
+  Part* parts;       // B x rows x splits x kRowWaves; rows: G + 1 of the target, G of the draft
   double* sums;      // B x chunks
   Chosen* chosen;    // B
   uint32_t* arrived; // 2 x B counters, zero before and after each launch
@@ -115,14 +123,21 @@ __device__ __forceinline__ double power(const Powers& table, uint32_t k) {
 }
 
 // A thread's entry, asked for before it is needed, and the table from them.
-__device__ __forceinline__ u32x2 table_entry() {
-  static_assert(kTable == kThreads, "a thread has one entry");
-  return __builtin_bit_cast(u32x2, kPowers.v[threadIdx.x]);
-}
-__device__ __forceinline__ void fill_table(Powers& table, u32x2 entry) {
-  table[threadIdx.x] = entry;
-  __syncthreads();
-}
+template <uint32_t THREADS>
+struct TableEntries {
+  static constexpr uint32_t N = (kTable + THREADS - 1u) / THREADS;
+  u32x2 e[N];
+  __device__ __forceinline__ TableEntries() {
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i) e[i] = __builtin_bit_cast(u32x2, kPowers.v[(threadIdx.x + i * THREADS) & (kTable - 1u)]);
+  }
+  __device__ __forceinline__ void fill(Powers& table) const {
+#pragma unroll
+    for (uint32_t i = 0; i < N; ++i)
+      if (threadIdx.x + i * THREADS < kTable) table[threadIdx.x + i * THREADS] = e[i];
+    __syncthreads();
+  }
+};
 
 // 2^(f / 256) = 1 + kC1 f + kC2 f^2 + kC3 f^3 for |f| <= 1/2.
 constexpr double kC1 = 0.69314718055994530942 / kTable, kC2 = kC1 * kC1 / 2.0, kC3 = kC1 * kC1 * kC1 / 6.0;
@@ -296,7 +311,7 @@ __device__ __forceinline__ void values(const u32x4& w, float (&v)[N]) {
 template <int DT>
 struct RowPart {
   static constexpr uint32_t E = 16u / kSize<DT>, U = 2u;
-  static constexpr uint32_t kStep = U * kThreads;  // a split has whole steps, but the last
+  static constexpr uint32_t kStep = U * kRowThreads;  // a split has whole steps, but the last
   static constexpr uint32_t kLowest = DT == kDtF32 ? 0xFF800000u : 0xFF80FF80u;  // -inf
   const uint8_t* p;
   const u32x4* from;
@@ -318,7 +333,7 @@ struct RowPart {
   // Blocks of the step at j0 (those past the end: the last one).
   __device__ __forceinline__ void load(uint32_t j0, u32x4 (&w)[U]) const {
 #pragma unroll
-    for (uint32_t u = 0; u < U; ++u) w[u] = from[min(j0 + u * kThreads + threadIdx.x, b1 - 1u)];
+    for (uint32_t u = 0; u < U; ++u) w[u] = from[min(j0 + u * kRowThreads + threadIdx.x, b1 - 1u)];
   }
   __device__ __forceinline__ Running run(double c, const Powers& table);
 };
@@ -329,11 +344,11 @@ __device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& tabl
   if (c < 0.0) {
     float best = -INFINITY;
     uint32_t at = 0u;
-    for (uint32_t j0 = b0; j0 < b1; j0 += U * kThreads) {
+    for (uint32_t j0 = b0; j0 < b1; j0 += U * kRowThreads) {
       u32x4 w[U];
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u) w[u] = next[u];
-      load(j0 + U * kThreads, next);
+      load(j0 + U * kRowThreads, next);
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u) {
         float v[E];
@@ -344,7 +359,7 @@ __device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& tabl
           best = m;
 #pragma unroll
           for (int i = (int)E - 1; i >= 0; --i)
-            at = v[i] == m ? head + min(j0 + u * kThreads + threadIdx.x, b1 - 1u) * E + i : at;
+            at = v[i] == m ? head + min(j0 + u * kRowThreads + threadIdx.x, b1 - 1u) * E + i : at;
         }
       }
     }
@@ -359,16 +374,16 @@ __device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& tabl
   }
   WaveSum sum(c);
   uint32_t j0 = b0;
-  for (; j0 < b1; j0 += U * kThreads) {  // (the same steps for every lane)
+  for (; j0 < b1; j0 += U * kRowThreads) {  // (the same steps for every lane)
     u32x4 w[U];
     float m = -INFINITY;  // the lane's largest logit of this step
 #pragma unroll
     for (uint32_t u = 0; u < U; ++u) w[u] = next[u];
-    load(j0 + U * kThreads, next);  // (past the end: the last block)
-    if (j0 + U * kThreads > b1) {
+    load(j0 + U * kRowThreads, next);  // (past the end: the last block)
+    if (j0 + U * kRowThreads > b1) {
 #pragma unroll
       for (uint32_t u = 0; u < U; ++u)
-        if (j0 + u * kThreads + threadIdx.x >= b1) w[u] = u32x4{kLowest, kLowest, kLowest, kLowest};
+        if (j0 + u * kRowThreads + threadIdx.x >= b1) w[u] = u32x4{kLowest, kLowest, kLowest, kLowest};
     }
 #pragma unroll
     for (uint32_t u = 0; u < U; ++u) {
@@ -395,7 +410,7 @@ __device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& tabl
     }
   }
   // Temperatures at the edge of their range: from the step that showed it on.
-  for (; j0 < b1; j0 += kThreads) {
+  for (; j0 < b1; j0 += kRowThreads) {
     const bool in = j0 + threadIdx.x < b1;
     const u32x4 w = from[min(j0 + threadIdx.x, b1 - 1u)];
     float v[E];
@@ -421,22 +436,22 @@ __device__ __forceinline__ Running RowPart<DT>::run(double c, const Powers& tabl
 // Every row's sum, a wave a row at a time; a lane has kLaneParts of its parts.
 __device__ __forceinline__ void join_rows(const Args& a, Shared& sh, uint32_t b, double c) {
   constexpr uint32_t kAhead = 4;  // rows whose parts are asked for together
-  const uint32_t lane = threadIdx.x & 63u, rows = c < 0.0 ? a.G + 1u : a.rows, parts = a.splits * kWaves;
-  for (uint32_t row0 = threadIdx.x >> 6; row0 < rows; row0 += kWaves * kAhead) {
+  const uint32_t lane = threadIdx.x & 63u, rows = c < 0.0 ? a.G + 1u : a.rows, parts = a.splits * kRowWaves;
+  for (uint32_t row0 = threadIdx.x >> 6; row0 < rows; row0 += kRowWaves * kAhead) {
     uint64_t value[kAhead][kLaneParts], r_bad[kAhead][kLaneParts];
 #pragma unroll
     for (uint32_t i = 0; i < kAhead; ++i) {
-      const Part* from = a.parts + ((size_t)b * a.rows + row0 + i * kWaves) * parts;
+      const Part* from = a.parts + ((size_t)b * a.rows + row0 + i * kRowWaves) * parts;
 #pragma unroll
       for (uint32_t k = 0; k < kLaneParts; ++k) {
-        const bool in = row0 + i * kWaves < rows && lane + 64u * k < parts;
+        const bool in = row0 + i * kRowWaves < rows && lane + 64u * k < parts;
         value[i][k] = in ? get(&from[lane + 64u * k].value) : 0ull;
         r_bad[i][k] = in ? get(&from[lane + 64u * k].r_bad) : (uint64_t)0xFF800000u;  // -inf
       }
     }
 #pragma unroll
     for (uint32_t i = 0; i < kAhead; ++i) {
-      if (row0 + i * kWaves >= rows) break;
+      if (row0 + i * kRowWaves >= rows) break;
       bool bad = false;
       RowSum s{};
       if (c < 0.0) {
@@ -466,7 +481,7 @@ __device__ __forceinline__ void join_rows(const Args& a, Shared& sh, uint32_t b,
         s.inv = 1.0 / wave_sum(sum);
         s.ok = __ballot(bad) == 0ull && s.r > -INFINITY && s.r < INFINITY;
       }
-      if (lane == 0u) sh.row[row0 + i * kWaves] = s;
+      if (lane == 0u) sh.row[row0 + i * kRowWaves] = s;
     }
   }
   __syncthreads();
@@ -515,27 +530,27 @@ __device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t
 }
 
 template <int DT>
-__global__ __launch_bounds__(kThreads) void stats_kernel(Args a) {
+__global__ __launch_bounds__(kRowThreads) void stats_kernel(Args a) {
   __shared__ Shared sh;
   const uint32_t split = blockIdx.x % a.splits, n = blockIdx.x / a.splits, b = n / a.rows, row = n - b * a.rows;
   const float temperature = temperature_of(a, b);
-  const u32x2 entry = table_entry();
+  const TableEntries<kRowThreads> entries;
   RowPart<DT> part(row_at<DT>(a, b, row), a.V, split, a.splits);
   const double c = units_of(temperature);
   const bool greedy = c < 0.0;
   if (greedy && row > a.G) return;  // the draft's distribution is not asked for
-  fill_table(sh.table, entry);
+  entries.fill(sh.table);
   const Running s = part.run(c, sh.table);
   {
     const uint64_t value = greedy ? wave_max(s.key) : __builtin_bit_cast(uint64_t, wave_sum(s.sum));  // (lanes share r)
     const uint64_t bad = __ballot(s.bad) != 0ull ? 1ull : 0ull;
     if ((threadIdx.x & 63u) == 0u) {
-      Part* to = a.parts + ((size_t)n * a.splits + split) * kWaves + (threadIdx.x >> 6);
+      Part* to = a.parts + ((size_t)n * a.splits + split) * kRowWaves + (threadIdx.x >> 6);
       put(&to->value, value);
       put(&to->r_bad, bad << 32 | f2u(s.r));
     }
   }
-  if (!last_of(a.arrived + b, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
+  if (!last_of(a.arrived + (size_t)b * kCounterWords, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
   // The drafts' own logits are asked for before the rows are joined.
   int32_t d = -1;
   float xp = 0.0f, xq = 0.0f, u = 0.0f;
@@ -618,11 +633,11 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   const uint32_t group = blockIdx.x % a.groups, b = blockIdx.x / a.groups, lane = threadIdx.x & 63u;
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const float temperature = temperature_of(a, b);
-  const u32x2 entry = table_entry();
+  const TableEntries<kThreads> entries;
   Chosen s = a.chosen[b];
   if (s.q == kNoDraw) return;
   const double c = units_of(temperature);
-  fill_table(sh.table, entry);
+  entries.fill(sh.table);
   const uint8_t* p = row_at<DT>(a, b, s.row);
   const uint8_t* q = s.q == kQDraft ? row_at<DT>(a, b, a.G + 1u + s.row) : nullptr;
   double* sums = a.sums + (size_t)b * a.chunks;
@@ -632,7 +647,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
     const double sum = chunk_sum<DT>(a, s, p, q, i, c, sh.table, w);
     if (lane == 0u) put(sums + i, sum);
   }
-  if (!last_of(a.arrived + a.B + b, a.groups, sh.flag)) return;
+  if (!last_of(a.arrived + (size_t)(a.B + b) * kCounterWords, a.groups, sh.flag)) return;
   if (wave != 0u) return;
   const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
   // A lane has a run of the chunks: the run, then the chunk, that passes the border;
@@ -686,7 +701,7 @@ uint32_t chunks_of(int64_t V) { return (uint32_t)((V + kChunk - 1) / kChunk); }
 
 template <int DT>
 hipError_t launch(const Args& a, hipStream_t stream) {
-  stats_kernel<DT><<<dim3(a.B * a.rows * a.splits), dim3(kThreads), 0, stream>>>(a);
+  stats_kernel<DT><<<dim3(a.B * a.rows * a.splits), dim3(kRowThreads), 0, stream>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   draw_kernel<DT><<<dim3(a.B * a.groups), dim3(kThreads), 0, stream>>>(a);
@@ -697,14 +712,14 @@ hipError_t launch(const Args& a, hipStream_t stream) {
 
 // A launch takes at most kBatch sequences, whose counters come first: at one
 // place whatever the call, so that no call's data lie where another's counters do.
-static constexpr int64_t kBatch = 1024;
-static constexpr size_t kCounterBytes = kBatch * 8;
+static constexpr int64_t kBatch = 256;
+static constexpr size_t kCounterBytes = 2u * kBatch * kCounterWords * 4u;
 
 // For calls with and without draft logits.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
   const int64_t n = std::min(B, kBatch);
   const int64_t with = n * (2 * G + 1) * splits_of(n, 2 * G + 1, V), without = n * (G + 1) * splits_of(n, G + 1, V);
-  return kCounterBytes + (size_t)std::max(with, without) * kWaves * sizeof(Part) + (size_t)n * chunks_of(V) * 8u +
+  return kCounterBytes + (size_t)std::max(with, without) * kRowWaves * sizeof(Part) + (size_t)n * chunks_of(V) * 8u +
          (size_t)n * sizeof(Chosen);
 }
 
