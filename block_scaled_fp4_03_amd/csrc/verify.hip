@@ -14,6 +14,11 @@
 // a sequence to arrive joins them and decides.  Then, of the row drawn from, the
 // sums of chunks of r, a wave each: the last workgroup to arrive finds the token
 // among the chunks, and within one.
+//
+// 64 sequences x 7 drafts over 100003 BF16 logits, a quarter of them greedy: 54 us
+// for the rows (173 MB; 21.2 M vector instructions, 9 of 15 a logit FP64, are 37 us
+// at 2.4 GHz) and 16 for the draws.  One sequence x 4 over 131072 FP32: 11 + 9 us,
+// two chains of about eight memory latencies.
 #include "fp4_device.h"
 #include "fp4_launch.h"
 
