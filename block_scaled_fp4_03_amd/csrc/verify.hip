@@ -31,6 +31,7 @@ constexpr uint32_t kThreads = 256, kWaves = 4;            // of the draw's workg
 constexpr uint32_t kRowThreads = 256, kRowWaves = 4;      // of the rows'
 constexpr uint32_t kRounds = 8;               // tokens of a chunk a lane has
 constexpr uint32_t kChunk = 64u * kRounds;
+constexpr uint32_t kRun = 4;                  // chunks' sums that a lane keeps (V up to 131072)
 constexpr uint32_t kMaxSplits = 32;           // workgroups of a row
 constexpr uint32_t kLaneParts = kMaxSplits * kRowWaves / 64u;  // a row's parts that a lane joins
 constexpr uint32_t kMaxDrafts = 32;
@@ -223,8 +224,14 @@ struct RowSum {
   bool ok;     // it has a distribution: no NaN, no +inf, not all -inf
   uint32_t best;
 };
+// A draft: its token, the two models' logits of it, and its random number.
+struct Draft {
+  int32_t token;
+  float xp, xq, u;
+};
 struct Shared {
   Powers table;
+  Draft draft[kMaxDrafts];
   RowSum row[2 * kMaxDrafts + 1];
   uint32_t flag;
 };
@@ -493,11 +500,12 @@ __device__ __forceinline__ void join_rows(const Args& a, Shared& sh, uint32_t b,
 }
 
 // Decides over a sequence's drafts (wave 0, a lane a position) and writes all
-// but a drawn token.  d: the lane's draft; xp, xq: its logits.
-__device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t b, double c, int32_t d, float xp,
-                                       float xq, float u) {
+// but a drawn token.
+__device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t b, double c) {
   const bool greedy = c < 0.0;
   const uint32_t i = threadIdx.x;
+  const Draft own = sh.draft[min(i, kMaxDrafts - 1u)];  // (of lanes past the drafts: not used)
+  const int32_t d = i < a.G ? own.token : -1;
   bool keep = false;
   double odds = 0.0;
   if (i < a.G && (uint32_t)d < a.V && sh.row[i].ok) {
@@ -507,9 +515,9 @@ __device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t
       odds = keep ? 1.0 : 0.0;
     } else if (!a.v.draft || sh.row[a.G + 1u + i].ok) {
       const RowSum& q = sh.row[a.v.draft ? a.G + 1u + i : i];
-      const double pd = weight(xp, p.r, c, sh.table) * p.inv;
-      const double qd = a.v.draft ? weight(xq, q.r, c, sh.table) * q.inv : 1.0;
-      keep = (double)u * qd < pd;
+      const double pd = weight(own.xp, p.r, c, sh.table) * p.inv;
+      const double qd = a.v.draft ? weight(own.xq, q.r, c, sh.table) * q.inv : 1.0;
+      keep = (double)own.u * qd < pd;
       odds = pd >= qd ? (pd > 0.0 ? 1.0 : 0.0) : pd / qd;
     }
   }
@@ -541,6 +549,17 @@ __global__ __launch_bounds__(kRowThreads) void stats_kernel(Args a) {
   const float temperature = temperature_of(a, b);
   const TableEntries<kRowThreads> entries;
   RowPart<DT> part(row_at<DT>(a, b, row), a.V, split, a.splits);
+  // The drafts' own logits: the last workgroup decides with them, and which that is
+  // shows only when there is nothing left to hide their latency.
+  if (threadIdx.x < a.G) {
+    const uint32_t i = threadIdx.x;
+    Draft d{a.v.tokens[(size_t)b * a.G + i], 0.0f, 0.0f, a.v.u[(size_t)b * (a.G + 1u) + i]};
+    if ((uint32_t)d.token < a.V) {
+      d.xp = logit<DT>(row_at<DT>(a, b, i), (uint32_t)d.token);
+      if (a.v.draft) d.xq = logit<DT>(row_at<DT>(a, b, a.G + 1u + i), (uint32_t)d.token);
+    }
+    sh.draft[i] = d;
+  }
   const double c = units_of(temperature);
   const bool greedy = c < 0.0;
   if (greedy && row > a.G) return;  // the draft's distribution is not asked for
@@ -556,20 +575,8 @@ __global__ __launch_bounds__(kRowThreads) void stats_kernel(Args a) {
     }
   }
   if (!last_of(a.arrived + (size_t)b * kCounterWords, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
-  // The drafts' own logits are asked for before the rows are joined.
-  int32_t d = -1;
-  float xp = 0.0f, xq = 0.0f, u = 0.0f;
-  if (threadIdx.x < a.G) {
-    const uint32_t i = threadIdx.x;
-    d = a.v.tokens[(size_t)b * a.G + i];
-    u = a.v.u[(size_t)b * (a.G + 1u) + i];
-    if ((uint32_t)d < a.V) {
-      xp = logit<DT>(row_at<DT>(a, b, i), (uint32_t)d);
-      if (a.v.draft) xq = logit<DT>(row_at<DT>(a, b, a.G + 1u + i), (uint32_t)d);
-    }
-  }
   join_rows(a, sh, b, c);
-  if (threadIdx.x < 64u) decide(a, sh, b, c, d, xp, xq, u);
+  if (threadIdx.x < 64u) decide(a, sh, b, c);
 }
 
 // ---- the draw ----------------------------------------------------------------
@@ -639,6 +646,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   const uint32_t wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const float temperature = temperature_of(a, b);
   const TableEntries<kThreads> entries;
+  const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
   Chosen s = a.chosen[b];
   if (s.q == kNoDraw) return;
   const double c = units_of(temperature);
@@ -654,12 +662,15 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   }
   if (!last_of(a.arrived + (size_t)(a.B + b) * kCounterWords, a.groups, sh.flag)) return;
   if (wave != 0u) return;
-  const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
   // A lane has a run of the chunks: the run, then the chunk, that passes the border;
   // the last with any weight, if none does.
   const uint32_t run = (a.chunks + 63u) / 64u, i0 = min(lane * run, a.chunks), i1 = min(i0 + run, a.chunks);
-  double mine = 0.0;
-  for (uint32_t i = i0; i < i1; ++i) mine += get(sums + i);
+  double own_parts[kRun], mine = 0.0;  // the first of the run
+#pragma unroll
+  for (uint32_t i = 0; i < kRun; ++i) own_parts[i] = i0 + i < i1 ? get(sums + i0 + i) : 0.0;
+#pragma unroll
+  for (uint32_t i = 0; i < kRun; ++i) mine += own_parts[i];
+  for (uint32_t i = i0 + kRun; i < i1; ++i) mine += get(sums + i);
   double upto = scan(mine, lane);
   const double total = from_lane(upto, 63), border = u * total;
   int32_t token = -1;
@@ -669,7 +680,20 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
     double before = __shfl(upto - mine, (int)l), chunk_before = before;
     uint32_t chunk = l * run;
     const uint32_t end = min((l + 1u) * run, a.chunks);
-    for (uint32_t i = l * run; i < end; i += 64u) {
+    if (run <= kRun) {
+      bool hit = false;
+#pragma unroll
+      for (uint32_t i = 0; i < kRun; ++i) {
+        const double part = __shfl(own_parts[i], (int)l);
+        if (part > 0.0 && !hit) {
+          chunk = l * run + i;
+          chunk_before = before;
+          hit = before + part > border;
+        }
+        before += part;
+      }
+    }
+    for (uint32_t i = l * run; run > kRun && i < end; i += 64u) {
       const double part = i + lane < end ? get(sums + i + lane) : 0.0;
       upto = before + scan(part, lane);
       const uint64_t any = __ballot(part > 0.0), hit = __ballot(upto > border) & any;
