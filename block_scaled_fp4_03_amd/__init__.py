@@ -1093,6 +1093,12 @@ def _want_heads(q, k):
     return code, dev, q.shape, k.shape, qs, ks
 
 
+def _want_weight(t, name, dim, dev):
+    _want(t, name, _torch().float32, 1, dev)
+    if t.shape[0] != dim:
+        raise ValueError("%s holds %d values, a head %d" % (name, t.shape[0], dim))
+
+
 def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Norms of queries and keys for each head (over head_dim, times q_weight /
     k_weight; left out where that is None) and the rotation of their positions,
@@ -1102,14 +1108,13 @@ def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=
     one projection's output); pos: int32 axes x rows (or rows, with one axis);
     rope: a Rope, or None for no rotation; weights: float32 head_dim.  q_out,
     k_out may be q, k themselves.  Returns the two (new dense tensors unless
-    given)."""
+    given), without autograd history: qk_norm_rope_backward gives the gradient."""
     code, dev, (rows, qh, dim), (_, kh, _), qs, ks = _want_heads(q, k)
     ref, at = _want_pos(rope, pos, rows, dev)
-    f32 = _torch().float32
     if q_weight is not None:
-        _want(q_weight, "q_weight", f32, 1, dev, dim)
+        _want_weight(q_weight, "q_weight", dim, dev)
     if k_weight is not None:
-        _want(k_weight, "k_weight", f32, 1, dev, dim)
+        _want_weight(k_weight, "k_weight", dim, dev)
     if q_out is None:
         q_out, qos = _like(q, stream), qh * dim
     else:
@@ -1151,7 +1156,7 @@ def qk_norm_rope_backward(gq, gk, q, k, rope, pos, q_weight=None, k_weight=None,
         if t is None:
             grads.append(None)
             continue
-        _want(t, name, torch.float32, 1, dev, dim)
+        _want_weight(t, name, dim, dev)
         # (Without heads the call has no weight to give a gradient of.)
         grads.append(_alloc(stream, torch.empty if heads else torch.zeros, dim, dtype=torch.float32, device=dev))
     if dq is None:

@@ -213,6 +213,7 @@ def test_refusals():
     bad(TypeError, 3, s["pos"].long())
     bad(ValueError, 3, s["pos"][:, :3])
     bad(ValueError, 4, s["wq"][:32])
+    bad(ValueError, 5, torch.ones(65, device="cuda"))
     bad(TypeError, 5, s["wk"].to(torch.bfloat16))
     with pytest.raises(ValueError):
         fp4.Rope(s["freq"][:30])
