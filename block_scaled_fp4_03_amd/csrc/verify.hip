@@ -16,7 +16,7 @@
 // among the chunks, and within one.
 //
 // 64 sequences x 7 drafts over 100003 BF16 logits, a quarter of them greedy: 54 us
-// for the rows (173 MB; 21.2 M vector instructions, 9 of 15 a logit FP64, are 37 us
+// for the rows (173 MB; 21.3 M vector instructions, 9 of 15 a logit FP64, are 35 us
 // at 2.4 GHz) and 16 for the draws.  One sequence x 4 over 131072 FP32: 11 + 9 us,
 // two chains of about eight memory latencies.
 #include "fp4_device.h"
