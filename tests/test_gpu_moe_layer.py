@@ -296,3 +296,50 @@ def test_debug_mode_refuses_short_buffers():
     finally:
         fp4.fp4_set_debug(prev)
         bufs.free()
+
+
+def test_offsets_beyond_32_bits():
+    """Rows more than 2^32 elements apart or into a tensor: the bits of dense copies."""
+    import block_scaled_fp4_03_amd as fp4
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(9)
+    big = torch.empty(6 << 30, dtype=torch.bfloat16, device="cuda")
+    say("layer: heads 2^30 apart")
+    qk = [torch.randn((6, h, 64), generator=g, device="cuda").to(torch.bfloat16) for h in (3, 2)]
+    far = [big.as_strided((6, h, 64), ((1 << 30) - 8, 64, 1), at) for h, at in ((3, 0), (2, 4096))]
+    for a, b in zip(far, qk):
+        a.copy_(b)
+    rope = fp4.Rope(torch.rand(32, generator=g, device="cuda"))
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    w = torch.rand(64, generator=g, device="cuda")
+    want = fp4.qk_norm_rope(*qk, rope, pos, w, w)
+    grads = fp4.qk_norm_rope_backward(*want, *qk, rope, pos, w, w)
+    got = fp4.qk_norm_rope_backward(*want, *far, rope, pos, w, w)
+    assert all(torch.equal(a, b) for a, b in zip(got, grads))
+    fp4.qk_norm_rope(*far, rope, pos, w, w, q_out=far[0], k_out=far[1])
+    assert all(torch.equal(a, b) for a, b in zip(far, want))
+
+    say("layer: rows beyond 2^32 elements")
+    H = 4096
+    y = big[:(big.numel() // H) * H].view(-1, H)
+    rows = torch.tensor([[0, 1 << 20], [y.shape[0] - 1, (1 << 20) + 7]], device="cuda")
+    x = torch.randn((2, H), generator=g, device="cuda").to(torch.bfloat16)
+    wt = torch.rand((2, 2), generator=g, device="cuda")
+    fp4.moe_gather(x, rows.to(torch.int32), out=y)
+    assert torch.equal(y[rows], x[:, None].expand(2, 2, H))
+    few = y[rows.flatten()].contiguous()
+    at = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    out = fp4.moe_combine(few, at, wt)
+    assert torch.equal(fp4.moe_combine(y, rows.to(torch.int32), wt), out)
+    dfew, dw = fp4.moe_combine_backward(x, few, at, wt)
+    assert torch.equal(fp4.moe_combine_backward(x, y, rows.to(torch.int32), wt, dy=torch.empty_like(y))[1], dw)
+
+    say("layer: logits 2^31 apart")
+    V = 5003
+    target = torch.randn((2, 2, V), generator=g, device="cuda").to(torch.bfloat16)
+    far = big.as_strided((2, 2, V), ((1 << 32) - 8191, (1 << 31) - 3, 1), 5)
+    far.copy_(target)
+    tokens = target[:, :1].float().argmax(2).to(torch.int32)
+    u = torch.rand((2, 2), generator=g, device="cuda")
+    a, b = (fp4.verify_drafts(t, None, tokens, u) for t in (target, far))
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
