@@ -1326,7 +1326,8 @@ def moe_combine(y, pos, weights=None, out=None, stream=None):
 def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
     """Gradient of moe_combine from that of its result (g, T x H of y's dtype,
     any row stride); see fp4_moe_combine_backward in include/fp4.h.  Returns
-    (dy, of y's shape, and the weights' gradient, float32 T x top_k)."""
+    (dy, of y's shape, and the weights' gradient, float32 T x top_k).  Rows of dy
+    that no entry names are not written."""
     if weights is None:
         raise ValueError("without weights the gradient is moe_gather's")
     code, dev, T, k, H = _want_entries(y, pos, weights)

@@ -598,7 +598,9 @@ typedef struct fp4_rope {
  *   than a row.  An output may be its input (same address and stride); it must
  *   not overlap an input otherwise.  Either may have no heads.
  *   head_dim: a multiple of 8 from 32 to 256.  q_weight, k_weight: head_dim FP32
- *   or NULL.  eps >= 0.  pos: device int32, axes x rows, dense, any values.
+ *   or NULL.  eps >= 0; mean x^2 + eps has to lie in FP32's normal range (a head
+ *   of zeros with eps 0 gives NaN).  pos: device int32, axes x rows, dense, any
+ *   values.
  *   rope NULL: no rotation.  rows < 2^25.
  * rows == 0 is a no-op. */
 int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, int64_t q_stride, int64_t q_heads,
@@ -667,7 +669,8 @@ int fp4_moe_sort(const int32_t* ids, int64_t T, int32_t top_k, int64_t E, int32_
  * -1 - pos[t,j] where that is negative: every row is written).
  *   x: T rows of H values of dtype, row t at element t * stride; out: `rows` rows
  *   of H, dense.  16-byte aligned, H and stride multiples of 16 bytes.  An entry
- *   whose r is no row (r >= rows) is skipped; two entries for one row race.
+ *   whose r is no row (r >= rows) is skipped; two entries for one row race.  out
+ *   must not overlap x.
  *   0 <= top_k <= 64; T < 2^24 and T * (H rounded up to 1 KB) below 2^32 * 16 bytes,
  *   for this call and the two below.  Its gradient is fp4_moe_combine without weights.
  * T == 0 is a no-op. */
@@ -688,6 +691,7 @@ int fp4_moe_combine(const void* y, int dtype, const int32_t* pos, const float* w
  * weights[t,j] * g[t] (rows of dtype, dense), dweights[t,j] = g[t] . y[pos[t,j]]
  * (T x top_k FP32).  An entry that no expert takes (pos negative) has dweights 0
  * and its row -1 - pos in dy zeros; one that names no row of y has dweights 0.
+ * Two entries for one row race in dy; rows that no entry names stay as they are.
  * dy must not overlap y or g. */
 int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int dtype, const int32_t* pos,
                              const float* weights, int64_t T, int32_t top_k, int64_t H, int64_t rows, void* dy,
