@@ -269,7 +269,7 @@ struct WaveSum {
     if (!(m > r)) return;
     if (r != -INFINITY) sum *= rest(table) * weight(r, m, c, table);
     r = m;
-    passes = r + c_passes;
+    passes = fminf(r + c_passes, 0x1.fffffep127f);  // (a +inf logit passes it at every temperature)
     const double rc = (double)r * c;
     fast = c > 1e-30 && __builtin_fabs(rc) < 0x1p38;
     if (!fast) return;
