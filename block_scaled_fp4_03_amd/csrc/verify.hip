@@ -267,7 +267,8 @@ struct WaveSum {
     bad |= m != m;
     m = wave_fmax(m);  // (a NaN left out)
     if (!(m > r)) return;
-    if (r != -INFINITY) sum *= rest(table) * weight(r, m, c, table);
+    const bool some = r != -INFINITY;
+    if (some) sum *= rest(table) * weight(r, m, c, table);
     r = m;
     passes = fminf(r + c_passes, 0x1.fffffep127f);  // (a +inf logit passes it at every temperature)
     const double rc = (double)r * c;
@@ -275,6 +276,8 @@ struct WaveSum {
     if (!fast) return;
     shift = kRound - __builtin_rint(rc);
     low = (float)((double)r - 256.0 * 900.0 / c);  // (FP32's rounding is 2^14 of those units at most)
+    // From against r to against R: rest()'s inverse.
+    if (some) sum *= exp_units(__builtin_fma((double)r, c, shift - kRound), table);
   }
   template <int N>
   __device__ __forceinline__ void add_fast(const float (&v)[N], const Powers& table) {

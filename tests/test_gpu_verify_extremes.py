@@ -26,3 +26,25 @@ def test_infinite_logit_at_high_temperatures(dtype):
     say("verify, +inf at high temperatures %s" % dtype)
     kept = _check(s)
     assert kept.max() <= 3 and (kept[:6] <= 1).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_terms_before_and_behind_a_move_of_the_reference(dtype):
+    """Logits about 0, then some just short of 2^500 above, then some just past it: the
+    last move the reference when the sum already holds terms as large as theirs."""
+    import torch
+    # (Rows in one piece: one step of a wave's is 4096 BF16 or 2048 FP32 logits.)
+    B, G, V, step = (256, 7, 12300, 4096) if dtype == "bf16" else (5, 6, 8191, 2048)
+    s = _case(torch, B, G, V, dtype, 32, draft=False)
+    g = torch.Generator(device="cuda").manual_seed(33)
+    s["target"] = -torch.rand((B, G + 1, V), generator=g, device="cuda")
+    rest = s["target"].shape[:2] + (V - step - 8,)
+    past = torch.arange(V - step - 8, device="cuda") >= step
+    # 500 log 2 is 346.57; BF16 has the even numbers there.
+    low, high = (346.0, 348.0) if dtype == "bf16" else (345.5, 346.8)
+    s["target"][..., step + 8:] = torch.where(past, high, low) + 0.6 * torch.rand(rest, generator=g, device="cuda")
+    s["target"] = s["target"].to(torch.float32 if dtype == "f32" else torch.bfloat16)
+    s["temperature"] = None
+    s["tokens"] = torch.randint(step + 8, V, (B, G), generator=g, device="cuda").to(torch.int32)
+    say("verify, moves of the reference %s" % dtype)
+    _check(s)
