@@ -272,10 +272,10 @@ struct WaveSum {
     r = m;
     passes = fminf(r + c_passes, 0x1.fffffep127f);  // (a +inf logit passes it at every temperature)
     const double rc = (double)r * c;
-    fast = c > 1e-30 && __builtin_fabs(rc) < 0x1p38;
+    low = (float)((double)r - 256.0 * 900.0 / c);  // (FP32's rounding is 2^14 of those units at most)
+    fast = c > 1e-30 && __builtin_fabs(rc) < 0x1p38 && low > -INFINITY;
     if (!fast) return;
     shift = kRound - __builtin_rint(rc);
-    low = (float)((double)r - 256.0 * 900.0 / c);  // (FP32's rounding is 2^14 of those units at most)
     // From against r to against R: rest()'s inverse.
     if (some) sum *= exp_units(__builtin_fma((double)r, c, shift - kRound), table);
   }

@@ -48,3 +48,20 @@ def test_terms_before_and_behind_a_move_of_the_reference(dtype):
     s["tokens"] = torch.randint(step + 8, V, (B, G), generator=g, device="cuda").to(torch.int32)
     say("verify, moves of the reference %s" % dtype)
     _check(s)
+
+
+def test_lowest_logits_beside_masked_ones():
+    """Rows, or their beginnings, of FP32's lowest value and -inf at a temperature that
+    makes a step of the reference reach below that value."""
+    import torch
+    lowest, inf, V = torch.finfo(torch.float32).min, float("inf"), 8191
+    s = _case(torch, 6, 3, V, "f32", 34, draft=False)
+    for b, until in enumerate((V, V, 5000, 5000, 300, 5)):
+        s["target"][b, :, :until] = lowest
+        s["target"][b, :, :until:3] = -inf
+    s["temperature"] = torch.tensor([1e30, 2e30] * 3, device="cuda")
+    s["tokens"][:] = torch.tensor([1, 301, 8000], dtype=torch.int32, device="cuda")
+    s["u"][:, :3] *= 2.0 ** -14
+    say("verify, the lowest value beside -inf")
+    kept = _check(s)
+    assert (kept[:2] > 0).any()
