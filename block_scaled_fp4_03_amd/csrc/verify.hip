@@ -750,6 +750,7 @@ static constexpr size_t kCounterBytes = 2u * kBatch * kCounterWords * 4u;
 // For calls with and without draft logits.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
   const int64_t n = std::min(B, kBatch);
+  if (n == 0) return 0u;
   const int64_t with = n * (2 * G + 1) * splits_of(n, 2 * G + 1, V), without = n * (G + 1) * splits_of(n, G + 1, V);
   return kCounterBytes + (size_t)std::max(with, without) * kRowWaves * sizeof(Part) + (size_t)n * chunks_of(V) * 8u +
          (size_t)n * sizeof(Chosen);

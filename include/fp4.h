@@ -699,8 +699,8 @@ int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int d
 
 /* ---- Behind the head: drafted tokens. ---- */
 
-/* Workspace bytes of fp4_verify_drafts (0 for invalid arguments).  It must be
- * zero-filled once; calls leave its control words zero. */
+/* Workspace bytes of fp4_verify_drafts (0: none needed, for B == 0 and invalid
+ * arguments).  It must be zero-filled once; calls leave its control words zero. */
 size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V);
 
 /* Verify up to G drafted tokens of each of B sequences against the target's

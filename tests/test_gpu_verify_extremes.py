@@ -65,3 +65,15 @@ def test_lowest_logits_beside_masked_ones():
     say("verify, the lowest value beside -inf")
     kept = _check(s)
     assert (kept[:2] > 0).any()
+
+
+def test_empty_batch():
+    """No sequences: empty results (with a workspace allocated here, and without one)."""
+    import block_scaled_fp4_03_amd as fp4
+    import torch
+    say("verify, an empty batch")
+    for draft in (True, False):
+        s = _case(torch, 2, 3, 50, "bf16", 35, draft=draft)
+        s = {n: None if t is None else t[:0] for n, t in s.items()}
+        out, kept, chance = fp4.verify_drafts(s["target"], s["draft"], s["tokens"], s["u"], s["temperature"])
+        assert out.shape == (0, 4) and kept.shape == (0,) and chance.shape == (0, 3)
