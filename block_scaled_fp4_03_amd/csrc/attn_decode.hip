@@ -42,6 +42,7 @@
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
+#include "workspace.h"
 
 namespace fp4 {
 namespace {
@@ -843,6 +844,7 @@ void launch_fmt(const AttnArgs& a, uint32_t grid, bool exact, hipStream_t stream
 
 }  // namespace
 
+static_assert(kGroups * 4u == kControlBytes);
 size_t attn_decode_workspace(int64_t B, int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t max_len,
                              bool weights) {
   if (B == 0 || q_heads == 0) return 0;

@@ -33,6 +33,7 @@
 #include "fp4_launch.h"
 #include "kv_device.h"
 #include "logit_rows.h"
+#include "workspace.h"
 
 #include <cfloat>
 
@@ -726,6 +727,7 @@ constexpr int64_t kRowGroups = 512;
 // call's data ever lies where a call expects zeros.  (Rows are split only
 // where there are fewer than kRowGroups.)
 constexpr size_t kDoneBytes = (size_t)kRowGroups * 4;
+static_assert(kDoneBytes == kControlBytes);
 uint32_t splits_of(int64_t N, int64_t V, int32_t top_k) {
   int64_t s = (kRowGroups + N - 1) / N;
   const int64_t most = (V + 2047) / 2048;

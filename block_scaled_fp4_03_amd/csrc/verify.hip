@@ -21,6 +21,7 @@
 // two chains of about eight memory latencies.
 #include "fp4_device.h"
 #include "fp4_launch.h"
+#include "workspace.h"
 
 #include <algorithm>
 
@@ -29,15 +30,15 @@ namespace {
 
 constexpr uint32_t kThreads = 256, kWaves = 4;            // of the draw's workgroups
 constexpr uint32_t kRowThreads = 256, kRowWaves = 4;      // of the rows'
+static_assert(kRowWaves == kVerifyRowWaves);
 constexpr uint32_t kRounds = 8;               // tokens of a chunk a lane has
 constexpr uint32_t kChunk = 64u * kRounds;
+static_assert(kChunk == kVerifyChunk);
 constexpr uint32_t kRun = 4;                  // chunks' sums that a lane keeps (V up to 131072)
-constexpr uint32_t kMaxSplits = 32;           // workgroups of a row
-constexpr uint32_t kLaneParts = kMaxSplits * kRowWaves / 64u;  // a row's parts that a lane joins
+constexpr uint32_t kLaneParts = kVerifyMaxSplits * kRowWaves / 64u;  // a row's parts that a lane joins
 constexpr uint32_t kMaxDrafts = 32;
-// Workgroups for the rows and waves for the draw, of a launch (64 x 15 rows of
-// 100003 BF16: 3000 and 6000 workgroups +6% and +1%, 960 +10%; 4096 waves +3%).
-constexpr int64_t kWantedGroups = 2048, kWantedWaves = 16384;
+// Waves for the draw, of a launch (64 x 15 rows of 100003 BF16: 4096 waves +3%).
+constexpr int64_t kWantedWaves = 16384;
 constexpr double kLog2e = 1.4426950408889634074;
 
 // A wave's part of a row: the sum of 2^(c (x - r) / 256), r a logit; where the
@@ -46,11 +47,7 @@ struct Part {
   uint64_t value;   // the sum's bits, or the key
   uint64_t r_bad;   // r's bits; above them, whether there is a NaN
 };
-
-// A sequence's counters lie in lines of their own: adds to one line are made one
-// after the other, 8 ns each (with 64 sequences' in two lines, 12000 small workgroups
-// took 139 us, 2880 at least 23).
-constexpr uint32_t kCounterWords = 32;
+static_assert(sizeof(Part) == kVerifyPartBytes);
 
 // What the draw needs of the row drawn from.
 struct Chosen {
@@ -59,6 +56,7 @@ struct Chosen {
   uint32_t row;         // of the sequence's target rows
   int32_t q;            // kQNone, kQDraft, or the token that holds all of q
 };
+static_assert(sizeof(Chosen) == kVerifyChosenBytes);
 constexpr int32_t kQNone = -1, kQDraft = -2, kNoDraw = -3;
 
 struct Args {
@@ -68,8 +66,11 @@ struct Args {
   Part* parts;       // B x rows x splits x kRowWaves; rows: G + 1 of the target, G of the draft
   double* sums;      // B x chunks
   Chosen* chosen;    // B
-  uint32_t* arrived; // 2 x B counters, zero before and after each launch
+  uint32_t* arrived; // B counters, counter_words apart, zero before and after each launch
+  uint32_t counter_words;
+  uint32_t* drawn;   // the draw's, a line apart; zeroed where the sequence is decided
 };
+constexpr uint32_t kLineWords = kLineBytes / 4u;
 
 template <int DT>
 constexpr uint32_t kSize = DT == kDtF32 ? 4u : 2u;
@@ -530,6 +531,7 @@ __device__ __forceinline__ void decide(const Args& a, const Shared& sh, uint32_t
   if (i <= a.G) a.v.out[(size_t)b * (a.G + 1u) + i] = i < n ? d : i == n && greedy && p.ok ? (int32_t)p.best : -1;
   const int32_t dn = __shfl(d, (int)n);
   if (i != 0u) return;
+  put(a.drawn + (size_t)b * kLineWords, 0u);
   a.v.accepted[b] = (int32_t)n;
   Chosen s{p.inv, 0.0, p.r, 0.0f, n, kQNone};
   if (n < a.G && (uint32_t)dn < a.V) {
@@ -577,7 +579,7 @@ __global__ __launch_bounds__(kRowThreads) void stats_kernel(Args a) {
       put(&to->r_bad, bad << 32 | f2u(s.r));
     }
   }
-  if (!last_of(a.arrived + (size_t)b * kCounterWords, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
+  if (!last_of(a.arrived + (size_t)b * a.counter_words, (greedy ? a.G + 1u : a.rows) * a.splits, sh.flag)) return;
   join_rows(a, sh, b, c);
   if (threadIdx.x < 64u) decide(a, sh, b, c);
 }
@@ -652,6 +654,9 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   const double u = (double)a.v.u[(size_t)b * (a.G + 1u) + a.G];
   Chosen s = a.chosen[b];
   if (s.q == kNoDraw) return;
+  // (In a workspace that was not zero-filled the rows may never have been decided:
+  // whatever lies there then leads to none outside the tensors.)
+  if (s.row > a.G || (s.q == kQDraft && (s.row == a.G || !a.v.draft))) return;
   const double c = units_of(temperature);
   entries.fill(sh.table);
   const uint8_t* p = row_at<DT>(a, b, s.row);
@@ -663,7 +668,7 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
     const double sum = chunk_sum<DT>(a, s, p, q, i, c, sh.table, w);
     if (lane == 0u) put(sums + i, sum);
   }
-  if (!last_of(a.arrived + (size_t)(a.B + b) * kCounterWords, a.groups, sh.flag)) return;
+  if (!last_of(a.drawn + (size_t)b * kLineWords, a.groups, sh.flag)) return;
   if (wave != 0u) return;
   // A lane has a run of the chunks: the run, then the chunk, that passes the border;
   // the last with any weight, if none does.
@@ -724,13 +729,6 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args a) {
   if (lane == 0u) a.v.out[(size_t)b * (a.G + 1u) + s.row] = token;
 }
 
-// Workgroups of a row: enough for the chip, each with 4096 logits or more.
-uint32_t splits_of(int64_t B, int64_t rows, int64_t V) {
-  const int64_t n = B * rows, wanted = (kWantedGroups + n - 1) / n, most = std::max<int64_t>(V / 4096, 1);
-  return (uint32_t)std::min<int64_t>({wanted, most, kMaxSplits});
-}
-uint32_t chunks_of(int64_t V) { return (uint32_t)((V + kChunk - 1) / kChunk); }
-
 template <int DT>
 hipError_t launch(const Args& a, hipStream_t stream) {
   stats_kernel<DT><<<dim3(a.B * a.rows * a.splits), dim3(kRowThreads), 0, stream>>>(a);
@@ -742,38 +740,34 @@ hipError_t launch(const Args& a, hipStream_t stream) {
 
 }  // namespace
 
-// A launch takes at most kBatch sequences, whose counters come first: at one
-// place whatever the call, so that no call's data lie where another's counters do.
-static constexpr int64_t kBatch = 256;
-static constexpr size_t kCounterBytes = 2u * kBatch * kCounterWords * 4u;
-
 // For calls with and without draft logits.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
-  const int64_t n = std::min(B, kBatch);
-  if (n == 0) return 0u;
-  const int64_t with = n * (2 * G + 1) * splits_of(n, 2 * G + 1, V), without = n * (G + 1) * splits_of(n, G + 1, V);
-  return kCounterBytes + (size_t)std::max(with, without) * kRowWaves * sizeof(Part) + (size_t)n * chunks_of(V) * 8u +
-         (size_t)n * sizeof(Chosen);
+  const int64_t n = std::min(B, kVerifyBatch);
+  return n == 0 ? 0u : std::max(verify_layout(n, 2 * G + 1, V).total, verify_layout(n, G + 1, V).total);
 }
 
 hipError_t launch_verify(const Verify& v, hipStream_t stream) {
   Args a{};
-  const int64_t most = std::min(v.B, kBatch), size = v.dtype == kDtF32 ? 4 : 2;
+  const int64_t most = std::min(v.B, kVerifyBatch), size = v.dtype == kDtF32 ? 4 : 2;
   a.G = (uint32_t)v.G;
   a.V = (uint32_t)v.V;
   a.rows = (uint32_t)(v.draft ? 2 * v.G + 1 : v.G + 1);
-  a.splits = splits_of(most, a.rows, v.V);
-  a.chunks = chunks_of(v.V);
+  const VerifyLayout w = verify_layout(most, a.rows, v.V);
+  a.splits = w.splits;
+  a.chunks = w.chunks;
   // A wave has one chunk while the chip has room, and more in a large batch.
   a.per = std::max<uint32_t>(1u, (uint32_t)(most * a.chunks / kWantedWaves));
   a.groups = (a.chunks + a.per * kWaves - 1u) / (a.per * kWaves);
-  a.arrived = static_cast<uint32_t*>(v.workspace);
-  a.chosen = reinterpret_cast<Chosen*>(static_cast<uint8_t*>(v.workspace) + kCounterBytes);
-  a.sums = reinterpret_cast<double*>(a.chosen + most);
-  a.parts = reinterpret_cast<Part*>(a.sums + (size_t)most * a.chunks);
-  for (int64_t b = 0; b < v.B; b += kBatch) {
+  uint8_t* ws = static_cast<uint8_t*>(v.workspace);
+  a.arrived = reinterpret_cast<uint32_t*>(ws);
+  a.counter_words = w.counter_words;
+  a.drawn = reinterpret_cast<uint32_t*>(ws + w.drawn);
+  a.chosen = reinterpret_cast<Chosen*>(ws + w.chosen);
+  a.sums = reinterpret_cast<double*>(ws + w.sums);
+  a.parts = reinterpret_cast<Part*>(ws + w.parts);
+  for (int64_t b = 0; b < v.B; b += kVerifyBatch) {
     a.v = v;
-    a.B = (uint32_t)std::min(v.B - b, kBatch);
+    a.B = (uint32_t)std::min(v.B - b, kVerifyBatch);
     a.v.target = static_cast<const uint8_t*>(v.target) + b * v.target_seq * size;
     if (v.draft) a.v.draft = static_cast<const uint8_t*>(v.draft) + b * v.draft_seq * size;
     if (v.tokens) a.v.tokens = v.tokens + b * v.G;

@@ -1,12 +1,20 @@
-"""The sizes of the operators' workspaces (CPU)."""
+"""The operators' workspaces: their sizes, and where a verification's data lie (CPU)."""
+import ctypes
+import os
+import subprocess
+
 import pytest
 
 import block_scaled_fp4_03_amd as fp4
 
+HERE = os.path.dirname(os.path.abspath(__file__))
+CSRC = os.path.join(os.path.dirname(HERE), "block_scaled_fp4_03_amd", "csrc")
+# Vocabularies around what a workgroup, a lane's run of chunks and all splits take.
+VOCABS = (1, 511, 513, 4095, 8191, 8192, 40000, 100003, 131072, 131073, 300001, 1 << 24)
+
 
 @pytest.fixture(scope="module", autouse=True)
 def library():
-    import os
     if not os.path.exists(fp4.LIB_PATH):
         import block_scaled_fp4_03_amd.build as b
         b.build()
@@ -18,3 +26,30 @@ def test_empty_calls_need_none():
     assert fp4.fp4_verify_drafts_workspace(0, 0, 1) == 0
     assert fp4.fp4_moe_sort_workspace(0, 4, 8) == 0 and fp4.fp4_moe_sort_workspace(4, 0, 8) == 0
     assert fp4.fp4_qk_norm_rope_workspace(0, 4, 2, 64) == 0 and fp4.fp4_qk_norm_rope_workspace(4, 0, 0, 64) == 0
+
+
+@pytest.fixture(scope="module")
+def layout(tmp_path_factory):
+    so = str(tmp_path_factory.mktemp("workspace") / "workspace_check.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-shared", "-fPIC", "-I", CSRC,
+                    os.path.join(HERE, "workspace_check.cpp"), "-o", so], check=True)
+    L = ctypes.CDLL(so)
+    I64 = ctypes.c_int64
+    L.verify_layout_check.argtypes = [I64, I64, I64, ctypes.c_void_p, ctypes.c_char_p, ctypes.c_size_t]
+    L.control_bytes.restype = ctypes.c_size_t
+    return L
+
+
+def test_verification_keeps_to_its_places(layout):
+    """Row counters within the control words, everything else behind them and apart,
+    and all of it within the size that the library asks for."""
+    total, msg = ctypes.c_size_t(), ctypes.create_string_buffer(256)
+    for B in (1, 2, 3, 5, 8, 16, 17, 33, 64, 100, 129, 255, 256):
+        for G in (0, 1, 4, 7, 32):
+            for V in VOCABS:
+                need = fp4.fp4_verify_drafts_workspace(B, G, V)
+                for rows in {G + 1, 2 * G + 1}:
+                    what = "%d sequences, %d rows of %d: " % (B, rows, V)
+                    rc = layout.verify_layout_check(B, rows, V, ctypes.byref(total), msg, 256)
+                    assert rc == 0, what + msg.value.decode()
+                    assert total.value <= need, what
