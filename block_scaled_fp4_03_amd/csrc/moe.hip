@@ -24,6 +24,7 @@
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
+#include "workspace.h"
 
 #include <type_traits>
 
@@ -628,14 +629,14 @@ static uint32_t sort_chunks(int64_t entries) {
 
 size_t moe_sort_workspace(int64_t entries, int64_t E) {
   const size_t chunks = sort_chunks(entries);
-  return chunks <= 1u ? 0u : (chunks + 1u) * (size_t)(E + 1) * 4u;
+  return chunks <= 1u ? 0u : kControlBytes + (chunks + 1u) * (size_t)(E + 1) * 4u;
 }
 
 hipError_t launch_moe_sort(const int32_t* ids, int64_t T, int32_t k, int64_t E, int32_t* group_off, int32_t* row_idx,
                            int32_t* pos, void* workspace, hipStream_t s) {
   const int64_t entries = T * k;
   const uint32_t n = (uint32_t)entries, bins = (uint32_t)E + 1u, chunks = sort_chunks(entries);
-  uint32_t* counts = chunks > 1u ? static_cast<uint32_t*>(workspace) : nullptr;
+  uint32_t* counts = chunks > 1u ? reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + kControlBytes) : nullptr;
   uint32_t bits = 1u;
   while ((1u << bits) < (uint32_t)E + 2u) ++bits;
   const size_t lds = kSortWaves * (size_t)(E + 2) * 4u;

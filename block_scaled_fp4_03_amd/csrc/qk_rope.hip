@@ -19,6 +19,7 @@
 #include "fp4_device.h"
 #include "fp4_launch.h"
 #include "kv_device.h"
+#include "workspace.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -462,8 +463,9 @@ hipError_t launch_lanes(Args& s, const QkRope& a, hipStream_t stream) {
 template <bool BACKWARD>
 hipError_t launch(const QkRope& a, hipStream_t stream) {
   Args s{};
+  float* partial = a.workspace ? reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kControlBytes) : nullptr;
   s.t[0] = Heads{{a.q, a.q_stride}, {a.gq, a.gq_stride}, {a.oq, a.oq_stride}, a.wq,
-                 static_cast<float*>(a.workspace), (uint32_t)a.hq, 0u, 0u, 0u};
+                 partial, (uint32_t)a.hq, 0u, 0u, 0u};
   s.t[1] = Heads{{a.k, a.k_stride}, {a.gk, a.gk_stride}, {a.ok, a.ok_stride}, a.wk, nullptr, (uint32_t)a.hk, 0u, 0u, 0u};
   s.freq = a.freq;
   s.pos = a.pos;
@@ -484,12 +486,13 @@ hipError_t launch(const QkRope& a, hipStream_t stream) {
 
 }  // namespace
 
-// Room for a sum of each workgroup: they are no more than heads of all rows, nor than
-// kMaxGroups and one (of q or of k, where that would have none).
+// Room for a sum of each workgroup, behind the control words: they are no more than heads
+// of all rows, nor than kMaxGroups and one (of q or of k, where that would have none).
 size_t qk_rope_workspace(int64_t rows, int64_t heads, int64_t D) {
-  constexpr int64_t kRoom = 1024;
-  static_assert(2 * kRoom >= kMaxGroups + 1);
-  return (size_t)std::min(rows * heads, kRoom) * 2u * (size_t)D * 4u;
+  constexpr size_t kRoom = 2048, kLeast = 32 * 4;  // sums, and bytes of one (D is 32 at least)
+  static_assert((kRoom - (kMaxGroups + 1u)) * kLeast >= kControlBytes);
+  const size_t all = (size_t)(rows * heads), sum = (size_t)D * 4u;
+  return all == 0u ? 0u : std::min(kControlBytes + all * 2u * sum, kRoom * sum);
 }
 hipError_t launch_qk_rope(const QkRope& a, hipStream_t stream) { return launch<false>(a, stream); }
 hipError_t launch_qk_rope_backward(const QkRope& a, hipStream_t stream) { return launch<true>(a, stream); }

@@ -154,8 +154,12 @@ int64_t fp4_scale_bytes(int fmt, int64_t rows, int64_t K);
  * workspace.  A workspace must be zero-filled once before its first use; every
  * call leaves the control words zero again when its work on the stream
  * completes, so one zero-filled workspace of the largest size needed serves
- * any sequence of calls.  Calls that share one workspace must be ordered (same
- * stream, or events); calls that overlap on one workspace race.  Host-only. */
+ * any sequence of calls, of these and of the operators below; all keep what
+ * else they leave there behind the first 2 KB.  The one exception is
+ * fp4_gemm_grouped's copy, which begins at the workspace's first byte: an
+ * operation with control words needs them zero-filled again after it.  Calls that
+ * share one workspace must be ordered (same stream, or events); calls that
+ * overlap on one workspace race.  Host-only. */
 size_t fp4_workspace_size(int op, int fmt, int64_t M, int64_t N, int64_t K, int32_t E);
 
 /* Quantise a rows x K matrix x (K contiguous) of `in_dtype` (FP32 or BF16).
@@ -609,7 +613,8 @@ int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, in
                      void* k_out, int64_t k_out_stride, int64_t rows, void* stream);
 
 /* Workspace bytes of fp4_qk_norm_rope_backward (0: none needed, also for
- * invalid arguments).  It holds no control words: no zero-fill needed. */
+ * invalid arguments).  No zero-fill needed; the control words of others are left
+ * alone. */
 size_t fp4_qk_norm_rope_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim);
 
 /* Gradient of fp4_qk_norm_rope: from the gradients gq, gk of its outputs and
@@ -649,7 +654,7 @@ int fp4_moe_route_backward(const void* logits, int dtype, int64_t stride, int64_
                            int renormalise, const int32_t* ids, const float* g, void* dlogits, void* stream);
 
 /* Workspace bytes of fp4_moe_sort (0: none needed, also for invalid
- * arguments).  No zero-fill needed. */
+ * arguments).  No zero-fill needed; the control words of others are left alone. */
 size_t fp4_moe_sort_workspace(int64_t T, int32_t top_k, int64_t E);
 
 /* The T * top_k entries of ids (T x top_k, device int32) in the order of their

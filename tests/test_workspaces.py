@@ -53,3 +53,15 @@ def test_verification_keeps_to_its_places(layout):
                     rc = layout.verify_layout_check(B, rows, V, ctypes.byref(total), msg, 256)
                     assert rc == 0, what + msg.value.decode()
                     assert total.value <= need, what
+
+
+def test_partial_sums_have_room_behind_the_control_words(layout):
+    """The least data of a sort and of a gradient of norms, and the control words."""
+    words = layout.control_bytes()
+    for E in (1, 32, 512):
+        for T in (2049, 8192, 524288, 524289, 1 << 22):
+            chunk = 2048 if T <= 524288 else 8192
+            assert fp4.fp4_moe_sort_workspace(T, 1, E) >= words + (-(-T // chunk) + 1) * (E + 1) * 4
+    for D in (32, 64, 256):
+        for rows, q, k in ((1, 1, 0), (1, 1, 1), (7, 5, 1), (640, 1, 1), (1 << 20, 64, 8)):
+            assert fp4.fp4_qk_norm_rope_workspace(rows, q, k, D) >= words + min(rows * (q + k), 1281) * D * 4
