@@ -26,6 +26,7 @@
 #include "kv_device.h"
 #include "workspace.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace fp4 {
@@ -627,8 +628,10 @@ static uint32_t sort_chunks(int64_t entries) {
   return (uint32_t)((entries + chunk - 1) / chunk);
 }
 
+// What any call of as many entries or fewer takes (small chunks are more than the first large ones).
 size_t moe_sort_workspace(int64_t entries, int64_t E) {
-  const size_t chunks = sort_chunks(entries);
+  const int64_t few = std::min(entries, (int64_t)kFewChunks * kSortThreads * kFewRounds);
+  const size_t chunks = std::max(sort_chunks(entries), sort_chunks(few));
   return chunks <= 1u ? 0u : kControlBytes + (chunks + 1u) * (size_t)(E + 1) * 4u;
 }
 

@@ -654,7 +654,8 @@ int fp4_moe_route_backward(const void* logits, int dtype, int64_t stride, int64_
                            int renormalise, const int32_t* ids, const float* g, void* dlogits, void* stream);
 
 /* Workspace bytes of fp4_moe_sort (0: none needed, also for invalid
- * arguments).  No zero-fill needed; the control words of others are left alone. */
+ * arguments); enough for any smaller call too.  No zero-fill needed; the control
+ * words of others are left alone. */
 size_t fp4_moe_sort_workspace(int64_t T, int32_t top_k, int64_t E);
 
 /* The T * top_k entries of ids (T x top_k, device int32) in the order of their

@@ -65,3 +65,30 @@ def test_partial_sums_have_room_behind_the_control_words(layout):
     for D in (32, 64, 256):
         for rows, q, k in ((1, 1, 0), (1, 1, 1), (7, 5, 1), (640, 1, 1), (1 << 20, 64, 8)):
             assert fp4.fp4_qk_norm_rope_workspace(rows, q, k, D) >= words + min(rows * (q + k), 1281) * D * 4
+
+
+def never_less(size, *ranges):
+    """size(*args) never falls as any one of its arguments grows over its range."""
+    for at in range(len(ranges)):
+        others = [[]]
+        for i, r in enumerate(ranges):
+            others = [o + [v] for o in others for v in ([None] if i == at else r)]
+        for o in others:
+            before = 0
+            for v in ranges[at]:
+                args = o[:at] + [v] + o[at + 1:]
+                now = size(*args)
+                assert now >= before, "%s: %d, %d with one argument less" % (args, now, before)
+                before = now
+
+
+def test_a_sort_workspace_serves_smaller_calls():
+    T = sorted({m * n + d for m in (1, 64, 256, 1024, 2048, 8192) for n in (1, 3, 16, 63, 64, 65, 255, 256, 257, 1000)
+                for d in (-1, 0, 1)})
+    never_less(fp4.fp4_moe_sort_workspace, T, range(65), (1, 2, 32, 128, 512))
+    assert fp4.fp4_moe_sort_workspace(131072, 8, 128) >= fp4.fp4_moe_sort_workspace(65536, 8, 128)
+
+
+def test_a_workspace_of_the_norms_gradient_serves_smaller_calls():
+    never_less(fp4.fp4_qk_norm_rope_workspace, (0, 1, 2, 5, 100, 128, 255, 1024, 1025, 1 << 20), range(0, 65, 3), range(17),
+               (32, 64, 72, 128, 256))
