@@ -740,10 +740,10 @@ hipError_t launch(const Args& a, hipStream_t stream) {
 
 }  // namespace
 
-// For calls with and without draft logits.
+// For calls with and without draft logits, and any smaller ones.
 size_t verify_workspace(int64_t B, int64_t G, int64_t V) {
   const int64_t n = std::min(B, kVerifyBatch);
-  return n == 0 ? 0u : std::max(verify_layout(n, 2 * G + 1, V).total, verify_layout(n, G + 1, V).total);
+  return n == 0 ? 0u : verify_bytes(n, 2 * G + 1, V);
 }
 
 hipError_t launch_verify(const Verify& v, hipStream_t stream) {

@@ -48,5 +48,12 @@ inline VerifyLayout verify_layout(int64_t n, int64_t rows, int64_t V) {
   return w;
 }
 static_assert(kControlBytes / 4 >= kVerifyBatch, "a row counter of each sequence");
+// What calls of up to n sequences, rows and logits take at most.  (The number of splits falls
+// as rows are added, and with it all rows' parts, by less than what one split of each is.)
+inline size_t verify_bytes(int64_t n, int64_t rows, int64_t V) {
+  const int64_t all = n * rows, most = std::min(std::max<int64_t>(V / 4096, 1), kVerifyMaxSplits);
+  const int64_t groups = std::min(all * most, all + kVerifyWantedGroups - 1);
+  return verify_layout(n, rows, V).parts + (size_t)(groups * kVerifyRowWaves) * kVerifyPartBytes;
+}
 
 }  // namespace fp4

@@ -613,8 +613,8 @@ int fp4_qk_norm_rope(const fp4_rope* rope, const int32_t* pos, const void* q, in
                      void* k_out, int64_t k_out_stride, int64_t rows, void* stream);
 
 /* Workspace bytes of fp4_qk_norm_rope_backward (0: none needed, also for
- * invalid arguments).  No zero-fill needed; the control words of others are left
- * alone. */
+ * invalid arguments); enough for any smaller call too.  No zero-fill needed; the
+ * control words of others are left alone. */
 size_t fp4_qk_norm_rope_workspace(int64_t rows, int64_t q_heads, int64_t k_heads, int64_t head_dim);
 
 /* Gradient of fp4_qk_norm_rope: from the gradients gq, gk of its outputs and
@@ -706,7 +706,8 @@ int fp4_moe_combine_backward(const void* g, int64_t stride, const void* y, int d
 /* ---- Behind the head: drafted tokens. ---- */
 
 /* Workspace bytes of fp4_verify_drafts (0: none needed, for B == 0 and invalid
- * arguments).  It must be zero-filled once; calls leave its control words zero. */
+ * arguments); enough for any smaller call too, with and without draft logits.  It
+ * must be zero-filled once; calls leave its control words zero. */
 size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V);
 
 /* Verify up to G drafted tokens of each of B sequences against the target's

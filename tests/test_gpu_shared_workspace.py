@@ -115,3 +115,25 @@ def test_graphs_on_one_workspace():
             i = (5 * turn + half) % len(calls)
             assert all(torch.equal(a, b) for a, b in zip(calls[i][2](ws), want[i]))
             torch.cuda.synchronize()
+
+
+def test_a_workspace_serves_smaller_calls():
+    """Sizes where a smaller call has more counters or parts than the larger one that the
+    workspace was made for."""
+    import torch
+    import block_scaled_fp4_03_amd as fp4
+    g = torch.Generator(device="cuda").manual_seed(43)
+    ws = fp4.moe_sort_workspace(131072, 8, 128)
+    for T in (131072, 65536, 2000):
+        say("sort of %d, a larger call's workspace" % (T * 8))
+        ids = torch.randint(-1, 128, (T, 8), generator=g, device="cuda").to(torch.int32)
+        assert all(torch.equal(a, b) for a, b in zip(fp4.moe_sort(ids, 128, ws=ws), fp4.moe_sort(ids, 128)))
+    ws = fp4.verify_workspace(64, 3, 131072)
+    for B, G, draft in ((64, 3, True), (58, 3, True), (33, 2, False), (9, 1, True), (1, 0, False)):
+        say("verification of %d, a larger call's workspace" % B)
+        target = torch.randn((B, G + 1, 131072), generator=g, device="cuda").to(torch.bfloat16)
+        d = target[:, :G] * 0.9 if draft else None
+        tokens = target[:, :G].float().argmax(2).to(torch.int32)
+        u = torch.rand((B, G + 1), generator=g, device="cuda")
+        a, b = (fp4.verify_drafts(target, d, tokens, u, ws=w) for w in (ws, None))
+        assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -92,3 +92,10 @@ def test_a_sort_workspace_serves_smaller_calls():
 def test_a_workspace_of_the_norms_gradient_serves_smaller_calls():
     never_less(fp4.fp4_qk_norm_rope_workspace, (0, 1, 2, 5, 100, 128, 255, 1024, 1025, 1 << 20), range(0, 65, 3), range(17),
                (32, 64, 72, 128, 256))
+
+
+def test_a_verification_workspace_serves_smaller_calls():
+    size = fp4.fp4_verify_drafts_workspace
+    never_less(size, list(range(0, 300)) + [1000, 20000], (0, 1, 2, 3, 4, 7, 8, 31, 32), (1, 5003, 8192, 100003, 131072, 1 << 19))
+    never_less(size, (1, 2, 58, 64, 227, 256), range(33), VOCABS)
+    assert size(256, 4, 131072) >= size(227, 4, 131072) and size(64, 3, 131072) >= size(58, 3, 131072)
