@@ -699,15 +699,43 @@ def _want_rows(t, name, ndim, device=None, like=None):
     return code, strides[0]
 
 
+class _OtherDevice(ValueError):
+    """A call's null stream is that of a device which is not the current one."""
+
+    def __init__(self, device):
+        self.device = device
+        super().__init__("the call's stream is the null stream of %s, which is not the current device" % device)
+
+
 def _run_on(stream, device):
     """The raw handle of the stream a call runs on: the given one, or the
-    device's current one.  The null stream is that of the current device, so
-    operands on another one are refused there (its other streams are its own)."""
-    C = _torch()._C
-    raw = stream.cuda_stream if stream is not None else C._cuda_getCurrentRawStream(device.index)
+    operands' device's current one.  The null stream has no handle of its own
+    (it is that of the current device; the other streams know theirs): where its
+    device is not the current one, _OtherDevice is raised."""
+    C = (_torch_module or _torch())._C
+    if stream is None:
+        raw = C._cuda_getCurrentRawStream(device.index)
+    else:
+        raw = stream.cuda_stream
+        if raw == 0:
+            device = stream.device
     if raw == 0 and C._cuda_getDevice() != device.index:
-        raise ValueError("the operands are on %s, which is not the current device" % device)
+        raise _OtherDevice(device)
     return raw
+
+
+def _on_its_device(call):
+    """A call that comes to _run_on before anything else of it is under way: made
+    again, where that raises _OtherDevice, with that device current."""
+    @functools.wraps(call)
+    def run(*args, **kw):
+        try:
+            return call(*args, **kw)
+        except _OtherDevice as e:
+            device = e.device
+        with _torch().cuda.device(device):
+            return call(*args, **kw)
+    return run
 
 
 def _alloc(stream, make, *args, **kw):
@@ -800,6 +828,7 @@ def _need_cache(cache, name="cache"):
     return cache.device
 
 
+@_on_its_device
 def kv_append(cache, k, v, table, seq, pos, stream=None):
     """Write new keys and values (n x kv_heads x head_dim float32/bfloat16, any
     row stride) into the cache: row i becomes token pos[i] of sequence seq[i]
@@ -833,6 +862,7 @@ def attention_workspace(cache, batch, q_heads, max_len, weights=False):
     return torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
 
 
+@_on_its_device
 def decode_attention(q, cache, table, lens, max_len=None, window=0, scale=None, out=None, out_dtype=None, lse=None,
                      weights=None, weights_out=None, ws=None, stream=None):
     """Attention of one new token per sequence over the paged cache; see
@@ -898,6 +928,7 @@ def evict_workspace(cache, batch, max_len, budget):
     return torch.zeros(n, dtype=torch.uint8, device=dev) if n else None
 
 
+@_on_its_device
 def kv_evict(cache, table, lens, weights, budget, recent, out_table, out_cache=None, ws=None, stream=None):
     """Keep `budget` tokens of every longer (sequence, kv head): the last
     `recent` and the largest accumulated attention weights; see fp4_kv_evict
@@ -960,6 +991,7 @@ def logprobs_workspace(n, vocab, top_k=0, device="cuda"):
     return torch.zeros(b, dtype=torch.uint8, device=device) if b else None
 
 
+@_on_its_device
 def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
     """Log probabilities of the given tokens (int32 N x M; outside [0, V):
     padding, 0) under softmax(scale * x), x: N x V float32/bfloat16 logits
@@ -996,6 +1028,7 @@ def logprobs(x, tokens, top_k=0, scale=1.0, ws=None, stream=None):
     return LogProbs(logp, entropy, lse, top, index)
 
 
+@_on_its_device
 def logprobs_backward(x, tokens, lse, g_logp, entropy=None, g_entropy=None, scale=1.0, out=None, stream=None):
     """Gradient of logprobs with respect to x from the gradients of logp
     (N x M) and, if given, of the entropy (N; then entropy too); lse and
@@ -1107,6 +1140,7 @@ def _want_weight(t, name, dim, dev):
         raise ValueError("%s holds %d values, a head %d" % (name, t.shape[0], dim))
 
 
+@_on_its_device
 def qk_norm_rope(q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, q_out=None, k_out=None, stream=None):
     """Norms of queries and keys for each head (over head_dim, times q_weight /
     k_weight; left out where that is None) and the rotation of their positions,
@@ -1146,6 +1180,7 @@ def qk_norm_rope_workspace(rows, q_heads, k_heads, head_dim, device="cuda"):
     return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
 
 
+@_on_its_device
 def qk_norm_rope_backward(gq, gk, q, k, rope, pos, q_weight=None, k_weight=None, eps=1e-6, dq=None, dk=None, ws=None,
                           stream=None):
     """Gradient of qk_norm_rope from the gradients gq, gk of its results (of
@@ -1189,6 +1224,7 @@ def qk_norm_rope_backward(gq, gk, q, k, rope, pos, q_weight=None, k_weight=None,
 
 
 # ---- around the grouped GEMM: routing, rows to the experts' order and back -----
+@_on_its_device
 def moe_route(logits, top_k, renormalise=True, stream=None):
     """The top_k <= 16 experts of each token (ties to the lowest) and their
     weights: the softmax over the chosen logits, or with renormalise False that
@@ -1209,6 +1245,7 @@ def moe_route(logits, top_k, renormalise=True, stream=None):
     return ids, weights
 
 
+@_on_its_device
 def moe_route_backward(logits, ids, g, renormalise=True, stream=None):
     """Gradient of moe_route's weights with respect to the logits, from theirs
     (g, float32 T x top_k); see fp4_moe_route_backward in include/fp4.h.
@@ -1240,6 +1277,7 @@ def moe_sort_workspace(tokens, top_k, experts, device="cuda"):
     return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
 
 
+@_on_its_device
 def moe_sort(ids, experts, ws=None, stream=None):
     """The entries of ids (int32 T x top_k) in the order of their experts; see
     fp4_moe_sort in include/fp4.h.  An id outside [0, experts) is taken by no
@@ -1265,6 +1303,7 @@ def moe_sort(ids, experts, ws=None, stream=None):
     return off, rows, pos
 
 
+@_on_its_device
 def moe_gather(x, pos, out=None, stream=None):
     """Rows of x (T x H float32/bfloat16, any row stride) in expert order: row
     pos[t, j] of the result is x[t]; see fp4_moe_gather in include/fp4.h.  pos as
@@ -1304,6 +1343,7 @@ def _want_entries(y, pos, weights):
     return _dtype_code(y), dev, pos.shape[0], pos.shape[1], y.shape[1]
 
 
+@_on_its_device
 def moe_combine(y, pos, weights=None, out=None, stream=None):
     """Rows of y (dense, in expert order) joined to tokens: sum over j of
     weights[t, j] (float32; None: 1) times y[pos[t, j]]; see fp4_moe_combine in
@@ -1323,6 +1363,7 @@ def moe_combine(y, pos, weights=None, out=None, stream=None):
     return out
 
 
+@_on_its_device
 def moe_combine_backward(g, y, pos, weights, dy=None, stream=None):
     """Gradient of moe_combine from that of its result (g, T x H of y's dtype,
     any row stride); see fp4_moe_combine_backward in include/fp4.h.  Returns
@@ -1377,6 +1418,7 @@ def _want_logits(t, name, rows, device=None, like=None):
     return code, t.stride(0), t.stride(1)
 
 
+@_on_its_device
 def verify_drafts(target, draft, tokens, u, temperature=None, ws=None, stream=None):
     """Verify drafted tokens against the target's probabilities with given
     random numbers, and draw the token that follows the last one kept; see
