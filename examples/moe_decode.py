@@ -108,10 +108,11 @@ def run(steps=16, batch=4, drafts=3, prompt=40, hidden=512, q_heads=8, kv_heads=
         rows = torch.stack([last.to(torch.int32)] + drafted, 1)
         pos = (lens[:, None] + ahead).reshape(-1)
         logits = layer.forward(rows.long().reshape(-1), step_seq, pos, cache, table).view(batch, drafts + 1, vocab)
-        # (The two models are unrelated; some of the draft's logits make some of its tokens welcome.)
-        logits[:, :drafts] += 1.5 * torch.stack(draft_logits, 1)
         u = torch.rand(batch, drafts + 1, generator=g, device="cuda")
-        drafted, draft_logits = torch.stack(drafted, 1), torch.stack(draft_logits, 1)
+        # (Without drafts a step draws one token from the target's distribution.)
+        drafted, draft_logits = rows[:, 1:].contiguous(), torch.stack(draft_logits, 1) if drafts else None
+        if drafts:   # (the two models are unrelated: some of the draft's logits make some of its tokens welcome)
+            logits[:, :drafts] += 1.5 * draft_logits
         out, kept, chance = fp4.verify_drafts(logits, draft_logits, drafted, u, temperature, ws=ws)
         last = out.gather(1, kept.long()[:, None])[:, 0].long()
         lens = lens + kept + 1
