@@ -732,7 +732,8 @@ size_t fp4_verify_drafts_workspace(int64_t B, int64_t G, int64_t V);
  *   sequence b at element b * seq_stride + i * row_stride, aligned to the element
  *   size.  tokens: int32 B x G, u: FP32 B x (G + 1), in [0, 1), dense.
  *   B < 2^16, 0 <= G <= 32, 1 <= V <= 2^24, B * (2G + 1) * V <= 2^40.
- *   Exponentials and sums in FP64, in a fixed order.
+ *   Exponentials and sums in FP64, in a fixed order; an exponential below 2^-1000
+ *   of its row's largest counts as 0.
  * B == 0 is a no-op. */
 int fp4_verify_drafts(const void* target, int64_t target_seq_stride, int64_t target_row_stride, const void* draft,
                       int64_t draft_seq_stride, int64_t draft_row_stride, int dtype, int64_t B, int64_t G, int64_t V,
